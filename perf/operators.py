@@ -108,17 +108,10 @@ def _activations(g, rows, K):
 
 def _weights_mx4(g, rows, K):
     """Row-major MX4 codes [rows, K/2] and scales [rows, K/32] of N(0, s^2 / K) rows with
-    a spread of row scales s, a stretch of rows at a time."""
-    codes = torch.empty(rows, K // 2, dtype=torch.uint8, device="cuda")
-    scales = torch.empty(rows, K // BLOCK, dtype=torch.uint8, device="cuda")
-    step = max(1, (1 << 26) // K)
-    for r in range(0, rows, step):
-        n = min(step, rows - r)
-        w = _randn(g, n, K) * (torch.exp(0.5 * _randn(g, n, 1)) / math.sqrt(K))
-        c, s = _quantize_plain(w)
-        codes[r:r + n] = c[:, 0::2] | (c[:, 1::2] << 4)
-        scales[r:r + n] = s
-    return codes, scales
+    a spread of row scales s."""
+    w = _randn(g, rows, K) * (torch.exp(0.5 * _randn(g, rows, 1)) / math.sqrt(K))
+    c, s = _quantize_plain(w)
+    return c[:, 0::2] | (c[:, 1::2] << 4), s
 
 
 def _inputs(case, seed):
@@ -229,12 +222,10 @@ def _moe_plain(s):
 
     guc, gus = (a.view(E, 2 * I, -1) for a in s["gate_up"])
     dnc, dns = (a.view(E, H, -1) for a in s["down"])
-    y = torch.empty(T, H, dtype=torch.float32, device="cuda")
-    for t in range(T):
-        e = idx[t]
-        h = swiglu(x[t].expand(k, 1, H), _weight_plain(guc[e], gus[e]))
-        o = h @ _weight_plain(dnc[e], dns[e]).transpose(-1, -2)
-        y[t] = (w[t].view(k, 1) * o.view(k, H)).sum(dim=0)
+    # every (token, choice) with its expert's weights beside it
+    h = swiglu(x.view(T, 1, 1, H).expand(T, k, 1, H), _weight_plain(guc[idx], gus[idx]))
+    o = h @ _weight_plain(dnc[idx], dns[idx]).transpose(-1, -2)
+    y = (w.unsqueeze(2) * o.view(T, k, H)).sum(dim=1)
     if s["shared"]:
         o = swiglu(x, _weight_plain(*s["shared"][0])) @ _weight_plain(*s["shared"][1]).t()
         if s["gate_w"] is not None:
@@ -302,24 +293,19 @@ def _values64(codes, scales):
 def _nearest64(x):
     """float64 values of x after MX4 quantization: the nearest of the code magnitudes
     under the block's scale, ties to the code whose last bit is 0."""
-    rows, K = x.shape
-    step = max(1, (1 << 25) // K)
-    out = torch.empty(rows, K, dtype=torch.float64, device=x.device)
     grid = torch.tensor(E2M1, dtype=torch.float64, device=x.device)
     mid = (grid[1:] + grid[:-1]) / 2
-    for r in range(0, rows, step):
-        b = x[r:r + step].double().reshape(-1, BLOCK)
-        big = b.abs().max(dim=1, keepdim=True)[0]
-        lg = torch.floor(torch.log2(torch.clamp(big, min=2.0 ** -140)))
-        lg = torch.where(_exp2_64(lg) > big, lg - 1, lg)          # log2 next to a power of two
-        lg = torch.where(_exp2_64(lg + 1) <= big, lg + 1, lg)
-        unit = _exp2_64(torch.clamp(lg - 2, min=-127.0))
-        a = (b / unit).abs()
-        lo = torch.bucketize(a, mid, right=False)                       # a tie stays with the lower code
-        hi = torch.bucketize(a, mid, right=True)                        # a tie goes to the upper code
-        code = torch.where(lo % 2 == 0, lo, hi)
-        out[r:r + step] = (torch.sign(b) * grid[code] * unit).reshape(-1, K)
-    return out
+    b = x.double().reshape(-1, BLOCK)
+    big = b.abs().max(dim=1, keepdim=True)[0]
+    lg = torch.floor(torch.log2(torch.clamp(big, min=2.0 ** -140)))
+    lg = torch.where(_exp2_64(lg) > big, lg - 1, lg)                    # log2 next to a power of two
+    lg = torch.where(_exp2_64(lg + 1) <= big, lg + 1, lg)
+    unit = _exp2_64(torch.clamp(lg - 2, min=-127.0))
+    a = (b / unit).abs()
+    lo = torch.bucketize(a, mid, right=False)                           # a tie stays with the lower code
+    hi = torch.bucketize(a, mid, right=True)                            # a tie goes to the upper code
+    code = torch.where(lo % 2 == 0, lo, hi)
+    return (torch.sign(b) * grid[code] * unit).reshape(x.shape)
 
 
 def _moe64(case, d):
