@@ -279,6 +279,79 @@ moe_status q8_pack_rows16(const void *w_rows, int64_t N, int64_t K, void *w_tile
                             void *stream);
 
 /*
+ * Microscaled 4-bit matrices (MX4): FP4 E2M1 elements (sign in bit 3, magnitudes 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6) in blocks of 32 consecutive columns of one row, one E8M0 scale byte
+ * per block:  W[r][c] = 2^(scale[r][c/32] - 127) * e2m1(code[r][c]);  scale 255 makes the
+ * block NaN.  Two layouts hold the same codes and scales:
+ *   MX4_ROWS   codes [rows][K/2], column 2i in the low nibble of byte i, 2i+1 in the high;
+ *              scales [rows][K/32].  The interchange layout.
+ *   MX4_TILES  what the products read, rows in panels of 16 and columns in steps of 128
+ *              (S = ceil(K/128) steps, P = ceil(rows/16) panels):  codes [P][S][64][16],
+ *              entry n + 16 g of tile (p, s) = row 16p + n, columns 128s + 32g .. +31 in
+ *              the byte order of MX4_ROWS;  scales [P][ceil(S/4)][64][4], byte i of entry
+ *              n + 16 g of (p, q) = row 16p + n, block 4 (4q + i) + g.  Rows and columns
+ *              past the matrix hold zeros.
+ * mx4_codes_size / mx4_scales_size: bytes of the two buffers (SIZE_MAX when a size or the
+ * layout is outside the limits).
+ * Limits of every mx4_ call (else MOE_ERR_UNSUPPORTED): K % 32 == 0, 32 <= K <= 65536,
+ * rows, N <= 2^26, T <= 2^20.  Zero rows (T == 0, N == 0) enqueue nothing.  codes buffers
+ * are 16-byte aligned, scales buffers 4-byte; matrices of values have 16-byte aligned rows
+ * (base pointer and row stride; strides ldx, ldy are in elements, >= the row's length),
+ * except y of the products, which only needs its element's alignment.
+ */
+#define MX4_ROWS  0
+#define MX4_TILES 1
+size_t mx4_codes_size(int64_t rows, int64_t K, int32_t layout);
+size_t mx4_scales_size(int64_t rows, int64_t K, int32_t layout);
+
+/*
+ * Quantization.  Per block, e = floor(log2(max|x|)) - 2, scale = clamp(e, -127, 127) + 127
+ * (a zero block: 0); each code is x / 2^e rounded to the nearest, ties to the even code,
+ * saturating at 6, the sign kept (of zeros too).  A block that holds a NaN or an infinity
+ * becomes a NaN block (scale 255, codes 0).
+ *   x       [rows][K], x_dtype MOE_BF16, MOE_F16 or MOE_F32, row stride ldx
+ *   codes, scales   in `layout`, written whole (padding of MX4_TILES included)
+ */
+moe_status mx4_quantize(const void *x, int32_t x_dtype, int64_t rows, int64_t K, int64_t ldx, int32_t layout,
+                        void *codes, void *scales, void *stream);
+
+/*
+ * The values of an MX4 matrix: y [rows][K], row stride ldy, y_dtype MOE_BF16 or MOE_F32
+ * (exact wherever the value exists in the type) or MOE_F16 (one rounding to nearest even;
+ * infinity past its range).
+ */
+moe_status mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t K, int32_t layout,
+                          void *y, int32_t y_dtype, int64_t ldy, void *stream);
+
+/*
+ * Load-time repacking MX4_ROWS -> MX4_TILES (byte moves; source and destination must not
+ * overlap).  A stack of matrices whose row count is a multiple of 16 is repacked as one
+ * matrix of all its rows.
+ */
+moe_status mx4_pack_rows16(const void *codes, const void *scales, int64_t rows, int64_t K,
+                           void *t_codes, void *t_scales, void *stream);
+
+/*
+ * Products with an MX4 weight matrix in MX4_TILES (N rows, K columns), fp32 accumulation:
+ *     mx4_gemm        y[t][n] = sum_c x[t][c] W[n][c],  x [T][K] bf16, row stride ldx
+ *     mx4_gemm_mx4x   the same with x quantized: x_codes, x_scales hold T rows in MX4_TILES
+ *   y   [T][N], row stride ldy, y_dtype MOE_BF16 (rounded to nearest even) or MOE_F32
+ *   ws  device workspace of ws_bytes >= mx4_gemm_workspace_size(N, K, T) (NULL when that is
+ *       0), 256-byte aligned, contents undefined before and after; calls that share it must
+ *       not overlap in time.
+ * Every product is exact; only the fp32 sums round (and y, where it is bf16).  A NaN or
+ * infinity in x makes its token's row of y NaN or infinite as the sum says (mx4x: NaN, as the
+ * block is), and only it; a NaN block of W makes its column of y NaN.
+ * A token's result may depend on T (the order of its sums), not on the other tokens.
+ */
+size_t mx4_gemm_workspace_size(int64_t N, int64_t K, int64_t T);
+moe_status mx4_gemm(const void *w_codes, const void *w_scales, int64_t N, int64_t K, const void *x, int64_t T,
+                    int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+moe_status mx4_gemm_mx4x(const void *w_codes, const void *w_scales, int64_t N, int64_t K, const void *x_codes,
+                         const void *x_scales, int64_t T, void *y, int32_t y_dtype, int64_t ldy,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Measured ceilings ([LILY] "Limits of further optimization": kernels are judged
  * against the fastest sustained rate of their resource, next to the data-sheet peak).
  * Measurement helpers only; they compute nothing the layer uses.

@@ -6,7 +6,8 @@ device memory and the current stream; outputs and workspaces the caller does not
 are allocated here with torch.  The functions carry the names of the C entry points:
 
     moe_workspace_size, moe_workspace_status, moe_route, moe_layer_forward, q8_gemv,
-    q8_quantize_x, q8_gemv_q8x, q8_gemv_qx, q8_pack_rows16
+    q8_quantize_x, q8_gemv_q8x, q8_gemv_qx, q8_pack_rows16,
+    mx4_quantize, mx4_dequantize, mx4_pack_rows16, mx4_gemm, mx4_gemm_mx4x
 
 There is no fallback: if the shared library is missing, loading raises.
 Build it with ``python -m quantized_sparse_moe_amd.build``.
@@ -22,6 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libqsmoe.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = 0, -1, -2, -3, -4
 MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MX4_ROWS, MX4_TILES = 0, 1                               # layouts of MX4 codes and scales
 MOE_WS_ERR_DECODE_WAIT, MOE_WS_ERR_GEMM_WAIT = 1, 2      # bits of the workspace error word
 
 _lib = None
@@ -53,7 +55,9 @@ class moe_layer_desc(ctypes.Structure):
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_size",
            "moe_workspace_size_chunked", "moe_workspace_status", "moe_route",
            "moe_layer_forward", "moe_layer_forward_static", "q8_gemv", "q8_quantize_x", "q8_gemv_q8x", "q8_gemv_qx",
-           "q8_pack_rows16", "moe_calib_read", "moe_calib_mfma")
+           "q8_pack_rows16", "mx4_codes_size", "mx4_scales_size", "mx4_quantize", "mx4_dequantize",
+           "mx4_pack_rows16", "mx4_gemm_workspace_size", "mx4_gemm", "mx4_gemm_mx4x",
+           "moe_calib_read", "moe_calib_mfma")
 
 
 def lib() -> ctypes.CDLL:
@@ -91,6 +95,22 @@ def lib() -> ctypes.CDLL:
         L.q8_gemv_qx.argtypes = [P, I64, I64, P, P, I32, P]
         L.q8_pack_rows16.restype = I32
         L.q8_pack_rows16.argtypes = [P, I64, I64, P, P]
+        L.mx4_codes_size.restype = SZ
+        L.mx4_codes_size.argtypes = [I64, I64, I32]
+        L.mx4_scales_size.restype = SZ
+        L.mx4_scales_size.argtypes = [I64, I64, I32]
+        L.mx4_quantize.restype = I32
+        L.mx4_quantize.argtypes = [P, I32, I64, I64, I64, I32, P, P, P]
+        L.mx4_dequantize.restype = I32
+        L.mx4_dequantize.argtypes = [P, P, I64, I64, I32, P, I32, I64, P]
+        L.mx4_pack_rows16.restype = I32
+        L.mx4_pack_rows16.argtypes = [P, P, I64, I64, P, P, P]
+        L.mx4_gemm_workspace_size.restype = SZ
+        L.mx4_gemm_workspace_size.argtypes = [I64, I64, I64]
+        L.mx4_gemm.restype = I32
+        L.mx4_gemm.argtypes = [P, P, I64, I64, P, I64, I64, P, I32, I64, P, SZ, P]
+        L.mx4_gemm_mx4x.restype = I32
+        L.mx4_gemm_mx4x.argtypes = [P, P, I64, I64, P, P, I64, P, I32, I64, P, SZ, P]
         L.moe_calib_read.restype = I32
         L.moe_calib_read.argtypes = [P, SZ, P]
         L.moe_calib_mfma.restype = I32
@@ -368,6 +388,139 @@ def q8_pack_rows16(w_rows, N: int, K: int, w_tiles=None, stream=None):
         w_tiles = _empty((N // 16 * (K // 32) * 544,), torch.uint8, w_rows.device, stream)
     _check(lib().q8_pack_rows16(_ptr(w_rows), N, K, _ptr(w_tiles), _stream(stream)), "q8_pack_rows16")
     return w_tiles
+
+
+# -------------------------------------------------------------------------- MX4
+def _mx4_sizes(rows: int, K: int, layout: int, where: str):
+    nc, ns = lib().mx4_codes_size(rows, K, layout), lib().mx4_scales_size(rows, K, layout)
+    if ctypes.c_size_t(-1).value in (nc, ns):
+        raise QsmoeError(MOE_ERR_UNSUPPORTED, where)
+    return nc, ns
+
+
+def _mx4_buf(t, nbytes: int, where: str):
+    """A caller's codes, scales or workspace buffer, checked for its size and layout in memory."""
+    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: a buffer is not contiguous or smaller than {nbytes} bytes")
+    return t
+
+
+def _mx4_values(x, where: str, codes):
+    """(rows, K, row stride, type code) of a 2-d matrix of values; 16-bit integers are bf16 bits."""
+    import torch
+    code = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}.get(x.dtype)
+    if x.dim() != 2 or code not in codes or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: a matrix with contiguous rows of a supported type is needed")
+    return x.shape[0], x.shape[1], (x.stride(0) if x.shape[0] > 1 else max(x.shape[1], 1)), code
+
+
+def _on_device(where: str, *tensors):
+    """The device all `tensors` share, as a context: the launch goes to it whatever the
+    current device is."""
+    import torch
+    dev = {t.device for t in tensors if t is not None}
+    if len(dev) != 1 or next(iter(dev)).type != "cuda":
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: the tensors must be on one GPU")
+    return torch.cuda.device(next(iter(dev)))
+
+
+def mx4_quantize(x, codes=None, scales=None, layout: int = MX4_TILES, stream=None):
+    """MX4 quantization of ``x`` [rows, K] (bf16, fp16 or fp32; rows may be strided);
+    returns (codes, scales), flat uint8 buffers in ``layout``."""
+    import torch
+    rows, K, ldx, code = _mx4_values(x, "mx4_quantize", (MOE_BF16, MOE_F16, MOE_F32))
+    nc, ns = _mx4_sizes(rows, K, layout, "mx4_quantize")
+    with _on_device("mx4_quantize", x, codes, scales):
+        codes = _empty((nc,), torch.uint8, x.device, stream) if codes is None else _mx4_buf(codes, nc, "mx4_quantize")
+        scales = _empty((ns,), torch.uint8, x.device, stream) if scales is None else _mx4_buf(scales, ns, "mx4_quantize")
+        _check(lib().mx4_quantize(_ptr(x), code, rows, K, ldx, layout, _ptr(codes), _ptr(scales), _stream(stream)),
+               "mx4_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, rows: int, K: int, y=None, y_dtype=None, layout: int = MX4_TILES, stream=None):
+    """The values of an MX4 matrix: ``y`` [rows, K] (bf16, fp16 or fp32; default fp32)."""
+    import torch
+    nc, ns = _mx4_sizes(rows, K, layout, "mx4_dequantize")
+    _mx4_buf(codes, nc, "mx4_dequantize"), _mx4_buf(scales, ns, "mx4_dequantize")
+    with _on_device("mx4_dequantize", codes, scales, y):
+        if y is None:
+            y = _empty((rows, K), y_dtype or torch.float32, codes.device, stream)
+        r, k, ldy, code = _mx4_values(y, "mx4_dequantize", (MOE_BF16, MOE_F16, MOE_F32))
+        if (r, k) != (rows, K):
+            raise QsmoeError(MOE_ERR_INVALID, "mx4_dequantize: y has another shape")
+        _check(lib().mx4_dequantize(_ptr(codes), _ptr(scales), rows, K, layout, _ptr(y), code, ldy, _stream(stream)),
+               "mx4_dequantize")
+    return y
+
+
+def mx4_pack_rows16(codes, scales, rows: int, K: int, t_codes=None, t_scales=None, stream=None):
+    """Row-major MX4 (``MX4_ROWS``) -> the tiles the products read (load-time, on the
+    device); returns (codes, scales) in ``MX4_TILES``."""
+    import torch
+    nc, ns = _mx4_sizes(rows, K, MX4_ROWS, "mx4_pack_rows16")
+    _mx4_buf(codes, nc, "mx4_pack_rows16"), _mx4_buf(scales, ns, "mx4_pack_rows16")
+    nc, ns = _mx4_sizes(rows, K, MX4_TILES, "mx4_pack_rows16")
+    with _on_device("mx4_pack_rows16", codes, scales, t_codes, t_scales):
+        if t_codes is None:
+            t_codes = _empty((nc,), torch.uint8, codes.device, stream)
+        if t_scales is None:
+            t_scales = _empty((ns,), torch.uint8, codes.device, stream)
+        _mx4_buf(t_codes, nc, "mx4_pack_rows16"), _mx4_buf(t_scales, ns, "mx4_pack_rows16")
+        _check(lib().mx4_pack_rows16(_ptr(codes), _ptr(scales), rows, K, _ptr(t_codes), _ptr(t_scales),
+                                     _stream(stream)), "mx4_pack_rows16")
+    return t_codes, t_scales
+
+
+def mx4_gemm_workspace_size(N: int, K: int, T: int) -> int:
+    n = lib().mx4_gemm_workspace_size(int(N), int(K), int(T))
+    if n == ctypes.c_size_t(-1).value:
+        raise QsmoeError(MOE_ERR_UNSUPPORTED, "mx4_gemm_workspace_size")
+    return n
+
+
+def mx4_new_workspace(T: int, N: int, K: int, device="cuda", stream=None):
+    """A workspace for products of T tokens with an [N, K] matrix (None when none is needed)."""
+    import torch
+    n = mx4_gemm_workspace_size(N, K, T)
+    return _empty((n,), torch.uint8, device, stream) if n else None
+
+
+def _mx4_product(where, w_codes, w_scales, N, K, T, keep, y, y_dtype, workspace, stream, call):
+    import torch
+    nc, ns = _mx4_sizes(N, K, MX4_TILES, where)
+    _mx4_buf(w_codes, nc, where), _mx4_buf(w_scales, ns, where)
+    with _on_device(where, w_codes, w_scales, y, workspace, *keep):
+        if y is None:
+            y = _empty((T, N), y_dtype or torch.float32, w_codes.device, stream)
+        if y.dim() != 2 or tuple(y.shape) != (T, N) or (N > 1 and y.stride(1) != 1):
+            raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be [T, N] with contiguous rows")
+        if workspace is None and T > 0:
+            workspace = mx4_new_workspace(T, N, K, w_codes.device, stream)
+        nb = 0 if workspace is None else _mx4_buf(workspace, 0, where).numel() * workspace.element_size()
+        ldy = y.stride(0) if T > 1 else max(N, 1)
+        _check(call(_ptr(y), _out_code(y, where), ldy, _ptr(workspace), nb, _stream(stream)), where)
+    return y
+
+
+def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspace=None, stream=None):
+    """``y`` [T, N] = ``x`` [T, K] (bf16) times the transpose of an MX4 matrix in tiles."""
+    T, k, ldx, code = _mx4_values(x, "mx4_gemm", (MOE_BF16,))
+    if k != K:
+        raise QsmoeError(MOE_ERR_INVALID, "mx4_gemm: x must have K columns")
+    return _mx4_product("mx4_gemm", w_codes, w_scales, N, K, T, (x,), y, y_dtype, workspace, stream,
+                        lambda yp, yc, ldy, ws, nb, st: lib().mx4_gemm(
+                            _ptr(w_codes), _ptr(w_scales), N, K, _ptr(x), T, ldx, yp, yc, ldy, ws, nb, st))
+
+
+def mx4_gemm_mx4x(w_codes, w_scales, N: int, K: int, x_codes, x_scales, T: int, y=None, y_dtype=None,
+                  workspace=None, stream=None):
+    """The same product with ``x`` quantized (``mx4_quantize`` into tiles, T rows)."""
+    nc, ns = _mx4_sizes(T, K, MX4_TILES, "mx4_gemm_mx4x")
+    _mx4_buf(x_codes, nc, "mx4_gemm_mx4x"), _mx4_buf(x_scales, ns, "mx4_gemm_mx4x")
+    return _mx4_product("mx4_gemm_mx4x", w_codes, w_scales, N, K, T, (x_codes, x_scales), y, y_dtype, workspace, stream,
+                        lambda yp, yc, ldy, ws, nb, st: lib().mx4_gemm_mx4x(
+                            _ptr(w_codes), _ptr(w_scales), N, K, _ptr(x_codes), _ptr(x_scales), T, yp, yc, ldy, ws, nb, st))
 
 
 def moe_calib_read(buf, stream=None):

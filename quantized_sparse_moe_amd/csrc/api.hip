@@ -279,6 +279,44 @@ moe_status scratch_for_current_device(void **out) {
     return MOE_OK;
 }
 
+// ------------------------------------------------------------------------------ MX4
+constexpr int64_t MX4_MAX_ROWS = 1 << 26, MX4_MAX_K = 65536;
+
+moe_status check_mx4(int64_t rows, int64_t K, int32_t layout) {
+    if (rows < 0 || K < 0 || (layout != MX4_ROWS && layout != MX4_TILES)) return MOE_ERR_INVALID;
+    if (K % 32 || K < 32 || K > MX4_MAX_K || rows > MX4_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status check_mx4_codes(const void *codes, const void *scales) {
+    return codes && aligned(codes, 16) && scales && aligned(scales, 4) ? MOE_OK : MOE_ERR_INVALID;
+}
+
+// a matrix of values with 16-byte aligned rows
+moe_status check_values(const void *x, int32_t dtype, int64_t K, int64_t ld) {
+    const int64_t per16 = dtype == MOE_F32 ? 4 : 8;
+    return x && aligned(x, 16) && ld >= K && ld % per16 == 0 ? MOE_OK : MOE_ERR_INVALID;
+}
+
+moe_status check_mx4_product(const void *wc, const void *wsc, int64_t N, int64_t K, int64_t T, const void *y,
+                             int32_t y_dtype, int64_t ldy, const void *ws, size_t ws_bytes) {
+    moe_status s = check_mx4(N, K, MX4_TILES);
+    if (s) return s;
+    if (T < 0) return MOE_ERR_INVALID;
+    if (T > MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    if (y_dtype != MOE_BF16 && y_dtype != MOE_F32) return MOE_ERR_INVALID;
+    if (T == 0 || N == 0) return MOE_OK;
+    if ((s = check_mx4_codes(wc, wsc))) return s;
+    if (!y || !aligned(y, y_dtype == MOE_F32 ? 4 : 2) || ldy < N) return MOE_ERR_INVALID;
+    const size_t need = mx4_gemm_ws(T, N, K);
+    if (need && (!ws || !aligned(ws, ALIGN) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
+bool overlap(const void *a, size_t an, const void *b, size_t bn) {
+    return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
+
 }  // namespace
 
 extern "C" {
@@ -432,6 +470,80 @@ moe_status q8_pack_rows16(const void *w_rows, int64_t N, int64_t K, void *w_tile
     const uintptr_t a = (uintptr_t)w_rows, b = (uintptr_t)w_tiles;
     if (a < b + bytes && b < a + bytes) return MOE_ERR_INVALID;   // overlap
     return dev(launch_q8_pack((const uint8_t *)w_rows, N, K, (uint8_t *)w_tiles, (hipStream_t)stream));
+}
+
+size_t mx4_codes_size(int64_t rows, int64_t K, int32_t layout) {
+    if (check_mx4(rows, K, layout) != MOE_OK) return SIZE_MAX;
+    return layout == MX4_ROWS ? (size_t)(rows * (K / 2)) : (size_t)((rows + 15) / 16 * mx4_steps(K) * 1024);
+}
+
+size_t mx4_scales_size(int64_t rows, int64_t K, int32_t layout) {
+    if (check_mx4(rows, K, layout) != MOE_OK) return SIZE_MAX;
+    return layout == MX4_ROWS ? (size_t)(rows * (K / 32)) : (size_t)((rows + 15) / 16 * mx4_quads(K) * 256);
+}
+
+moe_status mx4_quantize(const void *x, int32_t x_dtype, int64_t rows, int64_t K, int64_t ldx, int32_t layout,
+                        void *codes, void *scales, void *stream) {
+    moe_status s = check_mx4(rows, K, layout);
+    if (s) return s;
+    if (x_dtype != MOE_BF16 && x_dtype != MOE_F16 && x_dtype != MOE_F32) return MOE_ERR_INVALID;
+    if (rows == 0) return MOE_OK;
+    if ((s = check_mx4_codes(codes, scales)) || (s = check_values(x, x_dtype, K, ldx))) return s;
+    return dev(launch_mx4_quantize(x, x_dtype, rows, K, ldx, layout, (uint8_t *)codes, (uint8_t *)scales,
+                                   (hipStream_t)stream));
+}
+
+moe_status mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t K, int32_t layout, void *y,
+                          int32_t y_dtype, int64_t ldy, void *stream) {
+    moe_status s = check_mx4(rows, K, layout);
+    if (s) return s;
+    if (y_dtype != MOE_BF16 && y_dtype != MOE_F16 && y_dtype != MOE_F32) return MOE_ERR_INVALID;
+    if (rows == 0) return MOE_OK;
+    if ((s = check_mx4_codes(codes, scales)) || (s = check_values(y, y_dtype, K, ldy))) return s;
+    return dev(launch_mx4_dequantize((const uint8_t *)codes, (const uint8_t *)scales, rows, K, layout, y, y_dtype, ldy,
+                                     (hipStream_t)stream));
+}
+
+moe_status mx4_pack_rows16(const void *codes, const void *scales, int64_t rows, int64_t K, void *t_codes,
+                           void *t_scales, void *stream) {
+    moe_status s = check_mx4(rows, K, MX4_ROWS);
+    if (s) return s;
+    if (rows == 0) return MOE_OK;
+    if ((s = check_mx4_codes(codes, scales)) || (s = check_mx4_codes(t_codes, t_scales))) return s;
+    const struct { const void *p; size_t n; } in[2] = {{codes, mx4_codes_size(rows, K, MX4_ROWS)},
+                                                       {scales, mx4_scales_size(rows, K, MX4_ROWS)}},
+                                              out[2] = {{t_codes, mx4_codes_size(rows, K, MX4_TILES)},
+                                                        {t_scales, mx4_scales_size(rows, K, MX4_TILES)}};
+    for (const auto &i : in)
+        for (const auto &o : out)
+            if (overlap(i.p, i.n, o.p, o.n)) return MOE_ERR_INVALID;
+    if (overlap(t_codes, out[0].n, t_scales, out[1].n)) return MOE_ERR_INVALID;
+    return dev(launch_mx4_pack((const uint8_t *)codes, (const uint8_t *)scales, rows, K, (uint8_t *)t_codes,
+                               (uint8_t *)t_scales, (hipStream_t)stream));
+}
+
+size_t mx4_gemm_workspace_size(int64_t N, int64_t K, int64_t T) {
+    if (check_mx4(N, K, MX4_TILES) != MOE_OK || T > MAX_TOKENS) return SIZE_MAX;
+    return N == 0 || T <= 0 ? 0 : mx4_gemm_ws(T, N, K);
+}
+
+moe_status mx4_gemm(const void *w_codes, const void *w_scales, int64_t N, int64_t K, const void *x, int64_t T,
+                    int64_t ldx, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes, void *stream) {
+    moe_status s = check_mx4_product(w_codes, w_scales, N, K, T, y, y_dtype, ldy, ws, ws_bytes);
+    if (s || T == 0 || N == 0) return s;
+    if ((s = check_values(x, MOE_BF16, K, ldx))) return s;
+    return dev(launch_mx4_gemm((const uint8_t *)w_codes, (const uint8_t *)w_scales, N, K, (const uint16_t *)x, T, ldx, y,
+                               y_dtype, ldy, (uint8_t *)ws, (hipStream_t)stream));
+}
+
+moe_status mx4_gemm_mx4x(const void *w_codes, const void *w_scales, int64_t N, int64_t K, const void *x_codes,
+                         const void *x_scales, int64_t T, void *y, int32_t y_dtype, int64_t ldy, void *ws,
+                         size_t ws_bytes, void *stream) {
+    moe_status s = check_mx4_product(w_codes, w_scales, N, K, T, y, y_dtype, ldy, ws, ws_bytes);
+    if (s || T == 0 || N == 0) return s;
+    if ((s = check_mx4_codes(x_codes, x_scales))) return s;
+    return dev(launch_mx4_gemm_mx4x((const uint8_t *)w_codes, (const uint8_t *)w_scales, N, K, (const uint8_t *)x_codes,
+                                    (const uint8_t *)x_scales, T, y, y_dtype, ldy, (uint8_t *)ws, (hipStream_t)stream));
 }
 
 moe_status moe_calib_read(const void *buf, size_t bytes, void *stream) {

@@ -118,6 +118,23 @@ hipError_t launch_q8_gemv_q8x(const uint8_t *tiles, int64_t N, int64_t K, const 
 hipError_t launch_q8_pack(const uint8_t *rows, int64_t N, int64_t K, uint8_t *tiles,
                           hipStream_t s);
 
+// ---------------------------------------------------------------------------- MX4
+// column steps of 128 and groups of four steps of a row of K values (layouts: mx4.h)
+__host__ __device__ inline int64_t mx4_steps(int64_t K) { return (K + 127) / 128; }
+__host__ __device__ inline int64_t mx4_quads(int64_t K) { return (K + 511) / 512; }
+hipError_t launch_mx4_quantize(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int layout,
+                               uint8_t *codes, uint8_t *scales, hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, int layout,
+                                 void *y, int dtype, int64_t ldy, hipStream_t s);
+hipError_t launch_mx4_pack(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, uint8_t *tc,
+                           uint8_t *ts, hipStream_t s);
+size_t mx4_gemm_ws(int64_t T, int64_t N, int64_t K);      // bytes of workspace of launch_mx4_gemm
+hipError_t launch_mx4_gemm(const uint8_t *wc, const uint8_t *wsc, int64_t N, int64_t K, const uint16_t *x, int64_t T,
+                           int64_t ldx, void *y, int y_dtype, int64_t ldy, uint8_t *ws, hipStream_t s);
+hipError_t launch_mx4_gemm_mx4x(const uint8_t *wc, const uint8_t *wsc, int64_t N, int64_t K, const uint8_t *xc,
+                                const uint8_t *xs, int64_t T, void *y, int y_dtype, int64_t ldy, uint8_t *ws,
+                                hipStream_t s);
+
 // ---------------------------------------------------------------- measured ceilings
 hipError_t launch_calib_read(const void *buf, int64_t bytes, uint32_t *out, hipStream_t s);
 hipError_t launch_calib_mfma(int iters, int blocks, float *out, hipStream_t s);
