@@ -64,6 +64,7 @@ typedef int32_t moe_status;
 #define MOE_BF16 0
 #define MOE_F16  1
 #define MOE_F32  2
+#define MOE_E8M0 3   /* scale_dtype only: an MX4 layer */
 
 /*
  * A stack of affine-quantized matrices, each [rows][cols], quantized in groups of
@@ -105,6 +106,13 @@ typedef struct {
  *   (top_k + 1) * inter <= 24576 (the batch-1 kernel hands every h value of a call
  *   between workgroups through a fixed region of the workspace).
  * Every qmat needs mat_stride >= its rows (MOE_ERR_INVALID otherwise).
+ *
+ * MX4 layers: scale_dtype MOE_E8M0 with bits == 4 and group == 32 makes every qmat a stack
+ *   of microscaled 4-bit matrices in MX4_TILES (see the mx4_ functions below; a stack is
+ *   repacked as one matrix of all its rows): codes 16-byte aligned, scales 4-byte aligned,
+ *   biases unused, mat_stride a multiple of 16 (for the up half of a fused [gate; up] stack
+ *   codes and scales start inter/16 panels behind gate's).  The other limits hold, except
+ *   the one on (top_k + 1) * inter.
  */
 typedef struct {
     int32_t hidden, inter, n_experts, top_k, bits, group;
@@ -200,6 +208,12 @@ moe_status moe_route(const moe_layer_desc *d, const void *x, int64_t T,
  * fp32 accumulation, fp16 intermediates, each under its range scale).
  * For a given T the result does not depend on whether gate/up are fused or separate,
  * nor on the other tokens of the call (tokens are independent), bit for bit.
+ * MX4 layers take a path of their own for every T, meant for few tokens: three launches for
+ * up to 64 tokens that read each chosen expert once (MFMA on bf16 operands: x as it is, the
+ * weights exact, h as a bf16 pair of 2^-17), and passes of 64 tokens beyond, each reading
+ * its experts anew.  Their workspace is that of min(T, 64) tokens (chunk does not matter);
+ * a token's result may differ in its last fp32 bits with the other tokens of its pass (the
+ * order in which its experts are summed depends on the pass's experts).
  */
 moe_status moe_layer_forward(const moe_layer_desc *d, const void *x, int64_t T,
                                void *y, int32_t y_dtype,

@@ -22,7 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqsmoe.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = 0, -1, -2, -3, -4
-MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MOE_BF16, MOE_F16, MOE_F32, MOE_E8M0 = 0, 1, 2, 3
 MX4_ROWS, MX4_TILES = 0, 1                               # layouts of MX4 codes and scales
 MOE_WS_ERR_DECODE_WAIT, MOE_WS_ERR_GEMM_WAIT = 1, 2      # bits of the workspace error word
 
@@ -139,7 +139,7 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -190,6 +190,42 @@ class LayerDesc:
         ng = cols // 64
         return moe_qmat(codes.data_ptr() + row0 * rb, scales.data_ptr() + row0 * ng * 2,
                           biases.data_ptr() + row0 * ng * 2, stride)
+
+    @classmethod
+    def from_mx4(cls, hidden, inter, n_experts, top_k, router_w, gate_up, down, router_bias=None, shared=None,
+                 shared_gate_w=None) -> "LayerDesc":
+        """A layer with microscaled 4-bit experts.  ``gate_up`` = (codes, scales) of the
+        [n_experts, 2 inter, hidden] stack and ``down`` of the [n_experts, hidden, inter]
+        one, in tiles (``mx4_pack_rows16`` of all the stack's rows); ``shared`` = (gate_up,
+        down) of the shared expert."""
+        for what, m, rows, cols in (("gate_up", gate_up, n_experts * 2 * inter, hidden),
+                                    ("down", down, n_experts * hidden, inter)) + (
+                () if shared is None else (("shared gate_up", shared[0], 2 * inter, hidden),
+                                           ("shared down", shared[1], hidden, inter))):
+            nc, ns = _mx4_sizes(rows, cols, MX4_TILES)
+            _mx4_buf(m[0], nc, f"LayerDesc.from_mx4: {what}"), _mx4_buf(m[1], ns, f"LayerDesc.from_mx4: {what}")
+
+        def half(m, cols, rows, row0):
+            nc, ns = _mx4_sizes(row0, cols, MX4_TILES)
+            return moe_qmat(m[0].data_ptr() + nc, m[1].data_ptr() + ns, None, rows)
+
+        self = cls.__new__(cls)
+        self.hidden, self.inter, self.n_experts, self.top_k, self.bits = hidden, inter, n_experts, top_k, 4
+        self._keep = [router_w, router_bias, gate_up, down, shared, shared_gate_w]
+        d = moe_layer_desc()
+        d.hidden, d.inter, d.n_experts, d.top_k, d.bits, d.group = hidden, inter, n_experts, top_k, 4, 32
+        d.scale_dtype = MOE_E8M0
+        d.router_w = router_w.data_ptr()
+        d.router_bias = None if router_bias is None else router_bias.data_ptr()
+        d.shared_gate_w = None if shared_gate_w is None else shared_gate_w.data_ptr()
+        d.gate, d.up = half(gate_up, hidden, 2 * inter, 0), half(gate_up, hidden, 2 * inter, inter)
+        d.down = half(down, inter, hidden, 0)
+        d.has_shared = 0 if shared is None else 1
+        if shared is not None:
+            d.s_gate, d.s_up = half(shared[0], hidden, 2 * inter, 0), half(shared[0], hidden, 2 * inter, inter)
+            d.s_down = half(shared[1], inter, hidden, 0)
+        self.desc = d
+        return self
 
     @property
     def ptr(self) -> int:
@@ -270,6 +306,8 @@ def _workspace(desc: LayerDesc, T: int, workspace, device, stream):
 
 def _empty(shape, dtype, device, stream):
     import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(_alloc_stream(stream)):
         return torch.empty(shape, dtype=dtype, device=device)
 
@@ -391,66 +429,94 @@ def q8_pack_rows16(w_rows, N: int, K: int, w_tiles=None, stream=None):
 
 
 # -------------------------------------------------------------------------- MX4
-def _mx4_sizes(rows: int, K: int, layout: int, where: str):
-    nc, ns = lib().mx4_codes_size(rows, K, layout), lib().mx4_scales_size(rows, K, layout)
-    if ctypes.c_size_t(-1).value in (nc, ns):
-        raise QsmoeError(MOE_ERR_UNSUPPORTED, where)
-    return nc, ns
+# (These wrappers check what the C call cannot see -- buffer sizes, strides, devices -- with
+# plain attribute reads: a decode-sized call takes a few microseconds on the GPU, so the
+# host must not take more.)
+def _mx4_sizes(rows: int, K: int, layout: int):
+    """Bytes of the codes and of the scales (the C call refuses sizes outside its limits)."""
+    if layout == MX4_ROWS:
+        return rows * K // 2, rows * K // 32
+    p = (rows + 15) // 16
+    return p * ((K + 127) // 128) * 1024, p * ((K + 511) // 512) * 256
 
 
-def _mx4_buf(t, nbytes: int, where: str):
-    """A caller's codes, scales or workspace buffer, checked for its size and layout in memory."""
-    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+def _mx4_buf(t, nbytes: int, where: str) -> int:
+    """The address of a caller's buffer, checked for its size and for being contiguous."""
+    if t.nbytes < nbytes or not t.is_contiguous():
         raise QsmoeError(MOE_ERR_INVALID, f"{where}: a buffer is not contiguous or smaller than {nbytes} bytes")
-    return t
+    return t.data_ptr()
 
 
-def _mx4_values(x, where: str, codes):
-    """(rows, K, row stride, type code) of a 2-d matrix of values; 16-bit integers are bf16 bits."""
+_mx4_codes = None
+
+
+def _mx4_code(dtype):
+    """MOE_* code of a torch type of values (16-bit integers are bf16 bits), or None."""
+    global _mx4_codes
+    if _mx4_codes is None:
+        import torch
+        _mx4_codes = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+    return _mx4_codes.get(dtype)
+
+
+def _mx4_values(x, where: str):
+    """(rows, K, row stride, type code) of a 2-d matrix of values."""
+    code = _mx4_code(x.dtype)
+    if code is None or x.dim() != 2:
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: a matrix of a supported type is needed")
+    rows, K = x.shape
+    ld, inner = x.stride()
+    if K > 1 and inner != 1:
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: the rows of a matrix must be contiguous")
+    return rows, K, (ld if rows > 1 else K), code
+
+
+def _launch(where: str, stream, call, first, *others):
+    """call(stream handle) on the GPU that all the tensors share, whatever the current
+    device is; `stream` None is that GPU's current stream."""
     import torch
-    code = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}.get(x.dtype)
-    if x.dim() != 2 or code not in codes or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise QsmoeError(MOE_ERR_INVALID, f"{where}: a matrix with contiguous rows of a supported type is needed")
-    return x.shape[0], x.shape[1], (x.stride(0) if x.shape[0] > 1 else max(x.shape[1], 1)), code
-
-
-def _on_device(where: str, *tensors):
-    """The device all `tensors` share, as a context: the launch goes to it whatever the
-    current device is."""
-    import torch
-    dev = {t.device for t in tensors if t is not None}
-    if len(dev) != 1 or next(iter(dev)).type != "cuda":
+    dev = first.device
+    if dev.type != "cuda" or any(t is not None and t.device != dev for t in others):
         raise QsmoeError(MOE_ERR_INVALID, f"{where}: the tensors must be on one GPU")
-    return torch.cuda.device(next(iter(dev)))
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == dev.index:
+        _check(call(handle), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(call(handle), where)
 
 
 def mx4_quantize(x, codes=None, scales=None, layout: int = MX4_TILES, stream=None):
     """MX4 quantization of ``x`` [rows, K] (bf16, fp16 or fp32; rows may be strided);
     returns (codes, scales), flat uint8 buffers in ``layout``."""
     import torch
-    rows, K, ldx, code = _mx4_values(x, "mx4_quantize", (MOE_BF16, MOE_F16, MOE_F32))
-    nc, ns = _mx4_sizes(rows, K, layout, "mx4_quantize")
-    with _on_device("mx4_quantize", x, codes, scales):
-        codes = _empty((nc,), torch.uint8, x.device, stream) if codes is None else _mx4_buf(codes, nc, "mx4_quantize")
-        scales = _empty((ns,), torch.uint8, x.device, stream) if scales is None else _mx4_buf(scales, ns, "mx4_quantize")
-        _check(lib().mx4_quantize(_ptr(x), code, rows, K, ldx, layout, _ptr(codes), _ptr(scales), _stream(stream)),
-               "mx4_quantize")
+    rows, K, ldx, code = _mx4_values(x, "mx4_quantize")
+    nc, ns = _mx4_sizes(rows, K, layout)
+    if codes is None:
+        codes = _empty((nc,), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((ns,), torch.uint8, x.device, stream)
+    pc, ps = _mx4_buf(codes, nc, "mx4_quantize"), _mx4_buf(scales, ns, "mx4_quantize")
+    _launch("mx4_quantize", stream,
+            lambda st: lib().mx4_quantize(x.data_ptr(), code, rows, K, ldx, layout, pc, ps, st), x, codes, scales)
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, rows: int, K: int, y=None, y_dtype=None, layout: int = MX4_TILES, stream=None):
     """The values of an MX4 matrix: ``y`` [rows, K] (bf16, fp16 or fp32; default fp32)."""
     import torch
-    nc, ns = _mx4_sizes(rows, K, layout, "mx4_dequantize")
-    _mx4_buf(codes, nc, "mx4_dequantize"), _mx4_buf(scales, ns, "mx4_dequantize")
-    with _on_device("mx4_dequantize", codes, scales, y):
-        if y is None:
-            y = _empty((rows, K), y_dtype or torch.float32, codes.device, stream)
-        r, k, ldy, code = _mx4_values(y, "mx4_dequantize", (MOE_BF16, MOE_F16, MOE_F32))
-        if (r, k) != (rows, K):
-            raise QsmoeError(MOE_ERR_INVALID, "mx4_dequantize: y has another shape")
-        _check(lib().mx4_dequantize(_ptr(codes), _ptr(scales), rows, K, layout, _ptr(y), code, ldy, _stream(stream)),
-               "mx4_dequantize")
+    nc, ns = _mx4_sizes(rows, K, layout)
+    pc, ps = _mx4_buf(codes, nc, "mx4_dequantize"), _mx4_buf(scales, ns, "mx4_dequantize")
+    if y is None:
+        y = _empty((rows, K), y_dtype or torch.float32, codes.device, stream)
+    r, k, ldy, code = _mx4_values(y, "mx4_dequantize")
+    if r != rows or k != K:
+        raise QsmoeError(MOE_ERR_INVALID, "mx4_dequantize: y has another shape")
+    _launch("mx4_dequantize", stream,
+            lambda st: lib().mx4_dequantize(pc, ps, rows, K, layout, y.data_ptr(), code, ldy, st), codes, scales, y)
     return y
 
 
@@ -458,17 +524,16 @@ def mx4_pack_rows16(codes, scales, rows: int, K: int, t_codes=None, t_scales=Non
     """Row-major MX4 (``MX4_ROWS``) -> the tiles the products read (load-time, on the
     device); returns (codes, scales) in ``MX4_TILES``."""
     import torch
-    nc, ns = _mx4_sizes(rows, K, MX4_ROWS, "mx4_pack_rows16")
-    _mx4_buf(codes, nc, "mx4_pack_rows16"), _mx4_buf(scales, ns, "mx4_pack_rows16")
-    nc, ns = _mx4_sizes(rows, K, MX4_TILES, "mx4_pack_rows16")
-    with _on_device("mx4_pack_rows16", codes, scales, t_codes, t_scales):
-        if t_codes is None:
-            t_codes = _empty((nc,), torch.uint8, codes.device, stream)
-        if t_scales is None:
-            t_scales = _empty((ns,), torch.uint8, codes.device, stream)
-        _mx4_buf(t_codes, nc, "mx4_pack_rows16"), _mx4_buf(t_scales, ns, "mx4_pack_rows16")
-        _check(lib().mx4_pack_rows16(_ptr(codes), _ptr(scales), rows, K, _ptr(t_codes), _ptr(t_scales),
-                                     _stream(stream)), "mx4_pack_rows16")
+    nc, ns = _mx4_sizes(rows, K, MX4_ROWS)
+    pc, ps = _mx4_buf(codes, nc, "mx4_pack_rows16"), _mx4_buf(scales, ns, "mx4_pack_rows16")
+    nc, ns = _mx4_sizes(rows, K, MX4_TILES)
+    if t_codes is None:
+        t_codes = _empty((nc,), torch.uint8, codes.device, stream)
+    if t_scales is None:
+        t_scales = _empty((ns,), torch.uint8, codes.device, stream)
+    tc, ts = _mx4_buf(t_codes, nc, "mx4_pack_rows16"), _mx4_buf(t_scales, ns, "mx4_pack_rows16")
+    _launch("mx4_pack_rows16", stream, lambda st: lib().mx4_pack_rows16(pc, ps, rows, K, tc, ts, st),
+            codes, scales, t_codes, t_scales)
     return t_codes, t_scales
 
 
@@ -486,41 +551,42 @@ def mx4_new_workspace(T: int, N: int, K: int, device="cuda", stream=None):
     return _empty((n,), torch.uint8, device, stream) if n else None
 
 
-def _mx4_product(where, w_codes, w_scales, N, K, T, keep, y, y_dtype, workspace, stream, call):
+def _mx4_out(where, w_codes, w_scales, N, K, T, y, y_dtype, workspace, stream):
+    """(y, (weight addresses), (y address, type code, row stride), workspace, (its address,
+    bytes)) of a product, what the caller did not pass allocated."""
     import torch
-    nc, ns = _mx4_sizes(N, K, MX4_TILES, where)
-    _mx4_buf(w_codes, nc, where), _mx4_buf(w_scales, ns, where)
-    with _on_device(where, w_codes, w_scales, y, workspace, *keep):
-        if y is None:
-            y = _empty((T, N), y_dtype or torch.float32, w_codes.device, stream)
-        if y.dim() != 2 or tuple(y.shape) != (T, N) or (N > 1 and y.stride(1) != 1):
-            raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be [T, N] with contiguous rows")
-        if workspace is None and T > 0:
-            workspace = mx4_new_workspace(T, N, K, w_codes.device, stream)
-        nb = 0 if workspace is None else _mx4_buf(workspace, 0, where).numel() * workspace.element_size()
-        ldy = y.stride(0) if T > 1 else max(N, 1)
-        _check(call(_ptr(y), _out_code(y, where), ldy, _ptr(workspace), nb, _stream(stream)), where)
-    return y
+    nc, ns = _mx4_sizes(N, K, MX4_TILES)
+    w = (_mx4_buf(w_codes, nc, where), _mx4_buf(w_scales, ns, where))
+    if y is None:
+        y = _empty((T, N), y_dtype or torch.float32, w_codes.device, stream)
+    if y.dim() != 2 or y.shape[0] != T or y.shape[1] != N or (N > 1 and y.stride(1) != 1):
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be [T, N] with contiguous rows")
+    if workspace is None and T > 0:
+        workspace = mx4_new_workspace(T, N, K, w_codes.device, stream)
+    ws = (None, 0) if workspace is None else (_mx4_buf(workspace, 0, where), workspace.nbytes)
+    return y, w, (y.data_ptr(), _out_code(y, where), y.stride(0) if T > 1 else N), workspace, ws
 
 
 def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspace=None, stream=None):
     """``y`` [T, N] = ``x`` [T, K] (bf16) times the transpose of an MX4 matrix in tiles."""
-    T, k, ldx, code = _mx4_values(x, "mx4_gemm", (MOE_BF16,))
-    if k != K:
-        raise QsmoeError(MOE_ERR_INVALID, "mx4_gemm: x must have K columns")
-    return _mx4_product("mx4_gemm", w_codes, w_scales, N, K, T, (x,), y, y_dtype, workspace, stream,
-                        lambda yp, yc, ldy, ws, nb, st: lib().mx4_gemm(
-                            _ptr(w_codes), _ptr(w_scales), N, K, _ptr(x), T, ldx, yp, yc, ldy, ws, nb, st))
+    T, k, ldx, code = _mx4_values(x, "mx4_gemm")
+    if k != K or code != MOE_BF16:
+        raise QsmoeError(MOE_ERR_INVALID, "mx4_gemm: x must be bf16 with K columns")
+    y, w, out, workspace, ws = _mx4_out("mx4_gemm", w_codes, w_scales, N, K, T, y, y_dtype, workspace, stream)
+    _launch("mx4_gemm", stream, lambda st: lib().mx4_gemm(*w, N, K, x.data_ptr(), T, ldx, *out, *ws, st),
+            x, w_codes, w_scales, y, workspace)
+    return y
 
 
 def mx4_gemm_mx4x(w_codes, w_scales, N: int, K: int, x_codes, x_scales, T: int, y=None, y_dtype=None,
                   workspace=None, stream=None):
     """The same product with ``x`` quantized (``mx4_quantize`` into tiles, T rows)."""
-    nc, ns = _mx4_sizes(T, K, MX4_TILES, "mx4_gemm_mx4x")
-    _mx4_buf(x_codes, nc, "mx4_gemm_mx4x"), _mx4_buf(x_scales, ns, "mx4_gemm_mx4x")
-    return _mx4_product("mx4_gemm_mx4x", w_codes, w_scales, N, K, T, (x_codes, x_scales), y, y_dtype, workspace, stream,
-                        lambda yp, yc, ldy, ws, nb, st: lib().mx4_gemm_mx4x(
-                            _ptr(w_codes), _ptr(w_scales), N, K, _ptr(x_codes), _ptr(x_scales), T, yp, yc, ldy, ws, nb, st))
+    nc, ns = _mx4_sizes(T, K, MX4_TILES)
+    xc, xs = _mx4_buf(x_codes, nc, "mx4_gemm_mx4x"), _mx4_buf(x_scales, ns, "mx4_gemm_mx4x")
+    y, w, out, workspace, ws = _mx4_out("mx4_gemm_mx4x", w_codes, w_scales, N, K, T, y, y_dtype, workspace, stream)
+    _launch("mx4_gemm_mx4x", stream, lambda st: lib().mx4_gemm_mx4x(*w, N, K, xc, xs, T, *out, *ws, st),
+            x_codes, x_scales, w_codes, w_scales, y, workspace)
+    return y
 
 
 def moe_calib_read(buf, stream=None):

@@ -26,6 +26,15 @@ inline size_t up(size_t n) { return (n + ALIGN - 1) / ALIGN * ALIGN; }
 
 inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// a stack of MX4 matrices in tiles (no biases)
+moe_status check_qmat_mx4(const moe_qmat &m, int64_t rows) {
+    if (!m.codes || !m.scales || !aligned(m.codes, 16) || !aligned(m.scales, 4)) return MOE_ERR_INVALID;
+    if (m.mat_stride < rows || m.mat_stride % 16) return MOE_ERR_INVALID;
+    return MOE_OK;
+}
+
+bool is_mx4(const moe_layer_desc *d) { return d->scale_dtype == MOE_E8M0; }
+
 moe_status check_qmat(const moe_qmat &m, int64_t rows) {
     if (!m.codes || !m.scales || !m.biases) return MOE_ERR_INVALID;
     if (!aligned(m.codes, 16) || !aligned(m.scales, 2) || !aligned(m.biases, 2)) return MOE_ERR_INVALID;
@@ -35,25 +44,26 @@ moe_status check_qmat(const moe_qmat &m, int64_t rows) {
 
 moe_status check_desc(const moe_layer_desc *d) {
     if (!d) return MOE_ERR_INVALID;
-    if (d->group != 64 || (d->bits != 4 && d->bits != 8) ||
-        (d->scale_dtype != MOE_F16 && d->scale_dtype != MOE_BF16))
+    const bool mx = is_mx4(d);
+    if (mx ? d->group != 32 || d->bits != 4
+           : d->group != 64 || (d->bits != 4 && d->bits != 8) ||
+                 (d->scale_dtype != MOE_F16 && d->scale_dtype != MOE_BF16))
         return MOE_ERR_UNSUPPORTED;
     if (d->n_experts < 1 || d->n_experts > 256) return MOE_ERR_UNSUPPORTED;
     if (d->top_k < 1 || d->top_k > 16 || d->top_k > d->n_experts) return MOE_ERR_UNSUPPORTED;
     if (d->hidden < 64 || d->hidden > 8192 || d->hidden % 64) return MOE_ERR_UNSUPPORTED;
     if (d->inter < 64 || d->inter > 2048 || d->inter % 64) return MOE_ERR_UNSUPPORTED;
-    if ((int64_t)(d->top_k + 1) * d->inter > 24576) return MOE_ERR_UNSUPPORTED;
+    if (!mx && (int64_t)(d->top_k + 1) * d->inter > 24576) return MOE_ERR_UNSUPPORTED;
     if (!d->router_w || !aligned(d->router_w, 16)) return MOE_ERR_INVALID;
     if (d->router_bias && !aligned(d->router_bias, 4)) return MOE_ERR_INVALID;
     if (d->has_shared != 0 && d->has_shared != 1) return MOE_ERR_INVALID;
     if (d->shared_gate_w && (!d->has_shared || !aligned(d->shared_gate_w, 16))) return MOE_ERR_INVALID;
     moe_status s;
-    if ((s = check_qmat(d->gate, d->inter)) || (s = check_qmat(d->up, d->inter)) ||
-        (s = check_qmat(d->down, d->hidden)))
+    auto check = [&](const moe_qmat &m, int64_t rows) { return mx ? check_qmat_mx4(m, rows) : check_qmat(m, rows); };
+    if ((s = check(d->gate, d->inter)) || (s = check(d->up, d->inter)) || (s = check(d->down, d->hidden)))
         return s;
-    if (d->has_shared &&
-        ((s = check_qmat(d->s_gate, d->inter)) || (s = check_qmat(d->s_up, d->inter)) ||
-         (s = check_qmat(d->s_down, d->hidden))))
+    if (d->has_shared && ((s = check(d->s_gate, d->inter)) || (s = check(d->s_up, d->inter)) ||
+                          (s = check(d->s_down, d->hidden))))
         return s;
     return MOE_OK;
 }
@@ -89,6 +99,7 @@ Layer to_layer(const moe_layer_desc *d) {
     }
     L.sb_bf16 = d->scale_dtype == MOE_BF16;
     L.shared_gate_w = (const uint16_t *)d->shared_gate_w;
+    L.mx4 = is_mx4(d);
     return L;
 }
 
@@ -140,11 +151,36 @@ PrefillBufs carve_prefill(const moe_layer_desc *d, int64_t T, void *ws, size_t *
     return b;
 }
 
+// the MX4 layer: one pass of T <= MX_TMAX tokens
+MxBufs carve_mx4(const moe_layer_desc *d, int64_t T, void *ws, size_t *bytes) {
+    Carver c{(char *)ws};
+    const int64_t H = d->hidden, I = d->inter, K = d->top_k, E = d->n_experts;
+    MxBufs b;
+    uint32_t *ctl = c.take<uint32_t>(WS_CTL_BYTES / 4);
+    b.cnt = ctl ? ctl + MX_CNT_OFF / 4 : nullptr;
+    b.logits = c.take<float>((size_t)(T * (E + 1)));
+    b.idx = c.take<int32_t>((size_t)(T * K));
+    b.w = c.take<float>((size_t)(T * K));
+    b.act = c.take<int32_t>((size_t)E);
+    b.nact = c.take<int32_t>(1);
+    b.pos = c.take<int16_t>((size_t)(E * MX_TMAX));
+    b.h = c.take<uint16_t>((size_t)((T * K + T) * 2 * I));
+    b.part = c.take<float>((size_t)(MX_SHARES * T * H));
+    *bytes = c.off;
+    return b;
+}
+size_t ws_size_mx4(const moe_layer_desc *d, int64_t T) {
+    size_t n = 0;
+    if (T > 0) carve_mx4(d, T < MX_TMAX ? T : MX_TMAX, nullptr, &n);
+    return n;
+}
+
 // T >= 2 runs in chunks, one after another on the stream, each through the whole
 // prefill sequence in the same workspace: chunks of `chunk` tokens need this much
 size_t ws_size_chunked(const moe_layer_desc *d, int64_t T, int64_t chunk) {
     size_t n = 0;
     if (T <= 0) return 0;
+    if (is_mx4(d)) return ws_size_mx4(d, T);
     if (T == 1) carve_decode(d, nullptr, &n);
     else carve_prefill(d, T < chunk ? T : chunk, nullptr, &n);
     return n;
@@ -201,11 +237,31 @@ moe_status check_layer_call(const moe_layer_desc *d, const void *x, int64_t T, c
     return MOE_OK;
 }
 
+// an MX4 layer (or its routing only): passes of MX_TMAX tokens, each in the same workspace
+moe_status run_mx4(const moe_layer_desc *d, const uint16_t *x, int64_t T, void *y, int32_t y_dtype, int32_t *topk_idx,
+                   float *topk_w, void *ws, bool route_only, hipStream_t st) {
+    const Layer L = to_layer(d);
+    const int64_t K = d->top_k, H = d->hidden;
+    const size_t ysz = y_dtype == MOE_F32 ? 4 : 2;
+    size_t n;
+    const MxBufs b = carve_mx4(d, T < MX_TMAX ? T : MX_TMAX, ws, &n);
+    for (int64_t t0 = 0; t0 < T; t0 += MX_TMAX) {
+        const int64_t Tc = T - t0 < MX_TMAX ? T - t0 : MX_TMAX;
+        if (launch_mx_layer(L, x + t0 * H, Tc, b, y ? (char *)y + (size_t)(t0 * H) * ysz : nullptr, y_dtype,
+                            topk_idx ? topk_idx + t0 * K : nullptr, topk_w ? topk_w + t0 * K : nullptr, route_only,
+                            st) != hipSuccess)
+            return MOE_ERR_DEVICE;
+    }
+    return MOE_OK;
+}
+
 moe_status forward_impl(const moe_layer_desc *d, const void *x, int64_t T, void *y, int32_t y_dtype,
                         int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes, void *stream) {
     moe_status s = check_layer_call(d, x, T, y, y_dtype, topk_idx, topk_w);
     if (s || T == 0) return s;
     if ((s = check_ws(d, T, ws, ws_bytes))) return s;
+    if (is_mx4(d))
+        return run_mx4(d, (const uint16_t *)x, T, y, y_dtype, topk_idx, topk_w, ws, false, (hipStream_t)stream);
     const Layer L = to_layer(d);
     hipStream_t st = (hipStream_t)stream;
     const uint16_t *xx = (const uint16_t *)x;
@@ -363,6 +419,8 @@ moe_status moe_route(const moe_layer_desc *d, const void *x, int64_t T, int32_t 
     if (!x || !aligned(x, 16) || !topk_idx || !topk_w || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
         return MOE_ERR_INVALID;
     if ((s = check_ws(d, T, ws, ws_bytes))) return s;
+    if (is_mx4(d))
+        return run_mx4(d, (const uint16_t *)x, T, nullptr, MOE_F32, topk_idx, topk_w, ws, true, (hipStream_t)stream);
     const Layer L = to_layer(d);
     hipStream_t st = (hipStream_t)stream;
     if (T == 1) {

@@ -25,6 +25,7 @@ struct Layer {
     QMat s_gate, s_up, s_down;
     int sb_bf16;                   // scales and biases are bf16 (else fp16)
     const uint16_t *shared_gate_w; // bf16 [H]: shared output scaled by sigmoid(g . x); or null
+    int mx4;                       // MX4 tiles instead of affine codes (scales: E8M0 tiles, no biases)
 };
 
 // -------------------------------------------------------------------- decode T = 1
@@ -134,6 +135,25 @@ hipError_t launch_mx4_gemm(const uint8_t *wc, const uint8_t *wsc, int64_t N, int
 hipError_t launch_mx4_gemm_mx4x(const uint8_t *wc, const uint8_t *wsc, int64_t N, int64_t K, const uint8_t *xc,
                                 const uint8_t *xs, int64_t T, void *y, int y_dtype, int64_t ldy, uint8_t *ws,
                                 hipStream_t s);
+
+// The MoE layer with MX4 experts (mx4_moe.hip), MX_TMAX tokens a pass.  Its counters lie in
+// the workspace's state region behind the affine kernels' words: zero before the first call,
+// and put back to zero by every call.
+constexpr int MX_TMAX = 64, MX_SHARES = 8;
+constexpr size_t MX_CNT_OFF = WS_CTL_BYTES - 4096;        // bytes; 1 + H / 32 counters
+struct MxBufs {
+    uint32_t *cnt;                 // [0] route, [1 + i] down, 32 output rows each
+    float *logits;                 // [T][E + 1] (column E: the shared expert's gate)
+    int32_t *idx;                  // [T][K]
+    float *w;                      // [T][K]
+    int32_t *act;                  // [E] the chosen experts, ascending
+    int32_t *nact;                 // [1] how many
+    int16_t *pos;                  // [E][MX_TMAX] a token's row of h under a chosen expert, or -1
+    uint16_t *h;                   // [T*K + T][2][I] bf16: w silu(g) u as hi and lo
+    float *part;                   // [MX_SHARES][T][H] the down shares' sums
+};
+hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const MxBufs &b, void *y, int y_dtype,
+                           int32_t *out_idx, float *out_w, bool route_only, hipStream_t s);
 
 // ---------------------------------------------------------------- measured ceilings
 hipError_t launch_calib_read(const void *buf, int64_t bytes, uint32_t *out, hipStream_t s);

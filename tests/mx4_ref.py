@@ -86,3 +86,83 @@ def product_bound(x, w):
     of which |x| @ |w| is a bound."""
     n = 4 * -(-x.shape[1] // 128) + 16 + 2
     return n * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
+
+
+# ------------------------------------------------------------------------- MoE layer
+class Layer:
+    """A seeded MoE layer with MX4 experts: codes (one per value), scales, values (float64)."""
+
+    def __init__(self, hidden, inter, n_experts, top_k, seed=0, shared=True, gated=False, bias=False, std=None):
+        rng = np.random.default_rng(seed)
+        self.hidden, self.inter, self.n_experts, self.top_k = hidden, inter, n_experts, top_k
+        H, I, E = hidden, inter, n_experts
+
+        def mat(rows, cols):
+            w = rng.standard_normal((rows, cols)) * np.exp(0.5 * rng.standard_normal((rows, 1))) / np.sqrt(cols)
+            c, s = quantize(w)
+            return c, s, values(c, s)
+
+        def bf16(v):
+            f = np.asarray(v, np.float32).view(np.uint32).astype(np.uint64)
+            return ((f + 0x7FFF + ((f >> 16) & 1)) >> 16).astype(np.uint16)
+
+        self.router_bits = bf16(rng.standard_normal((E, H)) / np.sqrt(H) * (std or 1.0))
+        self.bias = (-1.1 * np.log(rng.permutation(E) + 1.0)).astype(np.float32) if bias else None
+        self.gate_up, self.down = mat(E * 2 * I, H), mat(E * H, I)
+        self.shared = (mat(2 * I, H), mat(H, I)) if shared else None
+        self.gate_bits = bf16(rng.standard_normal(H) / np.sqrt(H)) if gated else None
+
+    def logits(self, x):
+        l = x @ bf16_values(self.router_bits).T
+        return l if self.bias is None else l + self.bias.astype(np.float64)
+
+    def route(self, x):
+        """(idx ascending, gap between the k-th and the next logit) of float64 x [T, H]."""
+        l = self.logits(x)
+        order = np.argsort(-l, axis=1, kind="stable")
+        k = self.top_k
+        srt = np.take_along_axis(l, order, axis=1)
+        gap = srt[:, k - 1] - srt[:, k] if k < l.shape[1] else np.full(len(l), np.inf)
+        return np.sort(order[:, :k], axis=1), gap
+
+    def weights(self, x, idx):
+        part = np.take_along_axis(self.logits(x), idx, axis=1)
+        w = np.exp(part - part.max(axis=1, keepdims=True))
+        return w / w.sum(axis=1, keepdims=True)
+
+    def forward(self, x, idx):
+        """(y, error bound of the fp32 evaluation) for float64 x and a routing.
+
+        The bound follows a value through the layer: g and u are sums as in product_bound;
+        silu moves by at most 1.1 of its argument's error and is evaluated to 2^-16 of itself
+        (the argument of its exponential, up to 2^6, is rounded once: 2^-18, and a few fp32
+        roundings); h = w silu(g) u is kept to 2^-16 (a bf16 pair), w is off by twice the
+        logits' error and 2^-20; the down sums as in product_bound, over all experts."""
+        H, I, T = self.hidden, self.inter, x.shape[0]
+        w = self.weights(x, idx)
+        dl = product_bound(x, bf16_values(self.router_bits)).max(axis=1)
+        y, b, tot = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
+
+        def expert(t, gu, dn, wt, dw):
+            xs = x[t]
+            g, u = xs @ gu[:I].T, xs @ gu[I:].T
+            dg, du = product_bound(xs, gu[:I]), product_bound(xs, gu[I:])
+            s = g / (1 + np.exp(-g))
+            h = wt[:, None] * s * u
+            dh = np.abs(wt)[:, None] * (1.1 * dg * np.abs(u) + np.abs(s) * du + 1.1 * dg * du)
+            dh += np.abs(h) * (2.0 ** -15 + dw[:, None])
+            y[t] += h @ dn.T
+            b[t] += dh @ np.abs(dn).T
+            tot[t] += np.abs(h) @ np.abs(dn).T
+
+        for e in np.unique(idx):
+            t, j = np.nonzero(idx == e)
+            expert(t, self.gate_up[2][e * 2 * I:(e + 1) * 2 * I], self.down[2][e * H:(e + 1) * H], w[t, j],
+                   2 * dl[t] + 2.0 ** -20)
+        if self.shared:
+            wt = np.ones(T)
+            if self.gate_bits is not None:
+                wt = 1 / (1 + np.exp(-(x @ bf16_values(self.gate_bits))))
+            expert(np.arange(T), self.shared[0][2], self.shared[1][2], wt, 2 * dl + 2.0 ** -18)
+        n = 4 * -(-I // 128) * (self.top_k + 1) + 16 + 2
+        return y, b + n * 2.0 ** -23 * tot

@@ -1,0 +1,235 @@
+"""The MoE layer with MX4 experts against the plain 64-bit evaluation (mx4_ref.Layer),
+through the same entry points as the affine layers."""
+import numpy as np
+import pytest
+
+import mx4_ref as ref
+import qsmoe_synth as syn
+from gpu_util import TAU, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as t
+    assert t.cuda.is_available(), "GPU tests need a ROCm device"
+    return t
+
+
+@pytest.fixture(scope="module")
+def qs():
+    import quantized_sparse_moe_amd as q
+    q.lib()
+    return q
+
+
+def upload(L, torch, qs):
+    def pack(m, rows, cols):
+        return qs.mx4_pack_rows16(to_dev(ref.pack_rows(m[0]), torch), to_dev(m[1], torch), rows, cols)
+
+    H, I, E = L.hidden, L.inter, L.n_experts
+    sh = None if L.shared is None else (pack(L.shared[0], 2 * I, H), pack(L.shared[1], H, I))
+    return qs.LayerDesc.from_mx4(H, I, E, L.top_k, to_dev(L.router_bits, torch), pack(L.gate_up, E * 2 * I, H),
+                                 pack(L.down, E * H, I), shared=sh,
+                                 router_bias=None if L.bias is None else to_dev(L.bias, torch),
+                                 shared_gate_w=None if L.gate_bits is None else to_dev(L.gate_bits, torch))
+
+
+def run(torch, qs, desc, x, **kw):
+    T = x.shape[0]
+    idx = torch.full((T, desc.top_k), -1, dtype=torch.int32, device="cuda")
+    w = torch.full((T, desc.top_k), -1.0, device="cuda")
+    y = qs.moe_layer_forward(desc, x, topk_idx=idx, topk_w=w, **kw)
+    torch.cuda.synchronize()
+    return y, idx, w
+
+
+def check(L, xb, y, idx, w, what):
+    x = ref.bf16_values(xb)
+    want_idx, gap = L.route(x)
+    gi, gw = idx.cpu().numpy(), w.cpu().numpy().astype(np.float64)
+    clear = gap >= TAU
+    assert (np.diff(gi, axis=1) > 0).all(), what
+    assert np.array_equal(gi[clear], want_idx[clear]), what
+    # the weights: off by the logits' error (twice) and a few fp32 roundings
+    dl = ref.product_bound(x, ref.bf16_values(L.router_bits)).max(axis=1, keepdims=True)
+    assert (np.abs(gw - L.weights(x, gi)) <= 2 * dl + 2.0 ** -20).all(), what
+    want, bound = L.forward(x, gi)                              # (near ties: the GPU's own selection)
+    bf16 = str(y.dtype).endswith("bfloat16")
+    got = y.float().cpu().numpy().astype(np.float64)
+    err = np.abs(got - want)
+    lim = bound + (2.0 ** -8 * (np.abs(want) + bound) if bf16 else 0.0)
+    assert (err <= lim).all(), (what, float((err / lim).max()))
+
+
+LAYERS = {
+    "tiny": dict(hidden=256, inter=128, n_experts=16, top_k=2),
+    "ragged": dict(hidden=192, inter=320, n_experts=20, top_k=3, gated=True),
+    "narrow": dict(hidden=64, inter=64, n_experts=5, top_k=5, shared=False),
+    "one": dict(hidden=128, inter=64, n_experts=1, top_k=1),
+    "many": dict(hidden=576, inter=64, n_experts=256, top_k=16, bias=True, shared=False),
+    "skew": dict(hidden=1088, inter=192, n_experts=100, top_k=8, bias=True, gated=True),
+    "wide": dict(hidden=4160, inter=576, n_experts=6, top_k=2),
+}
+_cache = {}
+
+
+def layer(name):
+    if name not in _cache:
+        _cache[name] = ref.Layer(seed=len(name), **LAYERS[name])
+    return _cache[name]
+
+
+@pytest.mark.parametrize("name", sorted(LAYERS))
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 17, 33, 64, 65, 150])
+def test_layer(torch, qs, name, T):
+    L = layer(name)
+    desc = upload(L, torch, qs)
+    xb = syn.make_x(T, L.hidden, seed=T)
+    x = to_dev(xb, torch)
+    ws = qs.new_workspace(desc, T)
+    for yt in (torch.float32, torch.bfloat16):
+        y, idx, w = run(torch, qs, desc, x, y_dtype=yt, workspace=ws)
+        check(L, xb, y, idx, w, (name, T, yt))
+    # the routing alone, and the entry point that allocates nothing: the same bits
+    ri, rw = qs.moe_route(desc, x, workspace=ws)
+    assert torch.equal(ri, idx) and torch.equal(rw, w)
+    ys = qs.moe_layer_forward_static(desc, x, y_dtype=torch.bfloat16)
+    assert torch.equal(ys, y)
+    # completion counters are back at zero
+    assert (ws[(2 << 20) - 4096:2 << 20] == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 20])
+@pytest.mark.parametrize("sigma", [1e-12, 300.0])
+def test_activation_range(torch, qs, T, sigma):
+    L = layer("tiny")
+    desc = upload(L, torch, qs)
+    xb = syn.make_x(T, L.hidden, seed=T, std=sigma)
+    y, idx, w = run(torch, qs, desc, to_dev(xb, torch))
+    gi = idx.cpu().numpy()
+    x = ref.bf16_values(xb)
+    want_idx, gap = L.route(x)
+    clear = gap >= TAU * max(1.0, sigma)
+    assert np.array_equal(gi[clear], want_idx[clear])
+    want, bound = L.forward(x, gi)
+    # h and y of products of two activations: what leaves fp32's normal range may be flushed
+    assert (np.abs(y.cpu().numpy() - want) <= bound + 2.0 ** -126 * L.inter).all()
+
+
+@pytest.mark.parametrize("T", [1, 9, 64])
+def test_same_tokens_and_all_on_one_expert(torch, qs, T):
+    """Every token the same (one set of experts, every operand row live), twice the same bits."""
+    L = layer("tiny")
+    desc = upload(L, torch, qs)
+    xb = np.repeat(syn.make_x(1, L.hidden, seed=77), T, axis=0)
+    y, idx, w = run(torch, qs, desc, to_dev(xb, torch))
+    check(L, xb, y, idx, w, T)
+    assert (y == y[0]).all()
+    y2, _, _ = run(torch, qs, desc, to_dev(xb, torch))
+    assert torch.equal(y, y2)
+
+
+def test_exact_ties_go_to_the_lower_expert(torch, qs):
+    L = ref.Layer(hidden=128, inter=64, n_experts=12, top_k=4, seed=3)
+    L.router_bits[[1, 5, 9]] = L.router_bits[1]
+    L.router_bits[[2, 3]] = L.router_bits[2]
+    desc = upload(L, torch, qs)
+    xb = syn.make_x(40, 128, seed=1)
+    idx, _ = qs.moe_route(desc, to_dev(xb, torch))
+    l = L.logits(ref.bf16_values(xb))
+    assert np.array_equal(idx.cpu().numpy(), np.sort(np.argsort(-l, axis=1, kind="stable")[:, :4], axis=1))
+
+
+def test_workspace_shared_with_affine_layers_and_graph_replays(torch, qs):
+    """One workspace for an MX4 layer and an affine one, calls of every path in turn, eager
+    and in a captured graph replayed with eager calls in between: always the same bits."""
+    L = layer("skew")
+    mx = upload(L, torch, qs)
+    A = syn.make_layer(**syn.TINY)
+    af = qs.LayerDesc.from_host(A)
+    n = max(qs.moe_workspace_size(mx, 64), qs.moe_workspace_size(af, 40))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    xm = {T: to_dev(syn.make_x(T, L.hidden, seed=T), torch) for T in (1, 6, 30, 70)}
+    xa = {T: to_dev(syn.make_x(T, A.hidden, seed=T), torch) for T in (1, 3, 40)}
+    rm = {T: qs.moe_layer_forward(mx, x, workspace=qs.new_workspace(mx, T)) for T, x in xm.items()}
+    ra = {T: qs.moe_layer_forward(af, x, workspace=qs.new_workspace(af, T)) for T, x in xa.items()}
+    outs = {("m", T): torch.empty_like(r) for T, r in rm.items()} | {("a", T): torch.empty_like(r) for T, r in ra.items()}
+
+    def every():
+        for T in (1, 30, 6, 70):
+            qs.moe_layer_forward(mx, xm[T], y=outs["m", T], workspace=ws)
+            Ta = {1: 3, 30: 1, 6: 40, 70: 1}[T]
+            qs.moe_layer_forward(af, xa[Ta], y=outs["a", Ta], workspace=ws)
+
+    def same():
+        torch.cuda.synchronize()
+        for T in rm:
+            assert torch.equal(outs["m", T], rm[T]), T
+        for T in ra:
+            assert torch.equal(outs["a", T], ra[T]), T
+
+    every()
+    same()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        every()
+    for _ in range(4):
+        for o in outs.values():
+            o.fill_(7.0)
+        g.replay()
+        same()
+        every()
+        same()
+
+
+def test_side_stream_and_empty(torch, qs):
+    L = layer("tiny")
+    desc = upload(L, torch, qs)
+    x = to_dev(syn.make_x(12, L.hidden, seed=4), torch)
+    y = qs.moe_layer_forward(desc, x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y2 = qs.moe_layer_forward(desc, x, stream=side)
+    side.synchronize()
+    assert torch.equal(y, y2)
+    assert qs.moe_layer_forward(desc, x[:0]).shape == (0, L.hidden)
+
+
+def test_guards_around_the_outputs(torch, qs):
+    L = layer("ragged")
+    desc = upload(L, torch, qs)
+    for T in (3, 70):
+        x = to_dev(syn.make_x(T, L.hidden, seed=5), torch)
+        y = torch.full((T + 2, L.hidden), 7.0, device="cuda")
+        idx = torch.full((T + 2, 3), -9, dtype=torch.int32, device="cuda")
+        w = torch.full((T + 2, 3), -9.0, device="cuda")
+        qs.moe_layer_forward(desc, x, y=y[1:T + 1], topk_idx=idx[1:T + 1], topk_w=w[1:T + 1])
+        torch.cuda.synchronize()
+        for t, v in ((y, 7.0), (idx, -9), (w, -9.0)):
+            assert (t[0] == v).all() and (t[T + 1] == v).all() and not (t[1:T + 1] == v).any()
+
+
+def test_products_and_layer_run_together(torch, qs):
+    """A block as it is used: a projection with MX4 weights makes the layer's input, the layer
+    runs, its output is quantized and goes through another projection."""
+    L = layer("tiny")
+    desc = upload(L, torch, qs)
+    rng = np.random.default_rng(9)
+    T, H, N = 11, L.hidden, 160
+    ws = []
+    for shape in ((H, H), (N, H)):
+        c, s = ref.quantize(rng.standard_normal(shape) / 16)
+        ws.append((ref.values(c, s), qs.mx4_pack_rows16(to_dev(ref.pack_rows(c), torch), to_dev(s, torch), *shape)))
+    xb = syn.make_x(T, H, seed=8)
+    a = qs.mx4_gemm(*ws[0][1], H, H, to_dev(xb, torch), y_dtype=torch.bfloat16)
+    y, idx, w = run(torch, qs, desc, a, y_dtype=torch.bfloat16)
+    out = qs.mx4_gemm_mx4x(*ws[1][1], N, H, *qs.mx4_quantize(y), T)
+    torch.cuda.synchronize()
+    av = a.float().cpu().numpy().astype(np.float64)
+    want, bound = ref.bf16_values(xb) @ ws[0][0].T, ref.product_bound(ref.bf16_values(xb), ws[0][0])
+    assert (np.abs(av - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound)).all()
+    check(L, a.view(torch.int16).cpu().numpy().view(np.uint16), y, idx, w, "layer of the projection")
+    yq = ref.values(*ref.quantize(y.float().cpu().numpy().astype(np.float64)))
+    assert (np.abs(out.cpu().numpy() - yq @ ws[1][0].T) <= ref.product_bound(yq, ws[1][0])).all()
