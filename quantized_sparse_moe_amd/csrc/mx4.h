@@ -84,6 +84,18 @@ __device__ __forceinline__ f32x4 mx_mfma(u32x4 a, u32x4 b, f32x4 c, int i, uint3
     }
 }
 
+// the 32 x 32 form over 64 columns: lane r + 32 h holds row r, columns 32 h .. 32 h + 31
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, u32x4 b, f32x16 c, int i, uint32_t sa, uint32_t sb) {
+    const i32x8 A = frag4(a), B = frag4(b);
+    switch (i) {
+        case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, MX_FP4, MX_FP4, 0, (int)sa, 0, (int)sb);
+        case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, MX_FP4, MX_FP4, 1, (int)sa, 1, (int)sb);
+        case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, MX_FP4, MX_FP4, 2, (int)sa, 2, (int)sb);
+        default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, MX_FP4, MX_FP4, 3, (int)sa, 3, (int)sb);
+    }
+}
+
 __device__ __forceinline__ void mx_store(void *y, int64_t i, float v, int y_dtype) {
     if (y_dtype == MOE_F32) ((float *)y)[i] = v;
     else ((uint16_t *)y)[i] = f32_to_bf16(v);

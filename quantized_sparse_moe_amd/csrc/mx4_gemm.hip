@@ -16,6 +16,8 @@ struct GemmArgs {
     int y_dtype;
     int qs;                    // waves that share a panel: one quad each of a chunk of qs quads
     int ppw;                   // panels per workgroup
+    float *part;               // [shares][T][N] partial sums (shares > 1)
+    int shares;                // workgroups that split the columns of a tile between them
 };
 
 // Few tokens: bound by the weight stream.  A wave multiplies one 16-row weight panel by MT
@@ -142,6 +144,290 @@ hipError_t launch_skinny(GemmArgs a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------------- many tokens
+// Bound by the matrix cores: WM x WN waves, each FM x FN fragments of 32 tokens x 32 weight
+// rows (v_mfma 32x32, the weights as first operand so that a lane's registers are neighbouring
+// columns of y).  All operands go global -> LDS by direct-to-LDS loads in a ring of three
+// stages, so that two steps are in flight while one is multiplied; one barrier a step.
+//   bf16 x: a step is 64 columns.  128 bytes of a token's row, its eight 16-byte chunks XORed
+//     by (row / 2) % 8: a 16-byte LDS read is served 16 lanes a cycle, those of one wave half
+//     with equal parity of lane bits 2..4 (measured), and under this key they fall in 64
+//     distinct banks.  Half a weight tile (512 bytes) is one such run already.
+//   MX4 x: a step is 128 columns of both operands' tiles.
+// Scales come a quad (512 columns) at a time into a ring of two.
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ void dma16(const void *g, void *l) {
+    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 16, 0, 0);
+}
+__device__ __forceinline__ void dma4(const void *g, void *l) {
+    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 4, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// this wave's LDS reads are complete and every wave has arrived
+__device__ __forceinline__ void block_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// LDS writes of this wave before its later reads
+__device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+
+template <bool MX, int WM, int WN, int FM, int FN>
+struct Tiled {
+    static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
+    static constexpr int STEP = MX ? 128 : 64;                        // columns
+    static constexpr int PER_Q = 512 / STEP;                          // steps per quad of scales
+    static constexpr int A_BYTES = MX ? BM * 64 : BM * 128, B_BYTES = MX ? BN * 64 : BN * 32;
+    static constexpr int STAGE = A_BYTES + B_BYTES, NSTAGE = 3;
+    static constexpr int SC_BYTES = (MX ? BM * 16 : 0) + BN * 16;     // of a quad
+    static constexpr int A_DMA = A_BYTES / (1024 * NW), B_DMA = B_BYTES / (1024 * NW);
+    static constexpr int DMA = A_DMA + B_DMA;                         // per wave and step
+    static constexpr int SDMA = SC_BYTES / (256 * NW);                // per wave and quad
+    static constexpr int EP = 32 * (FN * 32 * 4 + 16);                // epilogue staging of a wave
+    static constexpr int RING = NSTAGE * STAGE + 2 * SC_BYTES;
+    static constexpr int LDS = RING > NW * EP ? RING : NW * EP;
+    static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole loads per wave");
+    static_assert(SC_BYTES % (256 * NW) == 0, "whole loads per wave");
+};
+
+template <bool MX, int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiled(GemmArgs a) {
+    using C = Tiled<MX, WM, WN, FM, FN>;
+    __shared__ __attribute__((aligned(1024))) uint8_t sm[C::LDS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int r32 = lane & 31, h = lane >> 5;
+    // ---- which tile: a contiguous range of tiles per XCD, eight column tiles wide, so that
+    // the workgroups an XCD runs at a time share their rows of x and of W in its L2
+    const int mtiles = (a.T + C::BM - 1) / C::BM, ntiles = (a.N + C::BN - 1) / C::BN, tiles = mtiles * ntiles;
+    const int id = ((int)blockIdx.x & 7) * ((tiles + 7) >> 3) + ((int)blockIdx.x >> 3);
+    if (id >= tiles || ((int)blockIdx.x >> 3) >= ((tiles + 7) >> 3)) return;
+    const int ng = id / (8 * mtiles), gw = ntiles - 8 * ng < 8 ? ntiles - 8 * ng : 8;
+    const int rem = id - ng * 8 * mtiles;
+    const int t0 = rem / gw * C::BM, n0 = (8 * ng + rem % gw) * C::BN;
+    const int wm = wave / WN, wn = wave % WN;
+
+    const int steps = (a.K + C::STEP - 1) / C::STEP;
+    // this workgroup's share of the steps (whole quads)
+    const int qper = (a.KQ + a.shares - 1) / a.shares;
+    const int k_lo = blockIdx.y * qper * C::PER_Q;
+    const int k_hi = k_lo + qper * C::PER_Q < steps ? k_lo + qper * C::PER_Q : steps;
+
+    // ---- sources of this wave's direct-to-LDS loads (piece i of a stage: 1024 bytes)
+    const uint8_t *asrc[C::A_DMA], *bsrc[C::B_DMA];
+    int kmax[C::A_DMA];                     // bf16 x: the last column offset at which the chunk is whole
+#pragma unroll
+    for (int i = 0; i < C::A_DMA; ++i) {
+        const int piece = wave * C::A_DMA + i;
+        if constexpr (MX) {
+            const int mt = t0 / 16 + piece, nm = (a.T + 15) / 16;
+            asrc[i] = a.xc + (int64_t)(mt < nm ? mt : nm - 1) * a.KS * MX_TILE + 16 * lane;
+            kmax[i] = 0;
+        } else {
+            const int row = 8 * piece + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+            const int t = t0 + row < a.T ? t0 + row : a.T - 1;
+            asrc[i] = (const uint8_t *)(a.x + (int64_t)t * a.ldx + 8 * c);
+            kmax[i] = a.K - 8 * c - 8;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C::B_DMA; ++i) {
+        // bf16 x: half a tile of two panels
+        const int piece = wave * C::B_DMA + i, p = n0 / 16 + (MX ? piece : 2 * piece + h);
+        bsrc[i] = a.wc + (int64_t)(p < a.P ? p : a.P - 1) * a.KS * MX_TILE + 16 * (MX ? lane : r32);
+    }
+    const uint8_t *ssrc[C::SDMA];
+#pragma unroll
+    for (int i = 0; i < C::SDMA; ++i) {
+        const int piece = wave * C::SDMA + i;                // 256 bytes: one panel
+        const int np = MX ? C::BM / 16 : 0, nm = (a.T + 15) / 16;
+        if (piece < np) {
+            const int mt = t0 / 16 + piece;
+            ssrc[i] = a.xs + (int64_t)(mt < nm ? mt : nm - 1) * a.KQ * MX_QS + 4 * lane;
+        } else {
+            const int p = n0 / 16 + piece - np;
+            ssrc[i] = a.ws + (int64_t)(p < a.P ? p : a.P - 1) * a.KQ * MX_QS + 4 * lane;
+        }
+    }
+    auto issue = [&](int k) __attribute__((always_inline)) {
+        uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
+#pragma unroll
+        for (int i = 0; i < C::A_DMA; ++i) {
+            // (bf16 x: columns past K meet zero weights, any value of the row will do)
+            const int off = C::STEP * k;
+            dma16(MX ? asrc[i] + (int64_t)k * MX_TILE : asrc[i] + 2 * (off <= kmax[i] ? off : kmax[i]),
+                  st + (wave * C::A_DMA + i) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < C::B_DMA; ++i)
+            dma16(bsrc[i] + (int64_t)k * (MX ? MX_TILE : MX_TILE / 2), st + C::A_BYTES + (wave * C::B_DMA + i) * 1024);
+        if (k % C::PER_Q == 0) {
+            const int q = k / C::PER_Q;
+            uint8_t *ss = sm + C::NSTAGE * C::STAGE + (q & 1) * C::SC_BYTES + wave * C::SDMA * 256;
+#pragma unroll
+            for (int i = 0; i < C::SDMA; ++i) dma4(ssrc[i] + (int64_t)q * MX_QS, ss + 256 * i);
+        }
+    };
+
+    f32x16 acc[FN][FM];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
+
+    // scales of a quad: lane (row, h) keeps blocks h and 2 + h of each step of 128
+    uint32_t sw[FN][2], sx[FM][2];
+    auto load_scales = [&](int k) __attribute__((always_inline)) {
+        const uint8_t *ss = sm + C::NSTAGE * C::STAGE + ((k / C::PER_Q) & 1) * C::SC_BYTES;
+        const int e = (r32 >> 4) * 256 + 4 * ((r32 & 15) + 16 * h);
+        const uint8_t *sb = ss + (MX ? C::BM * 16 : 0) + wn * FN * 512 + e;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            sw[j][0] = *(const uint32_t *)(sb + 512 * j);
+            sw[j][1] = *(const uint32_t *)(sb + 512 * j + 128);
+        }
+        if constexpr (MX) {
+            const uint8_t *sa = ss + wm * FM * 512 + e;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                sx[i][0] = *(const uint32_t *)(sa + 512 * i);
+                sx[i][1] = *(const uint32_t *)(sa + 512 * i + 128);
+            }
+        }
+    };
+    auto sync_step = [&](int k) __attribute__((always_inline)) {
+        // stage k has landed once at most stage k + 1's loads are outstanding
+        if (k + 1 >= k_hi) wait_dma<0>();
+        else if ((k + 1) % C::PER_Q == 0) wait_dma<C::DMA + C::SDMA>();
+        else wait_dma<C::DMA>();
+        block_sync();
+        if (k + 2 < k_hi) issue(k + 2);
+    };
+
+    if (k_lo < k_hi) issue(k_lo);
+    if (k_lo + 1 < k_hi) issue(k_lo + 1);
+    if constexpr (MX) {
+        for (int k4 = k_lo; k4 < k_hi; k4 += 4) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = k4 + s;
+                if (k >= k_hi) break;
+                sync_step(k);
+                if (s == 0) load_scales(k);
+                const uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
+                const int e = (r32 >> 4) * MX_TILE + 16 * ((r32 & 15) + 16 * h);
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {                // columns 64 f .. 64 f + 63 of the step
+                    u32x4 A[FM], B[FN];
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        B[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 2 * MX_TILE + e + 512 * f);
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        A[i] = *(const u32x4 *)(st + (wm * FM + i) * 2 * MX_TILE + e + 512 * f);
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) acc[j][i] = mx_mfma32(B[j], A[i], acc[j][i], s, sw[j][f], sx[i][f]);
+                }
+            }
+        }
+    } else {
+        for (int k = k_lo; k < k_hi; ++k) {
+            sync_step(k);
+            if (k % C::PER_Q == 0 || k == k_lo) load_scales(k);
+            const uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
+            u32x4 b[FN];
+            float sc[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                b[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 1024 + (r32 >> 4) * 512 + 16 * ((r32 & 15) + 16 * h));
+                sc[j] = mx_scale((k & 1) ? sw[j][1] : sw[j][0], (k >> 1) & 3);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {                    // columns 32 h + 8 m .. + 7
+                bf16x8 A[FM], B[FN];
+                const int pos = (4 * h + m) ^ ((r32 >> 1) & 7);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+                    A[i] = *(const bf16x8 *)(st + ((wm * FM + i) * 32 + r32) * 128 + 16 * pos);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) B[j] = mx_bf16(b[j][m], sc[j]);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(B[j], A[i], acc[j][i], 0, 0, 0);
+            }
+        }
+    }
+    block_sync();                                            // the ring is free
+
+    // ---- epilogue: 32 tokens at a time through LDS, then whole 16-byte pieces of y's rows.
+    // acc[j][i][r]: token 32 i + lane % 32, weight row 32 j + 8 (r / 4) + 4 h + r % 4
+    uint8_t *ep = sm + wave * C::EP;
+    const bool f32 = a.y_dtype == MOE_F32 || a.shares > 1;
+    const int tw = t0 + wm * FM * 32, nw = n0 + wn * FN * 32;
+    void *y = a.shares > 1 ? (void *)(a.part + (int64_t)blockIdx.y * a.T * a.N) : a.y;
+    const int64_t ldy = a.shares > 1 ? a.N : a.ldy;
+    const int esz = f32 ? 4 : 2, per = 16 / esz;             // elements of a 16-byte piece
+    const int pitch = FN * 32 * esz + 16;
+    const bool vec = ((uintptr_t)y & 15) == 0 && (ldy * esz & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                uint8_t *d = ep + r32 * pitch + (32 * j + 8 * r4 + 4 * h) * esz;
+                const f32x16 &v = acc[j][i];
+                if (f32) {
+                    *(f32x4 *)d = (f32x4){v[4 * r4], v[4 * r4 + 1], v[4 * r4 + 2], v[4 * r4 + 3]};
+                } else {
+                    const uint32_t lo = (uint32_t)f32_to_bf16(v[4 * r4]) | ((uint32_t)f32_to_bf16(v[4 * r4 + 1]) << 16);
+                    const uint32_t hi = (uint32_t)f32_to_bf16(v[4 * r4 + 2]) | ((uint32_t)f32_to_bf16(v[4 * r4 + 3]) << 16);
+                    *(uint64_t *)d = (uint64_t)lo | ((uint64_t)hi << 32);
+                }
+            }
+        wave_lds_sync();
+        const int pr = FN * 32 / per;                        // pieces per row
+        for (int c = lane; c < 32 * pr; c += 64) {
+            const int row = c / pr, t = tw + 32 * i + row, n = nw + c % pr * per;
+            if (t >= a.T || n >= a.N) continue;
+            const uint8_t *s = ep + row * pitch + c % pr * 16;
+            uint8_t *d = (uint8_t *)y + (t * ldy + n) * esz;
+            if (vec && n + per <= a.N) *(u32x4 *)d = *(const u32x4 *)s;
+            else
+                for (int q = 0; q < per && n + q < a.N; ++q) {
+                    if (f32) ((float *)d)[q] = ((const float *)s)[q];
+                    else ((uint16_t *)d)[q] = ((const uint16_t *)s)[q];
+                }
+        }
+        wave_lds_sync();
+    }
+}
+
+// the shares' partial sums, in share order
+__global__ __launch_bounds__(256) void k_mx4_join(GemmArgs a) {
+    const int64_t total = (int64_t)a.T * a.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        float v = a.part[i];
+        for (int s = 1; s < a.shares; ++s) v += a.part[s * total + i];
+        mx_store(a.y, i / a.N * a.ldy + i % a.N, v, a.y_dtype);
+    }
+}
+
+template <bool MX, int WM, int WN, int FM, int FN>
+hipError_t launch_tiled(GemmArgs a, hipStream_t s) {
+    using C = Tiled<MX, WM, WN, FM, FN>;
+    const int tiles = ((a.T + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN);
+    hipLaunchKernelGGL((k_mx4_tiled<MX, WM, WN, FM, FN>), dim3((tiles + 7) / 8 * 8, a.shares), dim3(64 * C::NW), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.shares == 1) return e;
+    const int64_t total = (int64_t)a.T * a.N, b = (total + 255) / 256, cap = 8 * (int64_t)n_compute_units();
+    hipLaunchKernelGGL(k_mx4_join, dim3((unsigned)(b < cap ? b : cap)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 GemmArgs make_args(const uint8_t *wc, const uint8_t *ws, int64_t N, int64_t K, int64_t T, void *y, int y_dtype,
                    int64_t ldy) {
     GemmArgs a{};
@@ -156,19 +442,56 @@ GemmArgs make_args(const uint8_t *wc, const uint8_t *ws, int64_t N, int64_t K, i
     a.y = y;
     a.y_dtype = y_dtype;
     a.ldy = ldy;
+    a.shares = 1;
     return a;
 }
 
 }  // namespace
 
-size_t mx4_gemm_ws(int64_t T, int64_t N, int64_t K) { return 0; }
+// Which kernel: up to 16 tokens the skinny one, which has one pass of the weights.  More take
+// tiles, the largest that still give every compute unit one; where even the smallest do not,
+// the columns are split into shares of at least two quads.
+enum Plan { SKINNY, TILE64, TILE128, TILE256 };
+struct Choice {
+    Plan plan;
+    int shares;
+};
+static Choice choose(int64_t T, int64_t N, int64_t K) {
+    if (T <= 16) return {SKINNY, 1};
+    const int64_t cu = n_compute_units();
+    auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((N + n - 1) / n); };
+    if (tiles(256, 256) >= cu) return {TILE256, 1};
+    if (tiles(128, 128) >= cu) return {TILE128, 1};
+    int64_t sh = cu / tiles(64, 128), most = mx4_quads(K) / 2;
+    if (sh > most) sh = most;
+    if (sh > 16) sh = 16;
+    return {TILE64, sh < 1 ? 1 : (int)sh};
+}
+
+size_t mx4_gemm_ws(int64_t T, int64_t N, int64_t K) {
+    const Choice c = choose(T, N, K);
+    return c.shares > 1 ? (size_t)c.shares * T * N * 4 : 0;
+}
+
+template <bool MX>
+static hipError_t launch_product(GemmArgs a, uint8_t *ws, hipStream_t s) {
+    const Choice c = choose(a.T, a.N, a.K);
+    a.shares = c.shares;
+    a.part = (float *)ws;
+    switch (c.plan) {
+        case SKINNY: return launch_skinny<MX>(a, s);
+        case TILE64: return launch_tiled<MX, 2, 2, 1, 2>(a, s);
+        case TILE128: return launch_tiled<MX, 2, 2, 2, 2>(a, s);
+        default: return launch_tiled<MX, 2, 4, 4, 2>(a, s);
+    }
+}
 
 hipError_t launch_mx4_gemm(const uint8_t *wc, const uint8_t *wsc, int64_t N, int64_t K, const uint16_t *x, int64_t T,
                            int64_t ldx, void *y, int y_dtype, int64_t ldy, uint8_t *ws, hipStream_t s) {
     GemmArgs a = make_args(wc, wsc, N, K, T, y, y_dtype, ldy);
     a.x = x;
     a.ldx = ldx;
-    return launch_skinny<false>(a, s);
+    return launch_product<false>(a, ws, s);
 }
 
 hipError_t launch_mx4_gemm_mx4x(const uint8_t *wc, const uint8_t *wsc, int64_t N, int64_t K, const uint8_t *xc,
@@ -177,7 +500,7 @@ hipError_t launch_mx4_gemm_mx4x(const uint8_t *wc, const uint8_t *wsc, int64_t N
     GemmArgs a = make_args(wc, wsc, N, K, T, y, y_dtype, ldy);
     a.xc = xc;
     a.xs = xs;
-    return launch_skinny<true>(a, s);
+    return launch_product<true>(a, ws, s);
 }
 
 }  // namespace qs
