@@ -442,7 +442,7 @@ def _mx4_sizes(rows: int, K: int, layout: int):
 
 def _mx4_buf(t, nbytes: int, where: str) -> int:
     """The address of a caller's buffer, checked for its size and for being contiguous."""
-    if t.nbytes < nbytes or not t.is_contiguous():
+    if not t.is_contiguous() or t.nbytes < nbytes:
         raise QsmoeError(MOE_ERR_INVALID, f"{where}: a buffer is not contiguous or smaller than {nbytes} bytes")
     return t.data_ptr()
 
@@ -551,20 +551,25 @@ def mx4_new_workspace(T: int, N: int, K: int, device="cuda", stream=None):
     return _empty((n,), torch.uint8, device, stream) if n else None
 
 
-def _mx4_out(where, w_codes, w_scales, N, K, T, y, y_dtype, workspace, stream):
-    """(y, (weight addresses), (y address, type code, row stride), workspace, (its address,
-    bytes)) of a product, what the caller did not pass allocated."""
+def _mx4_product(where, call, w_codes, w_scales, N, K, T, x1, x2, args, y, y_dtype, workspace, stream):
     import torch
     nc, ns = _mx4_sizes(N, K, MX4_TILES)
-    w = (_mx4_buf(w_codes, nc, where), _mx4_buf(w_scales, ns, where))
+    wc, ws = _mx4_buf(w_codes, nc, where), _mx4_buf(w_scales, ns, where)
+    ldy = N
     if y is None:
         y = _empty((T, N), y_dtype or torch.float32, w_codes.device, stream)
-    if y.dim() != 2 or y.shape[0] != T or y.shape[1] != N or (N > 1 and y.stride(1) != 1):
-        raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be [T, N] with contiguous rows")
+    else:
+        if y.dim() != 2 or y.shape != (T, N) or (N > 1 and y.stride(1) != 1):
+            raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be [T, N] with contiguous rows")
+        if T > 1:
+            ldy = y.stride(0)
     if workspace is None and T > 0:
         workspace = mx4_new_workspace(T, N, K, w_codes.device, stream)
-    ws = (None, 0) if workspace is None else (_mx4_buf(workspace, 0, where), workspace.nbytes)
-    return y, w, (y.data_ptr(), _out_code(y, where), y.stride(0) if T > 1 else N), workspace, ws
+    pw, nb = (None, 0) if workspace is None else (_mx4_buf(workspace, 0, where), workspace.nbytes)
+    code = _mx4_code(y.dtype)
+    _launch(where, stream, lambda st: call(wc, ws, N, K, *args, y.data_ptr(), code, ldy, pw, nb, st),
+            x1, x2, w_codes, w_scales, y, workspace)
+    return y
 
 
 def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspace=None, stream=None):
@@ -572,10 +577,8 @@ def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspa
     T, k, ldx, code = _mx4_values(x, "mx4_gemm")
     if k != K or code != MOE_BF16:
         raise QsmoeError(MOE_ERR_INVALID, "mx4_gemm: x must be bf16 with K columns")
-    y, w, out, workspace, ws = _mx4_out("mx4_gemm", w_codes, w_scales, N, K, T, y, y_dtype, workspace, stream)
-    _launch("mx4_gemm", stream, lambda st: lib().mx4_gemm(*w, N, K, x.data_ptr(), T, ldx, *out, *ws, st),
-            x, w_codes, w_scales, y, workspace)
-    return y
+    return _mx4_product("mx4_gemm", lib().mx4_gemm, w_codes, w_scales, N, K, T, x, None, (x.data_ptr(), T, ldx),
+                        y, y_dtype, workspace, stream)
 
 
 def mx4_gemm_mx4x(w_codes, w_scales, N: int, K: int, x_codes, x_scales, T: int, y=None, y_dtype=None,
@@ -583,10 +586,8 @@ def mx4_gemm_mx4x(w_codes, w_scales, N: int, K: int, x_codes, x_scales, T: int, 
     """The same product with ``x`` quantized (``mx4_quantize`` into tiles, T rows)."""
     nc, ns = _mx4_sizes(T, K, MX4_TILES)
     xc, xs = _mx4_buf(x_codes, nc, "mx4_gemm_mx4x"), _mx4_buf(x_scales, ns, "mx4_gemm_mx4x")
-    y, w, out, workspace, ws = _mx4_out("mx4_gemm_mx4x", w_codes, w_scales, N, K, T, y, y_dtype, workspace, stream)
-    _launch("mx4_gemm_mx4x", stream, lambda st: lib().mx4_gemm_mx4x(*w, N, K, xc, xs, T, *out, *ws, st),
-            x_codes, x_scales, w_codes, w_scales, y, workspace)
-    return y
+    return _mx4_product("mx4_gemm_mx4x", lib().mx4_gemm_mx4x, w_codes, w_scales, N, K, T, x_codes, x_scales,
+                        (xc, xs, T), y, y_dtype, workspace, stream)
 
 
 def moe_calib_read(buf, stream=None):

@@ -140,15 +140,17 @@ hipError_t launch_mx4_gemm_mx4x(const uint8_t *wc, const uint8_t *wsc, int64_t N
 // the workspace's state region behind the affine kernels' words: zero before the first call,
 // and put back to zero by every call.
 constexpr int MX_TMAX = 64, MX_SHARES = 8;
-constexpr size_t MX_CNT_OFF = WS_CTL_BYTES - 4096;        // bytes; 1 + H / 32 counters
+constexpr size_t MX_CNT_OFF = WS_CTL_BYTES - 4096;        // bytes
+constexpr int MX_CNT_DOWN = 16;                           // counters before: route's
 struct MxBufs {
-    uint32_t *cnt;                 // [0] route, [1 + i] down, 32 output rows each
+    uint32_t *cnt;                 // completion counters: [i] token tile i of route, [MX_TMAX / 16]
+                                   // its tiles, [MX_CNT_DOWN + i] down, 32 output rows each
     float *logits;                 // [T][E + 1] (column E: the shared expert's gate)
     int32_t *idx;                  // [T][K]
     float *w;                      // [T][K]
-    int32_t *act;                  // [E] the chosen experts, ascending
+    int32_t *act;                  // [E] the chosen experts, ascending: id | tokens << 16
     int32_t *nact;                 // [1] how many
-    int16_t *pos;                  // [E][MX_TMAX] a token's row of h under a chosen expert, or -1
+    int16_t *pos;                  // [E][MX_TMAX] under each its tokens' rows of h (t K + j), in order
     uint16_t *h;                   // [T*K + T][2][I] bf16: w silu(g) u as hi and lo
     float *part;                   // [MX_SHARES][T][H] the down shares' sums
 };

@@ -1,21 +1,20 @@
 // mx4_moe.hip -- the sparse MoE layer with MX4 experts for a few tokens (up to MX_TMAX in one
 // pass; more run in passes of MX_TMAX): three launches.
 //
-//   route    router logits on v_mfma_f32_16x16x32_bf16 (16 experts per workgroup, the columns
-//            split over its waves).  The workgroup that finishes last -- counted, so nothing
-//            ever waits -- takes every token's top-k, and lists the experts any token chose
-//            (ascending), with each token's place among their rows of h.
+//   route    router logits on v_mfma_f32_16x16x32_bf16 (16 experts and 16 tokens per
+//            workgroup, the columns split over its waves).  The workgroup that finishes a tile
+//            of tokens last -- counted, so nothing ever waits -- takes their top-k, and the
+//            last of those lists the experts any token chose (ascending) and each one's
+//            tokens.
 //   gate/up  one workgroup per (listed expert, 32 columns of h): gathers the expert's tokens
 //            as the rows of the activation operand, so each expert's weights are read once
 //            however many tokens chose it, and an expert that one token chose costs one
-//            16-row tile.  h = w silu(g) u carries the token's routing weight and leaves as
-//            the bf16 pair hi + lo (h to 2^-17), two operand rows.
-//   down     one workgroup per 32 rows of the output and share of the listed experts: the
-//            experts' down matrices lie side by side along the reduction axis, so the sum over
-//            experts is made by the accumulators; a token's rows of an expert it did not
-//            choose are zero registers (masked loads).  hi and lo of a token are neighbouring
-//            accumulator registers and are added in the lane.  Shares are added in a fixed
-//            order by the share that finishes last.
+//            16-row tile.  h = w silu(g) u carries the token's routing weight and leaves as the
+//            bf16 pair hi + lo (h to 2^-17), two operand rows.
+//   down     one workgroup per 32 rows of the output and share of the listed experts, gathering
+//            each expert's rows of h; hi and lo of a token are neighbouring accumulator
+//            registers and are added in the lane.  Shares are added in a fixed order by the
+//            share that finishes last.
 //
 // All three are bound by the weight stream: (union of the chosen experts + shared) x
 // 3 H I x 17/32 bytes.  Every sum is fp32 in a fixed order; there are no float atomics.
@@ -26,6 +25,7 @@ namespace qs {
 namespace {
 
 constexpr int MT_THREADS = 512, MT_WAVES = 8;
+constexpr int RT_THREADS = 1024, RT_WAVES = 16;
 
 struct MxArgs {
     Layer L;
@@ -33,6 +33,7 @@ struct MxArgs {
     const uint16_t *x;
     int T;
     int gated;
+    int route_only;
     int32_t *out_idx;
     float *out_w;
     void *y;
@@ -45,6 +46,26 @@ __device__ __forceinline__ void st_agent(uint32_t *p, uint32_t v) {
 }
 __device__ __forceinline__ float ld_agent(const float *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// 16 bytes written through to device scope (padded: a vector-ALU write to the data registers
+// within two wait states would replace data the store has not yet read)
+__device__ __forceinline__ void st_agent128(void *p, f32x4 v) {
+    asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 4" ::"v"(p), "v"(v) : "memory");
+}
+
+// four times 16 bytes read at device scope, and waited for here (the compiler does not track
+// loads issued from inline assembly)
+__device__ __forceinline__ void ld_agent128x4(const float *p0, const float *p1, const float *p2, const float *p3,
+                                              f32x4 &a, f32x4 &b, f32x4 &c, f32x4 &d) {
+    asm volatile(
+        "global_load_dwordx4 %0, %4, off sc1\n\t"
+        "global_load_dwordx4 %1, %5, off sc1\n\t"
+        "global_load_dwordx4 %2, %6, off sc1\n\t"
+        "global_load_dwordx4 %3, %7, off sc1\n\t"
+        "s_waitcnt vmcnt(0)"
+        : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+        : "v"(p0), "v"(p1), "v"(p2), "v"(p3)
+        : "memory");
 }
 
 // Whether this workgroup is the last of n to come here.  What it reads of the others' work they
@@ -63,166 +84,167 @@ __device__ __forceinline__ bool last_of(uint32_t *cnt, uint32_t n, int *s_last) 
 }
 
 // ---------------------------------------------------------------------------- route
-template <int MT>
-__global__ __launch_bounds__(MT_THREADS) void k_mx_route(MxArgs a) {
-    __shared__ f32x4 red[MT_WAVES][64];
+// One workgroup per 16 experts (row E: the shared expert's gate) and 16 tokens, the columns
+// split over its waves.  The workgroup that finishes a tile of 16 tokens last takes their
+// top-k, a wave per token (one compute unit takes 4 us over 16 of them, so tiles do not wait
+// for one another); the last of those lists the experts.
+__global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
+    __shared__ f32x4 red[RT_WAVES][64];
     __shared__ int s_last;
-    __shared__ int s_idx[MX_TMAX][16];
     __shared__ int s_slot[256], s_cnt[4];
-    __shared__ uint8_t s_used[256];
+    __shared__ uint32_t s_mask[256][2];                      // tokens that chose the expert
+    __shared__ int16_t s_sel[MX_TMAX * 16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, E = a.L.E, K = a.L.K, T = a.T, NE = E + a.gated;
-    // ---- logits of 16 experts (row E: the shared expert's gate), columns split over waves
     {
-        const int e = blockIdx.x * 16 + n, ec = e < NE ? e : NE - 1;
+        const int e = blockIdx.x * 16 + n, ec = e < NE ? e : NE - 1, tr = blockIdx.y * 16 + n;
         const uint16_t *wr = ec < E ? a.L.router_w + (int64_t)ec * H : a.L.shared_gate_w;
-        f32x4 acc[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        const uint16_t *xr = a.x + (int64_t)tr * H;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         const int steps = H / 32;
-        for (int s0 = wave; s0 < steps; s0 += 4 * MT_WAVES) {
-            u32x4 B[4], A[MT][4];
+        for (int s0 = wave; s0 < steps; s0 += 4 * RT_WAVES) {
+            u32x4 B[4], A[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int s = s0 + i * MT_WAVES, k = 32 * s + 8 * g;
-                const bool live = s < steps;
-                B[i] = live ? *(const u32x4 *)(wr + k) : (u32x4){0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const int t = 16 * m + n;
-                    A[m][i] = live && t < T ? *(const u32x4 *)(a.x + (int64_t)t * H + k) : (u32x4){0u, 0u, 0u, 0u};
+                const int s = s0 + i * RT_WAVES, k = 32 * s + 8 * g;
+                B[i] = A[i] = (u32x4){0u, 0u, 0u, 0u};
+                if (s < steps) {
+                    B[i] = *(const u32x4 *)(wr + k);
+                    if (tr < T) A[i] = *(const u32x4 *)(xr + k);
                 }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A[m][i]),
-                                                                     __builtin_bit_cast(bf16x8, B[i]), acc[m], 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A[i]),
+                                                              __builtin_bit_cast(bf16x8, B[i]), acc, 0, 0, 0);
         }
+        red[wave][lane] = acc;
+        __syncthreads();
+        const int t = blockIdx.y * 16 + (tid >> 4), ee = blockIdx.x * 16 + (tid & 15);
+        if (tid < 256 && t < T && ee < NE) {
+            const int l = (tid & 15) + 16 * (tid >> 6), r = (tid >> 4) & 3;
+            float v = red[0][l][r];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            red[wave][lane] = acc[m];
-            __syncthreads();
-            const int t = 16 * m + (tid >> 4), ee = blockIdx.x * 16 + (tid & 15);
-            if (tid < 256 && t < T && ee < NE) {
-                const int l = (tid & 15) + 16 * (tid >> 6), r = (tid >> 4) & 3;
-                float v = red[0][l][r];
-#pragma unroll
-                for (int w = 1; w < MT_WAVES; ++w) v += red[w][l][r];
-                if (a.L.router_bias && ee < E) v += a.L.router_bias[ee];
-                st_agent((uint32_t *)a.b.logits + t * (E + 1) + ee, __float_as_uint(v));
-            }
-            __syncthreads();
+            for (int w = 1; w < RT_WAVES; ++w) v += red[w][l][r];
+            if (a.L.router_bias && ee < E) v += a.L.router_bias[ee];
+            st_agent((uint32_t *)a.b.logits + t * (E + 1) + ee, __float_as_uint(v));
         }
     }
-    if (!last_of(a.b.cnt, gridDim.x, &s_last)) return;
-    // ---- the last workgroup: one wave per token takes the top-k
-    if (tid < 256) s_used[tid] = 0;
-    __syncthreads();
-    for (int t = wave; t < T; t += MT_WAVES) {
+    if (!last_of(a.b.cnt + blockIdx.y, gridDim.x, &s_last)) return;
+    const int t = blockIdx.y * 16 + wave;
+    if (t < T) {
+        const float *lg = a.b.logits + t * (E + 1);
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float l = lane + 64 * i < E ? ld_agent(a.b.logits + t * (E + 1) + lane + 64 * i) : 0.0f;
+            const int e = lane + 64 * i;
+            const float l = e < E ? ld_agent(lg + e) : 0.0f;
             v[i] = l != l ? -__builtin_inff() : l;
         }
         TopkOut tk = wave_topk_regs(v, E, K);
         tk.idx = min(max(tk.idx, 0), E - 1);
         if (lane < K) {
-            s_idx[t][lane] = tk.idx;
-            s_used[tk.idx] = 1;
-            a.b.idx[t * K + lane] = tk.idx;
+            st_agent((uint32_t *)a.b.idx + t * K + lane, (uint32_t)tk.idx);
             a.b.w[t * K + lane] = tk.w;
             if (a.out_idx) a.out_idx[t * K + lane] = tk.idx;
             if (a.out_w) a.out_w[t * K + lane] = tk.w;
         }
     }
+    if (a.route_only) return;
+    if (gridDim.y > 1 && !last_of(a.b.cnt + MX_TMAX / 16, gridDim.y, &s_last)) return;
+    if (gridDim.y == 1) {                                    // (idx went through memory)
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    }
+    // ---- the chosen experts in ascending order, and under each its tokens in order
+    if (tid < 256) s_mask[tid][0] = s_mask[tid][1] = 0u;
     __syncthreads();
-    // ---- the chosen experts in ascending order, and each token's row of h under them
-    const bool used = tid < 256 && s_used[tid];
-    const uint64_t bal = __ballot(used);
+    for (int i = tid; i < T * K; i += RT_THREADS) {
+        const int e = (int)__hip_atomic_load((const uint32_t *)a.b.idx + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int tt = i / K;
+        s_sel[i] = (int16_t)e;
+        atomicOr(&s_mask[e][tt >> 5], 1u << (tt & 31));
+    }
+    __syncthreads();
+    const uint64_t mask = tid < 256 ? s_mask[tid][0] | (uint64_t)s_mask[tid][1] << 32 : 0ull;
+    const uint64_t bal = __ballot(mask != 0);
     if (tid < 256 && lane == 0) s_cnt[wave] = __popcll(bal);
     __syncthreads();
-    const int nact = s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3];
     if (tid < 256) {
         int base = 0;
         for (int w = 0; w < wave; ++w) base += s_cnt[w];
         const int slot = base + __popcll(bal & ((1ull << lane) - 1));
         s_slot[tid] = slot;
-        if (used) a.b.act[slot] = tid;
+        if (mask) a.b.act[slot] = tid | __popcll(mask) << 16;
     }
-    if (tid == 0) *a.b.nact = nact;
-    for (int i = tid; i < nact * MX_TMAX; i += MT_THREADS) a.b.pos[i] = -1;
+    if (tid == 0) *a.b.nact = s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3];
     __syncthreads();
-    for (int i = tid; i < T * K; i += MT_THREADS) {
-        const int t = i / K;
-        a.b.pos[s_slot[s_idx[t][i % K]] * MX_TMAX + t] = (int16_t)i;
+    for (int i = tid; i < T * K; i += RT_THREADS) {
+        const int e = s_sel[i], tt = i / K;
+        const uint64_t m = s_mask[e][0] | (uint64_t)s_mask[e][1] << 32;
+        a.b.pos[s_slot[e] * MX_TMAX + __popcll(m & ((1ull << tt) - 1))] = (int16_t)i;
     }
 }
 
 // -------------------------------------------------------------------------- gate/up
-__global__ __launch_bounds__(MT_THREADS) void k_mx_gate_up(MxArgs a) {
+__global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_gate_up(MxArgs a) {
     __shared__ f32x4 red[MT_WAVES][2][64];
-    __shared__ int s_tok[MX_TMAX], s_pos[MX_TMAX];
     __shared__ float s_w[MX_TMAX];
-    __shared__ int s_n;
+    __shared__ int s_pos[MX_TMAX];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, I = a.L.I, K = a.L.K, T = a.T;
     const int slot = (int)blockIdx.y - (a.L.has_shared ? 1 : 0);
     const bool sh = slot < 0;
-    if (!sh && slot >= *a.b.nact) return;
-    const int64_t e = sh ? 0 : a.b.act[slot];
-    const QMat mg = sh ? a.L.s_gate : a.L.gate, mu = sh ? a.L.s_up : a.L.up;
+    // the expert and its tokens (one round trip), in order: the rows of the activation operand
+    int e = 0, cnt = T, pos = T * K + lane;
+    if (!sh) {
+        const int nact = *a.b.nact, act = a.b.act[slot];
+        pos = a.b.pos[slot * MX_TMAX + lane];
+        if (slot >= nact) return;
+        e = act & 0xffff;
+        cnt = act >> 16;
+    }
+    // (field by field: a choice between two descriptors would put the arguments in memory)
+    const uint8_t *gc = sh ? a.L.s_gate.codes : a.L.gate.codes, *uc = sh ? a.L.s_up.codes : a.L.up.codes;
+    const uint8_t *gs = (const uint8_t *)(sh ? a.L.s_gate.scales : a.L.gate.scales);
+    const uint8_t *us = (const uint8_t *)(sh ? a.L.s_up.scales : a.L.up.scales);
+    const int64_t gst = sh ? a.L.s_gate.stride : a.L.gate.stride, ust = sh ? a.L.s_up.stride : a.L.up.stride;
     const int KS = (H + 127) >> 7, KQ = (KS + 3) >> 2;
     const int pw = wave & 1, kg = wave >> 1;                 // 16-column panel, share of the columns
     const int p = 2 * blockIdx.x + pw;
-    const int64_t pg = (e * mg.stride) / 16 + p, pu = (e * mu.stride) / 16 + p;
-
-    // the expert's tokens, in order: the rows of the activation operand
-    if (wave == 0) {
-        int pos = -1;
-        float w = 1.0f;
-        if (lane < T) {
-            pos = sh ? T * K + lane : a.b.pos[slot * MX_TMAX + lane];
-            if (pos >= 0 && !sh) w = a.b.w[pos];
-            if (sh && a.gated) w = sigmoid(a.b.logits[lane * (a.L.E + 1) + a.L.E]);
+    const int64_t pg = (e * gst) / 16 + p, pu = (e * ust) / 16 + p;
+    u32x4 bg[4], bu[4];
+    uint32_t sg = 0, su = 0;
+    auto load_w = [&](int q) __attribute__((always_inline)) {
+        sg = *(const uint32_t *)(gs + (pg * KQ + q) * MX_QS + 4 * lane);
+        su = *(const uint32_t *)(us + (pu * KQ + q) * MX_QS + 4 * lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = 4 * q + (4 * q + i < KS ? i : 0);
+            bg[i] = __builtin_nontemporal_load((const u32x4 *)(gc + (pg * KS + s) * MX_TILE + 16 * lane));
+            bu[i] = __builtin_nontemporal_load((const u32x4 *)(uc + (pu * KS + s) * MX_TILE + 16 * lane));
         }
-        const uint64_t bal = __ballot(pos >= 0);
-        if (pos >= 0) {
-            const int r = __popcll(bal & ((1ull << lane) - 1));
-            s_tok[r] = lane;
-            s_pos[r] = pos;
-            s_w[r] = w;
-        }
-        if (lane == 0) s_n = __popcll(bal);
+    };
+    if (kg < KQ) load_w(kg);
+    if (wave == 0 && lane < cnt) {
+        s_pos[lane] = pos;
+        s_w[lane] = !sh ? a.b.w[pos] : a.gated ? sigmoid(a.b.logits[lane * (a.L.E + 1) + a.L.E]) : 1.0f;
     }
-    __syncthreads();
-    const int cnt = s_n;
     for (int m0 = 0; m0 < cnt; m0 += 16) {
-        const bool live = m0 + n < cnt;
-        const uint16_t *xr = a.x + (int64_t)(live ? s_tok[m0 + n] : 0) * H;
+        const int ps = __shfl(pos, m0 + n < cnt ? m0 + n : 0);
+        const uint16_t *xr = a.x + (int64_t)(sh ? ps - T * K : ps / K) * H;
         f32x4 ag = {0.f, 0.f, 0.f, 0.f}, au = {0.f, 0.f, 0.f, 0.f};
         for (int q = kg; q < KQ; q += MT_WAVES / 2) {
-            u32x4 bg[4], bu[4];
-            const uint32_t sg = *(const uint32_t *)((const uint8_t *)mg.scales + (pg * KQ + q) * MX_QS + 4 * lane);
-            const uint32_t su = *(const uint32_t *)((const uint8_t *)mu.scales + (pu * KQ + q) * MX_QS + 4 * lane);
+            // (the first quad of the first tokens is loaded; rows of at most 2048 columns have
+            // one quad per wave, which then stays in its registers for all tokens)
+            if (q != kg || (m0 && KQ > MT_WAVES / 2)) load_w(q);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int s = 4 * q + (4 * q + i < KS ? i : 0);
-                bg[i] = __builtin_nontemporal_load((const u32x4 *)(mg.codes + (pg * KS + s) * MX_TILE + 16 * lane));
-                bu[i] = __builtin_nontemporal_load((const u32x4 *)(mu.codes + (pu * KS + s) * MX_TILE + 16 * lane));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int s = 4 * q + i;
-                if (s >= KS) break;
+                if (4 * q + i >= KS) break;
+                // (rows past the tokens repeat the first, columns past H meet zero weights)
                 u32x4 A[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = 128 * s + 32 * g + 8 * j;
-                    A[j] = live && k < H ? *(const u32x4 *)(xr + k) : (u32x4){0u, 0u, 0u, 0u};
-                }
+                for (int j = 0; j < 4; ++j) A[j] = *(const u32x4 *)(xr + min(128 * (4 * q + i) + 32 * g + 8 * j, H - 8));
                 const float cg = mx_scale(sg, i), cu = mx_scale(su, i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -258,98 +280,115 @@ __global__ __launch_bounds__(MT_THREADS) void k_mx_gate_up(MxArgs a) {
 }
 
 // ----------------------------------------------------------------------------- down
-// MT activation tiles of 8 tokens (16 rows: hi and lo of each)
-template <int MT>
-__global__ __launch_bounds__(MT_THREADS) void k_mx_down(MxArgs a) {
-    __shared__ f32x2 red[MT_WAVES][2][64];
+// An item is a quad of one expert's columns (the shared expert first) for 32 output rows; its
+// tokens come eight at a time (16 operand rows, hi and lo of each).  Each wave adds its items'
+// results into sums of its own in LDS, in item order (a register accumulator per token would
+// have to run every item over all tokens); the waves' sums are added in wave order.
+__global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_down(MxArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float sums[];   // [MT_WAVES][T][32]
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, I = a.L.I, K = a.L.K, T = a.T;
     const int KS = (I + 127) >> 7, KQ = (KS + 3) >> 2;
     const int nsh = a.L.has_shared ? 1 : 0;
-    const int items = (*a.b.nact + nsh) * KQ;
     const int z = blockIdx.y;
     const int p0 = 2 * blockIdx.x;                           // H is a multiple of 64
-    f32x4 acc[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int it = z * MT_WAVES + wave; it < items; it += a.shares * MT_WAVES) {
-        const int slot = it / KQ - nsh, q = it % KQ;         // the shared expert first
-        const bool sh = slot < 0;
-        const int64_t e = sh ? 0 : a.b.act[slot];
-        const QMat md = sh ? a.L.s_down : a.L.down;
+    float *mine = sums + wave * T * 32;
+    // the expert and the tokens of the next item are fetched while this one is multiplied
+    int act_nx = 0, pos_nx = 0;
+    auto fetch = [&](int it) __attribute__((always_inline)) {
+        const int slot = it / KQ - nsh;
+        const bool ok = slot >= 0 && slot < a.L.E;
+        act_nx = ok ? a.b.act[slot] : T << 16;
+        pos_nx = ok ? (int)a.b.pos[slot * MX_TMAX + lane] : T * K + lane;
+    };
+    int it = z * MT_WAVES + wave;
+    fetch(it);
+    const int items = (*a.b.nact + nsh) * KQ;
+    for (int i = lane; i < T * 32; i += 64) mine[i] = 0.0f;
+    for (; it < items; it += a.shares * MT_WAVES) {
+        const int q = it % KQ;
+        const bool sh = it / KQ < nsh;
+        const int e = __builtin_amdgcn_readfirstlane(act_nx & 0xffff), cnt = __builtin_amdgcn_readfirstlane(act_nx >> 16);
+        const int pos = pos_nx;
+        const uint8_t *codes = sh ? a.L.s_down.codes : a.L.down.codes;
+        const uint8_t *scales = (const uint8_t *)(sh ? a.L.s_down.scales : a.L.down.scales);
+        const int64_t pe = (e * (sh ? a.L.s_down.stride : a.L.down.stride)) / 16 + p0;
         u32x4 b[2][4];
         uint32_t sc[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int64_t p = (e * md.stride) / 16 + p0 + u;
-            sc[u] = *(const uint32_t *)((const uint8_t *)md.scales + (p * KQ + q) * MX_QS + 4 * lane);
+            sc[u] = *(const uint32_t *)(scales + ((pe + u) * KQ + q) * MX_QS + 4 * lane);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int s = 4 * q + (4 * q + i < KS ? i : 0);
-                b[u][i] = __builtin_nontemporal_load((const u32x4 *)(md.codes + (p * KS + s) * MX_TILE + 16 * lane));
+                b[u][i] = __builtin_nontemporal_load((const u32x4 *)(codes + ((pe + u) * KS + s) * MX_TILE + 16 * lane));
             }
         }
-        int pos[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int t = 8 * m + (n >> 1);
-            pos[m] = t < T ? (sh ? T * K + t : (int)a.b.pos[slot * MX_TMAX + t]) : -1;
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (__ballot(pos[m] >= 0) == 0ull) continue;     // none of these tokens chose it
-            const uint16_t *hr = a.b.h + (int64_t)(pos[m] >= 0 ? 2 * pos[m] + (n & 1) : 0) * I;
+        for (int m0 = 0; m0 < cnt; m0 += 8) {
+            const int r = m0 + (n >> 1), ps = __shfl(pos, r < cnt ? r : 0);
+            const uint16_t *hr = a.b.h + (int64_t)(2 * ps + (n & 1)) * I;
+            f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            if (m0 == 0) fetch(it + a.shares * MT_WAVES);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int s = 4 * q + i;
-                if (s >= KS) break;
+                if (4 * q + i >= KS) break;
+                // (rows past the tokens repeat the first, columns past I meet zero weights)
                 u32x4 A[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = 128 * s + 32 * g + 8 * j;
-                    A[j] = pos[m] >= 0 && k < I ? *(const u32x4 *)(hr + k) : (u32x4){0u, 0u, 0u, 0u};
-                }
+                for (int j = 0; j < 4; ++j) A[j] = *(const u32x4 *)(hr + min(128 * (4 * q + i) + 32 * g + 8 * j, I - 8));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float cs = mx_scale(sc[u], i);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, A[j]), mx_bf16(b[u][i][j], cs), acc[m][u], 0, 0, 0);
+                        acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, A[j]), mx_bf16(b[u][i][j], cs), acc[u], 0, 0, 0);
+                }
+            }
+            // hi and lo of a token are registers 0, 1 (or 2, 3) of one lane
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int rr = m0 + 2 * g + x, pt = __shfl(pos, rr < cnt ? rr : 0);
+                if (rr < cnt) {
+                    float *d = mine + (sh ? pt - T * K : pt / K) * 32 + n;
+                    d[0] += acc[0][2 * x] + acc[0][2 * x + 1];
+                    d[16] += acc[1][2 * x] + acc[1][2 * x + 1];
                 }
             }
         }
     }
-    // join the waves in order, a tile of tokens at a time; rows 2 t and 2 t + 1 of a token
-    // are registers 0, 1 (or 2, 3) of one lane
-    float *part = a.b.part + (int64_t)z * T * H;
+    __syncthreads();
+    // thread: token tid / 8, columns 4 (tid % 8) .. + 3
+    const int tk = tid >> 3, c4 = 4 * (tid & 7);
+    const bool live = tk < T;
+    const int64_t o = (int64_t)tk * H + 32 * blockIdx.x + c4;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (live)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            red[wave][u][lane] = (f32x2){acc[m][u][0] + acc[m][u][1], acc[m][u][2] + acc[m][u][3]};
-        __syncthreads();
-        if (tid < 256) {
-            const int u = tid >> 7, l = (tid >> 1) & 63, r = tid & 1;
-            float v = red[0][u][l][r];
-#pragma unroll
-            for (int w = 1; w < MT_WAVES; ++w) v += red[w][u][l][r];
-            const int t = 8 * m + 2 * (l >> 4) + r, col = 16 * (p0 + u) + (l & 15);
-            if (t < T) {
-                if (a.shares == 1) mx_store(a.y, (int64_t)t * H + col, v, a.y_dtype);
-                else st_agent((uint32_t *)part + (int64_t)t * H + col, __float_as_uint(v));
+        for (int w = 0; w < MT_WAVES; ++w) v += *(const f32x4 *)(sums + (w * T + tk) * 32 + c4);
+    if (a.shares > 1) {
+        if (live) st_agent128(a.b.part + (int64_t)z * T * H + o, v);
+        if (!last_of(a.b.cnt + MX_CNT_DOWN + blockIdx.x, a.shares, &s_last)) return;
+        if (live) {
+            v = (f32x4){0.f, 0.f, 0.f, 0.f};
+            const float *pp = a.b.part + o;
+            const int64_t st = (int64_t)T * H;
+            for (int s = 0; s < a.shares; s += 4) {          // (past the last: repeated, not added)
+                const int l = a.shares - 1;
+                f32x4 q0, q1, q2, q3;
+                ld_agent128x4(pp + s * st, pp + min(s + 1, l) * st, pp + min(s + 2, l) * st, pp + min(s + 3, l) * st, q0,
+                              q1, q2, q3);
+                v += q0;
+                if (s + 1 <= l) v += q1;
+                if (s + 2 <= l) v += q2;
+                if (s + 3 <= l) v += q3;
             }
         }
-        __syncthreads();
     }
-    if (a.shares == 1 || !last_of(a.b.cnt + 1 + blockIdx.x, a.shares, &s_last)) return;
-    for (int i = tid; i < T * 32; i += MT_THREADS) {
-        const int64_t o = (int64_t)(i >> 5) * H + 32 * blockIdx.x + (i & 31);
-        float v = ld_agent(a.b.part + o);
-        for (int s = 1; s < a.shares; ++s) v += ld_agent(a.b.part + (int64_t)s * T * H + o);
-        mx_store(a.y, o, v, a.y_dtype);
-    }
+    if (live)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx_store(a.y, o + c, v[c], a.y_dtype);
 }
 
 // workgroups per 32 output rows: enough for two per compute unit, at most one per wave-item
@@ -377,21 +416,17 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     a.y = y;
     a.y_dtype = y_dtype;
     a.shares = down_shares(L, T);
-    const dim3 thr(MT_THREADS);
-    const unsigned rg = (unsigned)((L.E + a.gated + 15) / 16);
-    if (T <= 16) hipLaunchKernelGGL(k_mx_route<1>, dim3(rg), thr, 0, s, a);
-    else if (T <= 32) hipLaunchKernelGGL(k_mx_route<2>, dim3(rg), thr, 0, s, a);
-    else hipLaunchKernelGGL(k_mx_route<4>, dim3(rg), thr, 0, s, a);
+    a.route_only = route_only;
+    hipLaunchKernelGGL(k_mx_route, dim3((unsigned)((L.E + a.gated + 15) / 16), (unsigned)((T + 15) / 16)),
+                       dim3(RT_THREADS), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || route_only) return e;
     const int64_t routed = T * L.K < L.E ? T * L.K : L.E;
-    hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)(routed + (L.has_shared ? 1 : 0))), thr, 0, s, a);
+    hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)(routed + (L.has_shared ? 1 : 0))),
+                       dim3(MT_THREADS), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const dim3 grid((unsigned)(L.H / 32), (unsigned)a.shares);
-    if (T <= 8) hipLaunchKernelGGL(k_mx_down<1>, grid, thr, 0, s, a);
-    else if (T <= 16) hipLaunchKernelGGL(k_mx_down<2>, grid, thr, 0, s, a);
-    else if (T <= 32) hipLaunchKernelGGL(k_mx_down<4>, grid, thr, 0, s, a);
-    else hipLaunchKernelGGL(k_mx_down<8>, grid, thr, 0, s, a);
+    hipLaunchKernelGGL(k_mx_down, dim3((unsigned)(L.H / 32), (unsigned)a.shares), dim3(MT_THREADS),
+                       (size_t)MT_WAVES * T * 32 * 4, s, a);
     return hipGetLastError();
 }
 
