@@ -38,7 +38,7 @@ struct MxArgs {
     float *out_w;
     void *y;
     int y_dtype;
-    int shares;                       // down: workgroups per 32 output rows
+    int shares;                       // down: workgroups that share the items of the same output rows
 };
 
 __device__ __forceinline__ void st_agent(uint32_t *p, uint32_t v) {
@@ -144,26 +144,25 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
         TopkOut tk = wave_topk_regs(v, E, K);
         tk.idx = min(max(tk.idx, 0), E - 1);
         if (lane < K) {
-            st_agent((uint32_t *)a.b.idx + t * K + lane, (uint32_t)tk.idx);
+            s_sel[t * K + lane] = (int16_t)tk.idx;
+            if (gridDim.y > 1) st_agent((uint32_t *)a.b.idx + t * K + lane, (uint32_t)tk.idx);
             a.b.w[t * K + lane] = tk.w;
             if (a.out_idx) a.out_idx[t * K + lane] = tk.idx;
             if (a.out_w) a.out_w[t * K + lane] = tk.w;
         }
     }
     if (a.route_only) return;
-    if (gridDim.y > 1 && !last_of(a.b.cnt + MX_TMAX / 16, gridDim.y, &s_last)) return;
-    if (gridDim.y == 1) {                                    // (idx went through memory)
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-    }
+    const bool tiles = gridDim.y > 1;                        // (else the selections are all in LDS)
+    if (tiles && !last_of(a.b.cnt + MX_TMAX / 16, gridDim.y, &s_last)) return;
     // ---- the chosen experts in ascending order, and under each its tokens in order
     if (tid < 256) s_mask[tid][0] = s_mask[tid][1] = 0u;
     __syncthreads();
     for (int i = tid; i < T * K; i += RT_THREADS) {
-        const int e = (int)__hip_atomic_load((const uint32_t *)a.b.idx + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (tiles)
+            s_sel[i] = (int16_t)__hip_atomic_load((const uint32_t *)a.b.idx + i, __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT);
         const int tt = i / K;
-        s_sel[i] = (int16_t)e;
-        atomicOr(&s_mask[e][tt >> 5], 1u << (tt & 31));
+        atomicOr(&s_mask[s_sel[i]][tt >> 5], 1u << (tt & 31));
     }
     __syncthreads();
     const uint64_t mask = tid < 256 ? s_mask[tid][0] | (uint64_t)s_mask[tid][1] << 32 : 0ull;
@@ -280,20 +279,22 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
 }
 
 // ----------------------------------------------------------------------------- down
-// An item is a quad of one expert's columns (the shared expert first) for 32 output rows; its
+// An item is a quad of one expert's columns (the shared expert first) for 16 NP output rows; its
 // tokens come eight at a time (16 operand rows, hi and lo of each).  Each wave adds its items'
 // results into sums of its own in LDS, in item order (a register accumulator per token would
 // have to run every item over all tokens); the waves' sums are added in wave order.
-__global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_down(MxArgs a) {
-    extern __shared__ __attribute__((aligned(16))) float sums[];   // [MT_WAVES][T][32]
+template <int NP, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_down(MxArgs a) {
+    constexpr int C = 16 * NP;                               // output rows
+    extern __shared__ __attribute__((aligned(16))) float sums[];   // [W][T][C]
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, I = a.L.I, K = a.L.K, T = a.T;
     const int KS = (I + 127) >> 7, KQ = (KS + 3) >> 2;
     const int nsh = a.L.has_shared ? 1 : 0;
     const int z = blockIdx.y;
-    const int p0 = 2 * blockIdx.x;                           // H is a multiple of 64
-    float *mine = sums + wave * T * 32;
+    const int p0 = NP * blockIdx.x;                          // H is a multiple of 64
+    float *mine = sums + wave * T * C;
     // the expert and the tokens of the next item are fetched while this one is multiplied
     int act_nx = 0, pos_nx = 0;
     auto fetch = [&](int it) __attribute__((always_inline)) {
@@ -302,11 +303,11 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
         act_nx = ok ? a.b.act[slot] : T << 16;
         pos_nx = ok ? (int)a.b.pos[slot * MX_TMAX + lane] : T * K + lane;
     };
-    int it = z * MT_WAVES + wave;
+    int it = z * W + wave;
     fetch(it);
     const int items = (*a.b.nact + nsh) * KQ;
-    for (int i = lane; i < T * 32; i += 64) mine[i] = 0.0f;
-    for (; it < items; it += a.shares * MT_WAVES) {
+    for (int i = lane; i < T * C; i += 64) mine[i] = 0.0f;
+    for (; it < items; it += a.shares * W) {
         const int q = it % KQ;
         const bool sh = it / KQ < nsh;
         const int e = __builtin_amdgcn_readfirstlane(act_nx & 0xffff), cnt = __builtin_amdgcn_readfirstlane(act_nx >> 16);
@@ -314,10 +315,10 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
         const uint8_t *codes = sh ? a.L.s_down.codes : a.L.down.codes;
         const uint8_t *scales = (const uint8_t *)(sh ? a.L.s_down.scales : a.L.down.scales);
         const int64_t pe = (e * (sh ? a.L.s_down.stride : a.L.down.stride)) / 16 + p0;
-        u32x4 b[2][4];
-        uint32_t sc[2];
+        u32x4 b[NP][4];
+        uint32_t sc[NP];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < NP; ++u) {
             sc[u] = *(const uint32_t *)(scales + ((pe + u) * KQ + q) * MX_QS + 4 * lane);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -328,8 +329,10 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
         for (int m0 = 0; m0 < cnt; m0 += 8) {
             const int r = m0 + (n >> 1), ps = __shfl(pos, r < cnt ? r : 0);
             const uint16_t *hr = a.b.h + (int64_t)(2 * ps + (n & 1)) * I;
-            f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            if (m0 == 0) fetch(it + a.shares * MT_WAVES);
+            f32x4 acc[NP];
+#pragma unroll
+            for (int u = 0; u < NP; ++u) acc[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            if (m0 == 0) fetch(it + a.shares * W);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (4 * q + i >= KS) break;
@@ -338,7 +341,7 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
 #pragma unroll
                 for (int j = 0; j < 4; ++j) A[j] = *(const u32x4 *)(hr + min(128 * (4 * q + i) + 32 * g + 8 * j, I - 8));
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < NP; ++u) {
                     const float cs = mx_scale(sc[u], i);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -351,22 +354,23 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
             for (int x = 0; x < 2; ++x) {
                 const int rr = m0 + 2 * g + x, pt = __shfl(pos, rr < cnt ? rr : 0);
                 if (rr < cnt) {
-                    float *d = mine + (sh ? pt - T * K : pt / K) * 32 + n;
-                    d[0] += acc[0][2 * x] + acc[0][2 * x + 1];
-                    d[16] += acc[1][2 * x] + acc[1][2 * x + 1];
+                    float *d = mine + (sh ? pt - T * K : pt / K) * C + n;
+#pragma unroll
+                    for (int u = 0; u < NP; ++u) d[16 * u] += acc[u][2 * x] + acc[u][2 * x + 1];
                 }
             }
         }
     }
     __syncthreads();
-    // thread: token tid / 8, columns 4 (tid % 8) .. + 3
-    const int tk = tid >> 3, c4 = 4 * (tid & 7);
+    // thread: a token and four columns
+    constexpr int PC = C / 4;
+    const int tk = tid / PC, c4 = 4 * (tid % PC);
     const bool live = tk < T;
-    const int64_t o = (int64_t)tk * H + 32 * blockIdx.x + c4;
+    const int64_t o = (int64_t)tk * H + C * blockIdx.x + c4;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (live)
 #pragma unroll
-        for (int w = 0; w < MT_WAVES; ++w) v += *(const f32x4 *)(sums + (w * T + tk) * 32 + c4);
+        for (int w = 0; w < W; ++w) v += *(const f32x4 *)(sums + (w * T + tk) * C + c4);
     if (a.shares > 1) {
         if (live) st_agent128(a.b.part + (int64_t)z * T * H + o, v);
         if (!last_of(a.b.cnt + MX_CNT_DOWN + blockIdx.x, a.shares, &s_last)) return;
@@ -391,14 +395,31 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
         for (int c = 0; c < 4; ++c) mx_store(a.y, o + c, v[c], a.y_dtype);
 }
 
-// workgroups per 32 output rows: enough for two per compute unit, at most one per wave-item
-int down_shares(const Layer &L, int64_t T) {
-    const int groups = L.H / 32, want = (2 * n_compute_units() + groups - 1) / groups;
-    int64_t slots = T * L.K < L.E ? T * L.K : L.E;           // (at most)
-    slots = (slots + (L.has_shared ? 1 : 0)) * ((L.I + 511) / 512);
-    const int64_t most = (slots + MT_WAVES - 1) / MT_WAVES;
-    const int s = want < MX_SHARES ? want : MX_SHARES;
-    return (int)(most < s ? most : s);
+// At most 32 items (one to three tokens of top-8): one panel per workgroup and 16 waves, so one
+// or two rounds of loads and no shares (T = 1: 6.6 us against 7.9; T = 7, 57 items: 15.4
+// against 12.3).  More: two panels and 8 waves, each row of h read for twice the weights, the
+// items shared out until there are two workgroups per compute unit.
+struct DownPlan {
+    int np, waves, shares;
+};
+DownPlan down_plan(const Layer &L, int64_t T) {
+    DownPlan d;
+    int64_t items = T * L.K < L.E ? T * L.K : L.E;           // (at most)
+    items = (items + (L.has_shared ? 1 : 0)) * ((L.I + 511) / 512);
+    if (items <= 32) {
+        d.np = 1;
+        d.waves = 16;
+        d.shares = 1;
+        return d;
+    }
+    d.np = 2;
+    d.waves = 8;
+    const int groups = L.H / (16 * d.np), want = (2 * n_compute_units() + groups - 1) / groups;
+    const int64_t most = (items + d.waves - 1) / d.waves;
+    int64_t s = want < MX_SHARES ? want : MX_SHARES;
+    if (s > most) s = most;
+    d.shares = (int)s;
+    return d;
 }
 
 }  // namespace
@@ -415,7 +436,8 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     a.out_w = out_w;
     a.y = y;
     a.y_dtype = y_dtype;
-    a.shares = down_shares(L, T);
+    const DownPlan d = down_plan(L, T);
+    a.shares = d.shares;
     a.route_only = route_only;
     hipLaunchKernelGGL(k_mx_route, dim3((unsigned)((L.E + a.gated + 15) / 16), (unsigned)((T + 15) / 16)),
                        dim3(RT_THREADS), 0, s, a);
@@ -425,8 +447,10 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)(routed + (L.has_shared ? 1 : 0))),
                        dim3(MT_THREADS), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(k_mx_down, dim3((unsigned)(L.H / 32), (unsigned)a.shares), dim3(MT_THREADS),
-                       (size_t)MT_WAVES * T * 32 * 4, s, a);
+    const dim3 grid((unsigned)(L.H / (16 * d.np)), (unsigned)a.shares), thr((unsigned)(64 * d.waves));
+    const size_t lds = (size_t)d.waves * T * 16 * d.np * 4;
+    if (d.np == 1) hipLaunchKernelGGL((k_mx_down<1, 16>), grid, thr, lds, s, a);
+    else hipLaunchKernelGGL((k_mx_down<2, 8>), grid, thr, lds, s, a);
     return hipGetLastError();
 }
 
