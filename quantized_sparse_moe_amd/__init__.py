@@ -440,22 +440,26 @@ def _mx4_sizes(rows: int, K: int, layout: int):
     return p * ((K + 127) // 128) * 1024, p * ((K + 511) // 512) * 256
 
 
+def _mx4_bad(where: str, what: str):
+    raise QsmoeError(MOE_ERR_INVALID, f"{where}: {what}")
+
+
 def _mx4_buf(t, nbytes: int, where: str) -> int:
     """The address of a caller's buffer, checked for its size and for being contiguous."""
-    if not t.is_contiguous() or t.nbytes < nbytes:
-        raise QsmoeError(MOE_ERR_INVALID, f"{where}: a buffer is not contiguous or smaller than {nbytes} bytes")
+    if t.nbytes < nbytes or not t.is_contiguous():
+        _mx4_bad(where, f"a buffer is not contiguous or smaller than {nbytes} bytes")
     return t.data_ptr()
 
 
-_mx4_codes = None
+_mx4_codes = {}
 
 
 def _mx4_code(dtype):
     """MOE_* code of a torch type of values (16-bit integers are bf16 bits), or None."""
-    global _mx4_codes
-    if _mx4_codes is None:
+    if not _mx4_codes:
         import torch
-        _mx4_codes = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+        _mx4_codes.update({torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16,
+                           torch.float32: MOE_F32})
     return _mx4_codes.get(dtype)
 
 
@@ -463,30 +467,48 @@ def _mx4_values(x, where: str):
     """(rows, K, row stride, type code) of a 2-d matrix of values."""
     code = _mx4_code(x.dtype)
     if code is None or x.dim() != 2:
-        raise QsmoeError(MOE_ERR_INVALID, f"{where}: a matrix of a supported type is needed")
+        _mx4_bad(where, "a matrix of a supported type is needed")
     rows, K = x.shape
+    if x.is_contiguous():
+        return rows, K, K, code
     ld, inner = x.stride()
     if K > 1 and inner != 1:
-        raise QsmoeError(MOE_ERR_INVALID, f"{where}: the rows of a matrix must be contiguous")
+        _mx4_bad(where, "the rows of a matrix must be contiguous")
     return rows, K, (ld if rows > 1 else K), code
 
 
-def _launch(where: str, stream, call, first, *others):
-    """call(stream handle) on the GPU that all the tensors share, whatever the current
-    device is; `stream` None is that GPU's current stream."""
-    import torch
-    dev = first.device
-    if dev.type != "cuda" or any(t is not None and t.device != dev for t in others):
-        raise QsmoeError(MOE_ERR_INVALID, f"{where}: the tensors must be on one GPU")
+_current = None
+
+
+def _mx4_stream(where: str, stream, gpu: int, *others):
+    """(stream handle, whether `gpu` is the current device), once it is made sure that all
+    tensors are on that GPU; `stream` None is its current stream."""
+    global _current
+    if gpu < 0:
+        _mx4_bad(where, "the tensors must be on a GPU")
+    for t in others:
+        if t is not None and t.get_device() != gpu:
+            _mx4_bad(where, "the tensors must be on one GPU")
+    if _current is None:
+        import torch
+        _current = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        handle = _current[0](gpu)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch._C._cuda_getDevice() == dev.index:
-        _check(call(handle), where)
+    return handle, _current[1]() == gpu
+
+
+def _mx4_call(where: str, f, gpu: int, here: bool, *args) -> None:
+    """The C call, on the tensors' GPU whatever the current device is."""
+    if here:
+        status = f(*args)
     else:
-        with torch.cuda.device(dev):
-            _check(call(handle), where)
+        import torch
+        with torch.cuda.device(gpu):
+            status = f(*args)
+    if status != MOE_OK:
+        raise QsmoeError(status, where)
 
 
 def mx4_quantize(x, codes=None, scales=None, layout: int = MX4_TILES, stream=None):
@@ -500,8 +522,9 @@ def mx4_quantize(x, codes=None, scales=None, layout: int = MX4_TILES, stream=Non
     if scales is None:
         scales = _empty((ns,), torch.uint8, x.device, stream)
     pc, ps = _mx4_buf(codes, nc, "mx4_quantize"), _mx4_buf(scales, ns, "mx4_quantize")
-    _launch("mx4_quantize", stream,
-            lambda st: lib().mx4_quantize(x.data_ptr(), code, rows, K, ldx, layout, pc, ps, st), x, codes, scales)
+    gpu = x.get_device()
+    st, here = _mx4_stream("mx4_quantize", stream, gpu, codes, scales)
+    _mx4_call("mx4_quantize", lib().mx4_quantize, gpu, here, x.data_ptr(), code, rows, K, ldx, layout, pc, ps, st)
     return codes, scales
 
 
@@ -514,9 +537,10 @@ def mx4_dequantize(codes, scales, rows: int, K: int, y=None, y_dtype=None, layou
         y = _empty((rows, K), y_dtype or torch.float32, codes.device, stream)
     r, k, ldy, code = _mx4_values(y, "mx4_dequantize")
     if r != rows or k != K:
-        raise QsmoeError(MOE_ERR_INVALID, "mx4_dequantize: y has another shape")
-    _launch("mx4_dequantize", stream,
-            lambda st: lib().mx4_dequantize(pc, ps, rows, K, layout, y.data_ptr(), code, ldy, st), codes, scales, y)
+        _mx4_bad("mx4_dequantize", "y has another shape")
+    gpu = codes.get_device()
+    st, here = _mx4_stream("mx4_dequantize", stream, gpu, scales, y)
+    _mx4_call("mx4_dequantize", lib().mx4_dequantize, gpu, here, pc, ps, rows, K, layout, y.data_ptr(), code, ldy, st)
     return y
 
 
@@ -532,8 +556,9 @@ def mx4_pack_rows16(codes, scales, rows: int, K: int, t_codes=None, t_scales=Non
     if t_scales is None:
         t_scales = _empty((ns,), torch.uint8, codes.device, stream)
     tc, ts = _mx4_buf(t_codes, nc, "mx4_pack_rows16"), _mx4_buf(t_scales, ns, "mx4_pack_rows16")
-    _launch("mx4_pack_rows16", stream, lambda st: lib().mx4_pack_rows16(pc, ps, rows, K, tc, ts, st),
-            codes, scales, t_codes, t_scales)
+    gpu = codes.get_device()
+    st, here = _mx4_stream("mx4_pack_rows16", stream, gpu, scales, t_codes, t_scales)
+    _mx4_call("mx4_pack_rows16", lib().mx4_pack_rows16, gpu, here, pc, ps, rows, K, tc, ts, st)
     return t_codes, t_scales
 
 
@@ -551,24 +576,26 @@ def mx4_new_workspace(T: int, N: int, K: int, device="cuda", stream=None):
     return _empty((n,), torch.uint8, device, stream) if n else None
 
 
-def _mx4_product(where, call, w_codes, w_scales, N, K, T, x1, x2, args, y, y_dtype, workspace, stream):
+def _mx4_product(where, f, w_codes, w_scales, N, K, T, x1, x2, x_args, y, y_dtype, workspace, stream):
     import torch
     nc, ns = _mx4_sizes(N, K, MX4_TILES)
     wc, ws = _mx4_buf(w_codes, nc, where), _mx4_buf(w_scales, ns, where)
     ldy = N
     if y is None:
         y = _empty((T, N), y_dtype or torch.float32, w_codes.device, stream)
-    else:
-        if y.dim() != 2 or y.shape != (T, N) or (N > 1 and y.stride(1) != 1):
-            raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be [T, N] with contiguous rows")
-        if T > 1:
-            ldy = y.stride(0)
+    elif y.dim() != 2 or y.shape != (T, N) or (N > 1 and y.stride(1) != 1):
+        _mx4_bad(where, "y must be [T, N] with contiguous rows")
+    elif T > 1:
+        ldy = y.stride(0)
     if workspace is None and T > 0:
         workspace = mx4_new_workspace(T, N, K, w_codes.device, stream)
-    pw, nb = (None, 0) if workspace is None else (_mx4_buf(workspace, 0, where), workspace.nbytes)
     code = _mx4_code(y.dtype)
-    _launch(where, stream, lambda st: call(wc, ws, N, K, *args, y.data_ptr(), code, ldy, pw, nb, st),
-            x1, x2, w_codes, w_scales, y, workspace)
+    if code is None:
+        _mx4_bad(where, "y must be float32 or bfloat16")
+    pw, nb = (None, 0) if workspace is None else (_mx4_buf(workspace, 0, where), workspace.nbytes)
+    gpu = w_codes.get_device()
+    st, here = _mx4_stream(where, stream, gpu, x1, x2, w_scales, y, workspace)
+    _mx4_call(where, f, gpu, here, wc, ws, N, K, *x_args, y.data_ptr(), code, ldy, pw, nb, st)
     return y
 
 
@@ -576,7 +603,7 @@ def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspa
     """``y`` [T, N] = ``x`` [T, K] (bf16) times the transpose of an MX4 matrix in tiles."""
     T, k, ldx, code = _mx4_values(x, "mx4_gemm")
     if k != K or code != MOE_BF16:
-        raise QsmoeError(MOE_ERR_INVALID, "mx4_gemm: x must be bf16 with K columns")
+        _mx4_bad("mx4_gemm", "x must be bf16 with K columns")
     return _mx4_product("mx4_gemm", lib().mx4_gemm, w_codes, w_scales, N, K, T, x, None, (x.data_ptr(), T, ldx),
                         y, y_dtype, workspace, stream)
 

@@ -154,7 +154,8 @@ hipError_t launch_skinny(GemmArgs a, hipStream_t s) {
 //     with equal parity of lane bits 2..4 (measured), and under this key they fall in 64
 //     distinct banks.  Half a weight tile (512 bytes) is one such run already.
 //   MX4 x: a step is 128 columns of both operands' tiles.
-// Scales come a quad (512 columns) at a time into a ring of two.
+// Scales come a quad (512 columns) at a time; every wave has them in registers a step later, long
+// before the next quad's arrive in their place.
 typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ void dma16(const void *g, void *l) {
     __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 16, 0, 0);
@@ -182,14 +183,58 @@ struct Tiled {
     static constexpr int DMA = A_DMA + B_DMA;                         // per wave and step
     static constexpr int SDMA = SC_BYTES / (256 * NW);                // per wave and quad
     static constexpr int EP = 32 * (FN * 32 * 4 + 16);                // epilogue staging of a wave
-    static constexpr int RING = NSTAGE * STAGE + 2 * SC_BYTES;
+    static constexpr int RING = NSTAGE * STAGE + SC_BYTES;
     static constexpr int LDS = RING > NW * EP ? RING : NW * EP;
     static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole loads per wave");
     static_assert(SC_BYTES % (256 * NW) == 0, "whole loads per wave");
 };
 
+// Epilogue of a wave: 32 tokens at a time through its LDS area ep, then whole 16-byte pieces of
+// y's rows.  acc[j][i][r]: token 32 i + lane % 32, weight row 32 j + 8 (r / 4) + 4 h + r % 4.
+template <bool F32, int FM, int FN>
+__device__ __forceinline__ void tiled_store(const f32x16 (&acc)[FN][FM], uint8_t *ep, void *y, int64_t ldy, int T, int N,
+                                            int t0, int n0) {
+    constexpr int ESZ = F32 ? 4 : 2, PER = 16 / ESZ;         // elements of a 16-byte piece
+    constexpr int PITCH = FN * 32 * ESZ + 16, PR = FN * 32 / PER;   // pieces of a row
+    constexpr int RP = 64 / PR;                              // rows per store
+    const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
+    const int row = lane / PR, n = n0 + lane % PR * PER;
+    const bool vec = ((uintptr_t)y & 15) == 0 && (ldy * ESZ & 15) == 0 && n + PER <= N;
+    const uint8_t *src = ep + row * PITCH + lane % PR * 16;
+    uint8_t *dst = (uint8_t *)y + ((t0 + row) * ldy + n) * ESZ;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                uint8_t *d = ep + r32 * PITCH + (32 * j + 8 * r4 + 4 * h) * ESZ;
+                const f32x16 &v = acc[j][i];
+                const f32x4 f = {v[4 * r4], v[4 * r4 + 1], v[4 * r4 + 2], v[4 * r4 + 3]};
+                if constexpr (F32) *(f32x4 *)d = f;
+                else *(bf16x4 *)d = __builtin_convertvector(f, bf16x4);   // (nearest even)
+            }
+        wave_lds_sync();
+#pragma unroll
+        for (int c = 0; c < 32 / RP; ++c) {
+            const int t = t0 + 32 * i + RP * c + row;
+            const u32x4 v = *(const u32x4 *)(src + RP * c * PITCH);
+            if (t < T) {
+                uint8_t *d = dst + (32 * i + RP * c) * ldy * ESZ;
+                if (vec) __builtin_nontemporal_store(v, (u32x4 *)d);   // (y is not read here)
+                else
+                    for (int q = 0; q < PER && n + q < N; ++q) {
+                        if constexpr (F32) ((uint32_t *)d)[q] = v[q];
+                        else ((uint16_t *)d)[q] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
+                    }
+            }
+        }
+        wave_lds_sync();
+    }
+}
+
 template <bool MX, int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiled(GemmArgs a) {
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void k_mx4_tiled(GemmArgs a) {
     using C = Tiled<MX, WM, WN, FM, FN>;
     __shared__ __attribute__((aligned(1024))) uint8_t sm[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -260,7 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiled(GemmArgs a) {
             dma16(bsrc[i] + (int64_t)k * (MX ? MX_TILE : MX_TILE / 2), st + C::A_BYTES + (wave * C::B_DMA + i) * 1024);
         if (k % C::PER_Q == 0) {
             const int q = k / C::PER_Q;
-            uint8_t *ss = sm + C::NSTAGE * C::STAGE + (q & 1) * C::SC_BYTES + wave * C::SDMA * 256;
+            uint8_t *ss = sm + C::NSTAGE * C::STAGE + wave * C::SDMA * 256;
 #pragma unroll
             for (int i = 0; i < C::SDMA; ++i) dma4(ssrc[i] + (int64_t)q * MX_QS, ss + 256 * i);
         }
@@ -276,8 +321,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiled(GemmArgs a) {
 
     // scales of a quad: lane (row, h) keeps blocks h and 2 + h of each step of 128
     uint32_t sw[FN][2], sx[FM][2];
-    auto load_scales = [&](int k) __attribute__((always_inline)) {
-        const uint8_t *ss = sm + C::NSTAGE * C::STAGE + ((k / C::PER_Q) & 1) * C::SC_BYTES;
+    auto load_scales = [&]() __attribute__((always_inline)) {
+        const uint8_t *ss = sm + C::NSTAGE * C::STAGE;
         const int e = (r32 >> 4) * 256 + 4 * ((r32 & 15) + 16 * h);
         const uint8_t *sb = ss + (MX ? C::BM * 16 : 0) + wn * FN * 512 + e;
 #pragma unroll
@@ -312,7 +357,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiled(GemmArgs a) {
                 const int k = k4 + s;
                 if (k >= k_hi) break;
                 sync_step(k);
-                if (s == 0) load_scales(k);
+                if (s == 0) load_scales();
                 const uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
                 const int e = (r32 >> 4) * MX_TILE + 16 * ((r32 & 15) + 16 * h);
 #pragma unroll
@@ -334,7 +379,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiled(GemmArgs a) {
     } else {
         for (int k = k_lo; k < k_hi; ++k) {
             sync_step(k);
-            if (k % C::PER_Q == 0 || k == k_lo) load_scales(k);
+            if (k % C::PER_Q == 0 || k == k_lo) load_scales();
             const uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
             u32x4 b[FN];
             float sc[FN];
@@ -343,67 +388,39 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx4_tiled(GemmArgs a) {
                 b[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 1024 + (r32 >> 4) * 512 + 16 * ((r32 & 15) + 16 * h));
                 sc[j] = mx_scale((k & 1) ? sw[j][1] : sw[j][0], (k >> 1) & 3);
             }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {                    // columns 32 h + 8 m .. + 7
-                bf16x8 A[FM], B[FN];
+            // columns 32 h + 8 m .. + 7: x of m + 1 is read while m is multiplied
+            bf16x8 A[2][FM];
+            auto load_a = [&](int m) __attribute__((always_inline)) {
                 const int pos = (4 * h + m) ^ ((r32 >> 1) & 7);
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
-                    A[i] = *(const bf16x8 *)(st + ((wm * FM + i) * 32 + r32) * 128 + 16 * pos);
+                    A[m & 1][i] = *(const bf16x8 *)(st + ((wm * FM + i) * 32 + r32) * 128 + 16 * pos);
+            };
+            load_a(0);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                if (m < 3) load_a(m + 1);
+                bf16x8 B[FN];
 #pragma unroll
                 for (int j = 0; j < FN; ++j) B[j] = mx_bf16(b[j][m], sc[j]);
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
-                        acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(B[j], A[i], acc[j][i], 0, 0, 0);
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(B[j], A[m & 1][i], acc[j][i], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);           // (no reads of later columns drawn ahead)
             }
         }
     }
     block_sync();                                            // the ring is free
 
-    // ---- epilogue: 32 tokens at a time through LDS, then whole 16-byte pieces of y's rows.
-    // acc[j][i][r]: token 32 i + lane % 32, weight row 32 j + 8 (r / 4) + 4 h + r % 4
-    uint8_t *ep = sm + wave * C::EP;
-    const bool f32 = a.y_dtype == MOE_F32 || a.shares > 1;
     const int tw = t0 + wm * FM * 32, nw = n0 + wn * FN * 32;
-    void *y = a.shares > 1 ? (void *)(a.part + (int64_t)blockIdx.y * a.T * a.N) : a.y;
-    const int64_t ldy = a.shares > 1 ? a.N : a.ldy;
-    const int esz = f32 ? 4 : 2, per = 16 / esz;             // elements of a 16-byte piece
-    const int pitch = FN * 32 * esz + 16;
-    const bool vec = ((uintptr_t)y & 15) == 0 && (ldy * esz & 15) == 0;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                uint8_t *d = ep + r32 * pitch + (32 * j + 8 * r4 + 4 * h) * esz;
-                const f32x16 &v = acc[j][i];
-                if (f32) {
-                    *(f32x4 *)d = (f32x4){v[4 * r4], v[4 * r4 + 1], v[4 * r4 + 2], v[4 * r4 + 3]};
-                } else {
-                    const uint32_t lo = (uint32_t)f32_to_bf16(v[4 * r4]) | ((uint32_t)f32_to_bf16(v[4 * r4 + 1]) << 16);
-                    const uint32_t hi = (uint32_t)f32_to_bf16(v[4 * r4 + 2]) | ((uint32_t)f32_to_bf16(v[4 * r4 + 3]) << 16);
-                    *(uint64_t *)d = (uint64_t)lo | ((uint64_t)hi << 32);
-                }
-            }
-        wave_lds_sync();
-        const int pr = FN * 32 / per;                        // pieces per row
-        for (int c = lane; c < 32 * pr; c += 64) {
-            const int row = c / pr, t = tw + 32 * i + row, n = nw + c % pr * per;
-            if (t >= a.T || n >= a.N) continue;
-            const uint8_t *s = ep + row * pitch + c % pr * 16;
-            uint8_t *d = (uint8_t *)y + (t * ldy + n) * esz;
-            if (vec && n + per <= a.N) *(u32x4 *)d = *(const u32x4 *)s;
-            else
-                for (int q = 0; q < per && n + q < a.N; ++q) {
-                    if (f32) ((float *)d)[q] = ((const float *)s)[q];
-                    else ((uint16_t *)d)[q] = ((const uint16_t *)s)[q];
-                }
-        }
-        wave_lds_sync();
-    }
+    if (a.shares > 1)
+        tiled_store<true, FM, FN>(acc, sm + wave * C::EP, a.part + (int64_t)blockIdx.y * a.T * a.N, a.N, a.T, a.N, tw, nw);
+    else if (a.y_dtype == MOE_F32)
+        tiled_store<true, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
+    else
+        tiled_store<false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
 }
 
 // the shares' partial sums, in share order
@@ -460,7 +477,7 @@ static Choice choose(int64_t T, int64_t N, int64_t K) {
     if (T <= 16) return {SKINNY, 1};
     const int64_t cu = n_compute_units();
     auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((N + n - 1) / n); };
-    if (tiles(256, 256) >= cu) return {TILE256, 1};
+    if (tiles(128, 256) >= 2 * cu) return {TILE256, 1};
     if (tiles(128, 128) >= cu) return {TILE128, 1};
     int64_t sh = cu / tiles(64, 128), most = mx4_quads(K) / 2;
     if (sh > most) sh = most;
@@ -482,7 +499,7 @@ static hipError_t launch_product(GemmArgs a, uint8_t *ws, hipStream_t s) {
         case SKINNY: return launch_skinny<MX>(a, s);
         case TILE64: return launch_tiled<MX, 2, 2, 1, 2>(a, s);
         case TILE128: return launch_tiled<MX, 2, 2, 2, 2>(a, s);
-        default: return launch_tiled<MX, 2, 4, 4, 2>(a, s);
+        default: return launch_tiled<MX, 1, 4, 4, 2>(a, s);
     }
 }
 
