@@ -186,8 +186,16 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
 }
 
 // -------------------------------------------------------------------------- gate/up
+// The tokens' rows of x are staged in LDS, 2048 columns at a time: read as MFMA operands from
+// global memory they are 64 separate 16-byte pieces a load, which costs the address unit four
+// times a contiguous one.
+constexpr int GU_QUADS = MT_WAVES / 2;                       // quads of a chunk: one per wave pair
+constexpr int GU_PITCH = GU_QUADS * 1024 + 16;               // bytes of a staged row (padded: banks)
+
 __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_gate_up(MxArgs a) {
-    __shared__ f32x4 red[MT_WAVES][2][64];
+    // [min(T, 16)][GU_PITCH] of x, then the waves' sums in its place
+    extern __shared__ __attribute__((aligned(16))) uint8_t sx[];
+    f32x4(*red)[2][64] = (f32x4(*)[2][64])sx;
     __shared__ float s_w[MX_TMAX];
     __shared__ int s_pos[MX_TMAX];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
@@ -209,7 +217,7 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
     const uint8_t *us = (const uint8_t *)(sh ? a.L.s_up.scales : a.L.up.scales);
     const int64_t gst = sh ? a.L.s_gate.stride : a.L.gate.stride, ust = sh ? a.L.s_up.stride : a.L.up.stride;
     const int KS = (H + 127) >> 7, KQ = (KS + 3) >> 2;
-    const int pw = wave & 1, kg = wave >> 1;                 // 16-column panel, share of the columns
+    const int pw = wave & 1, kg = wave >> 1;                 // 16-column panel, quad of a chunk
     const int p = 2 * blockIdx.x + pw;
     const int64_t pg = (e * gst) / 16 + p, pu = (e * ust) / 16 + p;
     u32x4 bg[4], bu[4];
@@ -230,41 +238,49 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
         s_w[lane] = !sh ? a.b.w[pos] : a.gated ? sigmoid(a.b.logits[lane * (a.L.E + 1) + a.L.E]) : 1.0f;
     }
     for (int m0 = 0; m0 < cnt; m0 += 16) {
-        const int ps = __shfl(pos, m0 + n < cnt ? m0 + n : 0);
-        const uint16_t *xr = a.x + (int64_t)(sh ? ps - T * K : ps / K) * H;
+        const int rows = min(cnt - m0, 16), r = n < rows ? n : rows - 1;   // (past the tokens: repeated, discarded)
         f32x4 ag = {0.f, 0.f, 0.f, 0.f}, au = {0.f, 0.f, 0.f, 0.f};
-        for (int q = kg; q < KQ; q += MT_WAVES / 2) {
+        for (int q0 = 0; q0 < KQ; q0 += GU_QUADS) {
             // (the first quad of the first tokens is loaded; rows of at most 2048 columns have
             // one quad per wave, which then stays in its registers for all tokens)
-            if (q != kg || (m0 && KQ > MT_WAVES / 2)) load_w(q);
+            const int q = q0 + kg;
+            if ((q0 || (m0 && KQ > GU_QUADS)) && q < KQ) load_w(q);
+            // a wave stages whole rows, 1 KB per load (columns past H meet zero weights: any value
+            // of the row will do)
+            for (int i = wave; i < rows * GU_QUADS; i += MT_WAVES) {
+                const int row = i / GU_QUADS, c = i % GU_QUADS, ps = __builtin_amdgcn_readlane(pos, m0 + row);
+                const int t = sh ? ps - T * K : ps / K, k = min((q0 + c) * 512 + 8 * lane, H - 8);
+                *(u32x4 *)(sx + row * GU_PITCH + 1024 * c + 16 * lane) = *(const u32x4 *)(a.x + (int64_t)t * H + k);
+            }
+            __syncthreads();
+            if (q < KQ) {
+                const uint8_t *xr = sx + r * GU_PITCH + 1024 * kg + 64 * g;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (4 * q + i >= KS) break;
-                // (rows past the tokens repeat the first, columns past H meet zero weights)
-                u32x4 A[4];
+                for (int i = 0; i < 4; ++i) {
+                    if (4 * q + i >= KS) break;
+                    const float cg = mx_scale(sg, i), cu = mx_scale(su, i);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) A[j] = *(const u32x4 *)(xr + min(128 * (4 * q + i) + 32 * g + 8 * j, H - 8));
-                const float cg = mx_scale(sg, i), cu = mx_scale(su, i);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bf16x8 Aj = __builtin_bit_cast(bf16x8, A[j]);
-                    ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Aj, mx_bf16(bg[i][j], cg), ag, 0, 0, 0);
-                    au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Aj, mx_bf16(bu[i][j], cu), au, 0, 0, 0);
+                    for (int j = 0; j < 4; ++j) {
+                        const bf16x8 A = *(const bf16x8 *)(xr + 256 * i + 16 * j);
+                        ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, mx_bf16(bg[i][j], cg), ag, 0, 0, 0);
+                        au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, mx_bf16(bu[i][j], cu), au, 0, 0, 0);
+                    }
                 }
             }
+            __syncthreads();                                 // the chunk is consumed
         }
         red[wave][0][lane] = ag;
         red[wave][1][lane] = au;
         __syncthreads();
         // thread: token m0 + tid / 32, column tid % 32 of the block
         const int tk = tid >> 5, c = tid & 31;
-        if (m0 + tk < cnt) {
-            const int l = (c & 15) + 16 * (tk >> 2), r = tk & 3, w0 = c >> 4;
+        if (tk < rows) {
+            const int l = (c & 15) + 16 * (tk >> 2), rr = tk & 3, w0 = c >> 4;
             float gv = 0.0f, uv = 0.0f;
 #pragma unroll
             for (int k = 0; k < MT_WAVES / 2; ++k) {
-                gv += red[w0 + 2 * k][0][l][r];
-                uv += red[w0 + 2 * k][1][l][r];
+                gv += red[w0 + 2 * k][0][l][rr];
+                uv += red[w0 + 2 * k][1][l][rr];
             }
             // h = w silu(g) u as the bf16 pair hi + lo
             const float h = silu(gv) * uv * s_w[m0 + tk];
@@ -444,8 +460,9 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || route_only) return e;
     const int64_t routed = T * L.K < L.E ? T * L.K : L.E;
+    const size_t gu_x = (size_t)(T < 16 ? T : 16) * GU_PITCH, gu_red = MT_WAVES * 2048, gu_lds = gu_x > gu_red ? gu_x : gu_red;
     hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)(routed + (L.has_shared ? 1 : 0))),
-                       dim3(MT_THREADS), 0, s, a);
+                       dim3(MT_THREADS), gu_lds, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const dim3 grid((unsigned)(L.H / (16 * d.np)), (unsigned)a.shares), thr((unsigned)(64 * d.waves));
     const size_t lds = (size_t)d.waves * T * 16 * d.np * 4;
