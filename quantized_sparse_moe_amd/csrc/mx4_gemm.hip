@@ -14,20 +14,24 @@ struct GemmArgs {
     int64_t ldx, ldy;
     int N, T, K, KS, KQ, P;    // KS, KQ: steps and quads of K; P: weight panels
     int y_dtype;
-    int qs;                    // waves that share a panel: one quad each of a chunk of qs quads
+    int qs;                    // waves that share a panel, taking quads wq, wq + qs, ...
     int ppw;                   // panels per workgroup
-    float *part;               // [shares][T][N] partial sums (shares > 1)
+    float *part;               // [shares][T][part_pitch(N)] partial sums (shares > 1)
     int shares;                // workgroups that split the columns of a tile between them
 };
 
-// Few tokens: bound by the weight stream.  A wave multiplies one 16-row weight panel by MT
-// 16-token activation tiles over its share of the columns; every weight tile is read once, with
+constexpr int MAX_SHARES = 16;
+// row pitch of the shares' partial sums: whole 16-byte pieces
+__host__ __device__ inline int64_t part_pitch(int64_t N) { return (N + 3) / 4 * 4; }
+
+// Up to 16 tokens: bound by the weight stream.  A wave multiplies one 16-row weight panel by the
+// 16-token activation tile over its share of the columns; every weight tile is read once, with
 // contiguous 16-byte loads straight into registers, a chunk (one quad per wave, 4 KB of codes)
-// ahead of its use.  bf16 activations are staged in LDS a chunk at a time, with coalesced
-// reads (an MFMA operand read from global memory touches 64 separate 16-byte pieces, which
-// costs the address unit four times the 16 cycles of a contiguous one); MX4 activations come
-// as tiles and need no staging.  The qs waves of a panel meet in LDS, summed in wave order.
-template <bool MX, int MT>
+// ahead of its use.  bf16 activations are staged in LDS with coalesced reads (an MFMA operand
+// read from global memory touches 64 separate 16-byte pieces, which costs the address unit four
+// times the 16 cycles of a contiguous one); MX4 activations come as tiles and need no staging.
+// The qs waves of a panel meet in LDS, summed in wave order.
+template <bool MX>
 __global__ __launch_bounds__(512) void k_mx4_skinny(GemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nt = blockDim.x;
@@ -35,9 +39,6 @@ __global__ __launch_bounds__(512) void k_mx4_skinny(GemmArgs a) {
     const int pw = wave / a.qs, wq = wave % a.qs;
     const int pp = blockIdx.x * a.ppw + pw;
     const int p = pp < a.P ? pp : a.P - 1;
-    const int t0 = blockIdx.y * (16 * MT);
-    const int rows = a.T - t0 < 16 * MT ? a.T - t0 : 16 * MT;    // tokens of this workgroup
-    const int nm = (a.T + 15) / 16;                          // activation tiles in all
 
     u32x4 b[4];
     uint32_t sb = 0;
@@ -50,97 +51,68 @@ __global__ __launch_bounds__(512) void k_mx4_skinny(GemmArgs a) {
     };
     if (wq < a.KQ) load_w(wq);
 
-    const int pitch = a.qs * 1024 + 16;                      // bytes of a staged row (padded: banks)
-    f32x4 acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int q0 = 0; q0 < a.KQ; q0 += a.qs) {
-        if constexpr (!MX) {
-            if (q0) __syncthreads();                         // the last chunk is consumed
-            const int k0 = 512 * q0, nc = a.qs * 64;         // 16-byte pieces per row
-            for (int i = tid; i < rows * nc; i += nt) {
-                const int r = i / nc, c = i % nc, k = k0 + 8 * c;
-                u32x4 v = {0u, 0u, 0u, 0u};
-                if (k < a.K) v = *(const u32x4 *)(a.x + (t0 + r) * a.ldx + k);
-                *(u32x4 *)(sm + r * pitch + 16 * c) = v;
-            }
-            __syncthreads();
+    const int pitch = a.KQ * 1024 + 16;                      // bytes of a staged row (padded: banks)
+    if constexpr (!MX) {
+        const int nc = a.KQ * 64;                            // 16-byte pieces per row
+        for (int i = tid; i < a.T * nc; i += nt) {
+            const int r = i / nc, c = i % nc;
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (8 * c < a.K) v = *(const u32x4 *)(a.x + r * a.ldx + 8 * c);
+            *(u32x4 *)(sm + r * pitch + 16 * c) = v;
         }
-        const int q = q0 + wq;
-        if (q < a.KQ) {
-            u32x4 bb[4];
-            const uint32_t sbb = sb;
+        __syncthreads();
+    }
+    const int r = n < a.T ? n : a.T - 1;                     // (past the tokens: repeated, discarded)
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int q = wq; q < a.KQ; q += a.qs) {
+        u32x4 bb[4];
+        const uint32_t sbb = sb;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) bb[i] = b[i];
-            if (q + a.qs < a.KQ) load_w(q + a.qs);
+        for (int i = 0; i < 4; ++i) bb[i] = b[i];
+        if (q + a.qs < a.KQ) load_w(q + a.qs);
+        uint32_t sa = 0;
+        if constexpr (MX) sa = *(const uint32_t *)(a.xs + q * MX_QS + 4 * lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (4 * q + i >= a.KS) break;
-                if constexpr (MX) {
+        for (int i = 0; i < 4; ++i) {
+            if (4 * q + i >= a.KS) break;
+            if constexpr (MX) {
+                acc = mx_mfma(*(const u32x4 *)(a.xc + (4 * q + i) * MX_TILE + 16 * lane), bb[i], acc, i, sa, sbb);
+            } else {
+                const float sc = mx_scale(sbb, i);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const int mt = t0 / 16 + m < nm ? t0 / 16 + m : nm - 1;   // past T: repeated, discarded
-                        const uint32_t sa = *(const uint32_t *)(a.xs + ((int64_t)mt * a.KQ + q) * MX_QS + 4 * lane);
-                        const u32x4 A = *(const u32x4 *)(a.xc + ((int64_t)mt * a.KS + 4 * q + i) * MX_TILE + 16 * lane);
-                        acc[m] = mx_mfma(A, bb[i], acc[m], i, sa, sbb);
-                    }
-                } else {
-                    const float sc = mx_scale(sbb, i);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bf16x8 B = mx_bf16(bb[i][j], sc);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            const int r = 16 * m + n < rows ? 16 * m + n : rows - 1;
-                            const bf16x8 A = *(const bf16x8 *)(sm + r * pitch + wq * 1024 + 256 * i + 64 * g + 16 * j);
-                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B, acc[m], 0, 0, 0);
-                        }
-                    }
-                }
+                for (int j = 0; j < 4; ++j)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        *(const bf16x8 *)(sm + r * pitch + 1024 * q + 256 * i + 64 * g + 16 * j), mx_bf16(bb[i][j], sc),
+                        acc, 0, 0, 0);
             }
         }
     }
-
-    // join the panel's waves in wave order (through LDS, one activation tile at a time)
-    f32x4 *red = (f32x4 *)sm;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (a.qs > 1) {
-            __syncthreads();
-            red[wave * 64 + lane] = acc[m];
-            __syncthreads();
-            if (wq == 0) {
-                f32x4 s = red[wave * 64 + lane];
-                for (int w = 1; w < a.qs; ++w) s += red[(wave + w) * 64 + lane];
-                acc[m] = s;
-            }
-        }
-        const int col = 16 * p + n;
-        if (wq == 0 && pp < a.P && col < a.N) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = t0 + 16 * m + 4 * g + r;
-                if (t < a.T) mx_store(a.y, t * a.ldy + col, acc[m][r], a.y_dtype);
-            }
-        }
+    // join the panel's waves in wave order
+    if (a.qs > 1) {
+        f32x4 *red = (f32x4 *)sm;
+        __syncthreads();
+        red[wave * 64 + lane] = acc;
+        __syncthreads();
+        if (wq == 0)
+            for (int w = 1; w < a.qs; ++w) acc += red[(wave + w) * 64 + lane];
     }
+    const int col = 16 * p + n;
+    if (wq == 0 && pp < a.P && col < a.N)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (4 * g + x < a.T) mx_store(a.y, (4 * g + x) * a.ldy + col, acc[x], a.y_dtype);
 }
 
 template <bool MX>
 hipError_t launch_skinny(GemmArgs a, hipStream_t s) {
-    const int nm = (a.T + 15) / 16;
-    const int MT = nm >= 3 ? 4 : nm;
-    const int rows = a.T < 16 * MT ? a.T : 16 * MT;
     a.qs = 1;
-    // a chunk of activations takes rows * qs KB of LDS
-    while (a.qs < 8 && 2 * a.qs <= a.KQ && (MX || rows * 2 * a.qs <= 60)) a.qs *= 2;
+    while (a.qs < 8 && 2 * a.qs <= a.KQ) a.qs *= 2;
     a.ppw = 1;
     while (a.qs * a.ppw < 8 && a.P / (2 * a.ppw) >= 2 * n_compute_units()) a.ppw *= 2;
     const int waves = a.qs * a.ppw;
-    const size_t red = a.qs > 1 ? (size_t)waves * 1024 : 16, stage = MX ? 0 : (size_t)rows * (a.qs * 1024 + 16);
-    void (*k)(GemmArgs) = MT == 4 ? k_mx4_skinny<MX, 4> : MT == 2 ? k_mx4_skinny<MX, 2> : k_mx4_skinny<MX, 1>;
-    hipLaunchKernelGGL(k, dim3((a.P + a.ppw - 1) / a.ppw, (nm + MT - 1) / MT), dim3(64 * waves),
-                       red > stage ? red : stage, s, a);
+    const size_t red = a.qs > 1 ? (size_t)waves * 1024 : 16, stage = MX ? 0 : (size_t)a.T * (a.KQ * 1024 + 16);
+    hipLaunchKernelGGL(k_mx4_skinny<MX>, dim3((a.P + a.ppw - 1) / a.ppw), dim3(64 * waves), red > stage ? red : stage, s,
+                       a);
     return hipGetLastError();
 }
 
@@ -191,7 +163,7 @@ struct Tiled {
 
 // Epilogue of a wave: 32 tokens at a time through its LDS area ep, then whole 16-byte pieces of
 // y's rows.  acc[j][i][r]: token 32 i + lane % 32, weight row 32 j + 8 (r / 4) + 4 h + r % 4.
-template <bool F32, int FM, int FN>
+template <bool F32, bool PART, int FM, int FN>
 __device__ __forceinline__ void tiled_store(const f32x16 (&acc)[FN][FM], uint8_t *ep, void *y, int64_t ldy, int T, int N,
                                             int t0, int n0) {
     constexpr int ESZ = F32 ? 4 : 2, PER = 16 / ESZ;         // elements of a 16-byte piece
@@ -221,9 +193,12 @@ __device__ __forceinline__ void tiled_store(const f32x16 (&acc)[FN][FM], uint8_t
             const u32x4 v = *(const u32x4 *)(src + RP * c * PITCH);
             if (t < T) {
                 uint8_t *d = dst + (32 * i + RP * c) * ldy * ESZ;
-                if (vec) __builtin_nontemporal_store(v, (u32x4 *)d);   // (y is not read here)
+                if (vec && PART) *(u32x4 *)d = v;
+                else if (vec) __builtin_nontemporal_store(v, (u32x4 *)d);   // (y is not read here)
                 else
-                    for (int q = 0; q < PER && n + q < N; ++q) {
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) {
+                        if (n + q >= N) break;
                         if constexpr (F32) ((uint32_t *)d)[q] = v[q];
                         else ((uint16_t *)d)[q] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
                     }
@@ -416,20 +391,34 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
 
     const int tw = t0 + wm * FM * 32, nw = n0 + wn * FN * 32;
     if (a.shares > 1)
-        tiled_store<true, FM, FN>(acc, sm + wave * C::EP, a.part + (int64_t)blockIdx.y * a.T * a.N, a.N, a.T, a.N, tw, nw);
+        tiled_store<true, true, FM, FN>(acc, sm + wave * C::EP, a.part + blockIdx.y * (a.T * part_pitch(a.N)),
+                                  part_pitch(a.N), a.T, a.N, tw, nw);
     else if (a.y_dtype == MOE_F32)
-        tiled_store<true, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
+        tiled_store<true, false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
     else
-        tiled_store<false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
+        tiled_store<false, false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
 }
 
-// the shares' partial sums, in share order
+// The shares' partial sums, in share order: a thread adds four columns, all
+// shares' loads in flight at once.
 __global__ __launch_bounds__(256) void k_mx4_join(GemmArgs a) {
-    const int64_t total = (int64_t)a.T * a.N;
+    const int64_t np = part_pitch(a.N), n4 = np / 4, total = a.T * n4, st = a.T * np;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        float v = a.part[i];
-        for (int s = 1; s < a.shares; ++s) v += a.part[s * total + i];
-        mx_store(a.y, i / a.N * a.ldy + i % a.N, v, a.y_dtype);
+        const int64_t t = i / n4;
+        const int n = (int)(i - t * n4) * 4;
+        const float *p = a.part + t * np + n;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        f32x4 q[MAX_SHARES];
+#pragma unroll
+        for (int s = 0; s < MAX_SHARES; ++s)
+            if (s < a.shares) q[s] = *(const f32x4 *)(p + s * st);
+#pragma unroll
+        for (int s = 0; s < MAX_SHARES; ++s)
+            if (s < a.shares) v += q[s];
+        const int64_t o = t * a.ldy + n;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (n + c < a.N) mx_store(a.y, o + c, v[c], a.y_dtype);
     }
 }
 
@@ -440,7 +429,7 @@ hipError_t launch_tiled(GemmArgs a, hipStream_t s) {
     hipLaunchKernelGGL((k_mx4_tiled<MX, WM, WN, FM, FN>), dim3((tiles + 7) / 8 * 8, a.shares), dim3(64 * C::NW), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.shares == 1) return e;
-    const int64_t total = (int64_t)a.T * a.N, b = (total + 255) / 256, cap = 8 * (int64_t)n_compute_units();
+    const int64_t b = (a.T * (part_pitch(a.N) / 4) + 255) / 256, cap = 8 * (int64_t)n_compute_units();
     hipLaunchKernelGGL(k_mx4_join, dim3((unsigned)(b < cap ? b : cap)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
@@ -465,42 +454,47 @@ GemmArgs make_args(const uint8_t *wc, const uint8_t *ws, int64_t N, int64_t K, i
 
 }  // namespace
 
-// Which kernel: up to 16 tokens the skinny one, which has one pass of the weights.  More take
-// tiles, the largest that still give every compute unit one; where even the smallest do not,
-// the columns are split into shares of at least two quads.
-enum Plan { SKINNY, TILE64, TILE128, TILE256 };
+// Which kernel (times: bf16 x, us):
+//   skinny  up to 16 tokens, bf16 x only while all of it can be staged at once (64 KB): beyond,
+//           staging between barriers costs more than reading the weights once saves
+//           (T = 16 x 16384 x 2048: 8.1 against 14.6 in tiles; T = 16 x 2048 x 8192: 30.5 against 10.9)
+//   large   tiles of 128 x 256, two workgroups a compute unit, if they fill their last round of
+//           the device to 7/8 on average (T = 1024 x 16384 x 2048, one full round: 67 against 76
+//           in small tiles; T = 512, half a round: 49 against 40)
+//   small   tiles of 64 x 128, and where those are fewer than the compute units, the columns
+//           split into shares of at least one quad (T = 37 x 2048 x 8192: 11.2 with 16 shares,
+//           13.9 with 8; T = 20 x 2048 x 2048: 9.5 with 4, 13.3 with 2).
+enum Plan { SKINNY, SMALL, LARGE };
 struct Choice {
     Plan plan;
     int shares;
 };
-static Choice choose(int64_t T, int64_t N, int64_t K) {
-    if (T <= 16) return {SKINNY, 1};
-    const int64_t cu = n_compute_units();
+static Choice choose(bool mx, int64_t T, int64_t N, int64_t K) {
+    if (T <= 16 && (mx || T * mx4_quads(K) <= 64)) return {SKINNY, 1};
+    const int64_t cu = n_compute_units(), round = 2 * cu;
     auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((N + n - 1) / n); };
-    if (tiles(128, 256) >= 2 * cu) return {TILE256, 1};
-    if (tiles(128, 128) >= cu) return {TILE128, 1};
-    int64_t sh = cu / tiles(64, 128), most = mx4_quads(K) / 2;
+    const int64_t large = tiles(128, 256), rounds = (large + round - 1) / round;
+    if (8 * large >= 7 * rounds * round) return {LARGE, 1};
+    int64_t sh = cu / tiles(64, 128), most = mx4_quads(K);
     if (sh > most) sh = most;
-    if (sh > 16) sh = 16;
-    return {TILE64, sh < 1 ? 1 : (int)sh};
+    if (sh > MAX_SHARES) sh = MAX_SHARES;
+    return {SMALL, sh < 1 ? 1 : (int)sh};
 }
 
 size_t mx4_gemm_ws(int64_t T, int64_t N, int64_t K) {
-    const Choice c = choose(T, N, K);
-    return c.shares > 1 ? (size_t)c.shares * T * N * 4 : 0;
+    // (for either kind of x)
+    const int a = choose(false, T, N, K).shares, b = choose(true, T, N, K).shares, n = a > b ? a : b;
+    return n > 1 ? (size_t)(n * T * part_pitch(N) * 4) : 0;
 }
 
 template <bool MX>
 static hipError_t launch_product(GemmArgs a, uint8_t *ws, hipStream_t s) {
-    const Choice c = choose(a.T, a.N, a.K);
+    const Choice c = choose(MX, a.T, a.N, a.K);
     a.shares = c.shares;
     a.part = (float *)ws;
-    switch (c.plan) {
-        case SKINNY: return launch_skinny<MX>(a, s);
-        case TILE64: return launch_tiled<MX, 2, 2, 1, 2>(a, s);
-        case TILE128: return launch_tiled<MX, 2, 2, 2, 2>(a, s);
-        default: return launch_tiled<MX, 1, 4, 4, 2>(a, s);
-    }
+    if (c.plan == SKINNY) return launch_skinny<MX>(a, s);
+    if (c.plan == SMALL) return launch_tiled<MX, 2, 2, 1, 2>(a, s);
+    return launch_tiled<MX, 1, 4, 4, 2>(a, s);
 }
 
 hipError_t launch_mx4_gemm(const uint8_t *wc, const uint8_t *wsc, int64_t N, int64_t K, const uint16_t *x, int64_t T,
