@@ -161,10 +161,10 @@ MxBufs carve_mx4(const moe_layer_desc *d, int64_t T, void *ws, size_t *bytes) {
     b.logits = c.take<float>((size_t)(T * (E + 1)));
     b.idx = c.take<int32_t>((size_t)(T * K));
     b.w = c.take<float>((size_t)(T * K));
-    b.act = c.take<int32_t>((size_t)E);
+    b.act = c.take<int32_t>((size_t)MX_ITEMS);
     b.nact = c.take<int32_t>(1);
     b.pos = c.take<int16_t>((size_t)(E * MX_TMAX));
-    b.h = c.take<uint16_t>((size_t)((T * K + T) * 2 * I));
+    b.h = c.take<uint16_t>((size_t)((T * K + T) * ((I + 127) / 128 * 256)));
     b.part = c.take<float>((size_t)(MX_SHARES * T * H));
     *bytes = c.off;
     return b;

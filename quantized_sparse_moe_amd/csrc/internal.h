@@ -140,6 +140,7 @@ hipError_t launch_mx4_gemm_mx4x(const uint8_t *wc, const uint8_t *wsc, int64_t N
 // the workspace's state region behind the affine kernels' words: zero before the first call,
 // and put back to zero by every call.
 constexpr int MX_TMAX = 64, MX_SHARES = 8;
+constexpr int MX_ITEMS = 256 + MX_TMAX * 16 / 16;         // of the work list: experts, and one per 16 tokens
 constexpr size_t MX_CNT_OFF = WS_CTL_BYTES - 4096;        // bytes
 constexpr int MX_CNT_DOWN = 16;                           // counters before: route's
 struct MxBufs {
@@ -148,10 +149,10 @@ struct MxBufs {
     float *logits;                 // [T][E + 1] (column E: the shared expert's gate)
     int32_t *idx;                  // [T][K]
     float *w;                      // [T][K]
-    int32_t *act;                  // [E] the chosen experts, ascending: id | tokens << 16
-    int32_t *nact;                 // [1] how many
-    int16_t *pos;                  // [E][MX_TMAX] under each its tokens' rows of h (t K + j), in order
-    uint16_t *h;                   // [T*K + T][2][I] bf16: w silu(g) u as hi and lo
+    int32_t *act;                  // [MX_ITEMS] the work list: up to 16 tokens of a chosen expert each
+    int32_t *nact;                 // [1] its length
+    int16_t *pos;                  // [E][MX_TMAX] per chosen expert its tokens' rows of h (t K + j), in order
+    uint16_t *h;                   // [T*K + T][2 x I up to 128] bf16: w silu(g) u as hi and lo
     float *part;                   // [MX_SHARES][T][H] the down shares' sums
 };
 hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const MxBufs &b, void *y, int y_dtype,

@@ -83,6 +83,21 @@ __device__ __forceinline__ bool last_of(uint32_t *cnt, uint32_t n, int *s_last) 
     return *s_last != 0;
 }
 
+// An entry of the work list: up to 16 tokens of one expert, rows first .. first + count - 1 of
+// its slot's list of tokens.
+__device__ __forceinline__ int mx_item(int e, int slot, int tile, int count) {
+    return e | slot << 8 | tile << 16 | count << 20;
+}
+struct MxItem {
+    int e, list, count;                                      // expert, first entry of pos, tokens
+};
+// item i of a layer with nsh shared-expert items (16 tokens each) before the listed ones; act is
+// the listed entry (not used for a shared item)
+__device__ __forceinline__ MxItem mx_unpack(int i, int nsh, int act, int T) {
+    if (i < nsh) return {0, -1, min(T - 16 * i, 16)};
+    return {act & 255, (act >> 8 & 255) * MX_TMAX + 16 * (act >> 16 & 15), act >> 20};
+}
+
 // ---------------------------------------------------------------------------- route
 // One workgroup per 16 experts (row E: the shared expert's gate) and 16 tokens, the columns
 // split over its waves.  The workgroup that finishes a tile of 16 tokens last takes their
@@ -91,7 +106,7 @@ __device__ __forceinline__ bool last_of(uint32_t *cnt, uint32_t n, int *s_last) 
 __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
     __shared__ f32x4 red[RT_WAVES][64];
     __shared__ int s_last;
-    __shared__ int s_slot[256], s_cnt[4];
+    __shared__ int s_slot[256], s_cnt[4], s_itm[4];
     __shared__ uint32_t s_mask[256][2];                      // tokens that chose the expert
     __shared__ int16_t s_sel[MX_TMAX * 16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
@@ -165,18 +180,26 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
         atomicOr(&s_mask[s_sel[i]][tt >> 5], 1u << (tt & 31));
     }
     __syncthreads();
+    // an expert of more than 16 tokens is listed once per 16 of them (its items share the slot)
     const uint64_t mask = tid < 256 ? s_mask[tid][0] | (uint64_t)s_mask[tid][1] << 32 : 0ull;
-    const uint64_t bal = __ballot(mask != 0);
-    if (tid < 256 && lane == 0) s_cnt[wave] = __popcll(bal);
+    const int cnt = __popcll(mask), own = (cnt + 15) >> 4;
+    const uint64_t lt = (1ull << lane) - 1;
+    const uint64_t b0 = __ballot(own >= 1), b1 = __ballot(own >= 2), b2 = __ballot(own >= 3), b3 = __ballot(own >= 4);
+    if (tid < 256 && lane == 0) {
+        s_cnt[wave] = __popcll(b0);
+        s_itm[wave] = __popcll(b0) + __popcll(b1) + __popcll(b2) + __popcll(b3);
+    }
     __syncthreads();
     if (tid < 256) {
-        int base = 0;
-        for (int w = 0; w < wave; ++w) base += s_cnt[w];
-        const int slot = base + __popcll(bal & ((1ull << lane) - 1));
+        int slot = __popcll(b0 & lt), item = slot + __popcll(b1 & lt) + __popcll(b2 & lt) + __popcll(b3 & lt);
+        for (int w = 0; w < wave; ++w) {
+            slot += s_cnt[w];
+            item += s_itm[w];
+        }
         s_slot[tid] = slot;
-        if (mask) a.b.act[slot] = tid | __popcll(mask) << 16;
+        for (int i = 0; i < own; ++i) a.b.act[item + i] = mx_item(tid, slot, i, min(cnt - 16 * i, 16));
     }
-    if (tid == 0) *a.b.nact = s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3];
+    if (tid == 0) *a.b.nact = s_itm[0] + s_itm[1] + s_itm[2] + s_itm[3];
     __syncthreads();
     for (int i = tid; i < T * K; i += RT_THREADS) {
         const int e = s_sel[i], tt = i / K;
@@ -184,6 +207,12 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
         a.b.pos[s_slot[e] * MX_TMAX + __popcll(m & ((1ull << tt) - 1))] = (int16_t)i;
     }
 }
+
+// h of a token and expert, in the order down reads it as an MFMA operand: per step of 128 columns
+// and MFMA j, the 8 columns 32 g + 8 j .. + 7 of the four blocks g, hi then lo each, so that a
+// load's pieces of one row are 128 bytes together.
+__host__ __device__ inline int64_t h_row(int I) { return (I + 127) / 128 * 256; }              // values of a row
+__device__ __forceinline__ int h_place(int block) { return (block >> 2) * 256 + (block & 3) * 16; }   // of 32 columns
 
 // -------------------------------------------------------------------------- gate/up
 // The tokens' rows of x are staged in LDS, 2048 columns at a time: read as MFMA operands from
@@ -200,17 +229,18 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
     __shared__ int s_pos[MX_TMAX];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, I = a.L.I, K = a.L.K, T = a.T;
-    const int slot = (int)blockIdx.y - (a.L.has_shared ? 1 : 0);
-    const bool sh = slot < 0;
-    // the expert and its tokens (one round trip), in order: the rows of the activation operand
-    int e = 0, cnt = T, pos = T * K + lane;
+    const int nsh = a.L.has_shared ? (T + 15) >> 4 : 0, item = blockIdx.y;
+    const bool sh = item < nsh;
+    // the expert and its tokens, in order: the rows of the activation operand
+    int nact = 0, act = 0;
     if (!sh) {
-        const int nact = *a.b.nact, act = a.b.act[slot];
-        pos = a.b.pos[slot * MX_TMAX + lane];
-        if (slot >= nact) return;
-        e = act & 0xffff;
-        cnt = act >> 16;
+        nact = *a.b.nact;
+        act = a.b.act[item - nsh];
+        if (item - nsh >= nact) return;
     }
+    const MxItem w = mx_unpack(item, nsh, act, T);
+    const int e = w.e, cnt = w.count;
+    const int pos = sh ? T * K + 16 * item + n : (int)a.b.pos[w.list + n];
     // (field by field: a choice between two descriptors would put the arguments in memory)
     const uint8_t *gc = sh ? a.L.s_gate.codes : a.L.gate.codes, *uc = sh ? a.L.s_up.codes : a.L.up.codes;
     const uint8_t *gs = (const uint8_t *)(sh ? a.L.s_gate.scales : a.L.gate.scales);
@@ -235,20 +265,18 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
     if (kg < KQ) load_w(kg);
     if (wave == 0 && lane < cnt) {
         s_pos[lane] = pos;
-        s_w[lane] = !sh ? a.b.w[pos] : a.gated ? sigmoid(a.b.logits[lane * (a.L.E + 1) + a.L.E]) : 1.0f;
+        s_w[lane] = !sh ? a.b.w[pos] : a.gated ? sigmoid(a.b.logits[(16 * item + lane) * (a.L.E + 1) + a.L.E]) : 1.0f;
     }
-    for (int m0 = 0; m0 < cnt; m0 += 16) {
-        const int rows = min(cnt - m0, 16), r = n < rows ? n : rows - 1;   // (past the tokens: repeated, discarded)
+    {
+        const int r = n < cnt ? n : cnt - 1;                 // (past the tokens: repeated, discarded)
         f32x4 ag = {0.f, 0.f, 0.f, 0.f}, au = {0.f, 0.f, 0.f, 0.f};
         for (int q0 = 0; q0 < KQ; q0 += GU_QUADS) {
-            // (the first quad of the first tokens is loaded; rows of at most 2048 columns have
-            // one quad per wave, which then stays in its registers for all tokens)
             const int q = q0 + kg;
-            if ((q0 || (m0 && KQ > GU_QUADS)) && q < KQ) load_w(q);
+            if (q0 && q < KQ) load_w(q);                     // (the first is on its way)
             // a wave stages whole rows, 1 KB per load (columns past H meet zero weights: any value
             // of the row will do)
-            for (int i = wave; i < rows * GU_QUADS; i += MT_WAVES) {
-                const int row = i / GU_QUADS, c = i % GU_QUADS, ps = __builtin_amdgcn_readlane(pos, m0 + row);
+            for (int i = wave; i < cnt * GU_QUADS; i += MT_WAVES) {
+                const int row = i / GU_QUADS, c = i % GU_QUADS, ps = __builtin_amdgcn_readlane(pos, row);
                 const int t = sh ? ps - T * K : ps / K, k = min((q0 + c) * 512 + 8 * lane, H - 8);
                 *(u32x4 *)(sx + row * GU_PITCH + 1024 * c + 16 * lane) = *(const u32x4 *)(a.x + (int64_t)t * H + k);
             }
@@ -272,9 +300,9 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
         red[wave][0][lane] = ag;
         red[wave][1][lane] = au;
         __syncthreads();
-        // thread: token m0 + tid / 32, column tid % 32 of the block
+        // thread: token tid / 32, column tid % 32 of the block
         const int tk = tid >> 5, c = tid & 31;
-        if (tk < rows) {
+        if (tk < cnt) {
             const int l = (c & 15) + 16 * (tk >> 2), rr = tk & 3, w0 = c >> 4;
             float gv = 0.0f, uv = 0.0f;
 #pragma unroll
@@ -283,20 +311,25 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
                 uv += red[w0 + 2 * k][1][l][rr];
             }
             // h = w silu(g) u as the bf16 pair hi + lo
-            const float h = silu(gv) * uv * s_w[m0 + tk];
+            const float h = silu(gv) * uv * s_w[tk];
             const uint16_t hi = f32_to_bf16(h);
             const uint16_t lo = f32_to_bf16(h - bf16_to_f32(hi));
-            uint16_t *d = a.b.h + (int64_t)s_pos[m0 + tk] * 2 * I + 32 * blockIdx.x + c;
+            uint16_t *d = a.b.h + s_pos[tk] * h_row(I) + h_place(blockIdx.x) + 64 * (c >> 3) + (c & 7);
             d[0] = hi;
-            d[I] = lo;
+            d[8] = lo;
+            // a last step of 64 columns: its other two blocks meet zero weights, and must be finite
+            if ((I & 64) && blockIdx.x == gridDim.x - 1)
+                for (int x = 1; x <= 2; ++x) {
+                    uint16_t *z = a.b.h + s_pos[tk] * h_row(I) + h_place(blockIdx.x + x) + 64 * (c >> 3) + (c & 7);
+                    z[0] = z[8] = 0;
+                }
         }
-        __syncthreads();
     }
 }
 
 // ----------------------------------------------------------------------------- down
-// An item is a quad of one expert's columns (the shared expert first) for 16 NP output rows; its
-// tokens come eight at a time (16 operand rows, hi and lo of each).  Each wave adds its items'
+// An item is a quad of the columns of a work-list entry (the shared expert's first) for 16 NP
+// output rows; its tokens come eight at a time (16 operand rows, hi and lo of each).  Each wave adds its items'
 // results into sums of its own in LDS, in item order (a register accumulator per token would
 // have to run every item over all tokens); the waves' sums are added in wave order.
 template <int NP, int W>
@@ -307,26 +340,31 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, I = a.L.I, K = a.L.K, T = a.T;
     const int KS = (I + 127) >> 7, KQ = (KS + 3) >> 2;
-    const int nsh = a.L.has_shared ? 1 : 0;
+    const int nsh = a.L.has_shared ? (T + 15) >> 4 : 0;
     const int z = blockIdx.y;
     const int p0 = NP * blockIdx.x;                          // H is a multiple of 64
     float *mine = sums + wave * T * C;
-    // the expert and the tokens of the next item are fetched while this one is multiplied
+    // the next item's expert and tokens are fetched while this one is multiplied
     int act_nx = 0, pos_nx = 0;
     auto fetch = [&](int it) __attribute__((always_inline)) {
-        const int slot = it / KQ - nsh;
-        const bool ok = slot >= 0 && slot < a.L.E;
-        act_nx = ok ? a.b.act[slot] : T << 16;
-        pos_nx = ok ? (int)a.b.pos[slot * MX_TMAX + lane] : T * K + lane;
+        const int i = it / KQ;
+        act_nx = i >= nsh && i < nsh + MX_ITEMS ? a.b.act[i - nsh] : 0;
+    };
+    auto fetch_pos = [&](int it) __attribute__((always_inline)) {
+        const int i = it / KQ;
+        const MxItem w = mx_unpack(i, nsh, act_nx, T);
+        pos_nx = w.list < 0 ? T * K + 16 * i + n : (int)a.b.pos[w.list + n];
     };
     int it = z * W + wave;
     fetch(it);
     const int items = (*a.b.nact + nsh) * KQ;
+    if (it < items) fetch_pos(it);
     for (int i = lane; i < T * C; i += 64) mine[i] = 0.0f;
     for (; it < items; it += a.shares * W) {
         const int q = it % KQ;
         const bool sh = it / KQ < nsh;
-        const int e = __builtin_amdgcn_readfirstlane(act_nx & 0xffff), cnt = __builtin_amdgcn_readfirstlane(act_nx >> 16);
+        const MxItem w = mx_unpack(it / KQ, nsh, __builtin_amdgcn_readfirstlane(act_nx), T);
+        const int e = w.e, cnt = w.count;
         const int pos = pos_nx;
         const uint8_t *codes = sh ? a.L.s_down.codes : a.L.down.codes;
         const uint8_t *scales = (const uint8_t *)(sh ? a.L.s_down.scales : a.L.down.scales);
@@ -342,20 +380,20 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
                 b[u][i] = __builtin_nontemporal_load((const u32x4 *)(codes + ((pe + u) * KS + s) * MX_TILE + 16 * lane));
             }
         }
+        const int nx = it + a.shares * W;
+        fetch(nx);
         for (int m0 = 0; m0 < cnt; m0 += 8) {
             const int r = m0 + (n >> 1), ps = __shfl(pos, r < cnt ? r : 0);
-            const uint16_t *hr = a.b.h + (int64_t)(2 * ps + (n & 1)) * I;
+            const uint16_t *hr = a.b.h + ps * h_row(I) + 16 * g + 8 * (n & 1);
             f32x4 acc[NP];
 #pragma unroll
             for (int u = 0; u < NP; ++u) acc[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
-            if (m0 == 0) fetch(it + a.shares * W);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (4 * q + i >= KS) break;
-                // (rows past the tokens repeat the first, columns past I meet zero weights)
-                u32x4 A[4];
+                u32x4 A[4];                                  // (rows past the tokens repeat the first)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) A[j] = *(const u32x4 *)(hr + min(128 * (4 * q + i) + 32 * g + 8 * j, I - 8));
+                for (int j = 0; j < 4; ++j) A[j] = *(const u32x4 *)(hr + 256 * (4 * q + i) + 64 * j);
 #pragma unroll
                 for (int u = 0; u < NP; ++u) {
                     const float cs = mx_scale(sc[u], i);
@@ -365,6 +403,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
                             __builtin_bit_cast(bf16x8, A[j]), mx_bf16(b[u][i][j], cs), acc[u], 0, 0, 0);
                 }
             }
+            if (m0 == 0 && nx < items) fetch_pos(nx);
             // hi and lo of a token are registers 0, 1 (or 2, 3) of one lane
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -411,6 +450,12 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
         for (int c = 0; c < 4; ++c) mx_store(a.y, o + c, v[c], a.y_dtype);
 }
 
+// entries of the work list (at most), the shared expert's included
+int64_t max_items(const Layer &L, int64_t T) {
+    const int64_t experts = T * L.K < L.E ? T * L.K : L.E;
+    return experts + T * L.K / 16 + (L.has_shared ? (T + 15) / 16 : 0);
+}
+
 // At most 32 items (one to three tokens of top-8): one panel per workgroup and 16 waves, so one
 // or two rounds of loads and no shares (T = 1: 6.6 us against 7.9; T = 7, 57 items: 15.4
 // against 12.3).  More: two panels and 8 waves, each row of h read for twice the weights, the
@@ -420,8 +465,7 @@ struct DownPlan {
 };
 DownPlan down_plan(const Layer &L, int64_t T) {
     DownPlan d;
-    int64_t items = T * L.K < L.E ? T * L.K : L.E;           // (at most)
-    items = (items + (L.has_shared ? 1 : 0)) * ((L.I + 511) / 512);
+    const int64_t items = max_items(L, T) * ((L.I + 511) / 512);   // (at most)
     if (items <= 32) {
         d.np = 1;
         d.waves = 16;
@@ -459,9 +503,8 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
                        dim3(RT_THREADS), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || route_only) return e;
-    const int64_t routed = T * L.K < L.E ? T * L.K : L.E;
     const size_t gu_x = (size_t)(T < 16 ? T : 16) * GU_PITCH, gu_red = MT_WAVES * 2048, gu_lds = gu_x > gu_red ? gu_x : gu_red;
-    hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)(routed + (L.has_shared ? 1 : 0))),
+    hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)max_items(L, T)),
                        dim3(MT_THREADS), gu_lds, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const dim3 grid((unsigned)(L.H / (16 * d.np)), (unsigned)a.shares), thr((unsigned)(64 * d.waves));
