@@ -351,11 +351,11 @@ moe_status mx4_pack_rows16(const void *codes, const void *scales, int64_t rows, 
  *     mx4_gemm_mx4x   the same with x quantized: x_codes, x_scales hold T rows in MX4_TILES
  *   y   [T][N], row stride ldy, y_dtype MOE_BF16 (rounded to nearest even) or MOE_F32
  *   ws  device workspace of ws_bytes >= mx4_gemm_workspace_size(N, K, T) (NULL when that is
- *       0), 256-byte aligned, contents undefined before and after; calls that share it must
- *       not overlap in time.
+ *       0; one for T tokens also serves fewer), 256-byte aligned, contents undefined before
+ *       and after; calls that share it must not overlap in time.
  * Every product is exact; only the fp32 sums round (and y, where it is bf16).  A NaN or
- * infinity in x makes its token's row of y NaN or infinite as the sum says (mx4x: NaN, as the
- * block is), and only it; a NaN block of W makes its column of y NaN.
+ * infinity in x leaves no finite value in its token's row of y (mx4x: NaN, as the block is)
+ * and does not reach the others; a NaN block of W makes its column of y NaN.
  * A token's result may depend on T (the order of its sums), not on the other tokens.
  */
 size_t mx4_gemm_workspace_size(int64_t N, int64_t K, int64_t T);

@@ -87,27 +87,28 @@ template <int DT>
 __global__ __launch_bounds__(256) void k_mx4_quantize_tiles(const void *x, int64_t rows, int K, int64_t ldx,
                                                             uint8_t *codes, uint8_t *scales) {
     const int KS = (K + 127) >> 7, KQ = (KS + 3) >> 2;
-    const int64_t p = blockIdx.x / KQ;
-    const int q = blockIdx.x % KQ;
     const int t = threadIdx.x, j = t & 3, n = (t >> 2) & 15, g = t >> 6;
-    const int64_t row = 16 * p + n;
-    Vals8 a[4];
+    for (int64_t blk = blockIdx.x; blk < (rows + 15) / 16 * KQ; blk += gridDim.x) {
+        const int64_t p = blk / KQ, row = 16 * p + n;
+        const int q = (int)(blk - p * KQ);
+        Vals8 a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = 512 * q + 128 * i + 32 * g + 8 * j;
-        a[i] = load8<DT>(x, row * ldx + k, row < rows && k < K);
-    }
-    uint32_t sw = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t sb;
-        const uint32_t c = quant8<DT>(a[i], sb);
-        if (4 * q + i < KS) {
-            *(uint32_t *)(codes + (p * KS + 4 * q + i) * MX_TILE + 4 * t) = c;
-            sw |= sb << (8 * i);
+        for (int i = 0; i < 4; ++i) {
+            const int k = 512 * q + 128 * i + 32 * g + 8 * j;
+            a[i] = load8<DT>(x, row * ldx + k, row < rows && k < K);
         }
+        uint32_t sw = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t sb;
+            const uint32_t c = quant8<DT>(a[i], sb);
+            if (4 * q + i < KS) {
+                *(uint32_t *)(codes + (p * KS + 4 * q + i) * MX_TILE + 4 * t) = c;
+                sw |= sb << (8 * i);
+            }
+        }
+        if (j == 0) *(uint32_t *)(scales + (p * KQ + q) * MX_QS + 4 * (n + 16 * g)) = sw;
     }
-    if (j == 0) *(uint32_t *)(scales + (p * KQ + q) * MX_QS + 4 * (n + 16 * g)) = sw;
 }
 
 // Row layout: thread t takes values 8 t .. 8 t + 7 of the matrix in row-major order (K is a
@@ -164,19 +165,20 @@ template <int DT>
 __global__ __launch_bounds__(256) void k_mx4_dequantize_tiles(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                                               int K, void *y, int64_t ldy) {
     const int KS = (K + 127) >> 7, KQ = (KS + 3) >> 2;
-    const int64_t p = blockIdx.x / KQ;
-    const int q = blockIdx.x % KQ;
     const int t = threadIdx.x, j = t & 3, n = (t >> 2) & 15, g = t >> 6;
-    const int64_t row = 16 * p + n;
-    const uint32_t sw = *(const uint32_t *)(scales + (p * KQ + q) * MX_QS + 4 * (n + 16 * g));
-    uint32_t c[4];
+    for (int64_t blk = blockIdx.x; blk < (rows + 15) / 16 * KQ; blk += gridDim.x) {
+        const int64_t p = blk / KQ, row = 16 * p + n;
+        const int q = (int)(blk - p * KQ);
+        const uint32_t sw = *(const uint32_t *)(scales + (p * KQ + q) * MX_QS + 4 * (n + 16 * g));
+        uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        c[i] = 4 * q + i < KS ? *(const uint32_t *)(codes + (p * KS + 4 * q + i) * MX_TILE + 4 * t) : 0u;
+        for (int i = 0; i < 4; ++i)
+            c[i] = 4 * q + i < KS ? *(const uint32_t *)(codes + (p * KS + 4 * q + i) * MX_TILE + 4 * t) : 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = 512 * q + 128 * i + 32 * g + 8 * j;
-        if (row < rows && k < K) dequant8<DT>(c[i], (sw >> (8 * i)) & 255u, y, row * ldy + k);
+        for (int i = 0; i < 4; ++i) {
+            const int k = 512 * q + 128 * i + 32 * g + 8 * j;
+            if (row < rows && k < K) dequant8<DT>(c[i], (sw >> (8 * i)) & 255u, y, row * ldy + k);
+        }
     }
 }
 
@@ -195,20 +197,21 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize_rows(const uint8_t *code
 __global__ __launch_bounds__(256) void k_mx4_pack(const uint8_t *codes, const uint8_t *scales, int64_t rows, int K,
                                                   uint8_t *tc, uint8_t *ts) {
     const int KS = (K + 127) >> 7, KQ = (KS + 3) >> 2;
-    const int64_t p = blockIdx.x / KQ;
-    const int q = blockIdx.x % KQ;
     const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    const int64_t row = 16 * p + n;
-    const int s = 4 * q + i, k = 128 * s + 32 * g;
-    const bool live = row < rows && k < K;
-    u32x4 c = {0u, 0u, 0u, 0u};
-    uint8_t sb = 0;
-    if (live) {
-        c = *(const u32x4 *)(codes + (row * K + k) / 2);
-        sb = scales[row * (K / 32) + k / 32];
+    for (int64_t blk = blockIdx.x; blk < (rows + 15) / 16 * KQ; blk += gridDim.x) {
+        const int64_t p = blk / KQ, row = 16 * p + n;
+        const int q = (int)(blk - p * KQ);
+        const int s = 4 * q + i, k = 128 * s + 32 * g;
+        const bool live = row < rows && k < K;
+        u32x4 c = {0u, 0u, 0u, 0u};
+        uint8_t sb = 0;
+        if (live) {
+            c = *(const u32x4 *)(codes + (row * K + k) / 2);
+            sb = scales[row * (K / 32) + k / 32];
+        }
+        if (s < KS) *(u32x4 *)(tc + (p * KS + s) * MX_TILE + 16 * lane) = c;
+        ts[(p * KQ + q) * MX_QS + 4 * lane + i] = sb;
     }
-    if (s < KS) *(u32x4 *)(tc + (p * KS + s) * MX_TILE + 16 * lane) = c;
-    ts[(p * KQ + q) * MX_QS + 4 * lane + i] = sb;
 }
 
 }  // namespace
@@ -225,7 +228,12 @@ static unsigned row_grid(int64_t rows, int64_t K) {
     const int64_t b = (rows * (K / 8) + 255) / 256, cap = 64 * (int64_t)n_compute_units();
     return (unsigned)(b < cap ? b : cap);
 }
-static unsigned tile_grid(int64_t rows, int64_t K) { return (unsigned)((rows + 15) / 16 * mx4_quads(K)); }
+// one workgroup per (panel, quad), up to the 2^20 after which they take several (a launch is
+// limited to 2^32 threads)
+static unsigned tile_grid(int64_t rows, int64_t K) {
+    const int64_t b = (rows + 15) / 16 * mx4_quads(K);
+    return (unsigned)(b < (1 << 20) ? b : 1 << 20);
+}
 
 hipError_t launch_mx4_quantize(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int layout,
                                uint8_t *codes, uint8_t *scales, hipStream_t s) {

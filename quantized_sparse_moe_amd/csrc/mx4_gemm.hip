@@ -481,10 +481,16 @@ static Choice choose(bool mx, int64_t T, int64_t N, int64_t K) {
     return {SMALL, sh < 1 ? 1 : (int)sh};
 }
 
+// For either kind of x, and never less than for fewer tokens: the largest shares x tokens of the
+// row counts up to T (within a row of tiles the shares are the same, so its last count is it).
 size_t mx4_gemm_ws(int64_t T, int64_t N, int64_t K) {
-    // (for either kind of x)
-    const int a = choose(false, T, N, K).shares, b = choose(true, T, N, K).shares, n = a > b ? a : b;
-    return n > 1 ? (size_t)(n * T * part_pitch(N) * 4) : 0;
+    int64_t rows = 0;
+    for (int64_t t = 64;; t += 64) {
+        const int64_t n = t < T ? t : T, sh = choose(false, n, N, K).shares;
+        if (sh > 1 && sh * n > rows) rows = sh * n;
+        if (n == T || n_compute_units() < 2 * ((n + 63) / 64) * ((N + 127) / 128)) break;
+    }
+    return (size_t)(rows * part_pitch(N) * 4);
 }
 
 template <bool MX>

@@ -111,6 +111,22 @@ def test_quantize_extremes(torch, qs, dtype):
     assert np.array_equal(tc.cpu().numpy(), wc)
 
 
+def test_more_tiles_than_workgroups(torch, qs):
+    """More (panel, quad) pairs than the launch has workgroups: the two layouts, each made by its
+    own kernel, agree over the whole matrix."""
+    rows, K = 16 * (1 << 20) + 53, 32
+    x = torch.randn(rows, K, device="cuda", dtype=torch.bfloat16)
+    rc, rs = qs.mx4_quantize(x, layout=qs.MX4_ROWS)
+    tc, ts = qs.mx4_quantize(x)
+    pc, ps = qs.mx4_pack_rows16(rc, rs, rows, K)
+    assert torch.equal(pc, tc) and torch.equal(ps, ts)
+    assert torch.equal(qs.mx4_dequantize(tc, ts, rows, K, y_dtype=torch.bfloat16),
+                       qs.mx4_dequantize(rc, rs, rows, K, y_dtype=torch.bfloat16, layout=qs.MX4_ROWS))
+    c, s = ref.quantize(np64(x[-53:]))
+    assert np.array_equal(rc[-53 * 16:].cpu().numpy().reshape(53, 16), ref.pack_rows(c))
+    assert np.array_equal(rs[-53:].cpu().numpy().reshape(53, 1), s)
+
+
 def test_quantize_strided_rows(torch, qs):
     x = to_dtype(rand_x(19, 512, seed=3), "bfloat16", torch)
     part = x[:, 64:64 + 288]                                     # row stride 512, offset 128 bytes
@@ -167,7 +183,7 @@ def check(y, want, bound, what):
     assert not bad.any(), (what, int(bad.sum()), float((err - bound - extra).max()), np.argwhere(bad)[:4].tolist())
 
 
-GEMM = [(1, 16, 32), (1, 1, 64), (1, 2048, 2048), (2, 130, 96), (3, 2048, 8192), (5, 17, 160), (7, 64, 544),
+GEMM = [(4, 80, 65536), (16, 64, 4096), (18, 4100, 96), (520, 16400, 64), (1024, 16384, 160), (1, 16, 32), (1, 1, 64), (1, 2048, 2048), (2, 130, 96), (3, 2048, 8192), (5, 17, 160), (7, 64, 544),
         (8, 256, 512), (9, 33, 640), (16, 2048, 2048), (16, 48, 8192), (17, 100, 1056), (31, 64, 128),
         (33, 2080, 2080), (37, 2048, 8192), (64, 128, 2048), (65, 31, 288), (130, 250, 576), (257, 512, 1024),
         (300, 1000, 2080), (513, 2048, 512), (1000, 130, 4096)]

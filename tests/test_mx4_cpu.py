@@ -105,6 +105,13 @@ def test_workspace():
             assert f(N=N, K=K, T=T, ldy=N, ws=None, y=None, **kw) == INV
 
 
+@pytest.mark.parametrize("N,K", [(1, 32), (100, 8192), (2048, 2048), (2048, 8192), (16384, 2048), (40000, 65536)])
+def test_workspace_for_more_tokens_serves_fewer(N, K):
+    """The size never falls as T grows (a smaller batch may be split into more shares)."""
+    sizes = [q.lib().mx4_gemm_workspace_size(N, K, T) for T in [*range(1, 700), 1023, 1024, 1025, 4096, 1 << 20]]
+    assert sizes == sorted(sizes) and sizes[-1] != BAD
+
+
 def test_sizes_of_the_layouts():
     for rows, K in ((1, 32), (16, 128), (17, 160), (130, 2080)):
         c = np.zeros((rows, K), np.uint8)
