@@ -208,12 +208,13 @@ moe_status moe_route(const moe_layer_desc *d, const void *x, int64_t T,
  * fp32 accumulation, fp16 intermediates, each under its range scale).
  * For a given T the result does not depend on whether gate/up are fused or separate,
  * nor on the other tokens of the call (tokens are independent), bit for bit.
- * MX4 layers take a path of their own for every T, meant for few tokens: three launches for
- * up to 64 tokens that read each chosen expert once (MFMA on bf16 operands: x as it is, the
- * weights exact, h as a bf16 pair of 2^-17), and passes of 64 tokens beyond, each reading
- * its experts anew.  Their workspace is that of min(T, 64) tokens (chunk does not matter);
- * a token's result may differ in its last fp32 bits with the other tokens of its pass (the
- * order in which its experts are summed depends on the pass's experts).
+ * MX4 layers: up to 64 tokens run in three launches that read each chosen expert once (MFMA
+ * on bf16 operands: x as it is, the weights exact, h as a bf16 pair, to 2^-17), up to 128 in
+ * two such passes; more run the grouped path (the same products in tiles, weighted expert
+ * outputs in fp16 under range scales before the combine).  There a token's result does not
+ * depend on the others, bit for bit; up to 128 tokens it may in its last fp32 bits (the order
+ * in which its experts are summed depends on the pass's experts).  Their scratch at the start of the workspace's state
+ * follows the same rules (zero before the first call, then the library's).
  */
 moe_status moe_layer_forward(const moe_layer_desc *d, const void *x, int64_t T,
                                void *y, int32_t y_dtype,

@@ -894,13 +894,17 @@ hipError_t gemms(GemmArgs a, hipStream_t s) {
     }
     const unsigned g0 = grid_for(maxr + maxs, a0.nb), g1 = grid_for(maxr + maxs, a1.nb);
     hipLaunchKernelGGL((k_gemm<BITS>), dim3(g0 + g1), dim3(NT), 0, s, a0, a1, (int)g0);
-    const int64_t n = a.T * (L.H / 8);
-    hipLaunchKernelGGL(k_combine, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.slot, a.sexp,
-                       a.ntiles + 2, a.y, a.y_dtype, a.T, L.K, L.H, L.has_shared);
     return hipGetLastError();
 }
 
 }  // namespace
+
+hipError_t launch_prefill_combine(const Layer &L, int64_t T, const PrefillBufs &b, void *y, int y_dtype, hipStream_t s) {
+    const int64_t n = T * (L.H / 8);
+    hipLaunchKernelGGL(k_combine, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, b.slot, b.sexp, b.ntiles + 2, y,
+                       y_dtype, T, L.K, L.H, L.has_shared);
+    return hipGetLastError();
+}
 
 hipError_t launch_prefill_gemms(const Layer &L, int64_t T, const PrefillBufs &b, void *y,
                                 int y_dtype, hipStream_t s) {
@@ -924,7 +928,8 @@ hipError_t launch_prefill_gemms(const Layer &L, int64_t T, const PrefillBufs &b,
     a.y = y;
     a.y_dtype = y_dtype;
     a.nb = 1;
-    return L.bits == 4 ? gemms<4>(a, s) : gemms<8>(a, s);
+    const hipError_t e = L.bits == 4 ? gemms<4>(a, s) : gemms<8>(a, s);
+    return e == hipSuccess ? launch_prefill_combine(L, T, b, y, y_dtype, s) : e;
 }
 
 }  // namespace qs

@@ -109,6 +109,9 @@ hipError_t launch_prefill_binning(const Layer &L, int64_t T, const PrefillBufs &
 hipError_t launch_prefill_gemms(const Layer &L, int64_t T, const PrefillBufs &b, void *y,
                                 int y_dtype, hipStream_t s);
 
+// y from the slot rows (both kinds of experts)
+hipError_t launch_prefill_combine(const Layer &L, int64_t T, const PrefillBufs &b, void *y, int y_dtype, hipStream_t s);
+
 // --------------------------------------------------------------------------- Q8_0
 int n_compute_units();   // of the current device, queried once
 hipError_t launch_q8_gemv(const uint8_t *tiles, int64_t N, int64_t K, const uint16_t *x,
@@ -157,6 +160,10 @@ struct MxBufs {
 };
 hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const MxBufs &b, void *y, int y_dtype,
                            int32_t *out_idx, float *out_w, bool route_only, hipStream_t s);
+
+// The expert products of a prompt (mx4_group.hip), between the binning and the combine:
+// b.h holds bf16 pairs there, [T*K + T][hi, lo][I].
+hipError_t launch_mx_group(const Layer &L, const uint16_t *x, int64_t T, const PrefillBufs &b, hipStream_t s);
 
 // ---------------------------------------------------------------- measured ceilings
 hipError_t launch_calib_read(const void *buf, int64_t bytes, uint32_t *out, hipStream_t s);

@@ -97,6 +97,21 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, u32x4 b, f32x16 c, int i, u
     }
 }
 
+// direct-to-LDS loads (lane l's bytes land at l times their number), and the waits for them
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ void dma16(const void *g, void *l) {
+    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 16, 0, 0);
+}
+__device__ __forceinline__ void dma4(const void *g, void *l) {
+    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 4, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// this wave's LDS reads are complete and every wave has arrived
+__device__ __forceinline__ void block_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// LDS writes of this wave before its later reads
+__device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 __device__ __forceinline__ void mx_store(void *y, int64_t i, float v, int y_dtype) {
     if (y_dtype == MOE_F32) ((float *)y)[i] = v;
     else ((uint16_t *)y)[i] = f32_to_bf16(v);

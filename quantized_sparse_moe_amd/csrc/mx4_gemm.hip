@@ -128,21 +128,6 @@ hipError_t launch_skinny(GemmArgs a, hipStream_t s) {
 //   MX4 x: a step is 128 columns of both operands' tiles.
 // Scales come a quad (512 columns) at a time; every wave has them in registers a step later, long
 // before the next quad's arrive in their place.
-typedef __attribute__((address_space(3))) void lds_void;
-__device__ __forceinline__ void dma16(const void *g, void *l) {
-    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 16, 0, 0);
-}
-__device__ __forceinline__ void dma4(const void *g, void *l) {
-    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 4, 0, 0);
-}
-template <int N>
-__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
-// this wave's LDS reads are complete and every wave has arrived
-__device__ __forceinline__ void block_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-// LDS writes of this wave before its later reads
-__device__ __forceinline__ void wave_lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
-
 template <bool MX, int WM, int WN, int FM, int FN>
 struct Tiled {
     static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;

@@ -242,7 +242,8 @@ hipError_t launch_prefill_router(const Layer &L, const uint16_t *x, int64_t T,
     la.gate_w = gated ? L.shared_gate_w : nullptr;
     la.LS = L.E + (gated ? 1 : 0);
     la.logits = b.logits;
-    la.x16 = write_x16 ? b.x16 : nullptr;
+    const bool x16 = write_x16 && !L.mx4;          // (MX4 experts multiply x as it is)
+    la.x16 = x16 ? b.x16 : nullptr;
     la.xmax = b.xmax;
     la.T = T;
     la.H = L.H;
@@ -267,7 +268,7 @@ hipError_t launch_prefill_router(const Layer &L, const uint16_t *x, int64_t T,
     ta.out_w = out_w;
     ta.blkcnt = write_x16 ? b.blkcnt : nullptr;
     ta.x = x;
-    ta.x16 = write_x16 ? b.x16 : nullptr;
+    ta.x16 = x16 ? b.x16 : nullptr;
     ta.xmax = b.xmax;
     ta.nxmax = (int)lgrid.y;
     ta.xexp = b.xexp;

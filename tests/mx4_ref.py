@@ -130,14 +130,17 @@ class Layer:
         w = np.exp(part - part.max(axis=1, keepdims=True))
         return w / w.sum(axis=1, keepdims=True)
 
-    def forward(self, x, idx):
+    def forward(self, x, idx, prompt=False):
         """(y, error bound of the fp32 evaluation) for float64 x and a routing.
 
         The bound follows a value through the layer: g and u are sums as in product_bound;
         silu moves by at most 1.1 of its argument's error and is evaluated to 2^-16 of itself
         (the argument of its exponential, up to 2^6, is rounded once: 2^-18, and a few fp32
         roundings); h = w silu(g) u is kept to 2^-16 (a bf16 pair), w is off by twice the
-        logits' error and 2^-20; the down sums as in product_bound, over all experts."""
+        logits' error and 2^-20; the down sums as in product_bound, over all experts.  prompt: each
+        expert's weighted output passes through fp16 (half a step, 2^-11 of it), flushed to zero
+        below 2^-14 where the largest of its 64 columns is at least 2^-2, so by at most 2^-12 of
+        that largest value (smaller ones are scaled up to 2^14 and lose less)."""
         H, I, T = self.hidden, self.inter, x.shape[0]
         w = self.weights(x, idx)
         dl = product_bound(x, bf16_values(self.router_bits)).max(axis=1)
@@ -149,6 +152,10 @@ class Layer:
             dg, du = product_bound(xs, gu[:I]), product_bound(xs, gu[I:])
             s = g / (1 + np.exp(-g))
             h = wt[:, None] * s * u
+            if prompt:
+                o = np.abs(h @ dn.T)
+                big = o.reshape(len(t), -1, 64).max(axis=2)
+                b[t] += 2.0 ** -11 * o + np.repeat(2.0 ** -12 * big, 64, axis=1)
             dh = np.abs(wt)[:, None] * (1.1 * dg * np.abs(u) + np.abs(s) * du + 1.1 * dg * du)
             dh += np.abs(h) * (2.0 ** -15 + dw[:, None])
             y[t] += h @ dn.T

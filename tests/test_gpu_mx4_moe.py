@@ -55,7 +55,8 @@ def check(L, xb, y, idx, w, what):
     # the weights: off by the logits' error (twice) and a few fp32 roundings
     dl = ref.product_bound(x, ref.bf16_values(L.router_bits)).max(axis=1, keepdims=True)
     assert (np.abs(gw - L.weights(x, gi)) <= 2 * dl + 2.0 ** -20).all(), what
-    want, bound = L.forward(x, gi)                              # (near ties: the GPU's own selection)
+    # (near ties: the GPU's own selection)
+    want, bound = L.forward(x, gi, prompt=len(x) > 128)
     bf16 = str(y.dtype).endswith("bfloat16")
     got = y.float().cpu().numpy().astype(np.float64)
     err = np.abs(got - want)
@@ -82,7 +83,7 @@ def layer(name):
 
 
 @pytest.mark.parametrize("name", sorted(LAYERS))
-@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 17, 33, 64, 65, 150])
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 17, 33, 64, 65, 127, 129, 150, 700])
 def test_layer(torch, qs, name, T):
     L = layer(name)
     desc = upload(L, torch, qs)
@@ -149,18 +150,18 @@ def test_workspace_shared_with_affine_layers_and_graph_replays(torch, qs):
     mx = upload(L, torch, qs)
     A = syn.make_layer(**syn.TINY)
     af = qs.LayerDesc.from_host(A)
-    n = max(qs.moe_workspace_size(mx, 64), qs.moe_workspace_size(af, 40))
+    n = max(qs.moe_workspace_size(mx, 170), qs.moe_workspace_size(af, 40))
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
-    xm = {T: to_dev(syn.make_x(T, L.hidden, seed=T), torch) for T in (1, 6, 30, 70)}
+    xm = {T: to_dev(syn.make_x(T, L.hidden, seed=T), torch) for T in (1, 6, 30, 170)}
     xa = {T: to_dev(syn.make_x(T, A.hidden, seed=T), torch) for T in (1, 3, 40)}
     rm = {T: qs.moe_layer_forward(mx, x, workspace=qs.new_workspace(mx, T)) for T, x in xm.items()}
     ra = {T: qs.moe_layer_forward(af, x, workspace=qs.new_workspace(af, T)) for T, x in xa.items()}
     outs = {("m", T): torch.empty_like(r) for T, r in rm.items()} | {("a", T): torch.empty_like(r) for T, r in ra.items()}
 
     def every():
-        for T in (1, 30, 6, 70):
+        for T in (1, 30, 6, 170):
             qs.moe_layer_forward(mx, xm[T], y=outs["m", T], workspace=ws)
-            Ta = {1: 3, 30: 1, 6: 40, 70: 1}[T]
+            Ta = {1: 3, 30: 1, 6: 40, 170: 1}[T]
             qs.moe_layer_forward(af, xa[Ta], y=outs["a", Ta], workspace=ws)
 
     def same():
@@ -184,6 +185,37 @@ def test_workspace_shared_with_affine_layers_and_graph_replays(torch, qs):
         same()
 
 
+def test_prompt_in_chunks(torch, qs):
+    """A prompt in chunks (a smaller workspace) gives the bits of one chunk, and a token's result
+    does not depend on the others."""
+    L = layer("skew")
+    desc = upload(L, torch, qs)
+    T = 333
+    xb = syn.make_x(T, L.hidden, seed=12)
+    x = to_dev(xb, torch)
+    y, idx, w = run(torch, qs, desc, x)
+    for chunk in (2, 150, 200):
+        ws = torch.zeros(qs.moe_workspace_size(desc, T, chunk), dtype=torch.uint8, device="cuda")
+        y2, i2, w2 = run(torch, qs, desc, x, workspace=ws)
+        assert torch.equal(y, y2) and torch.equal(idx, i2) and torch.equal(w, w2), chunk
+    other = to_dev(syn.make_x(T, L.hidden, seed=13), torch)
+    other[200] = x[200]
+    y4, _, _ = run(torch, qs, desc, other)
+    assert torch.equal(y4[200], y[200])
+
+
+def test_prompt_range(torch, qs):
+    """Activations whose expert outputs leave fp16's range: the slot rows carry scales."""
+    L = layer("ragged")
+    desc = upload(L, torch, qs)
+    for sigma in (1e-6, 2000.0):
+        xb = syn.make_x(140, L.hidden, seed=6, std=sigma)
+        y, idx, w = run(torch, qs, desc, to_dev(xb, torch))
+        gi = idx.cpu().numpy()
+        want, bound = L.forward(ref.bf16_values(xb), gi, prompt=True)
+        assert (np.abs(y.cpu().numpy() - want) <= bound + 2.0 ** -126 * L.inter).all()
+
+
 def test_side_stream_and_empty(torch, qs):
     L = layer("tiny")
     desc = upload(L, torch, qs)
@@ -200,7 +232,7 @@ def test_side_stream_and_empty(torch, qs):
 def test_guards_around_the_outputs(torch, qs):
     L = layer("ragged")
     desc = upload(L, torch, qs)
-    for T in (3, 70):
+    for T in (3, 70, 200):
         x = to_dev(syn.make_x(T, L.hidden, seed=5), torch)
         y = torch.full((T + 2, L.hidden), 7.0, device="cuda")
         idx = torch.full((T + 2, 3), -9, dtype=torch.int32, device="cuda")

@@ -112,6 +112,63 @@ def test_workspace_for_more_tokens_serves_fewer(N, K):
     assert sizes == sorted(sizes) and sizes[-1] != BAD
 
 
+def mx4_desc(**kw):
+    d = q.moe_layer_desc()
+    d.hidden, d.inter, d.n_experts, d.top_k, d.bits, d.group = 2048, 512, 256, 8, 4, 32
+    d.scale_dtype = q.MOE_E8M0
+    d.router_w = FAKE
+    d.gate, d.up = q.moe_qmat(FAKE, FAKE, None, 1024), q.moe_qmat(FAKE + 512 * 1024, FAKE, None, 1024)
+    d.down = q.moe_qmat(FAKE, FAKE, None, 2048)
+    d.has_shared = 1
+    d.s_gate, d.s_up, d.s_down = d.gate, d.up, d.down
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def forward(d, T=4, x=FAKE, y=FAKE, dt=q.MOE_BF16, ws=FAKE, nb=1 << 40):
+    return q.lib().moe_layer_forward(ctypes.byref(d), x, T, y, dt, None, None, ws, nb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(group=64), UNS), (dict(bits=8), UNS), (dict(hidden=2080), UNS), (dict(inter=96), UNS),
+    (dict(n_experts=257), UNS), (dict(top_k=17), UNS),
+    (dict(gate=q.moe_qmat(FAKE, FAKE, None, 1000)), INV),              # matrices must start at a panel
+    (dict(down=q.moe_qmat(FAKE, FAKE, None, 2032)), INV),              # stride < rows
+    (dict(up=q.moe_qmat(FAKE + 8, FAKE, None, 1024)), INV), (dict(up=q.moe_qmat(FAKE, FAKE + 2, None, 1024)), INV),
+    (dict(s_down=q.moe_qmat(None, FAKE, None, 2048)), INV), (dict(s_gate=q.moe_qmat(FAKE, None, None, 1024)), INV),
+    (dict(router_w=None), INV), (dict(shared_gate_w=FAKE, has_shared=0), INV),
+])
+def test_layer_descriptor(kw, status):
+    d = mx4_desc(**kw)
+    for T in (4, 100, 400):
+        assert forward(d, T=T) == status
+    assert q.lib().moe_workspace_size(ctypes.byref(d), 4) == BAD
+
+
+def test_layer_descriptor_accepted():
+    """Biases are unused, and the affine layers' limit on (top_k + 1) * inter does not apply."""
+    assert forward(mx4_desc(), T=0) == q.MOE_OK
+    wide = mx4_desc(inter=2048, top_k=16, gate=q.moe_qmat(FAKE, FAKE, None, 4096), up=q.moe_qmat(FAKE, FAKE, None, 4096),
+                    s_gate=q.moe_qmat(FAKE, FAKE, None, 4096), s_up=q.moe_qmat(FAKE, FAKE, None, 4096))
+    assert q.lib().moe_workspace_size(ctypes.byref(wide), 64) != BAD
+    affine = mx4_desc(scale_dtype=q.MOE_F16, group=64)
+    assert forward(affine) == INV                                      # (needs biases)
+
+
+def test_layer_workspace():
+    d = mx4_desc()
+    f = lambda T, c=0: q.lib().moe_workspace_size_chunked(ctypes.byref(d), T, c)
+    sizes = [f(T) for T in [*range(1, 200), 1000, 4096]]
+    assert sizes == sorted(sizes) and f(0) == 0 and f(16384) == f(4096)
+    assert f(4096, 100) < f(4096, 1000) < f(4096, 4096)
+    for T in (1, 64, 65, 129, 5000):
+        least = f(T, 2)
+        assert forward(d, T=T, nb=least - 1) == WS and forward(d, T=T, ws=None) == WS
+        assert forward(d, T=T, ws=FAKE + 64) == WS
+    assert forward(d, x=FAKE + 2) == INV and forward(d, dt=q.MOE_F16) == INV and forward(d, T=-1) == INV
+
+
 def test_sizes_of_the_layouts():
     for rows, K in ((1, 32), (16, 128), (17, 160), (130, 2080)):
         c = np.zeros((rows, K), np.uint8)
