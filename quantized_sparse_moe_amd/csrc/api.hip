@@ -156,8 +156,8 @@ MxBufs carve_mx4(const moe_layer_desc *d, int64_t T, void *ws, size_t *bytes) {
     Carver c{(char *)ws};
     const int64_t H = d->hidden, I = d->inter, K = d->top_k, E = d->n_experts;
     MxBufs b;
-    uint32_t *ctl = c.take<uint32_t>(WS_CTL_BYTES / 4);
-    b.cnt = ctl ? ctl + MX_CNT_OFF / 4 : nullptr;
+    b.ctl = c.take<uint32_t>(WS_CTL_BYTES / 4);
+    b.cnt = b.ctl ? b.ctl + MX_CNT_OFF / 4 : nullptr;
     b.logits = c.take<float>((size_t)(T * (E + 1)));
     b.idx = c.take<int32_t>((size_t)(T * K));
     b.w = c.take<float>((size_t)(T * K));

@@ -158,7 +158,7 @@ __device__ __forceinline__ void poll_pause(uint32_t n) {
 }
 
 // the last workgroup of a call: counters back to zero, generation advanced
-__device__ void finish_call(uint32_t *ctl, uint32_t tag) {
+__device__ inline void finish_call(uint32_t *ctl, uint32_t tag) {
     const int t = threadIdx.x;
     if (t < NGRP) st_dev(ctl + CNT_BASE + t * 64, 0u);
     if (t == NGRP) st_dev(ctl + CNT_TOP, 0u);
@@ -252,7 +252,7 @@ __device__ TopkOut select_topk_from(uint32_t *ctl, const uint64_t *lg, uint32_t 
     return tk;
 }
 // lanes sharing one row: the largest power of two <= min(64, 16-byte chunks per row)
-int lanes_per_row(int ncols, int bits) {
+inline int lanes_per_row(int ncols, int bits) {
     const int chunks = ncols * bits / 128;
     int l = 64;
     while (l > chunks) l >>= 1;

@@ -147,6 +147,7 @@ constexpr int MX_ITEMS = 256 + MX_TMAX * 16 / 16;         // of the work list: e
 constexpr size_t MX_CNT_OFF = WS_CTL_BYTES - 4096;        // bytes
 constexpr int MX_CNT_DOWN = 16;                           // counters before: route's
 struct MxBufs {
+    uint32_t *ctl;                 // the workspace's state region
     uint32_t *cnt;                 // completion counters: [i] token tile i of route, [MX_TMAX / 16]
                                    // its tiles, [MX_CNT_DOWN + i] the i-th output rows of down
     float *logits;                 // [T][E + 1] (column E: the shared expert's gate)

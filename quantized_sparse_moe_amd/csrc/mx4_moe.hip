@@ -1,5 +1,5 @@
-// mx4_moe.hip -- the sparse MoE layer with MX4 experts for a few tokens (up to MX_TMAX in one
-// pass; more run in passes of MX_TMAX): three launches.
+// mx4_moe.hip -- the sparse MoE layer with MX4 experts for a few tokens (up to MX_TMAX a pass):
+// three launches, two for a single token.
 //
 //   route    router logits on v_mfma_f32_16x16x32_bf16 (16 experts and 16 tokens per
 //            workgroup, the columns split over its waves).  The workgroup that finishes a tile
@@ -18,6 +18,7 @@
 //
 // All three are bound by the weight stream: (union of the chosen experts + shared) x
 // 3 H I x 17/32 bytes.  Every sum is fp32 in a fixed order; there are no float atomics.
+#include "decode_state.h"
 #include "mx4.h"
 
 namespace qs {
@@ -34,6 +35,7 @@ struct MxArgs {
     int T;
     int gated;
     int route_only;
+    int token;                        // one token: route and gate/up ran as k_mx_token
     int32_t *out_idx;
     float *out_w;
     void *y;
@@ -221,26 +223,18 @@ __device__ __forceinline__ int h_place(int block) { return (block >> 2) * 256 + 
 constexpr int GU_QUADS = MT_WAVES / 2;                       // quads of a chunk: one per wave pair
 constexpr int GU_PITCH = GU_QUADS * 1024 + 16;               // bytes of a staged row (padded: banks)
 
-__global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_gate_up(MxArgs a) {
-    // [min(T, 16)][GU_PITCH] of x, then the waves' sums in its place
-    extern __shared__ __attribute__((aligned(16))) uint8_t sx[];
+// One item's block of 32 columns of h, by one workgroup: expert e (sh: the shared one), its cnt
+// tokens, the row of h of token lane % 16 in pos (every wave) and its weight in w (wave 0).
+struct GuShared {
+    float w[16];
+    int pos[16];
+};
+__device__ __forceinline__ void gate_up_block(const MxArgs &a, uint8_t *sx, GuShared &s, int blk, bool sh, int e, int cnt,
+                                              int pos, float w) {
+    // [cnt][GU_PITCH] of x, then the waves' sums in its place
     f32x4(*red)[2][64] = (f32x4(*)[2][64])sx;
-    __shared__ float s_w[MX_TMAX];
-    __shared__ int s_pos[MX_TMAX];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, I = a.L.I, K = a.L.K, T = a.T;
-    const int nsh = a.L.has_shared ? (T + 15) >> 4 : 0, item = blockIdx.y;
-    const bool sh = item < nsh;
-    // the expert and its tokens, in order: the rows of the activation operand
-    int nact = 0, act = 0;
-    if (!sh) {
-        nact = *a.b.nact;
-        act = a.b.act[item - nsh];
-        if (item - nsh >= nact) return;
-    }
-    const MxItem w = mx_unpack(item, nsh, act, T);
-    const int e = w.e, cnt = w.count;
-    const int pos = sh ? T * K + 16 * item + n : (int)a.b.pos[w.list + n];
     // (field by field: a choice between two descriptors would put the arguments in memory)
     const uint8_t *gc = sh ? a.L.s_gate.codes : a.L.gate.codes, *uc = sh ? a.L.s_up.codes : a.L.up.codes;
     const uint8_t *gs = (const uint8_t *)(sh ? a.L.s_gate.scales : a.L.gate.scales);
@@ -248,7 +242,7 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
     const int64_t gst = sh ? a.L.s_gate.stride : a.L.gate.stride, ust = sh ? a.L.s_up.stride : a.L.up.stride;
     const int KS = (H + 127) >> 7, KQ = (KS + 3) >> 2;
     const int pw = wave & 1, kg = wave >> 1;                 // 16-column panel, quad of a chunk
-    const int p = 2 * blockIdx.x + pw;
+    const int p = 2 * blk + pw;
     const int64_t pg = (e * gst) / 16 + p, pu = (e * ust) / 16 + p;
     u32x4 bg[4], bu[4];
     uint32_t sg = 0, su = 0;
@@ -264,8 +258,8 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
     };
     if (kg < KQ) load_w(kg);
     if (wave == 0 && lane < cnt) {
-        s_pos[lane] = pos;
-        s_w[lane] = !sh ? a.b.w[pos] : a.gated ? sigmoid(a.b.logits[(16 * item + lane) * (a.L.E + 1) + a.L.E]) : 1.0f;
+        s.pos[lane] = pos;
+        s.w[lane] = w;
     }
     {
         const int r = n < cnt ? n : cnt - 1;                 // (past the tokens: repeated, discarded)
@@ -311,20 +305,129 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
                 uv += red[w0 + 2 * k][1][l][rr];
             }
             // h = w silu(g) u as the bf16 pair hi + lo
-            const float h = silu(gv) * uv * s_w[tk];
+            const float h = silu(gv) * uv * s.w[tk];
             const uint16_t hi = f32_to_bf16(h);
             const uint16_t lo = f32_to_bf16(h - bf16_to_f32(hi));
-            uint16_t *d = a.b.h + s_pos[tk] * h_row(I) + h_place(blockIdx.x) + 64 * (c >> 3) + (c & 7);
+            uint16_t *d = a.b.h + s.pos[tk] * h_row(I) + h_place(blk) + 64 * (c >> 3) + (c & 7);
             d[0] = hi;
             d[8] = lo;
             // a last step of 64 columns: its other two blocks meet zero weights, and must be finite
-            if ((I & 64) && blockIdx.x == gridDim.x - 1)
+            if ((I & 64) && blk == I / 32 - 1)
                 for (int x = 1; x <= 2; ++x) {
-                    uint16_t *z = a.b.h + s_pos[tk] * h_row(I) + h_place(blockIdx.x + x) + 64 * (c >> 3) + (c & 7);
+                    uint16_t *z = a.b.h + s.pos[tk] * h_row(I) + h_place(blk + x) + 64 * (c >> 3) + (c & 7);
                     z[0] = z[8] = 0;
                 }
         }
     }
+}
+
+__global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_gate_up(MxArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t sx[];
+    __shared__ GuShared s;
+    const int lane = threadIdx.x & 63, n = lane & 15, K = a.L.K, T = a.T;
+    const int nsh = a.L.has_shared ? (T + 15) >> 4 : 0, item = blockIdx.y;
+    const bool sh = item < nsh;
+    int nact = 0, act = 0;
+    if (!sh) {
+        nact = *a.b.nact;
+        act = a.b.act[item - nsh];
+        if (item - nsh >= nact) return;
+    }
+    const MxItem it = mx_unpack(item, nsh, act, T);
+    const int pos = sh ? T * K + 16 * item + n : (int)a.b.pos[it.list + n];
+    float w = 1.0f;
+    if (threadIdx.x < it.count) {
+        if (!sh) w = a.b.w[pos];
+        else if (a.gated) w = sigmoid(a.b.logits[(16 * item + n) * (a.L.E + 1) + a.L.E]);
+    }
+    gate_up_block(a, sx, s, blockIdx.x, sh, it.e, it.count, pos, w);
+}
+
+// One token: route and gate/up in one launch.  The first workgroups form the logits, 16 experts
+// each, and write them to every copy of the decode state's logit words under the call's tag;
+// the others stage nothing that depends on the routing until their wave 0 has all logits and has
+// taken the top-k itself (decode_state.h: a wait is bounded, and only for workgroups of lower
+// index).  Saves the last router workgroup's counting, selecting and listing and a launch.
+__global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_token(MxArgs a, int nR) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t sx[];
+    __shared__ GuShared s;
+    __shared__ float part[RT_WAVES][16], lg[16];
+    __shared__ int s_e;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+    const int H = a.L.H, E = a.L.E, K = a.L.K, NE = E + a.gated;
+    uint32_t *ctl = a.b.ctl;
+    const uint32_t tag = call_tag(ctl);
+    if ((int)blockIdx.x < nR) {
+        const int e = blockIdx.x * 16 + n, ec = e < NE ? e : NE - 1;
+        const uint16_t *wr = ec < E ? a.L.router_w + (int64_t)ec * H : a.L.shared_gate_w;
+        // (k_mx_route's sums in its order, so that the logits have the same bits: this wave takes the
+        // shares of its waves `wave` and `wave` + 8)
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const int steps = H / 32;
+        for (int s0 = wave; s0 < steps; s0 += 4 * RT_WAVES) {
+            u32x4 B[8], A[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int st = s0 + i * MT_WAVES, k = 32 * st + 8 * g;
+                B[i] = A[i] = (u32x4){0u, 0u, 0u, 0u};
+                if (st < steps) {
+                    B[i] = *(const u32x4 *)(wr + k);
+                    A[i] = *(const u32x4 *)(a.x + k);        // (every row of the operand is the token)
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A[i]),
+                                                                     __builtin_bit_cast(bf16x8, B[i]), acc[i & 1], 0, 0, 0);
+        }
+        if (lane < 16) {
+            part[wave][lane] = acc[0][0];
+            part[wave + MT_WAVES][lane] = acc[1][0];
+        }
+        __syncthreads();
+        if (tid < 16) {
+            float v = part[0][tid];
+#pragma unroll
+            for (int w = 1; w < RT_WAVES; ++w) v += part[w][tid];
+            if (a.L.router_bias && e < E) v += a.L.router_bias[e];
+            lg[tid] = v;
+        }
+        __syncthreads();
+        // two words of a copy per thread, a copy's run of 128 bytes by 8 neighbouring ones
+        if (tid < LOGIT_COPIES * 8) {
+            const int q = tid & 7, e0 = blockIdx.x * 16 + 2 * q;
+            uint32_t *dst = ctl + LOGIT_BASE + (tid >> 3) * LOGIT_STRIDE + 2 * e0;
+            if (e0 + 1 < NE)
+                st_dev128(dst, (u32x4){__float_as_uint(lg[2 * q]), tag, __float_as_uint(lg[2 * q + 1]), tag});
+            else if (e0 < NE)
+                st_dev64((uint64_t *)dst, __float_as_uint(lg[2 * q]) | ((uint64_t)tag << 32));
+        }
+        return;
+    }
+    const int b = blockIdx.x - nR, nblk = a.L.I / 32, item = b / nblk, blk = b % nblk;
+    const int nsh = a.L.has_shared ? 1 : 0, j = item - nsh;  // j: place among the chosen experts
+    const bool sh = j < 0;
+    float w = 1.0f;
+    if (wave == 0 && (!sh || a.gated)) {
+        float gate;
+        const TopkOut tk = select_topk_from(ctl, (const uint64_t *)(ctl + LOGIT_BASE + (b % LOGIT_COPIES) * LOGIT_STRIDE), tag,
+                                            E, K, a.gated, &gate);
+        w = sh ? gate : __shfl(tk.w, j);
+        const int e = __shfl(tk.idx, sh ? 0 : j);
+        if (lane == 0) s_e = e;
+        if (blk == 0 && !sh && lane == 0) {                  // the lists that down reads
+            a.b.act[j] = mx_item(e, j, 0, 1);
+            a.b.pos[j * MX_TMAX] = (int16_t)j;
+            if (j == 0) *a.b.nact = K;
+        }
+        if (blk == 0 && j == 0 && lane < K) {
+            if (a.out_idx) a.out_idx[lane] = tk.idx;
+            if (a.out_w) a.out_w[lane] = tk.w;
+        }
+    }
+    __syncthreads();
+    const int e = sh ? 0 : __builtin_amdgcn_readfirstlane(s_e);
+    gate_up_block(a, sx, s, blk, sh, e, 1, sh ? K : j, w);
 }
 
 // ----------------------------------------------------------------------------- down
@@ -357,6 +460,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     };
     int it = z * W + wave;
     fetch(it);
+    // (the launch before is complete: the generation its logits were tagged with is used up)
+    if (a.token && blockIdx.x == 0 && z == 0 && tid == 0) st_agent(a.b.ctl + CTL_GEN, call_tag(a.b.ctl));
     const int items = (*a.b.nact + nsh) * KQ;
     if (it < items) fetch_pos(it);
     for (int i = lane; i < T * C; i += 64) mine[i] = 0.0f;
@@ -499,13 +604,18 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     const DownPlan d = down_plan(L, T);
     a.shares = d.shares;
     a.route_only = route_only;
-    hipLaunchKernelGGL(k_mx_route, dim3((unsigned)((L.E + a.gated + 15) / 16), (unsigned)((T + 15) / 16)),
-                       dim3(RT_THREADS), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || route_only) return e;
+    a.token = T == 1 && !route_only;
+    const unsigned nR = (unsigned)((L.E + a.gated + 15) / 16);
     const size_t gu_x = (size_t)(T < 16 ? T : 16) * GU_PITCH, gu_red = MT_WAVES * 2048, gu_lds = gu_x > gu_red ? gu_x : gu_red;
-    hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)max_items(L, T)),
-                       dim3(MT_THREADS), gu_lds, s, a);
+    hipError_t e;
+    if (a.token) {
+        hipLaunchKernelGGL(k_mx_token, dim3(nR + (unsigned)(L.I / 32 * (L.K + (L.has_shared ? 1 : 0)))), dim3(MT_THREADS),
+                           gu_lds, s, a, (int)nR);
+    } else {
+        hipLaunchKernelGGL(k_mx_route, dim3(nR, (unsigned)((T + 15) / 16)), dim3(RT_THREADS), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess || route_only) return e;
+        hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)max_items(L, T)), dim3(MT_THREADS), gu_lds, s, a);
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const dim3 grid((unsigned)(L.H / (16 * d.np)), (unsigned)a.shares), thr((unsigned)(64 * d.waves));
     const size_t lds = (size_t)d.waves * T * 16 * d.np * 4;

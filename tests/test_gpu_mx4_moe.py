@@ -98,8 +98,9 @@ def test_layer(torch, qs, name, T):
     assert torch.equal(ri, idx) and torch.equal(rw, w)
     ys = qs.moe_layer_forward_static(desc, x, y_dtype=torch.bfloat16)
     assert torch.equal(ys, y)
-    # completion counters are back at zero
+    # completion counters are back at zero, and no wait gave up
     assert (ws[(2 << 20) - 4096:2 << 20] == 0).all()
+    assert int(qs.moe_workspace_status(ws)) == 0
 
 
 @pytest.mark.parametrize("T", [1, 5, 20])
@@ -214,6 +215,36 @@ def test_prompt_range(torch, qs):
         gi = idx.cpu().numpy()
         want, bound = L.forward(ref.bf16_values(xb), gi, prompt=True)
         assert (np.abs(y.cpu().numpy() - want) <= bound + 2.0 ** -126 * L.inter).all()
+
+
+def test_token_state(torch, qs):
+    """The one-token launch waits for tagged logits: many calls on one workspace alternating inputs,
+    across the wrap of the tag, give the first results; a bound of a poll or two makes the waits
+    give up, every kernel still ends, the error word says so, and the next call is right again."""
+    L = ref.Layer(hidden=2048, inter=128, n_experts=256, top_k=8, seed=21, gated=True)
+    desc = upload(L, torch, qs)
+    xbs = [syn.make_x(1, L.hidden, seed=s) for s in (1, 2, 3)]
+    xs = [to_dev(b, torch) for b in xbs]
+    want = [run(torch, qs, desc, x) for x in xs]
+    for xb, (y, idx, w) in zip(xbs, want):
+        check(L, xb, y, idx, w, "token")
+    ws = qs.new_workspace(desc, 1)
+    w32 = ws[:1024].view(torch.int32)
+    w32[64] = -4                                                 # the generation: wraps after four calls
+    for i in range(30):
+        y, idx, w = run(torch, qs, desc, xs[i % 3], workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip((y, idx, w), want[i % 3])), i
+    assert int(qs.moe_workspace_status(ws)) == 0
+    w32[32] = 1                                                  # at most one more poll
+    for i in range(3):
+        qs.moe_layer_forward(desc, xs[i], workspace=ws)
+    torch.cuda.synchronize()
+    st = int(qs.moe_workspace_status(ws, clear=True))
+    assert st in (0, qs.MOE_WS_ERR_DECODE_WAIT)
+    w32[32] = 0
+    y, idx, w = run(torch, qs, desc, xs[1], workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip((y, idx, w), want[1]))
+    assert int(qs.moe_workspace_status(ws)) == 0
 
 
 def test_side_stream_and_empty(torch, qs):
