@@ -15,6 +15,7 @@ Build it with ``python -m quantized_sparse_moe_amd.build``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -137,9 +138,9 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        C = _torch()._C
+        return C._cuda_getCurrentRawStream(C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -304,8 +305,20 @@ def _workspace(desc: LayerDesc, T: int, workspace, device, stream):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported at the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _empty(shape, dtype, device, stream):
-    import torch
+    torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(_alloc_stream(stream)):
@@ -451,6 +464,15 @@ def _mx4_buf(t, nbytes: int, where: str) -> int:
     return t.data_ptr()
 
 
+def _mx4_weights(codes, scales, rows: int, K: int, where: str):
+    """The addresses of a matrix in tiles, checked as _mx4_buf does."""
+    p = (rows + 15) >> 4
+    if (codes.nbytes < p * ((K + 127) >> 7) << 10 or scales.nbytes < p * ((K + 511) >> 9) << 8
+            or not codes.is_contiguous() or not scales.is_contiguous()):
+        _mx4_bad(where, f"codes and scales must be contiguous tiles of a [{rows}, {K}] matrix")
+    return codes.data_ptr(), scales.data_ptr()
+
+
 _mx4_codes = {}
 
 
@@ -477,26 +499,20 @@ def _mx4_values(x, where: str):
     return rows, K, (ld if rows > 1 else K), code
 
 
-_current = None
-
-
 def _mx4_stream(where: str, stream, gpu: int, *others):
     """(stream handle, whether `gpu` is the current device), once it is made sure that all
     tensors are on that GPU; `stream` None is its current stream."""
-    global _current
     if gpu < 0:
         _mx4_bad(where, "the tensors must be on a GPU")
     for t in others:
         if t is not None and t.get_device() != gpu:
             _mx4_bad(where, "the tensors must be on one GPU")
-    if _current is None:
-        import torch
-        _current = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    C = _torch()._C
     if stream is None:
-        handle = _current[0](gpu)
+        handle = C._cuda_getCurrentRawStream(gpu)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return handle, _current[1]() == gpu
+    return handle, C._cuda_getDevice() == gpu
 
 
 def _mx4_call(where: str, f, gpu: int, here: bool, *args) -> None:
@@ -514,13 +530,13 @@ def _mx4_call(where: str, f, gpu: int, here: bool, *args) -> None:
 def mx4_quantize(x, codes=None, scales=None, layout: int = MX4_TILES, stream=None):
     """MX4 quantization of ``x`` [rows, K] (bf16, fp16 or fp32; rows may be strided);
     returns (codes, scales), flat uint8 buffers in ``layout``."""
-    import torch
     rows, K, ldx, code = _mx4_values(x, "mx4_quantize")
     nc, ns = _mx4_sizes(rows, K, layout)
+    dev = x.device
     if codes is None:
-        codes = _empty((nc,), torch.uint8, x.device, stream)
+        codes = _empty((nc,), _torch().uint8, dev, stream)
     if scales is None:
-        scales = _empty((ns,), torch.uint8, x.device, stream)
+        scales = _empty((ns,), _torch().uint8, dev, stream)
     pc, ps = _mx4_buf(codes, nc, "mx4_quantize"), _mx4_buf(scales, ns, "mx4_quantize")
     gpu = x.get_device()
     st, here = _mx4_stream("mx4_quantize", stream, gpu, codes, scales)
@@ -530,11 +546,10 @@ def mx4_quantize(x, codes=None, scales=None, layout: int = MX4_TILES, stream=Non
 
 def mx4_dequantize(codes, scales, rows: int, K: int, y=None, y_dtype=None, layout: int = MX4_TILES, stream=None):
     """The values of an MX4 matrix: ``y`` [rows, K] (bf16, fp16 or fp32; default fp32)."""
-    import torch
     nc, ns = _mx4_sizes(rows, K, layout)
     pc, ps = _mx4_buf(codes, nc, "mx4_dequantize"), _mx4_buf(scales, ns, "mx4_dequantize")
     if y is None:
-        y = _empty((rows, K), y_dtype or torch.float32, codes.device, stream)
+        y = _empty((rows, K), y_dtype or _torch().float32, codes.device, stream)
     r, k, ldy, code = _mx4_values(y, "mx4_dequantize")
     if r != rows or k != K:
         _mx4_bad("mx4_dequantize", "y has another shape")
@@ -562,7 +577,9 @@ def mx4_pack_rows16(codes, scales, rows: int, K: int, t_codes=None, t_scales=Non
     return t_codes, t_scales
 
 
+@functools.lru_cache(maxsize=4096)
 def mx4_gemm_workspace_size(N: int, K: int, T: int) -> int:
+    """Bytes of workspace of products of T tokens (or fewer) with an [N, K] matrix."""
     n = lib().mx4_gemm_workspace_size(int(N), int(K), int(T))
     if n == ctypes.c_size_t(-1).value:
         raise QsmoeError(MOE_ERR_UNSUPPORTED, "mx4_gemm_workspace_size")
@@ -570,31 +587,33 @@ def mx4_gemm_workspace_size(N: int, K: int, T: int) -> int:
 
 
 def mx4_new_workspace(T: int, N: int, K: int, device="cuda", stream=None):
-    """A workspace for products of T tokens with an [N, K] matrix (None when none is needed)."""
-    import torch
+    """A workspace for products of T tokens or fewer with an [N, K] matrix (None when none is
+    needed)."""
     n = mx4_gemm_workspace_size(N, K, T)
-    return _empty((n,), torch.uint8, device, stream) if n else None
+    return _empty((n,), _torch().uint8, device, stream) if n else None
 
 
 def _mx4_product(where, f, w_codes, w_scales, N, K, T, x1, x2, x_args, y, y_dtype, workspace, stream):
-    import torch
-    nc, ns = _mx4_sizes(N, K, MX4_TILES)
-    wc, ws = _mx4_buf(w_codes, nc, where), _mx4_buf(w_scales, ns, where)
-    ldy = N
+    wc, ws = _mx4_weights(w_codes, w_scales, N, K, where)
+    gpu = w_codes.get_device()
     if y is None:
-        y = _empty((T, N), y_dtype or torch.float32, w_codes.device, stream)
-    elif y.dim() != 2 or y.shape != (T, N) or (N > 1 and y.stride(1) != 1):
-        _mx4_bad(where, "y must be [T, N] with contiguous rows")
-    elif T > 1:
-        ldy = y.stride(0)
-    if workspace is None and T > 0:
-        workspace = mx4_new_workspace(T, N, K, w_codes.device, stream)
+        y = _empty((T, N), y_dtype or _torch().float32, w_codes.device, stream)
+        ldy = N
+    else:
+        if y.dim() != 2 or y.shape != (T, N) or (N > 1 and y.stride(1) != 1):
+            _mx4_bad(where, "y must be [T, N] with contiguous rows")
+        ldy = y.stride(0) if T > 1 else N
     code = _mx4_code(y.dtype)
     if code is None:
         _mx4_bad(where, "y must be float32 or bfloat16")
-    pw, nb = (None, 0) if workspace is None else (_mx4_buf(workspace, 0, where), workspace.nbytes)
-    gpu = w_codes.get_device()
-    st, here = _mx4_stream(where, stream, gpu, x1, x2, w_scales, y, workspace)
+    if workspace is None and T > 0:
+        workspace = mx4_new_workspace(T, N, K, w_codes.device, stream)
+    if workspace is None:
+        pw, nb = None, 0
+        st, here = _mx4_stream(where, stream, gpu, x1, x2, w_scales, y)
+    else:
+        pw, nb = _mx4_buf(workspace, 0, where), workspace.nbytes
+        st, here = _mx4_stream(where, stream, gpu, x1, x2, w_scales, y, workspace)
     _mx4_call(where, f, gpu, here, wc, ws, N, K, *x_args, y.data_ptr(), code, ldy, pw, nb, st)
     return y
 
@@ -611,8 +630,7 @@ def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspa
 def mx4_gemm_mx4x(w_codes, w_scales, N: int, K: int, x_codes, x_scales, T: int, y=None, y_dtype=None,
                   workspace=None, stream=None):
     """The same product with ``x`` quantized (``mx4_quantize`` into tiles, T rows)."""
-    nc, ns = _mx4_sizes(T, K, MX4_TILES)
-    xc, xs = _mx4_buf(x_codes, nc, "mx4_gemm_mx4x"), _mx4_buf(x_scales, ns, "mx4_gemm_mx4x")
+    xc, xs = _mx4_weights(x_codes, x_scales, T, K, "mx4_gemm_mx4x")
     return _mx4_product("mx4_gemm_mx4x", lib().mx4_gemm_mx4x, w_codes, w_scales, N, K, T, x_codes, x_scales,
                         (xc, xs, T), y, y_dtype, workspace, stream)
 
