@@ -105,6 +105,21 @@ __device__ __forceinline__ void dma16(const void *g, void *l) {
 __device__ __forceinline__ void dma4(const void *g, void *l) {
     __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 4, 0, 0);
 }
+// The same through a buffer resource (over everything from a wave-uniform pointer on): voff per
+// lane, soff uniform, both in bytes and below 2^31.  Beside loads into registers only this form
+// will do: the compiler cannot count global_load_lds among them (it may be LDS or memory that a
+// flat instruction waits for) and would wait for every load there is.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_from(const void *p) {
+    const uint64_t u = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(lo | (uint64_t)hi << 32), 0, 0xffffffffu, 0x00020000);
+}
+__device__ __forceinline__ void dma16_buffer(__amdgpu_buffer_rsrc_t r, void *l, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)l, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4_buffer(__amdgpu_buffer_rsrc_t r, void *l, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)l, 4, voff, soff, 0, 0);
+}
 template <int N>
 __device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 // this wave's LDS reads are complete and every wave has arrived

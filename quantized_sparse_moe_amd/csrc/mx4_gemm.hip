@@ -119,8 +119,11 @@ hipError_t launch_skinny(GemmArgs a, hipStream_t s) {
 // ------------------------------------------------------------------- many tokens
 // Bound by the matrix cores: WM x WN waves, each FM x FN fragments of 32 tokens x 32 weight
 // rows (v_mfma 32x32, the weights as first operand so that a lane's registers are neighbouring
-// columns of y).  All operands go global -> LDS by direct-to-LDS loads in a ring of three
-// stages, so that two steps are in flight while one is multiplied; one barrier a step.
+// columns of y).  Operands go global -> LDS by direct-to-LDS loads in a ring of three stages, so
+// that two steps are in flight while one is multiplied; one barrier a step.  Where WM is 1 no
+// other wave multiplies a wave's weight rows: it loads them straight into registers, two steps
+// ahead, which takes a quarter (bf16 x) to nearly half (MX4 x) off the LDS traffic (4096 x 16384
+// x 2048: bf16 x 242 -> 209 us, MX4 x 97 -> 77).
 //   bf16 x: a step is 64 columns.  128 bytes of a token's row, its eight 16-byte chunks XORed
 //     by (row / 2) % 8: a 16-byte LDS read is served 16 lanes a cycle, those of one wave half
 //     with equal parity of lane bits 2..4 (measured), and under this key they fall in 64
@@ -134,10 +137,14 @@ struct Tiled {
     static constexpr int STEP = MX ? 128 : 64;                        // columns
     static constexpr int PER_Q = 512 / STEP;                          // steps per quad of scales
     static constexpr int A_BYTES = MX ? BM * 64 : BM * 128, B_BYTES = MX ? BN * 64 : BN * 32;
-    static constexpr int STAGE = A_BYTES + B_BYTES, NSTAGE = 3;
+    static constexpr int STAGE = A_BYTES + (WM == 1 ? 0 : B_BYTES), NSTAGE = 3;
     static constexpr int SC_BYTES = (MX ? BM * 16 : 0) + BN * 16;     // of a quad
-    static constexpr int A_DMA = A_BYTES / (1024 * NW), B_DMA = B_BYTES / (1024 * NW);
-    static constexpr int DMA = A_DMA + B_DMA;                         // per wave and step
+    // a wave whose weight rows no other wave multiplies (WM = 1) loads them straight into registers
+    static constexpr bool DIRECT = WM == 1;
+    static constexpr int B_STEP = MX ? MX_TILE : MX_TILE / 2;         // bytes of a panel
+    static constexpr int BL = FN * (MX ? 2 : 1);                      // such loads of a step
+    static constexpr int A_DMA = A_BYTES / (1024 * NW), B_DMA = DIRECT ? 0 : B_BYTES / (1024 * NW);
+    static constexpr int DMA = A_DMA + (DIRECT ? BL : B_DMA);         // loads per wave and step
     static constexpr int SDMA = SC_BYTES / (256 * NW);                // per wave and quad
     static constexpr int EP = 32 * (FN * 32 * 4 + 16);                // epilogue staging of a wave
     static constexpr int RING = NSTAGE * STAGE + SC_BYTES;
@@ -215,60 +222,74 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     const int k_lo = blockIdx.y * qper * C::PER_Q;
     const int k_hi = k_lo + qper * C::PER_Q < steps ? k_lo + qper * C::PER_Q : steps;
 
-    // ---- sources of this wave's direct-to-LDS loads (piece i of a stage: 1024 bytes)
-    const uint8_t *asrc[C::A_DMA], *bsrc[C::B_DMA];
+    // ---- sources of this wave's loads: x, the weights and the scales, from the workgroup's first row on
+    const int xp0 = t0 / 16, xpl = (a.T + 15) / 16 - 1, wp0 = n0 / 16;      // panels (xpl: the last of x)
+    const uint8_t *xbase = MX ? a.xc + (int64_t)xp0 * a.KS * MX_TILE : (const uint8_t *)(a.x + t0 * a.ldx);
+    const uint8_t *wbase = a.wc + (int64_t)wp0 * a.KS * MX_TILE;
+    const uint8_t *xsbase = MX ? a.xs + (int64_t)xp0 * a.KQ * MX_QS : nullptr, *wsbase = a.ws + (int64_t)wp0 * a.KQ * MX_QS;
+    auto wpanel = [&](int p) __attribute__((always_inline)) { return wp0 + p < a.P ? p : a.P - 1 - wp0; };
+    auto xpanel = [&](int p) __attribute__((always_inline)) { return xp0 + p <= xpl ? p : xpl - xp0; };
+    // piece i of a stage: 1024 bytes; offsets from xbase (DIRECT: below 2^31, see choose)
+    int64_t aoff[C::A_DMA];
     int kmax[C::A_DMA];                     // bf16 x: the last column offset at which the chunk is whole
 #pragma unroll
     for (int i = 0; i < C::A_DMA; ++i) {
         const int piece = wave * C::A_DMA + i;
         if constexpr (MX) {
-            const int mt = t0 / 16 + piece, nm = (a.T + 15) / 16;
-            asrc[i] = a.xc + (int64_t)(mt < nm ? mt : nm - 1) * a.KS * MX_TILE + 16 * lane;
+            aoff[i] = (int64_t)xpanel(piece) * a.KS * MX_TILE + 16 * lane;
             kmax[i] = 0;
         } else {
             const int row = 8 * piece + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-            const int t = t0 + row < a.T ? t0 + row : a.T - 1;
-            asrc[i] = (const uint8_t *)(a.x + (int64_t)t * a.ldx + 8 * c);
+            aoff[i] = (t0 + row < a.T ? row : a.T - 1 - t0) * a.ldx * 2 + 16 * c;
             kmax[i] = a.K - 8 * c - 8;
         }
     }
+    const uint8_t *bsrc[C::DIRECT ? FN : C::B_DMA];
 #pragma unroll
-    for (int i = 0; i < C::B_DMA; ++i) {
-        // bf16 x: half a tile of two panels
-        const int piece = wave * C::B_DMA + i, p = n0 / 16 + (MX ? piece : 2 * piece + h);
-        bsrc[i] = a.wc + (int64_t)(p < a.P ? p : a.P - 1) * a.KS * MX_TILE + 16 * (MX ? lane : r32);
+    for (int i = 0; i < (C::DIRECT ? FN : C::B_DMA); ++i) {
+        // DIRECT: fragment i of the wave, the next step's; else (bf16 x: half a tile of two panels)
+        const int piece = wave * C::B_DMA + i;
+        const int p = C::DIRECT ? 2 * (wn * FN + i) + (r32 >> 4) : MX ? piece : 2 * piece + h;
+        bsrc[i] = wbase + (int64_t)wpanel(p) * a.KS * MX_TILE +
+                  16 * (C::DIRECT ? (r32 & 15) + 16 * h : MX ? lane : r32) + (C::DIRECT ? (int64_t)k_lo * C::B_STEP : 0);
     }
-    const uint8_t *ssrc[C::SDMA];
+    // scales, 256 bytes (a panel) a piece: XS of x, then WS of the weights
+    constexpr int XS = MX ? C::BM / (16 * C::NW) : 0, WS = C::BN / (16 * C::NW);
+    static_assert(XS + WS == C::SDMA && (!MX || C::BM % (16 * C::NW) == 0), "whole pieces of either");
+    int soff[C::SDMA];
 #pragma unroll
-    for (int i = 0; i < C::SDMA; ++i) {
-        const int piece = wave * C::SDMA + i;                // 256 bytes: one panel
-        const int np = MX ? C::BM / 16 : 0, nm = (a.T + 15) / 16;
-        if (piece < np) {
-            const int mt = t0 / 16 + piece;
-            ssrc[i] = a.xs + (int64_t)(mt < nm ? mt : nm - 1) * a.KQ * MX_QS + 4 * lane;
-        } else {
-            const int p = n0 / 16 + piece - np;
-            ssrc[i] = a.ws + (int64_t)(p < a.P ? p : a.P - 1) * a.KQ * MX_QS + 4 * lane;
-        }
-    }
-    auto issue = [&](int k) __attribute__((always_inline)) {
+    for (int i = 0; i < C::SDMA; ++i)
+        soff[i] = (i < XS ? xpanel(wave * XS + i) : wpanel(wave * WS + i - XS)) * a.KQ * MX_QS + 4 * lane;
+    auto issue = [&](int k, int s) __attribute__((always_inline)) {   // step k, the s-th of its quad
         uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
 #pragma unroll
         for (int i = 0; i < C::A_DMA; ++i) {
             // (bf16 x: columns past K meet zero weights, any value of the row will do)
-            const int off = C::STEP * k;
-            dma16(MX ? asrc[i] + (int64_t)k * MX_TILE : asrc[i] + 2 * (off <= kmax[i] ? off : kmax[i]),
-                  st + (wave * C::A_DMA + i) * 1024);
+            const int off = C::STEP * k, col = MX ? k * MX_TILE : 2 * (off <= kmax[i] ? off : kmax[i]);
+            uint8_t *d = st + (wave * C::A_DMA + i) * 1024;
+            if constexpr (C::DIRECT) dma16_buffer(buffer_from(xbase), d, (uint32_t)aoff[i] + (MX ? 0 : col), MX ? col : 0);
+            else dma16(xbase + aoff[i] + col, d);
         }
 #pragma unroll
         for (int i = 0; i < C::B_DMA; ++i)
-            dma16(bsrc[i] + (int64_t)k * (MX ? MX_TILE : MX_TILE / 2), st + C::A_BYTES + (wave * C::B_DMA + i) * 1024);
-        if (k % C::PER_Q == 0) {
-            const int q = k / C::PER_Q;
-            uint8_t *ss = sm + C::NSTAGE * C::STAGE + wave * C::SDMA * 256;
+            dma16(bsrc[i] + (int64_t)k * C::B_STEP, st + C::A_BYTES + (wave * C::B_DMA + i) * 1024);
+        if (s % C::PER_Q == 0) {
+            const int q = k / C::PER_Q * MX_QS;
+            uint8_t *ss = sm + C::NSTAGE * C::STAGE;
 #pragma unroll
-            for (int i = 0; i < C::SDMA; ++i) dma4(ssrc[i] + (int64_t)q * MX_QS, ss + 256 * i);
+            for (int i = 0; i < C::SDMA; ++i) {
+                uint8_t *d = ss + (i < XS ? (wave * XS + i) * 256 : (MX ? C::BM * 16 : 0) + (wave * WS + i - XS) * 256);
+                if constexpr (C::DIRECT) dma4_buffer(buffer_from(i < XS ? xsbase : wsbase), d, soff[i], q);
+                else dma4((i < XS ? xsbase : wsbase) + soff[i] + q, d);
+            }
         }
+    };
+    u32x4 bq[2][C::BL];                                      // DIRECT: by the step's parity
+    auto load_b = [&](u32x4 (&b)[C::BL]) __attribute__((always_inline)) {   // of the next step
+#pragma unroll
+        for (int i = 0; i < C::BL; ++i) b[i] = *(const u32x4 *)(bsrc[MX ? i >> 1 : i] + (MX ? 512 * (i & 1) : 0));
+#pragma unroll
+        for (int j = 0; j < FN; ++j) bsrc[j] += C::B_STEP;
     };
 
     f32x16 acc[FN][FM];
@@ -299,54 +320,53 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
             }
         }
     };
-    auto sync_step = [&](int k) __attribute__((always_inline)) {
+    // ahead: stage k + 2 exists
+    auto sync_step = [&](int k, int s, bool ahead) __attribute__((always_inline)) {
         // stage k has landed once at most stage k + 1's loads are outstanding
-        if (k + 1 >= k_hi) wait_dma<0>();
-        else if ((k + 1) % C::PER_Q == 0) wait_dma<C::DMA + C::SDMA>();
+        if (!ahead && k + 1 >= k_hi) wait_dma<0>();
+        else if ((s + 1) % C::PER_Q == 0) wait_dma<C::DMA + C::SDMA>();
         else wait_dma<C::DMA>();
         block_sync();
-        if (k + 2 < k_hi) issue(k + 2);
+        if (ahead) issue(k + 2, s + 2);
     };
 
-    if (k_lo < k_hi) issue(k_lo);
-    if (k_lo + 1 < k_hi) issue(k_lo + 1);
-    if constexpr (MX) {
-        for (int k4 = k_lo; k4 < k_hi; k4 += 4) {
+    auto start = [&](int s) __attribute__((always_inline)) {
+        issue(k_lo + s, s);
+        if constexpr (C::DIRECT) load_b(bq[s]);
+        __builtin_amdgcn_sched_barrier(0);                   // (and the next step's after these)
+    };
+    // step k, the s-th of its quad
+    auto step = [&](int k, int s, bool ahead) __attribute__((always_inline)) {
+        sync_step(k, s, ahead);
+        const uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
+        u32x4(&bk)[C::BL] = bq[s & 1];
+        if constexpr (MX) {
+            if (s == 0) load_scales();
+            const int e = (r32 >> 4) * MX_TILE + 16 * ((r32 & 15) + 16 * h);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int k = k4 + s;
-                if (k >= k_hi) break;
-                sync_step(k);
-                if (s == 0) load_scales();
-                const uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
-                const int e = (r32 >> 4) * MX_TILE + 16 * ((r32 & 15) + 16 * h);
+            for (int f = 0; f < 2; ++f) {                    // columns 64 f .. 64 f + 63 of the step
+                u32x4 A[FM], B[FN];
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {                // columns 64 f .. 64 f + 63 of the step
-                    u32x4 A[FM], B[FN];
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        B[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 2 * MX_TILE + e + 512 * f);
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-                        A[i] = *(const u32x4 *)(st + (wm * FM + i) * 2 * MX_TILE + e + 512 * f);
-#pragma unroll
-                    for (int i = 0; i < FM; ++i)
-#pragma unroll
-                        for (int j = 0; j < FN; ++j) acc[j][i] = mx_mfma32(B[j], A[i], acc[j][i], s, sw[j][f], sx[i][f]);
+                for (int j = 0; j < FN; ++j) {
+                    if constexpr (C::DIRECT) B[j] = bk[2 * j + f];
+                    else B[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 2 * MX_TILE + e + 512 * f);
                 }
+#pragma unroll
+                for (int i = 0; i < FM; ++i) A[i] = *(const u32x4 *)(st + (wm * FM + i) * 2 * MX_TILE + e + 512 * f);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) acc[j][i] = mx_mfma32(B[j], A[i], acc[j][i], s, sw[j][f], sx[i][f]);
             }
-        }
-    } else {
-        for (int k = k_lo; k < k_hi; ++k) {
-            sync_step(k);
-            if (k % C::PER_Q == 0 || k == k_lo) load_scales();
-            const uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
+        } else {
+            if (s == 0) load_scales();
             u32x4 b[FN];
             float sc[FN];
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                b[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 1024 + (r32 >> 4) * 512 + 16 * ((r32 & 15) + 16 * h));
-                sc[j] = mx_scale((k & 1) ? sw[j][1] : sw[j][0], (k >> 1) & 3);
+                if constexpr (C::DIRECT) b[j] = bk[j];
+                else b[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 1024 + (r32 >> 4) * 512 + 16 * ((r32 & 15) + 16 * h));
+                sc[j] = mx_scale(sw[j][s & 1], s >> 1);
             }
             // columns 32 h + 8 m .. + 7: x of m + 1 is read while m is multiplied
             bf16x8 A[2][FM];
@@ -371,7 +391,34 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
                 __builtin_amdgcn_sched_barrier(0);           // (no reads of later columns drawn ahead)
             }
         }
+        if constexpr (C::DIRECT)
+            if (ahead) load_b(bk);
+    };
+    // Whole quads load two steps ahead without a condition, so that the compiler knows how many
+    // loads are outstanding wherever it waits for one; what is left of K takes the last loop.
+    constexpr int U = C::PER_Q;
+    int k0 = k_lo;
+    if (k0 + U <= k_hi) {
+        start(0);
+        start(1);
+        for (; k0 + U + 2 <= k_hi; k0 += U)
+#pragma unroll
+            for (int s = 0; s < U; ++s) step(k0 + s, s, true);
+        if (k0 + U == k_hi) {
+#pragma unroll
+            for (int s = 0; s < U; ++s) step(k0 + s, s, s + 2 < U);
+            k0 += U;
+        }
+    } else {
+        if (k_lo < k_hi) start(0);
+        if (k_lo + 1 < k_hi) start(1);
     }
+    for (; k0 < k_hi; k0 += U)
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            if (k0 + s >= k_hi) break;
+            step(k0 + s, s, k0 + s + 2 < k_hi);
+        }
     block_sync();                                            // the ring is free
 
     const int tw = t0 + wm * FM * 32, nw = n0 + wn * FN * 32;
@@ -454,12 +501,13 @@ struct Choice {
     Plan plan;
     int shares;
 };
-static Choice choose(bool mx, int64_t T, int64_t N, int64_t K) {
+static Choice choose(bool mx, int64_t T, int64_t N, int64_t K, int64_t ldx = 0) {
     if (T <= 16 && (mx || T * mx4_quads(K) <= 64)) return {SKINNY, 1};
     const int64_t cu = n_compute_units(), round = 2 * cu;
     auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((N + n - 1) / n); };
     const int64_t large = tiles(128, 256), rounds = (large + round - 1) / round;
-    if (8 * large >= 7 * rounds * round) return {LARGE, 1};
+    // (rows of x within 2^31 bytes of the tile's first, for its 32-bit offsets)
+    if (8 * large >= 7 * rounds * round && ldx <= (int64_t)1 << 23) return {LARGE, 1};
     int64_t sh = cu / tiles(64, 128), most = mx4_quads(K);
     if (sh > most) sh = most;
     if (sh > MAX_SHARES) sh = MAX_SHARES;
@@ -480,7 +528,7 @@ size_t mx4_gemm_ws(int64_t T, int64_t N, int64_t K) {
 
 template <bool MX>
 static hipError_t launch_product(GemmArgs a, uint8_t *ws, hipStream_t s) {
-    const Choice c = choose(MX, a.T, a.N, a.K);
+    const Choice c = choose(MX, a.T, a.N, a.K, MX ? 0 : a.ldx);
     a.shares = c.shares;
     a.part = (float *)ws;
     if (c.plan == SKINNY) return launch_skinny<MX>(a, s);

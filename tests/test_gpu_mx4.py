@@ -206,6 +206,32 @@ def test_gemm(torch, qs, T, N, K):
     check(qs.mx4_gemm_mx4x(wc, ws, N, K, xc, xs, T, y_dtype=torch.bfloat16), want, bound, "mx bf16")
 
 
+# large tiles (128 x 256): whole and partial quads of columns, first and last steps alone
+@pytest.mark.parametrize("K", [32, 96, 128, 416, 512, 544, 640, 1024, 1184, 1664])
+def test_gemm_large_tiles(torch, qs, K):
+    T, N = 1000, 14500
+    w, wc, ws = weights(N, K, K, torch, qs)
+    x = activations(T, K, K + 1, torch)
+    xv = np64(x)
+    check(qs.mx4_gemm(wc, ws, N, K, x, y_dtype=torch.bfloat16), xv @ w.T, ref.product_bound(xv, w), "bf16")
+    c, s = ref.quantize(xv)
+    xq = ref.values(c, s)
+    xc, xs = qs.mx4_quantize(x)
+    check(qs.mx4_gemm_mx4x(wc, ws, N, K, xc, xs, T), xq @ w.T, ref.product_bound(xq, w), "mx f32")
+
+
+@pytest.mark.parametrize("ldx", [2 ** 23, 2 ** 23 + 8])
+def test_gemm_rows_far_apart(torch, qs, ldx):
+    """Rows of x so far apart that their offsets pass 31 bits inside a tile."""
+    T, N, K = 130, 58000, 96                     # two by 227 tiles of 128 x 256
+    w, wc, ws = weights(N, K, 8, torch, qs)
+    x = activations(T, K, 9, torch)
+    xb = torch.empty(T * ldx, dtype=torch.bfloat16, device="cuda").view(T, ldx)
+    xb[:, :K] = x
+    xv = np64(x)
+    check(qs.mx4_gemm(wc, ws, N, K, xb[:, :K]), xv @ w.T, ref.product_bound(xv, w), "f32")
+
+
 @pytest.mark.parametrize("T", [1, 6, 40, 300])
 def test_gemm_strides_and_guards(torch, qs, T):
     """Rows of x and y inside wider buffers; what lies beside and behind y is left as it was."""
