@@ -489,13 +489,15 @@ GemmArgs make_args(const uint8_t *wc, const uint8_t *ws, int64_t N, int64_t K, i
 // Which kernel (times: bf16 x, us):
 //   skinny  up to 16 tokens, bf16 x only while all of it can be staged at once (64 KB): beyond,
 //           staging between barriers costs more than reading the weights once saves
-//           (T = 16 x 16384 x 2048: 8.1 against 14.6 in tiles; T = 16 x 2048 x 8192: 30.5 against 10.9)
-//   large   tiles of 128 x 256, two workgroups a compute unit, if they fill their last round of
-//           the device to 7/8 on average (T = 1024 x 16384 x 2048, one full round: 67 against 76
-//           in small tiles; T = 512, half a round: 49 against 40)
+//           (T = 16 x 16384 x 2048: 7.5 against 13.0 in tiles; T = 16 x 2048 x 8192: 30.5 against 10.9)
+//   large   tiles of 128 x 256, from 7/8 of a tile for every compute unit on and over 64 tokens
+//           (which one row of small tiles holds); times in large and in small tiles at 16384 x
+//           2048: T = 256, half the compute units, 27 and 20; T = 384, 3/4, 31 and 31; T = 512,
+//           one each, 34 and 39; T = 640, 47 and 45; T = 1024, two each, 58 and 74; at 65536 x
+//           2048: T = 40, 33 and 23; T = 70, 33 and 38
 //   small   tiles of 64 x 128, and where those are fewer than the compute units, the columns
-//           split into shares of at least one quad (T = 37 x 2048 x 8192: 11.2 with 16 shares,
-//           13.9 with 8; T = 20 x 2048 x 2048: 9.5 with 4, 13.3 with 2).
+//           split into shares of at least one quad (T = 37 x 2048 x 8192: 11.4 with 16 shares,
+//           12.7 with 8; T = 20 x 2048 x 2048: 8.9 with 4, 11.4 with 2).
 enum Plan { SKINNY, SMALL, LARGE };
 struct Choice {
     Plan plan;
@@ -503,11 +505,10 @@ struct Choice {
 };
 static Choice choose(bool mx, int64_t T, int64_t N, int64_t K, int64_t ldx = 0) {
     if (T <= 16 && (mx || T * mx4_quads(K) <= 64)) return {SKINNY, 1};
-    const int64_t cu = n_compute_units(), round = 2 * cu;
+    const int64_t cu = n_compute_units();
     auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((N + n - 1) / n); };
-    const int64_t large = tiles(128, 256), rounds = (large + round - 1) / round;
-    // (rows of x within 2^31 bytes of the tile's first, for its 32-bit offsets)
-    if (8 * large >= 7 * rounds * round && ldx <= (int64_t)1 << 23) return {LARGE, 1};
+    // (ldx: rows of x within 2^31 bytes of the tile's first, for its 32-bit offsets)
+    if (T > 64 && 8 * tiles(128, 256) >= 7 * cu && ldx <= (int64_t)1 << 23) return {LARGE, 1};
     int64_t sh = cu / tiles(64, 128), most = mx4_quads(K);
     if (sh > most) sh = most;
     if (sh > MAX_SHARES) sh = MAX_SHARES;
