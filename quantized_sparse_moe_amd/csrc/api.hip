@@ -282,7 +282,8 @@ moe_status run_mx4(const moe_layer_desc *d, const uint16_t *x, int64_t T, void *
                                 topk_idx ? topk_idx + T0 * K : nullptr, topk_w ? topk_w + T0 * K : nullptr, route_only, st);
         return dev(e);
     }
-    const int64_t C = pick_chunk(d, T, ws_bytes);
+    // (x of a chunk within 2^31 bytes: the products' offsets into it have 32 bits)
+    const int64_t fit = pick_chunk(d, T, ws_bytes), most = ((int64_t)1 << 30) / H, C = fit < most ? fit : most;
     const PrefillBufs b = carve_mx4_prompt(d, C, ws, &n);
     for (int64_t t0 = 0; t0 < T; t0 += C) {
         const int64_t Tc = T - t0 < C ? T - t0 : C;

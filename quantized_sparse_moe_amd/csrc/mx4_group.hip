@@ -6,10 +6,12 @@
 // fragments of 32) against the tile's rows (five fragments, only as many as the tile fills),
 // the weights as first operand, so that a lane's registers are neighbouring columns.
 //
-// Data movement as in mx4_gemm.hip: everything global -> LDS by direct-to-LDS loads, steps of
-// 64 columns, activation rows of 128 bytes with their chunks XORed by (row / 2) % 8; here a
-// ring of two stages, so that two workgroups fit a compute unit and one's prologue and epilogue
-// run under the other's products.  Each wave loads the weight tiles it multiplies itself.
+// Data movement as in the large tiles of mx4_gemm.hip: activation rows global -> LDS in a ring of
+// three stages of 64 columns (128 bytes a row, chunks XORed by (row / 2) % 8), each wave's weights
+// straight into its registers, both two steps ahead; two workgroups fit a compute unit, and one's
+// prologue and epilogue run under the other's products.  T = 4096, 2048 x 512, top 8 of 256 experts
+// and a shared one: 474 -> 425 us a layer against weights through LDS in a ring of two; fragments past
+// a tile's rows skipped by a branch each (T = 512: 154 us; all five multiplied: 184).
 //
 //   gate/up  rows of x gathered through perm; the wave's fragments are 32 gate rows and the
 //            same 32 up rows, so h = silu(g) u is formed in registers.  It leaves as the bf16
@@ -39,11 +41,11 @@ struct GroupArgs {
 };
 
 constexpr int FM = GEMM_BM / 32, FN = 2, GW = 4;
-constexpr int A_STAGE = GEMM_BM * 128, B_STAGE = 256 * 32, STAGE = A_STAGE + B_STAGE;
-constexpr int SC_SLOT = 256 * 16, RING = 2 * STAGE + 2 * SC_SLOT;
-constexpr int A_DMA = A_STAGE / (1024 * GW), B_DMA = 2, S_DMA = 4;
+constexpr int STAGE = GEMM_BM * 128, NSTAGE = 3;
+constexpr int SC_SLOT = 256 * 16, RING = NSTAGE * STAGE + 2 * SC_SLOT;
+constexpr int A_DMA = STAGE / (1024 * GW), S_DMA = 4;
 constexpr int EP = 32 * (64 * 4 + 16);                       // a wave's epilogue staging
-static_assert(GW * EP <= RING && GEMM_BM % 32 == 0 && A_STAGE % (1024 * GW) == 0, "tile shape");
+static_assert(GW * EP <= RING && GEMM_BM % 32 == 0 && STAGE % (1024 * GW) == 0, "tile shape");
 
 template <bool DOWN>
 __global__ __launch_bounds__(64 * GW) __attribute__((amdgpu_waves_per_eu(2))) void k_mx_group(GroupArgs a) {
@@ -62,7 +64,8 @@ __global__ __launch_bounds__(64 * GW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const int S = Kdim / 64, steps = DOWN ? 2 * S : S;       // (H and I are multiples of 64)
 
     // ---- this wave's weight panels: four of 16 rows (gate/up: two of gate, two of up)
-    const uint8_t *bsrc[B_DMA], *ssrc[S_DMA];
+    const uint8_t *bsrc[FN], *sbase[2];
+    int soff[S_DMA];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint8_t *codes, *scales;
@@ -83,35 +86,38 @@ __global__ __launch_bounds__(64 * GW) __attribute__((amdgpu_waves_per_eu(2))) vo
         // (columns past the matrix: its last panel, discarded)
         const int first = DOWN ? nbi * 16 + wave * 4 + 2 * j : nbi * 8 + wave * 2, np = (DOWN ? H : I) / 16;
         const int64_t p0 = e * stride / 16;
-        bsrc[j] = codes + (p0 + min(first + h, np - 1)) * KS * MX_TILE + 16 * r32;
+        bsrc[j] = codes + (p0 + min(first + (r32 >> 4), np - 1)) * KS * MX_TILE + 16 * ((r32 & 15) + 16 * h);
+        sbase[j] = scales + p0 * KQ * MX_QS;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ssrc[2 * j + i] = scales + (p0 + min(first + i, np - 1)) * KQ * MX_QS + 4 * lane;
+        for (int i = 0; i < 2; ++i) soff[2 * j + i] = min(first + i, np - 1) * KQ * MX_QS + 4 * lane;
     }
-    // ---- activation rows: piece i of a stage is rows 8 (A_DMA wave + i) .. + 7
-    const uint8_t *asrc[A_DMA];
+    // ---- activation rows: piece i of a stage is rows 8 (A_DMA wave + i) .. + 7; their offsets
+    // from abase (gate/up: below 2^31, the caller's chunks see to it)
+    const void *abase = DOWN ? (const void *)(a.h + (int64_t)tile.row0 * 2 * I) : a.x;
+    uint32_t aoff[A_DMA];
 #pragma unroll
     for (int i = 0; i < A_DMA; ++i) {
         const int row = 8 * (A_DMA * wave + i) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-        const int r = tile.row0 + (row < nrows ? row : nrows - 1);         // (past the tile: its last row)
-        const uint16_t *src;
-        if (DOWN) src = a.h + (int64_t)r * 2 * I;
-        else src = a.x + (sh ? r - TK : (int64_t)(a.perm[r] / K)) * H;
-        asrc[i] = (const uint8_t *)(src + 8 * c);
+        const int r = row < nrows ? row : nrows - 1;         // (past the tile: its last row)
+        if (DOWN) aoff[i] = (uint32_t)(r * 4 * I + 16 * c);
+        else aoff[i] = (uint32_t)(sh ? tile.row0 + r - TK : (int64_t)(a.perm[tile.row0 + r] / K)) * (uint32_t)(2 * H) + 16 * c;
     }
-    auto issue = [&](int k) __attribute__((always_inline)) {
-        uint8_t *st = sm + (k & 1) * STAGE;
-        const int kb = DOWN && k >= S ? k - S : k;
+    // step k's columns are 64 kb .. of the weights; slot: of the quad's scales
+    auto issue = [&](int k, int kb, int slot) __attribute__((always_inline)) {
+        uint8_t *st = sm + (k % NSTAGE) * STAGE;
 #pragma unroll
-        for (int i = 0; i < A_DMA; ++i) dma16(asrc[i] + (int64_t)k * 128, st + (A_DMA * wave + i) * 1024);
-#pragma unroll
-        for (int j = 0; j < B_DMA; ++j)
-            dma16(bsrc[j] + (int64_t)kb * (MX_TILE / 2), st + A_STAGE + (B_DMA * wave + j) * 1024);
-        if (kb % 8 == 0) {                                   // a quad's scales; slots alternate
-            const int n = kb / 8 + (DOWN && k >= S ? KQ : 0);
+        for (int i = 0; i < A_DMA; ++i)
+            dma16_buffer(buffer_from(abase), st + (A_DMA * wave + i) * 1024, aoff[i], k * 128);
+        if (kb % 8 == 0)                                     // a quad's scales; slots alternate
 #pragma unroll
             for (int i = 0; i < S_DMA; ++i)
-                dma4(ssrc[i] + (int64_t)(kb / 8) * MX_QS, sm + 2 * STAGE + (n & 1) * SC_SLOT + (S_DMA * wave + i) * 256);
-        }
+                dma4_buffer(buffer_from(sbase[i >> 1]), sm + NSTAGE * STAGE + slot * SC_SLOT + (S_DMA * wave + i) * 256,
+                            soff[i], kb / 8 * MX_QS);
+    };
+    u32x4 bq[2][FN];                                         // weights, by the step's parity
+    auto load_b = [&](int kb, u32x4 (&b)[FN]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[j] = *(const u32x4 *)(bsrc[j] + kb * (MX_TILE / 2));
     };
 
     f32x16 acc[FN][FM];
@@ -121,30 +127,31 @@ __global__ __launch_bounds__(64 * GW) __attribute__((amdgpu_waves_per_eu(2))) vo
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
-    uint32_t sw[FN][2];
-    issue(0);
-    for (int k = 0; k < steps; ++k) {
-        wait_dma<0>();                                       // stage k has landed, and is read after the barrier,
-        block_sync();                                        // which also frees stage k - 1 for the next loads
-        if (k + 1 < steps) issue(k + 1);
-        const int kb = DOWN && k >= S ? k - S : k;
-        if (kb % 8 == 0) {
-            const int n = kb / 8 + (DOWN && k >= S ? KQ : 0);
-            const uint8_t *ss = sm + 2 * STAGE + (n & 1) * SC_SLOT + wave * 1024 + (r32 >> 4) * 256 + 4 * ((r32 & 15) + 16 * h);
+    uint32_t sw0[FN], sw1[FN];                               // scales of the quad's even and odd steps
+    // step k of parity par, columns 64 kb of the weights; the next two steps' kb and scale slots
+    struct Next {
+        int kb, slot;
+    };
+    auto step = [&](int k, int par, Next c, bool quad1, Next n2, bool ahead) __attribute__((always_inline)) {
+        // stage k has landed once at most step k + 1's loads are outstanding (quad1: scales too)
+        if (!ahead && k + 1 >= steps) wait_dma<0>();
+        else if (quad1) wait_dma<A_DMA + FN + S_DMA>();
+        else wait_dma<A_DMA + FN>();
+        block_sync();                                        // and frees stage k - 1
+        if (ahead) issue(k + 2, n2.kb, n2.slot);
+        if (c.kb % 8 == 0) {
+            const uint8_t *ss = sm + NSTAGE * STAGE + c.slot * SC_SLOT + wave * 1024 + (r32 >> 4) * 256 +
+                                4 * ((r32 & 15) + 16 * h);
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                sw[j][0] = *(const uint32_t *)(ss + 512 * j);
-                sw[j][1] = *(const uint32_t *)(ss + 512 * j + 128);
+                sw0[j] = *(const uint32_t *)(ss + 512 * j);
+                sw1[j] = *(const uint32_t *)(ss + 512 * j + 128);
             }
         }
-        const uint8_t *st = sm + (k & 1) * STAGE;
-        u32x4 b[FN];
+        const uint8_t *st = sm + (k % NSTAGE) * STAGE;
         float sc[FN];
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            b[j] = *(const u32x4 *)(st + A_STAGE + wave * 2048 + j * 1024 + (r32 >> 4) * 512 + 16 * ((r32 & 15) + 16 * h));
-            sc[j] = mx_scale((kb & 1) ? sw[j][1] : sw[j][0], (kb >> 1) & 3);
-        }
+        for (int j = 0; j < FN; ++j) sc[j] = mx_scale((c.kb & 1) ? sw1[j] : sw0[j], (c.kb >> 1) & 3);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {                        // columns 32 h + 8 m .. + 7
             bf16x8 A[FM], B[FN];
@@ -152,14 +159,56 @@ __global__ __launch_bounds__(64 * GW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
             for (int i = 0; i < FM; ++i) A[i] = *(const bf16x8 *)(st + (32 * i + r32) * 128 + 16 * pos);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) B[j] = mx_bf16(b[j][m], sc[j]);
+            for (int j = 0; j < FN; ++j) B[j] = mx_bf16(bq[par][j][m], sc[j]);
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FM; ++i) {
+                // (read above for every fragment: inside the branches each read would be waited for)
+                asm volatile("" : "+v"(A[i]));
                 if (i < nf)
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
                         acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(B[j], A[i], acc[j][i], 0, 0, 0);
+            }
         }
+        if (ahead) load_b(n2.kb, bq[par]);
+    };
+    auto start = [&](int k, Next n) __attribute__((always_inline)) {
+        issue(k, n.kb, n.slot);
+        load_b(n.kb, bq[k]);
+        __builtin_amdgcn_sched_barrier(0);                   // (and the next step's after these)
+    };
+    // Whole quads of columns: every step's place in its quad is known, and with it the number of
+    // loads outstanding, wherever the compiler waits for one.
+    if (S % 8 == 0) {
+        start(0, {0, 0});
+        start(1, {1, 0});
+        const int quads = steps / 8;
+        int qb = 0;                                          // the quad of the weights
+        for (int q = 0; q + 1 < quads; ++q) {
+            const int qn = qb + 1 == KQ ? 0 : qb + 1;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                step(8 * q + s, s & 1, {8 * qb + s, q & 1}, s == 7,
+                     s < 6 ? Next{8 * qb + s + 2, q & 1} : Next{8 * qn + s - 6, (q + 1) & 1}, true);
+            qb = qn;
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            step(steps - 8 + s, s & 1, {8 * qb + s, (quads - 1) & 1}, false, {8 * qb + s + 2, 0}, s < 6);
+    } else {
+        auto at = [&](int k) __attribute__((always_inline)) {
+            const int kb = k < S ? k : k - S;                // (k < steps <= 2 S)
+            return Next{kb, (kb / 8 + (k < S ? 0 : KQ)) & 1};
+        };
+        start(0, at(0));
+        if (steps > 1) start(1, at(1));
+        for (int k = 0; k < steps; k += 2)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (k + s >= steps) break;
+                const bool ahead = k + s + 2 < steps;
+                step(k + s, s, at(k + s), k + s + 1 < steps && at(k + s + 1).kb % 8 == 0, ahead ? at(k + s + 2) : Next{0, 0}, ahead);
+            }
     }
     block_sync();                                            // the ring is free
 

@@ -205,6 +205,35 @@ def test_prompt_in_chunks(torch, qs):
     assert torch.equal(y4[200], y[200])
 
 
+@pytest.mark.parametrize("T", [1, 30, 129, 400, 1500])
+@pytest.mark.parametrize("shape", [(512, 512), (1024, 1536), (1536, 64)])
+def test_whole_quads_of_columns(torch, qs, shape, T):
+    """Dimensions of whole quads (512 columns): the prompt kernels unroll those."""
+    L = ref.Layer(*shape, n_experts=12, top_k=3, seed=T, gated=True)
+    desc = upload(L, torch, qs)
+    xb = syn.make_x(T, L.hidden, seed=T + 1)
+    y, idx, w = run(torch, qs, desc, to_dev(xb, torch))
+    check(L, xb, y, idx, w, (shape, T))
+
+
+def test_prompt_past_32_bit_offsets(torch, qs):
+    """A workspace for all of a prompt whose x is larger than 2^31 bytes gives the bits of small chunks."""
+    L = ref.Layer(8192, 64, n_experts=4, top_k=1, shared=False, seed=3)
+    desc = upload(L, torch, qs)
+    T = 140000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, L.hidden, generator=g, device="cuda", dtype=torch.bfloat16)
+    idx = torch.empty((T, 1), dtype=torch.int32, device="cuda")
+    y = {}
+    for chunk in (4096, T):
+        ws = torch.zeros(qs.moe_workspace_size(desc, T, chunk), dtype=torch.uint8, device="cuda")
+        y[chunk] = qs.moe_layer_forward(desc, x, topk_idx=idx, workspace=ws, y_dtype=torch.bfloat16)
+    assert torch.equal(y[4096], y[T])
+    rows = [0, 131071, 131072, T - 1]                    # (2^31 bytes into x is row 131072)
+    few = qs.moe_layer_forward(desc, x[rows].contiguous().repeat(40, 1), y_dtype=torch.bfloat16)
+    assert torch.equal(few[:4], y[T][rows])
+
+
 def test_prompt_range(torch, qs):
     """Activations whose expert outputs leave fp16's range: the slot rows carry scales."""
     L = layer("ragged")
