@@ -7,7 +7,11 @@ are allocated here with torch.  The functions carry the names of the C entry poi
 
     moe_workspace_size, moe_workspace_status, moe_route, moe_layer_forward, q8_gemv,
     q8_quantize_x, q8_gemv_q8x, q8_gemv_qx, q8_pack_rows16,
-    mx4_quantize, mx4_dequantize, mx4_pack_rows16, mx4_gemm, mx4_gemm_mx4x
+    mx4_quantize, mx4_dequantize, mx4_pack_rows16, mx4_gemm, mx4_gemm_mx4x,
+    mx4_codes_size, mx4_scales_size, mx4_gemm_workspace_size
+
+``LayerDesc.from_host`` uploads an affine-quantized layer, ``LayerDesc.from_mx4`` takes one
+whose expert matrices are MX4 (quantized or repacked on the device by the functions above).
 
 There is no fallback: if the shared library is missing, loading raises.
 Build it with ``python -m quantized_sparse_moe_amd.build``.

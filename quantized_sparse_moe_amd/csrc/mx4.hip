@@ -8,7 +8,11 @@
 // becomes a NaN block (byte 255, codes 0).
 //
 // All of these move bytes: a thread takes 8 consecutive values (16-byte reads), four
-// neighbouring lanes a block, and the block's largest value goes round the four by DPP.
+// neighbouring lanes a block, and the block's largest value goes round the four by DPP.  They
+// are bound by memory: 4096 x 8192 bf16 to tiles 16.4 us (5.2 TB/s read and written; a large
+// copy reaches 4.7, part of these 85 MB stay in the Infinity Cache) and back 13.6; 16390 x 2080
+// fp32 to rows 29.0 (5.3 TB/s) and back 24.8; 268 MB of codes repacked 110 (5.2 TB/s).  One row
+// of 2048 takes 2.5 and 2.3, a launch.
 #include "mx4.h"
 
 namespace qs {

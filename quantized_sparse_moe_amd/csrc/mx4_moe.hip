@@ -16,8 +16,15 @@
 //            registers and are added in the lane.  Shares are added in a fixed order by the
 //            share that finishes last.
 //
-// All three are bound by the weight stream: (union of the chosen experts + shared) x
-// 3 H I x 17/32 bytes.  Every sum is fp32 in a fixed order; there are no float atomics.
+// A single token takes two: k_mx_token does route and gate/up.
+//
+// All are bound by the weight stream: (union of the chosen experts + shared) x
+// 3 H I x 17/32 bytes, and at few tokens by the chain of launches and round trips before and
+// after it (2048 x 512, top 8 of 256 and a shared expert, times of the layer in a graph):
+//   T = 1  15.8 us (15 MB: 2.4 at 6.3 TB/s)   T = 7  36.8 (89 MB: 14)     T = 20 61 (209 MB: 33)
+//   T = 32 73 (272 MB: 43)                    T = 48 under a skewed router (52 experts) 49
+// From T = 7 on more experts cost 5.2 TB/s; about 20 us do not depend on them.  Of T = 7, route
+// takes 9.0, gate/up 16, down 12.  Every sum is fp32 in a fixed order; there are no float atomics.
 #include "decode_state.h"
 #include "mx4.h"
 
@@ -219,7 +226,9 @@ __device__ __forceinline__ int h_place(int block) { return (block >> 2) * 256 + 
 // -------------------------------------------------------------------------- gate/up
 // The tokens' rows of x are staged in LDS, 2048 columns at a time: read as MFMA operands from
 // global memory they are 64 separate 16-byte pieces a load, which costs the address unit four
-// times a contiguous one.
+// times a contiguous one.  Two panels of 16 columns of h a workgroup: one is faster for few
+// tokens and slower for many (T = 7 36 against 37 us a layer, T = 20 68 against 61), four slower
+// throughout (39, 66); workgroups that loop over items, loading ahead, gain nothing (38, 61).
 constexpr int GU_QUADS = MT_WAVES / 2;                       // quads of a chunk: one per wave pair
 constexpr int GU_PITCH = GU_QUADS * 1024 + 16;               // bytes of a staged row (padded: banks)
 
