@@ -209,6 +209,13 @@ class LayerDesc:
                                            ("shared down", shared[1], hidden, inter))):
             nc, ns = _mx4_sizes(rows, cols, MX4_TILES)
             _mx4_buf(m[0], nc, f"LayerDesc.from_mx4: {what}"), _mx4_buf(m[1], ns, f"LayerDesc.from_mx4: {what}")
+            if m[0].device != router_w.device or m[1].device != router_w.device:
+                _mx4_bad("LayerDesc.from_mx4", f"{what} is on another device than router_w")
+        for what, t, n, size in (("router_w", router_w, n_experts * hidden, 2), ("router_bias", router_bias, n_experts, 4),
+                                 ("shared_gate_w", shared_gate_w, hidden, 2)):
+            if t is not None and (t.element_size() != size or t.numel() != n or not t.is_contiguous()
+                                  or t.device != router_w.device):
+                _mx4_bad("LayerDesc.from_mx4", f"{what} must be {n} contiguous values of {size} bytes")
 
         def half(m, cols, rows, row0):
             nc, ns = _mx4_sizes(row0, cols, MX4_TILES)

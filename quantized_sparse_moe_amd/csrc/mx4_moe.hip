@@ -34,6 +34,8 @@ namespace {
 
 constexpr int MT_THREADS = 512, MT_WAVES = 8;
 constexpr int RT_THREADS = 1024, RT_WAVES = 16;
+static_assert((TOPK_BASE + TOPK_COPIES * TOPK_STRIDE) * 4 <= (int)MX_CNT_OFF, "counters behind the decode state");
+static_assert(MX_CNT_DOWN + 8192 / 16 <= 1024, "a counter per 16 output rows");
 
 struct MxArgs {
     Layer L;

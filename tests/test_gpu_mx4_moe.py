@@ -303,6 +303,51 @@ def test_guards_around_the_outputs(torch, qs):
             assert (t[0] == v).all() and (t[T + 1] == v).all() and not (t[1:T + 1] == v).any()
 
 
+@pytest.mark.parametrize("T", [1, 2, 21, 64, 100, 150])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_not_finite_tokens_stay_alone(torch, qs, T, value):
+    """A NaN or an infinity in one token's x: the call returns, that token's row of y holds no finite
+    value where its experts see it, every other token's row is right."""
+    L = layer("skew")
+    desc = upload(L, torch, qs)
+    xb = syn.make_x(T, L.hidden, seed=31)
+    x = to_dev(xb, torch).view(torch.bfloat16).clone()
+    bad = T // 2
+    x[bad, 5] = value
+    ws = qs.new_workspace(desc, T)
+    y, idx, w = run(torch, qs, desc, x, workspace=ws)
+    assert not torch.isfinite(y[bad]).any()
+    gi = idx.cpu().numpy()
+    assert (np.diff(gi, axis=1) > 0).all() and gi.min() >= 0 and gi.max() < L.n_experts
+    rest = [t for t in range(T) if t != bad]
+    if rest:
+        want, bound = L.forward(ref.bf16_values(xb)[rest], gi[rest], prompt=T > 128)
+        assert (np.abs(y.cpu().numpy()[rest] - want) <= bound).all()
+    # and nothing of it stays in the workspace
+    y2, i2, w2 = run(torch, qs, desc, to_dev(xb, torch), workspace=ws)
+    check(L, xb, y2, i2, w2, T)
+
+
+def test_two_streams_two_workspaces(torch, qs):
+    """Calls that overlap in time, each on its own stream and workspace, give what they give alone."""
+    L = layer("skew")
+    desc = upload(L, torch, qs)
+    xs = [to_dev(syn.make_x(T, L.hidden, seed=40 + T), torch) for T in (1, 7)]
+    ws = [qs.new_workspace(desc, x.shape[0]) for x in xs]
+    want = [qs.moe_layer_forward(desc, x, workspace=w).clone() for x, w in zip(xs, ws)]
+    ys = [torch.empty((20,) + tuple(y.shape), device="cuda") for y in want]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for r in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                qs.moe_layer_forward(desc, xs[i], y=ys[i][r], workspace=ws[i])
+    torch.cuda.synchronize()
+    for y, w in zip(ys, want):
+        assert (y == w).all()
+    assert all(int(qs.moe_workspace_status(w)) == 0 for w in ws)
+
+
 def test_products_and_layer_run_together(torch, qs):
     """A block as it is used: a projection with MX4 weights makes the layer's input, the layer
     runs, its output is quantized and goes through another projection."""

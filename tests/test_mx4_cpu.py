@@ -156,6 +156,32 @@ def test_layer_descriptor_accepted():
     assert forward(affine) == INV                                      # (needs biases)
 
 
+def test_layer_tensors_are_checked():
+    """from_mx4 refuses tensors of another size, type or layout before anything reads them."""
+    import torch
+    H, I, E = 128, 64, 3
+
+    def mat(rows, cols):
+        return (torch.zeros(q.lib().mx4_codes_size(rows, cols, q.MX4_TILES), dtype=torch.uint8),
+                torch.zeros(q.lib().mx4_scales_size(rows, cols, q.MX4_TILES), dtype=torch.uint8))
+
+    def make(**kw):
+        a = dict(router_w=torch.zeros(E, H, dtype=torch.bfloat16), gate_up=mat(E * 2 * I, H), down=mat(E * H, I))
+        a.update(kw)
+        return q.LayerDesc.from_mx4(H, I, E, 2, **a)
+
+    make()
+    make(router_bias=torch.zeros(E), shared=(mat(2 * I, H), mat(H, I)), shared_gate_w=torch.zeros(H, dtype=torch.bfloat16))
+    gu = mat(E * 2 * I, H)
+    for bad in (dict(router_w=torch.zeros(E, H)), dict(router_w=torch.zeros(E, H - 32, dtype=torch.bfloat16)),
+                dict(router_w=torch.zeros(H, E, dtype=torch.bfloat16).t()),
+                dict(router_bias=torch.zeros(E, dtype=torch.float64)), dict(router_bias=torch.zeros(E + 1)),
+                dict(shared_gate_w=torch.zeros(H)), dict(gate_up=(gu[0][:-16], gu[1])), dict(gate_up=(gu[0], gu[1][4:])),
+                dict(down=(gu[0][::2], gu[1])), dict(shared=(mat(I, H), mat(H, I)))):
+        with pytest.raises(q.QsmoeError):
+            make(**bad)
+
+
 def test_layer_workspace():
     d = mx4_desc()
     f = lambda T, c=0: q.lib().moe_workspace_size_chunked(ctypes.byref(d), T, c)
