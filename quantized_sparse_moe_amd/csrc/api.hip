@@ -193,14 +193,14 @@ PrefillBufs carve_mx4_prompt(const moe_layer_desc *d, int64_t T, void *ws, size_
     *bytes = c.off;
     return b;
 }
-// up to 2 MX_TMAX tokens the few-token path in one or two passes (2048 x 512, 256 experts: T = 64
-// 92 us against 157 on the grouped path, T = 65 145 and 161, T = 96 168 and 169, T = 128 184 and
-// 179), more the grouped path in chunks (never less than for fewer tokens)
+// up to MX_TMAX tokens the few-token path (2048 x 512, 256 experts: T = 64 92 us against 157 on the
+// grouped path, T = 128 123 and 179; under a skewed router 82 and 112), more the grouped path in
+// chunks (never less than for fewer tokens)
 size_t ws_size_mx4(const moe_layer_desc *d, int64_t T, int64_t chunk) {
     size_t n = 0, m = 0;
     if (T <= 0) return 0;
     carve_mx4(d, T < MX_TMAX ? T : MX_TMAX, nullptr, &n);
-    if (T > 2 * MX_TMAX) carve_mx4_prompt(d, T < chunk ? T : chunk, nullptr, &m);
+    if (T > MX_TMAX) carve_mx4_prompt(d, T < chunk ? T : chunk, nullptr, &m);
     return n > m ? n : m;
 }
 
@@ -273,14 +273,9 @@ moe_status run_mx4(const moe_layer_desc *d, const uint16_t *x, int64_t T, void *
     const int64_t K = d->top_k, H = d->hidden;
     const size_t ysz = y_dtype == MOE_F32 ? 4 : 2;
     size_t n;
-    if (T <= 2 * MX_TMAX) {
-        const int64_t T0 = T <= MX_TMAX ? T : (T + 1) / 2;
-        const MxBufs b = carve_mx4(d, T0, ws, &n);
-        hipError_t e = launch_mx_layer(L, x, T0, b, y, y_dtype, topk_idx, topk_w, route_only, st);
-        if (e == hipSuccess && T0 < T)
-            e = launch_mx_layer(L, x + T0 * H, T - T0, b, y ? (char *)y + (size_t)(T0 * H) * ysz : nullptr, y_dtype,
-                                topk_idx ? topk_idx + T0 * K : nullptr, topk_w ? topk_w + T0 * K : nullptr, route_only, st);
-        return dev(e);
+    if (T <= MX_TMAX) {
+        const MxBufs b = carve_mx4(d, T, ws, &n);
+        return dev(launch_mx_layer(L, x, T, b, y, y_dtype, topk_idx, topk_w, route_only, st));
     }
     // (x of a chunk within 2^31 bytes: the products' offsets into it have 32 bits)
     const int64_t fit = pick_chunk(d, T, ws_bytes), most = ((int64_t)1 << 30) / H, C = fit < most ? fit : most;

@@ -142,7 +142,7 @@ hipError_t launch_mx4_gemm_mx4x(const uint8_t *wc, const uint8_t *wsc, int64_t N
 // The MoE layer with MX4 experts (mx4_moe.hip), MX_TMAX tokens a pass.  Its counters lie in
 // the workspace's state region behind the affine kernels' words: zero before the first call,
 // and put back to zero by every call.
-constexpr int MX_TMAX = 64, MX_SHARES = 8;
+constexpr int MX_TMAX = 128, MX_SHARES = 8;
 constexpr int MX_ITEMS = 256 + MX_TMAX * 16 / 16;         // of the work list: experts, and one per 16 tokens
 constexpr size_t MX_CNT_OFF = WS_CTL_BYTES - 4096;        // bytes
 constexpr int MX_CNT_DOWN = 16;                           // counters before: route's

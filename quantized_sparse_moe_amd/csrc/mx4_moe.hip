@@ -22,7 +22,8 @@
 // 3 H I x 17/32 bytes, and at few tokens by the chain of launches and round trips before and
 // after it (2048 x 512, top 8 of 256 and a shared expert, times of the layer in a graph):
 //   T = 1  15.8 us (15 MB: 2.4 at 6.3 TB/s)   T = 7  36.8 (89 MB: 14)     T = 20 61 (209 MB: 33)
-//   T = 32 73 (272 MB: 43)                    T = 48 under a skewed router (52 experts) 49
+//   T = 32 73 (272 MB: 43)   T = 64 92 (370 MB: 59)   T = 65 101   T = 128 123 (421 MB: 67)
+//   under a skewed router T = 48 49 (52 experts), T = 128 82 (76 experts)
 // From T = 7 on more experts cost 5.2 TB/s; about 20 us do not depend on them.  Of T = 7, route
 // takes 9.0, gate/up 16, down 12.  Every sum is fp32 in a fixed order; there are no float atomics.
 #include "decode_state.h"
@@ -118,7 +119,8 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
     __shared__ f32x4 red[RT_WAVES][64];
     __shared__ int s_last;
     __shared__ int s_slot[256], s_cnt[4], s_itm[4];
-    __shared__ uint32_t s_mask[256][2];                      // tokens that chose the expert
+    constexpr int MW = MX_TMAX / 32;
+    __shared__ uint32_t s_mask[256][MW];                     // tokens that chose the expert
     __shared__ int16_t s_sel[MX_TMAX * 16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int H = a.L.H, E = a.L.E, K = a.L.K, T = a.T, NE = E + a.gated;
@@ -181,7 +183,9 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
     const bool tiles = gridDim.y > 1;                        // (else the selections are all in LDS)
     if (tiles && !last_of(a.b.cnt + MX_TMAX / 16, gridDim.y, &s_last)) return;
     // ---- the chosen experts in ascending order, and under each its tokens in order
-    if (tid < 256) s_mask[tid][0] = s_mask[tid][1] = 0u;
+    if (tid < 256)
+#pragma unroll
+        for (int i = 0; i < MW; ++i) s_mask[tid][i] = 0u;
     __syncthreads();
     for (int i = tid; i < T * K; i += RT_THREADS) {
         if (tiles)
@@ -192,17 +196,29 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
     }
     __syncthreads();
     // an expert of more than 16 tokens is listed once per 16 of them (its items share the slot)
-    const uint64_t mask = tid < 256 ? s_mask[tid][0] | (uint64_t)s_mask[tid][1] << 32 : 0ull;
-    const int cnt = __popcll(mask), own = (cnt + 15) >> 4;
+    int cnt = 0;
+    if (tid < 256)
+#pragma unroll
+        for (int i = 0; i < MW; ++i) cnt += __popc(s_mask[tid][i]);
+    const int own = (cnt + 15) >> 4;
     const uint64_t lt = (1ull << lane) - 1;
-    const uint64_t b0 = __ballot(own >= 1), b1 = __ballot(own >= 2), b2 = __ballot(own >= 3), b3 = __ballot(own >= 4);
+    int slot = 0, item = 0, slots = 0, items = 0;            // before this lane's, and of the wave
+#pragma unroll
+    for (int i = 0; i < MX_TMAX / 16; ++i) {
+        const uint64_t b = __ballot(own > i);
+        if (i == 0) {
+            slot = __popcll(b & lt);
+            slots = __popcll(b);
+        }
+        item += __popcll(b & lt);
+        items += __popcll(b);
+    }
     if (tid < 256 && lane == 0) {
-        s_cnt[wave] = __popcll(b0);
-        s_itm[wave] = __popcll(b0) + __popcll(b1) + __popcll(b2) + __popcll(b3);
+        s_cnt[wave] = slots;
+        s_itm[wave] = items;
     }
     __syncthreads();
     if (tid < 256) {
-        int slot = __popcll(b0 & lt), item = slot + __popcll(b1 & lt) + __popcll(b2 & lt) + __popcll(b3 & lt);
         for (int w = 0; w < wave; ++w) {
             slot += s_cnt[w];
             item += s_itm[w];
@@ -214,8 +230,11 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
     __syncthreads();
     for (int i = tid; i < T * K; i += RT_THREADS) {
         const int e = s_sel[i], tt = i / K;
-        const uint64_t m = s_mask[e][0] | (uint64_t)s_mask[e][1] << 32;
-        a.b.pos[s_slot[e] * MX_TMAX + __popcll(m & ((1ull << tt) - 1))] = (int16_t)i;
+        int before = __popc(s_mask[e][tt >> 5] & ((1u << (tt & 31)) - 1));
+#pragma unroll
+        for (int q = 0; q < MW - 1; ++q)
+            if (q < tt >> 5) before += __popc(s_mask[e][q]);
+        a.b.pos[s_slot[e] * MX_TMAX + before] = (int16_t)i;
     }
 }
 
@@ -575,20 +594,21 @@ int64_t max_items(const Layer &L, int64_t T) {
 // At most 32 items (one to three tokens of top-8): one panel per workgroup and 16 waves, so one
 // or two rounds of loads and no shares (T = 1: 6.6 us against 7.9; T = 7, 57 items: 15.4
 // against 12.3).  More: two panels and 8 waves, each row of h read for twice the weights, the
-// items shared out until there are two workgroups per compute unit.
+// items shared out until there are two workgroups per compute unit.  Over 64 tokens one panel,
+// as the waves' sums of two would leave LDS for one workgroup per compute unit.
 struct DownPlan {
     int np, waves, shares;
 };
 DownPlan down_plan(const Layer &L, int64_t T) {
     DownPlan d;
     const int64_t items = max_items(L, T) * ((L.I + 511) / 512);   // (at most)
-    if (items <= 32) {
+    if (items <= 32 && T <= 64) {
         d.np = 1;
         d.waves = 16;
         d.shares = 1;
         return d;
     }
-    d.np = 2;
+    d.np = T <= 64 ? 2 : 1;
     d.waves = 8;
     const int groups = L.H / (16 * d.np), want = (2 * n_compute_units() + groups - 1) / groups;
     const int64_t most = (items + d.waves - 1) / d.waves;
@@ -630,7 +650,8 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const dim3 grid((unsigned)(L.H / (16 * d.np)), (unsigned)a.shares), thr((unsigned)(64 * d.waves));
     const size_t lds = (size_t)d.waves * T * 16 * d.np * 4;
-    if (d.np == 1) hipLaunchKernelGGL((k_mx_down<1, 16>), grid, thr, lds, s, a);
+    if (d.waves == 16) hipLaunchKernelGGL((k_mx_down<1, 16>), grid, thr, lds, s, a);
+    else if (d.np == 1) hipLaunchKernelGGL((k_mx_down<1, 8>), grid, thr, lds, s, a);
     else hipLaunchKernelGGL((k_mx_down<2, 8>), grid, thr, lds, s, a);
     return hipGetLastError();
 }

@@ -133,6 +133,21 @@ def test_same_tokens_and_all_on_one_expert(torch, qs, T):
     assert torch.equal(y, y2)
 
 
+@pytest.mark.parametrize("name", ["one", "many", "narrow"])
+@pytest.mark.parametrize("T", [65, 96, 128])
+@pytest.mark.parametrize("same", [False, True])
+def test_largest_few_token_passes(torch, qs, name, T, same):
+    """More than 64 tokens in one pass: every token on one expert (eight list entries), 16 experts a
+    token (the longest list), the same token in every row."""
+    L = layer(name)
+    desc = upload(L, torch, qs)
+    xb = np.repeat(syn.make_x(1, L.hidden, seed=78), T, axis=0) if same else syn.make_x(T, L.hidden, seed=T)
+    ws = qs.new_workspace(desc, T)
+    for _ in range(2):                                   # (the counters are back at zero)
+        y, idx, w = run(torch, qs, desc, to_dev(xb, torch), workspace=ws)
+        check(L, xb, y, idx, w, (name, T, same))
+
+
 def test_exact_ties_go_to_the_lower_expert(torch, qs):
     L = ref.Layer(hidden=128, inter=64, n_experts=12, top_k=4, seed=3)
     L.router_bits[[1, 5, 9]] = L.router_bits[1]
