@@ -57,8 +57,8 @@ typedef int32_t moe_status;
  * workgroup for another inside a launch is bounded; a wait that gives up sets its bit and
  * lets the kernel finish, so the grid always drains, and that call's outputs are not to be
  * trusted.  A correct call on a device that runs the whole grid sets no bit. */
-#define MOE_WS_ERR_DECODE_WAIT 1u   /* a one-launch decode kernel (T <= 8), or the first launch of a
-                                       one-token MX4 layer, gave up a wait                */
+#define MOE_WS_ERR_DECODE_WAIT 1u   /* a one-launch decode kernel (T <= 8), or the first launch of an
+                                       MX4 layer of up to 4 tokens, gave up a wait        */
 #define MOE_WS_ERR_GEMM_WAIT   2u   /* a grouped-GEMM down tile gave up waiting for its h  */
 
 /* element types */
@@ -209,7 +209,7 @@ moe_status moe_route(const moe_layer_desc *d, const void *x, int64_t T,
  * fp32 accumulation, fp16 intermediates, each under its range scale).
  * For a given T the result does not depend on whether gate/up are fused or separate,
  * nor on the other tokens of the call (tokens are independent), bit for bit.
- * MX4 layers: up to 128 tokens run in three launches (one token in two) that read each chosen
+ * MX4 layers: up to 128 tokens run in three launches (up to 4 in two) that read each chosen
  * expert once (MFMA on bf16 operands: x as it is, the weights exact, h as a bf16 pair, to
  * 2^-17); more run the grouped path (the same products in tiles, weighted expert outputs in
  * fp16 under range scales before the combine).  There a token's

@@ -1,5 +1,5 @@
 // mx4_moe.hip -- the sparse MoE layer with MX4 experts for a few tokens (up to MX_TMAX a pass):
-// three launches, two for a single token.
+// three launches, two for up to four.
 //
 //   route    router logits on v_mfma_f32_16x16x32_bf16 (16 experts and 16 tokens per
 //            workgroup, the columns split over its waves).  The workgroup that finishes a tile
@@ -16,13 +16,14 @@
 //            registers and are added in the lane.  Shares are added in a fixed order by the
 //            share that finishes last.
 //
-// A single token takes two: k_mx_token does route and gate/up.
+// One to four tokens take two: k_mx_token does route and gate/up.
 //
 // All are bound by the weight stream: (union of the chosen experts + shared) x
 // 3 H I x 17/32 bytes, and at few tokens by the chain of launches and round trips before and
 // after it (2048 x 512, top 8 of 256 and a shared expert, times of the layer in a graph):
-//   T = 1  15.8 us (15 MB: 2.4 at 6.3 TB/s)   T = 7  36.8 (89 MB: 14)     T = 20 61 (209 MB: 33)
-//   T = 32 73 (272 MB: 43)   T = 64 92 (370 MB: 59)   T = 65 101   T = 128 123 (421 MB: 67)
+//   T = 1 15.9 us (15 MB: 2.4 at 6.3 TB/s)   T = 2 20.1   T = 4 26.6 (53 MB: 8)   T = 7 36.8 (89 MB: 14)
+//   T = 20 61 (209 MB: 33)   T = 32 73 (272 MB: 43)   T = 64 92 (370 MB: 59)
+//   T = 65 101   T = 128 123 (421 MB: 67)
 //   under a skewed router T = 48 49 (52 experts), T = 128 82 (76 experts)
 // From T = 7 on more experts cost 5.2 TB/s; about 20 us do not depend on them.  Of T = 7, route
 // takes 9.0, gate/up 16, down 12.  Every sum is fp32 in a fixed order; there are no float atomics.
@@ -45,7 +46,7 @@ struct MxArgs {
     int T;
     int gated;
     int route_only;
-    int token;                        // one token: route and gate/up ran as k_mx_token
+    int tagged;                       // route and gate/up ran as k_mx_token
     int32_t *out_idx;
     float *out_w;
     void *y;
@@ -373,23 +374,38 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
     gate_up_block(a, sx, s, blockIdx.x, sh, it.e, it.count, pos, w);
 }
 
-// One token: route and gate/up in one launch.  The first workgroups form the logits, 16 experts
-// each, and write them to every copy of the decode state's logit words under the call's tag;
-// the others stage nothing that depends on the routing until their wave 0 has all logits and has
-// taken the top-k itself (decode_state.h: a wait is bounded, and only for workgroups of lower
-// index).  Saves the last router workgroup's counting, selecting and listing and a launch.
+// Up to this many tokens route and gate/up are one launch: us a layer against two launches (2048 x
+// 512, 256 experts), T = 1 15.9 and 18.8, T = 2 20.1 and 23.4, T = 3 24.3 and 26.3, T = 4 26.6 and
+// 28.8; T = 5 to 8 within 2 % (each workgroup takes every token's top-k, and they no longer all
+// fit the device at once).
+constexpr int TOKEN_MAX = 4;
+
+// One to MT tokens: route and gate/up in one launch.  The first workgroups form the logits, 16 experts
+// each, and write them to every copy of the decode state's logit words (shared out among the
+// tokens) under the call's tag; the others wait, a wave per token, until it has all logits, and take
+// the top-k themselves (decode_state.h: a wait is bounded, and only for workgroups of lower
+// index).  The workgroup of (j, 32 columns of h) takes the j-th of the experts any token chose.
+// Saves the last router workgroup's counting, selecting and listing and a launch.
+template <int MT>
 __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_token(MxArgs a, int nR) {
+    static_assert(MT <= MT_WAVES && MT * 16 <= LOGIT_COPIES * 16, "a wave and a logit copy per token");
     extern __shared__ __attribute__((aligned(16))) uint8_t sx[];
     __shared__ GuShared s;
-    __shared__ float part[RT_WAVES][16], lg[16];
-    __shared__ int s_e;
+    __shared__ float part[RT_WAVES][MT][16], lg[MT][16];
+    __shared__ int s_idx[MT * 16];
+    __shared__ float s_w[MT * 16], s_gate[MT];
+    __shared__ uint32_t s_any[8];                            // experts that any token chose
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-    const int H = a.L.H, E = a.L.E, K = a.L.K, NE = E + a.gated;
+    const int H = a.L.H, E = a.L.E, K = a.L.K, NE = E + a.gated, T = MT == 1 ? 1 : a.T;
+    int per = LOGIT_COPIES;                                  // copies of a token's logits
+    if constexpr (MT > 1)
+        while (per * T > LOGIT_COPIES) per >>= 1;
     uint32_t *ctl = a.b.ctl;
     const uint32_t tag = call_tag(ctl);
     if ((int)blockIdx.x < nR) {
         const int e = blockIdx.x * 16 + n, ec = e < NE ? e : NE - 1;
         const uint16_t *wr = ec < E ? a.L.router_w + (int64_t)ec * H : a.L.shared_gate_w;
+        const uint16_t *xr = a.x + (int64_t)(n < T ? n : 0) * H;       // (rows past the tokens: the first, discarded)
         // (k_mx_route's sums in its order, so that the logits have the same bits: this wave takes the
         // shares of its waves `wave` and `wave` + 8)
         f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -402,7 +418,7 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
                 B[i] = A[i] = (u32x4){0u, 0u, 0u, 0u};
                 if (st < steps) {
                     B[i] = *(const u32x4 *)(wr + k);
-                    A[i] = *(const u32x4 *)(a.x + k);        // (every row of the operand is the token)
+                    A[i] = *(const u32x4 *)(xr + k);
                 }
             }
 #pragma unroll
@@ -410,54 +426,107 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
                 acc[i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A[i]),
                                                                      __builtin_bit_cast(bf16x8, B[i]), acc[i & 1], 0, 0, 0);
         }
-        if (lane < 16) {
-            part[wave][lane] = acc[0][0];
-            part[wave + MT_WAVES][lane] = acc[1][0];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 4 * g + r;
+            if (t < MT) {
+                part[wave][t][n] = acc[0][r];
+                part[wave + MT_WAVES][t][n] = acc[1][r];
+            }
         }
         __syncthreads();
-        if (tid < 16) {
-            float v = part[0][tid];
+        if (tid < 16 * T) {
+            const int t = tid >> 4, ee = blockIdx.x * 16 + n;
+            float v = part[0][t][n];
 #pragma unroll
-            for (int w = 1; w < RT_WAVES; ++w) v += part[w][tid];
-            if (a.L.router_bias && e < E) v += a.L.router_bias[e];
-            lg[tid] = v;
+            for (int w = 1; w < RT_WAVES; ++w) v += part[w][t][n];
+            if (a.L.router_bias && ee < E) v += a.L.router_bias[ee];
+            lg[t][n] = v;
         }
         __syncthreads();
         // two words of a copy per thread, a copy's run of 128 bytes by 8 neighbouring ones
-        if (tid < LOGIT_COPIES * 8) {
+        const int t = (tid >> 3) / per;
+        if (tid < LOGIT_COPIES * 8 && t < T) {
             const int q = tid & 7, e0 = blockIdx.x * 16 + 2 * q;
             uint32_t *dst = ctl + LOGIT_BASE + (tid >> 3) * LOGIT_STRIDE + 2 * e0;
             if (e0 + 1 < NE)
-                st_dev128(dst, (u32x4){__float_as_uint(lg[2 * q]), tag, __float_as_uint(lg[2 * q + 1]), tag});
+                st_dev128(dst, (u32x4){__float_as_uint(lg[t][2 * q]), tag, __float_as_uint(lg[t][2 * q + 1]), tag});
             else if (e0 < NE)
-                st_dev64((uint64_t *)dst, __float_as_uint(lg[2 * q]) | ((uint64_t)tag << 32));
+                st_dev64((uint64_t *)dst, __float_as_uint(lg[t][2 * q]) | ((uint64_t)tag << 32));
         }
         return;
     }
     const int b = blockIdx.x - nR, nblk = a.L.I / 32, item = b / nblk, blk = b % nblk;
     const int nsh = a.L.has_shared ? 1 : 0, j = item - nsh;  // j: place among the chosen experts
     const bool sh = j < 0;
-    float w = 1.0f;
-    if (wave == 0 && (!sh || a.gated)) {
+    if constexpr (MT > 1) {
+        if (tid < 8) s_any[tid] = 0u;
+        __syncthreads();
+    }
+    if (wave < T && (!sh || a.gated)) {
         float gate;
-        const TopkOut tk = select_topk_from(ctl, (const uint64_t *)(ctl + LOGIT_BASE + (b % LOGIT_COPIES) * LOGIT_STRIDE), tag,
-                                            E, K, a.gated, &gate);
-        w = sh ? gate : __shfl(tk.w, j);
-        const int e = __shfl(tk.idx, sh ? 0 : j);
-        if (lane == 0) s_e = e;
-        if (blk == 0 && !sh && lane == 0) {                  // the lists that down reads
-            a.b.act[j] = mx_item(e, j, 0, 1);
-            a.b.pos[j * MX_TMAX] = (int16_t)j;
-            if (j == 0) *a.b.nact = K;
+        const TopkOut tk = select_topk_from(
+            ctl, (const uint64_t *)(ctl + LOGIT_BASE + (wave * per + b % per) * LOGIT_STRIDE), tag, E, K, a.gated, &gate);
+        if (lane < K) {
+            s_idx[wave * K + lane] = tk.idx;
+            s_w[wave * K + lane] = tk.w;
+            if constexpr (MT > 1) atomicOr(&s_any[tk.idx >> 5], 1u << (tk.idx & 31));
         }
-        if (blk == 0 && j == 0 && lane < K) {
-            if (a.out_idx) a.out_idx[lane] = tk.idx;
-            if (a.out_w) a.out_w[lane] = tk.w;
-        }
+        if (lane == 0) s_gate[wave] = gate;
     }
     __syncthreads();
-    const int e = sh ? 0 : __builtin_amdgcn_readfirstlane(s_e);
-    gate_up_block(a, sx, s, blk, sh, e, 1, sh ? K : j, w);
+    int e = 0, cnt = T, pos = T * K + n;
+    float w = 1.0f;
+    if (sh) {
+        if (a.gated && tid < T) w = s_gate[tid];
+    } else {
+        int total = K;
+        if constexpr (MT == 1) {                             // (ascending already)
+            e = __builtin_amdgcn_readfirstlane(s_idx[j]);
+            pos = j;
+        } else {
+            // the j-th expert of the union, and which choices (token t's k-th: t K + k) are of it
+            uint32_t word = 0;
+            int k = 0, base = 0;
+            total = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = __builtin_amdgcn_readfirstlane(s_any[i]);
+                const int c = __popc(u);
+                if (j >= total && j < total + c) {
+                    word = u;
+                    k = j - total;
+                    base = 32 * i;
+                }
+                total += c;
+            }
+            if (j >= total) return;
+            for (; k > 0; --k) word &= word - 1;
+            e = base + __builtin_ctz(word);
+            constexpr int Q = (MT * 16 + 63) / 64;
+            cnt = 0;
+            pos = 0;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int i = 64 * q + lane;
+                for (uint64_t m = __ballot(i < T * K && s_idx[i] == e); m; m &= m - 1) {
+                    if (n == cnt) pos = 64 * q + __builtin_ctzll(m);
+                    ++cnt;
+                }
+            }
+        }
+        if (tid < cnt) w = s_w[pos];
+        if (blk == 0 && wave == 0) {                         // the lists that down reads
+            if (lane < cnt) a.b.pos[j * MX_TMAX + lane] = (int16_t)pos;
+            if (lane == 0) a.b.act[j] = mx_item(e, j, 0, cnt);
+            if (lane == 0 && j == 0) *a.b.nact = total;
+        }
+        if (blk == 0 && j == 0 && tid < T * K) {
+            if (a.out_idx) a.out_idx[tid] = s_idx[tid];
+            if (a.out_w) a.out_w[tid] = s_w[tid];
+        }
+    }
+    gate_up_block(a, sx, s, blk, sh, e, cnt, pos, w);
 }
 
 // ----------------------------------------------------------------------------- down
@@ -491,7 +560,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     int it = z * W + wave;
     fetch(it);
     // (the launch before is complete: the generation its logits were tagged with is used up)
-    if (a.token && blockIdx.x == 0 && z == 0 && tid == 0) st_agent(a.b.ctl + CTL_GEN, call_tag(a.b.ctl));
+    if (a.tagged && blockIdx.x == 0 && z == 0 && tid == 0) st_agent(a.b.ctl + CTL_GEN, call_tag(a.b.ctl));
     const int items = (*a.b.nact + nsh) * KQ;
     if (it < items) fetch_pos(it);
     for (int i = lane; i < T * C; i += 64) mine[i] = 0.0f;
@@ -635,13 +704,14 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     const DownPlan d = down_plan(L, T);
     a.shares = d.shares;
     a.route_only = route_only;
-    a.token = T == 1 && !route_only;
+    a.tagged = T <= TOKEN_MAX && !route_only;
     const unsigned nR = (unsigned)((L.E + a.gated + 15) / 16);
     const size_t gu_x = (size_t)(T < 16 ? T : 16) * GU_PITCH, gu_red = MT_WAVES * 2048, gu_lds = gu_x > gu_red ? gu_x : gu_red;
     hipError_t e;
-    if (a.token) {
-        hipLaunchKernelGGL(k_mx_token, dim3(nR + (unsigned)(L.I / 32 * (L.K + (L.has_shared ? 1 : 0)))), dim3(MT_THREADS),
-                           gu_lds, s, a, (int)nR);
+    if (a.tagged) {
+        const dim3 grid(nR + (unsigned)(L.I / 32 * (T * L.K + (L.has_shared ? 1 : 0))));
+        if (T == 1) hipLaunchKernelGGL(k_mx_token<1>, grid, dim3(MT_THREADS), gu_lds, s, a, (int)nR);
+        else hipLaunchKernelGGL(k_mx_token<TOKEN_MAX>, grid, dim3(MT_THREADS), gu_lds, s, a, (int)nR);
     } else {
         hipLaunchKernelGGL(k_mx_route, dim3(nR, (unsigned)((T + 15) / 16)), dim3(RT_THREADS), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess || route_only) return e;

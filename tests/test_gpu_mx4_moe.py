@@ -291,6 +291,53 @@ def test_token_state(torch, qs):
     assert int(qs.moe_workspace_status(ws)) == 0
 
 
+def test_few_token_state(torch, qs):
+    """The same for two to four tokens, which share the copies of the logit words, and calls of other
+    sizes in between: one workspace, across the wrap of the tag."""
+    L = ref.Layer(hidden=2048, inter=128, n_experts=256, top_k=8, seed=22, gated=True)
+    desc = upload(L, torch, qs)
+    Ts = (1, 2, 4, 3, 5)
+    xbs = [syn.make_x(T, L.hidden, seed=50 + T) for T in Ts]
+    xs = [to_dev(b, torch) for b in xbs]
+    want = [run(torch, qs, desc, x) for x in xs]
+    for T, xb, (y, idx, w) in zip(Ts, xbs, want):
+        check(L, xb, y, idx, w, T)
+    ws = qs.new_workspace(desc, max(Ts))
+    w32 = ws[:1024].view(torch.int32)
+    w32[64] = -7                                                 # the generation: wraps in the second turn
+    for i in range(40):
+        y, idx, w = run(torch, qs, desc, xs[i % 5], workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip((y, idx, w), want[i % 5])), i
+    assert int(qs.moe_workspace_status(ws)) == 0
+    w32[32] = 1                                                  # at most one more poll
+    for i in (1, 2, 3):
+        qs.moe_layer_forward(desc, xs[i], workspace=ws)
+    torch.cuda.synchronize()
+    assert int(qs.moe_workspace_status(ws, clear=True)) in (0, qs.MOE_WS_ERR_DECODE_WAIT)
+    w32[32] = 0
+    for i in (3, 2, 1):
+        y, idx, w = run(torch, qs, desc, xs[i], workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip((y, idx, w), want[i]))
+    assert int(qs.moe_workspace_status(ws)) == 0
+
+
+@pytest.mark.parametrize("name", sorted(LAYERS))
+@pytest.mark.parametrize("T", [2, 3, 4])
+def test_few_tokens_share_experts(torch, qs, name, T):
+    """Two to four tokens, the first and last alike: experts of one and of several tokens."""
+    L = layer(name)
+    desc = upload(L, torch, qs)
+    xb = syn.make_x(T, L.hidden, seed=60 + T)
+    xb[T - 1] = xb[0]
+    ws = qs.new_workspace(desc, T)
+    for _ in range(2):
+        y, idx, w = run(torch, qs, desc, to_dev(xb, torch), workspace=ws)
+        check(L, xb, y, idx, w, (name, T))
+        assert torch.equal(y[0], y[T - 1])
+    i2, w2 = qs.moe_route(desc, to_dev(xb, torch), workspace=ws)
+    assert torch.equal(i2, idx) and torch.equal(w2, w)
+
+
 def test_side_stream_and_empty(torch, qs):
     L = layer("tiny")
     desc = upload(L, torch, qs)
