@@ -350,7 +350,8 @@ moe_status mx4_pack_rows16(const void *codes, const void *scales, int64_t rows, 
 
 /*
  * Products with an MX4 weight matrix in MX4_TILES (N rows, K columns), fp32 accumulation:
- *     mx4_gemm        y[t][n] = sum_c x[t][c] W[n][c],  x [T][K] bf16, row stride ldx
+ *     mx4_gemm        y[t][n] = sum_c x[t][c] W[n][c],  x [T][K] bf16, row stride ldx (at most
+ *                     2^27, else MOE_ERR_UNSUPPORTED)
  *     mx4_gemm_mx4x   the same with x quantized: x_codes, x_scales hold T rows in MX4_TILES
  *   y   [T][N], row stride ldy, y_dtype MOE_BF16 (rounded to nearest even) or MOE_F32
  *   ws  device workspace of ws_bytes >= mx4_gemm_workspace_size(N, K, T) (NULL when that is

@@ -378,6 +378,7 @@ moe_status scratch_for_current_device(void **out) {
 
 // ------------------------------------------------------------------------------ MX4
 constexpr int64_t MX4_MAX_ROWS = 1 << 26, MX4_MAX_K = 65536;
+constexpr int64_t MX4_MAX_LDX = 1 << 27;          // (32-bit offsets into eight rows of x)
 
 moe_status check_mx4(int64_t rows, int64_t K, int32_t layout) {
     if (rows < 0 || K < 0 || (layout != MX4_ROWS && layout != MX4_TILES)) return MOE_ERR_INVALID;
@@ -631,6 +632,7 @@ moe_status mx4_gemm(const void *w_codes, const void *w_scales, int64_t N, int64_
     moe_status s = check_mx4_product(w_codes, w_scales, N, K, T, y, y_dtype, ldy, ws, ws_bytes);
     if (s || T == 0 || N == 0) return s;
     if ((s = check_values(x, MOE_BF16, K, ldx))) return s;
+    if (ldx > MX4_MAX_LDX) return MOE_ERR_UNSUPPORTED;
     return dev(launch_mx4_gemm((const uint8_t *)w_codes, (const uint8_t *)w_scales, N, K, (const uint16_t *)x, T, ldx, y,
                                y_dtype, ldy, (uint8_t *)ws, (hipStream_t)stream));
 }

@@ -119,43 +119,39 @@ hipError_t launch_skinny(GemmArgs a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------- many tokens
-// Bound by the matrix cores: WM x WN waves, each FM x FN fragments of 32 tokens x 32 weight
-// rows (v_mfma 32x32, the weights as first operand so that a lane's registers are neighbouring
-// columns of y).  Operands go global -> LDS by direct-to-LDS loads in a ring of three stages, so
-// that two steps are in flight while one is multiplied; one barrier a step.  Where WM is 1 no
-// other wave multiplies a wave's weight rows: it loads them straight into registers, two steps
-// ahead, which takes a quarter (bf16 x) to nearly half (MX4 x) off the LDS traffic (4096 x 16384
-// x 2048: bf16 x 242 -> 209 us, MX4 x 97 -> 77).
+// Bound by the matrix cores: four waves, each FM x FN fragments of 32 tokens x 32 weight rows
+// (v_mfma 32x32, the weights as first operand so that a lane's registers are neighbouring columns
+// of y).  The waves split the weight rows and share the tokens: activations go global -> LDS by
+// direct-to-LDS loads in a ring of three stages, each wave's weights, which no other multiplies,
+// straight into its registers, both two steps ahead; one barrier a step.  Against weights through
+// LDS too: 4096 x 16384 x 2048 in large tiles 242 -> 209 us with bf16 x and 97 -> 77 with MX4 x,
+// 128 x 16384 x 2048 in small ones 15.5 -> 12.4 and 7.1 -> 6.1 (two waves to a weight row before).
 //   bf16 x: a step is 64 columns.  128 bytes of a token's row, its eight 16-byte chunks XORed
 //     by (row / 2) % 8: a 16-byte LDS read is served 16 lanes a cycle, those of one wave half
 //     with equal parity of lane bits 2..4 (measured), and under this key they fall in 64
-//     distinct banks.  Half a weight tile (512 bytes) is one such run already.
-//   MX4 x: a step is 128 columns of both operands' tiles.
+//     distinct banks.
+//   MX4 x: a step is 128 columns, a tile of each panel of x as it lies in memory.
 // Rates: 4096 x 16384 x 2048 196 to 209 us with bf16 x (1.3 to 1.4 PFLOP/s, a library bf16 product of
 // the shape takes 194 to 213), 69 to 77 with MX4 x (3.6 to 4.0); 4096 x 16384 x 8192 4.25 PFLOP/s with
 // MX4 x, where the loop without any of its loads from memory reaches 4.6.
 // Scales come a quad (512 columns) at a time; every wave has them in registers a step later, long
 // before the next quad's arrive in their place.
-template <bool MX, int WM, int WN, int FM, int FN>
+constexpr int NW = 4;                                        // waves of a tile's workgroup
+template <bool MX, int FM, int FN>
 struct Tiled {
-    static constexpr int NW = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
+    static constexpr int BM = 32 * FM, BN = 32 * FN * NW;
     static constexpr int STEP = MX ? 128 : 64;                        // columns
     static constexpr int PER_Q = 512 / STEP;                          // steps per quad of scales
-    static constexpr int A_BYTES = MX ? BM * 64 : BM * 128, B_BYTES = MX ? BN * 64 : BN * 32;
-    static constexpr int STAGE = A_BYTES + (WM == 1 ? 0 : B_BYTES), NSTAGE = 3;
+    static constexpr int STAGE = MX ? BM * 64 : BM * 128, NSTAGE = 3;  // of activations
     static constexpr int SC_BYTES = (MX ? BM * 16 : 0) + BN * 16;     // of a quad
-    // a wave whose weight rows no other wave multiplies (WM = 1) loads them straight into registers
-    static constexpr bool DIRECT = WM == 1;
-    static constexpr int B_STEP = MX ? MX_TILE : MX_TILE / 2;         // bytes of a panel
-    static constexpr int BL = FN * (MX ? 2 : 1);                      // such loads of a step
-    static constexpr int A_DMA = A_BYTES / (1024 * NW), B_DMA = DIRECT ? 0 : B_BYTES / (1024 * NW);
-    static constexpr int DMA = A_DMA + (DIRECT ? BL : B_DMA);         // loads per wave and step
-    static constexpr int SDMA = SC_BYTES / (256 * NW);                // per wave and quad
+    static constexpr int B_STEP = MX ? MX_TILE : MX_TILE / 2;         // bytes of a weight panel
+    // per wave: 16-byte loads of activations and of weights a step, of scales a quad
+    static constexpr int A_DMA = STAGE / (1024 * NW), BL = FN * (MX ? 2 : 1);
+    static constexpr int XS = MX ? BM / (16 * NW) : 0, WS = BN / (16 * NW), SDMA = XS + WS;
     static constexpr int EP = 32 * (FN * 32 * 4 + 16);                // epilogue staging of a wave
     static constexpr int RING = NSTAGE * STAGE + SC_BYTES;
     static constexpr int LDS = RING > NW * EP ? RING : NW * EP;
-    static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "whole loads per wave");
-    static_assert(SC_BYTES % (256 * NW) == 0, "whole loads per wave");
+    static_assert(STAGE % (1024 * NW) == 0 && (!MX || BM % (16 * NW) == 0), "whole loads per wave");
 };
 
 // Epilogue of a wave: 32 tokens at a time through its LDS area ep, then whole 16-byte pieces of
@@ -205,9 +201,9 @@ __device__ __forceinline__ void tiled_store(const f32x16 (&acc)[FN][FM], uint8_t
     }
 }
 
-template <bool MX, int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void k_mx4_tiled(GemmArgs a) {
-    using C = Tiled<MX, WM, WN, FM, FN>;
+template <bool MX, int FM, int FN>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_mx4_tiled(GemmArgs a) {
+    using C = Tiled<MX, FM, FN>;
     __shared__ __attribute__((aligned(1024))) uint8_t sm[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int r32 = lane & 31, h = lane >> 5;
@@ -219,7 +215,6 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     const int ng = id / (8 * mtiles), gw = ntiles - 8 * ng < 8 ? ntiles - 8 * ng : 8;
     const int rem = id - ng * 8 * mtiles;
     const int t0 = rem / gw * C::BM, n0 = (8 * ng + rem % gw) * C::BN;
-    const int wm = wave / WN, wn = wave % WN;
 
     const int steps = (a.K + C::STEP - 1) / C::STEP;
     // this workgroup's share of the steps (whole quads)
@@ -227,69 +222,62 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     const int k_lo = blockIdx.y * qper * C::PER_Q;
     const int k_hi = k_lo + qper * C::PER_Q < steps ? k_lo + qper * C::PER_Q : steps;
 
-    // ---- sources of this wave's loads: x, the weights and the scales, from the workgroup's first row on
+    // ---- sources of this wave's loads
     const int xp0 = t0 / 16, xpl = (a.T + 15) / 16 - 1, wp0 = n0 / 16;      // panels (xpl: the last of x)
-    const uint8_t *xbase = MX ? a.xc + (int64_t)xp0 * a.KS * MX_TILE : (const uint8_t *)(a.x + t0 * a.ldx);
-    const uint8_t *wbase = a.wc + (int64_t)wp0 * a.KS * MX_TILE;
-    const uint8_t *xsbase = MX ? a.xs + (int64_t)xp0 * a.KQ * MX_QS : nullptr, *wsbase = a.ws + (int64_t)wp0 * a.KQ * MX_QS;
     auto wpanel = [&](int p) __attribute__((always_inline)) { return wp0 + p < a.P ? p : a.P - 1 - wp0; };
     auto xpanel = [&](int p) __attribute__((always_inline)) { return xp0 + p <= xpl ? p : xpl - xp0; };
-    // piece i of a stage: 1024 bytes; offsets from xbase (DIRECT: below 2^31, see choose)
-    int64_t aoff[C::A_DMA];
+    // activations: piece i of a stage is 1024 bytes, through a resource of its own
+    __amdgpu_buffer_rsrc_t abuf[C::A_DMA];
+    uint32_t aoff[C::A_DMA];
     int kmax[C::A_DMA];                     // bf16 x: the last column offset at which the chunk is whole
 #pragma unroll
     for (int i = 0; i < C::A_DMA; ++i) {
         const int piece = wave * C::A_DMA + i;
         if constexpr (MX) {
-            aoff[i] = (int64_t)xpanel(piece) * a.KS * MX_TILE + 16 * lane;
+            abuf[i] = buffer_from(a.xc + (int64_t)(xp0 + xpanel(piece)) * a.KS * MX_TILE);
+            aoff[i] = 16 * lane;
             kmax[i] = 0;
-        } else {
-            const int row = 8 * piece + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-            aoff[i] = (t0 + row < a.T ? row : a.T - 1 - t0) * a.ldx * 2 + 16 * c;
+        } else {                            // eight rows (past the last: that one again)
+            const int first = min(t0 + 8 * piece, a.T - 1), row = 8 * piece + (lane >> 3);
+            const int c = (lane & 7) ^ ((row >> 1) & 7);
+            abuf[i] = buffer_from(a.x + first * a.ldx);
+            aoff[i] = (uint32_t)(min(t0 + row, a.T - 1) - first) * (uint32_t)(2 * a.ldx) + 16 * c;
             kmax[i] = a.K - 8 * c - 8;
         }
     }
-    const uint8_t *bsrc[C::DIRECT ? FN : C::B_DMA];
+    const uint8_t *bsrc[FN];                // weights of the next step, by fragment
 #pragma unroll
-    for (int i = 0; i < (C::DIRECT ? FN : C::B_DMA); ++i) {
-        // DIRECT: fragment i of the wave, the next step's; else (bf16 x: half a tile of two panels)
-        const int piece = wave * C::B_DMA + i;
-        const int p = C::DIRECT ? 2 * (wn * FN + i) + (r32 >> 4) : MX ? piece : 2 * piece + h;
-        bsrc[i] = wbase + (int64_t)wpanel(p) * a.KS * MX_TILE +
-                  16 * (C::DIRECT ? (r32 & 15) + 16 * h : MX ? lane : r32) + (C::DIRECT ? (int64_t)k_lo * C::B_STEP : 0);
-    }
+    for (int j = 0; j < FN; ++j)
+        bsrc[j] = a.wc + (int64_t)(wp0 + wpanel(2 * (wave * FN + j) + (r32 >> 4))) * a.KS * MX_TILE +
+                  16 * ((r32 & 15) + 16 * h) + (int64_t)k_lo * C::B_STEP;
     // scales, 256 bytes (a panel) a piece: XS of x, then WS of the weights
-    constexpr int XS = MX ? C::BM / (16 * C::NW) : 0, WS = C::BN / (16 * C::NW);
-    static_assert(XS + WS == C::SDMA && (!MX || C::BM % (16 * C::NW) == 0), "whole pieces of either");
+    const __amdgpu_buffer_rsrc_t xsbuf = buffer_from(MX ? a.xs + (int64_t)xp0 * a.KQ * MX_QS : a.ws);
+    const __amdgpu_buffer_rsrc_t wsbuf = buffer_from(a.ws + (int64_t)wp0 * a.KQ * MX_QS);
     int soff[C::SDMA];
 #pragma unroll
     for (int i = 0; i < C::SDMA; ++i)
-        soff[i] = (i < XS ? xpanel(wave * XS + i) : wpanel(wave * WS + i - XS)) * a.KQ * MX_QS + 4 * lane;
+        soff[i] = (i < C::XS ? xpanel(wave * C::XS + i) : wpanel(wave * C::WS + i - C::XS)) * a.KQ * MX_QS + 4 * lane;
     auto issue = [&](int k, int s) __attribute__((always_inline)) {   // step k, the s-th of its quad
         uint8_t *st = sm + (k % C::NSTAGE) * C::STAGE;
 #pragma unroll
         for (int i = 0; i < C::A_DMA; ++i) {
             // (bf16 x: columns past K meet zero weights, any value of the row will do)
-            const int off = C::STEP * k, col = MX ? k * MX_TILE : 2 * (off <= kmax[i] ? off : kmax[i]);
-            uint8_t *d = st + (wave * C::A_DMA + i) * 1024;
-            if constexpr (C::DIRECT) dma16_buffer(buffer_from(xbase), d, (uint32_t)aoff[i] + (MX ? 0 : col), MX ? col : 0);
-            else dma16(xbase + aoff[i] + col, d);
+            const int off = C::STEP * k;
+            dma16_buffer(abuf[i], st + (wave * C::A_DMA + i) * 1024,
+                         MX ? aoff[i] : aoff[i] + 2 * (off <= kmax[i] ? off : kmax[i]), MX ? k * MX_TILE : 0);
         }
-#pragma unroll
-        for (int i = 0; i < C::B_DMA; ++i)
-            dma16(bsrc[i] + (int64_t)k * C::B_STEP, st + C::A_BYTES + (wave * C::B_DMA + i) * 1024);
         if (s % C::PER_Q == 0) {
             const int q = k / C::PER_Q * MX_QS;
             uint8_t *ss = sm + C::NSTAGE * C::STAGE;
 #pragma unroll
-            for (int i = 0; i < C::SDMA; ++i) {
-                uint8_t *d = ss + (i < XS ? (wave * XS + i) * 256 : (MX ? C::BM * 16 : 0) + (wave * WS + i - XS) * 256);
-                if constexpr (C::DIRECT) dma4_buffer(buffer_from(i < XS ? xsbase : wsbase), d, soff[i], q);
-                else dma4((i < XS ? xsbase : wsbase) + soff[i] + q, d);
-            }
+            for (int i = 0; i < C::SDMA; ++i)
+                dma4_buffer(i < C::XS ? xsbuf : wsbuf,
+                            ss + (i < C::XS ? (wave * C::XS + i) * 256
+                                            : (MX ? C::BM * 16 : 0) + (wave * C::WS + i - C::XS) * 256),
+                            soff[i], q);
         }
     };
-    u32x4 bq[2][C::BL];                                      // DIRECT: by the step's parity
+    u32x4 bq[2][C::BL];                                      // weights, by the step's parity
     auto load_b = [&](u32x4 (&b)[C::BL]) __attribute__((always_inline)) {   // of the next step
 #pragma unroll
         for (int i = 0; i < C::BL; ++i) b[i] = *(const u32x4 *)(bsrc[MX ? i >> 1 : i] + (MX ? 512 * (i & 1) : 0));
@@ -310,14 +298,14 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     auto load_scales = [&]() __attribute__((always_inline)) {
         const uint8_t *ss = sm + C::NSTAGE * C::STAGE;
         const int e = (r32 >> 4) * 256 + 4 * ((r32 & 15) + 16 * h);
-        const uint8_t *sb = ss + (MX ? C::BM * 16 : 0) + wn * FN * 512 + e;
+        const uint8_t *sb = ss + (MX ? C::BM * 16 : 0) + wave * FN * 512 + e;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             sw[j][0] = *(const uint32_t *)(sb + 512 * j);
             sw[j][1] = *(const uint32_t *)(sb + 512 * j + 128);
         }
         if constexpr (MX) {
-            const uint8_t *sa = ss + wm * FM * 512 + e;
+            const uint8_t *sa = ss + e;
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 sx[i][0] = *(const uint32_t *)(sa + 512 * i);
@@ -329,15 +317,15 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     auto sync_step = [&](int k, int s, bool ahead) __attribute__((always_inline)) {
         // stage k has landed once at most stage k + 1's loads are outstanding
         if (!ahead && k + 1 >= k_hi) wait_dma<0>();
-        else if ((s + 1) % C::PER_Q == 0) wait_dma<C::DMA + C::SDMA>();
-        else wait_dma<C::DMA>();
+        else if ((s + 1) % C::PER_Q == 0) wait_dma<C::A_DMA + C::BL + C::SDMA>();
+        else wait_dma<C::A_DMA + C::BL>();
         block_sync();
         if (ahead) issue(k + 2, s + 2);
     };
 
     auto start = [&](int s) __attribute__((always_inline)) {
         issue(k_lo + s, s);
-        if constexpr (C::DIRECT) load_b(bq[s]);
+        load_b(bq[s]);
         __builtin_amdgcn_sched_barrier(0);                   // (and the next step's after these)
     };
     // step k, the s-th of its quad
@@ -350,36 +338,26 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
             const int e = (r32 >> 4) * MX_TILE + 16 * ((r32 & 15) + 16 * h);
 #pragma unroll
             for (int f = 0; f < 2; ++f) {                    // columns 64 f .. 64 f + 63 of the step
-                u32x4 A[FM], B[FN];
+                u32x4 A[FM];
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    if constexpr (C::DIRECT) B[j] = bk[2 * j + f];
-                    else B[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 2 * MX_TILE + e + 512 * f);
-                }
-#pragma unroll
-                for (int i = 0; i < FM; ++i) A[i] = *(const u32x4 *)(st + (wm * FM + i) * 2 * MX_TILE + e + 512 * f);
+                for (int i = 0; i < FM; ++i) A[i] = *(const u32x4 *)(st + i * 2 * MX_TILE + e + 512 * f);
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) acc[j][i] = mx_mfma32(B[j], A[i], acc[j][i], s, sw[j][f], sx[i][f]);
+                    for (int j = 0; j < FN; ++j) acc[j][i] = mx_mfma32(bk[2 * j + f], A[i], acc[j][i], s, sw[j][f], sx[i][f]);
             }
         } else {
             if (s == 0) load_scales();
-            u32x4 b[FN];
             float sc[FN];
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (C::DIRECT) b[j] = bk[j];
-                else b[j] = *(const u32x4 *)(st + C::A_BYTES + (wn * FN + j) * 1024 + (r32 >> 4) * 512 + 16 * ((r32 & 15) + 16 * h));
-                sc[j] = mx_scale(sw[j][s & 1], s >> 1);
-            }
+            for (int j = 0; j < FN; ++j) sc[j] = mx_scale(sw[j][s & 1], s >> 1);
             // columns 32 h + 8 m .. + 7: x of m + 1 is read while m is multiplied
             bf16x8 A[2][FM];
             auto load_a = [&](int m) __attribute__((always_inline)) {
                 const int pos = (4 * h + m) ^ ((r32 >> 1) & 7);
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
-                    A[m & 1][i] = *(const bf16x8 *)(st + ((wm * FM + i) * 32 + r32) * 128 + 16 * pos);
+                    A[m & 1][i] = *(const bf16x8 *)(st + (32 * i + r32) * 128 + 16 * pos);
             };
             load_a(0);
 #pragma unroll
@@ -387,7 +365,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
                 if (m < 3) load_a(m + 1);
                 bf16x8 B[FN];
 #pragma unroll
-                for (int j = 0; j < FN; ++j) B[j] = mx_bf16(b[j][m], sc[j]);
+                for (int j = 0; j < FN; ++j) B[j] = mx_bf16(bk[j][m], sc[j]);
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -396,8 +374,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
                 __builtin_amdgcn_sched_barrier(0);           // (no reads of later columns drawn ahead)
             }
         }
-        if constexpr (C::DIRECT)
-            if (ahead) load_b(bk);
+        if (ahead) load_b(bk);
     };
     // Whole quads load two steps ahead without a condition, so that the compiler knows how many
     // loads are outstanding wherever it waits for one; what is left of K takes the last loop.
@@ -426,14 +403,14 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
         }
     block_sync();                                            // the ring is free
 
-    const int tw = t0 + wm * FM * 32, nw = n0 + wn * FN * 32;
+    const int nw = n0 + wave * FN * 32;
     if (a.shares > 1)
         tiled_store<true, true, FM, FN>(acc, sm + wave * C::EP, a.part + blockIdx.y * (a.T * part_pitch(a.N)),
-                                  part_pitch(a.N), a.T, a.N, tw, nw);
+                                  part_pitch(a.N), a.T, a.N, t0, nw);
     else if (a.y_dtype == MOE_F32)
-        tiled_store<true, false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
+        tiled_store<true, false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, t0, nw);
     else
-        tiled_store<false, false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, tw, nw);
+        tiled_store<false, false, FM, FN>(acc, sm + wave * C::EP, a.y, a.ldy, a.T, a.N, t0, nw);
 }
 
 // The shares' partial sums, in share order: a thread adds four columns, all shares' loads in
@@ -459,11 +436,11 @@ __global__ __launch_bounds__(256) void k_mx4_join(GemmArgs a) {
     }
 }
 
-template <bool MX, int WM, int WN, int FM, int FN>
+template <bool MX, int FM, int FN>
 hipError_t launch_tiled(GemmArgs a, hipStream_t s) {
-    using C = Tiled<MX, WM, WN, FM, FN>;
+    using C = Tiled<MX, FM, FN>;
     const int tiles = ((a.T + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN);
-    hipLaunchKernelGGL((k_mx4_tiled<MX, WM, WN, FM, FN>), dim3((tiles + 7) / 8 * 8, a.shares), dim3(64 * C::NW), 0, s, a);
+    hipLaunchKernelGGL((k_mx4_tiled<MX, FM, FN>), dim3((tiles + 7) / 8 * 8, a.shares), dim3(64 * NW), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.shares == 1) return e;
     const int64_t b = (a.T * (part_pitch(a.N) / 4) + 255) / 256, cap = 8 * (int64_t)n_compute_units();
@@ -495,25 +472,24 @@ GemmArgs make_args(const uint8_t *wc, const uint8_t *ws, int64_t N, int64_t K, i
 //   skinny  up to 16 tokens, bf16 x only while all of it can be staged at once (64 KB): beyond,
 //           staging between barriers costs more than reading the weights once saves
 //           (T = 16 x 16384 x 2048: 7.5 against 13.0 in tiles; T = 16 x 2048 x 8192: 30.5 against 10.9)
-//   large   tiles of 128 x 256, from 7/8 of a tile for every compute unit on and over 64 tokens
-//           (which one row of small tiles holds); times in large and in small tiles at 16384 x
-//           2048: T = 256, half the compute units, 27 and 20; T = 384, 3/4, 31 and 31; T = 512,
-//           one each, 34 and 39; T = 640, 47 and 45; T = 1024, two each, 58 and 74; at 65536 x
-//           2048: T = 40, 33 and 23; T = 70, 33 and 38
+//   large   tiles of 128 x 256, two workgroups a compute unit, if they fill their last round of the
+//           device to 7/8 on average, and over 64 tokens (which one row of small tiles holds); times
+//           in large and in small tiles at 16384 x 2048: T = 512, half a round, 35 and 33; T = 768,
+//           3/4, 52 and 48; T = 1024, one round, 59 and 62 (MX4 x: 23 and 27); T = 1152 78 and 70
 //   small   tiles of 64 x 128, and where those are fewer than the compute units, the columns
 //           split into shares of at least one quad (T = 37 x 2048 x 8192: 11.4 with 16 shares,
-//           12.7 with 8; T = 20 x 2048 x 2048: 8.9 with 4, 11.4 with 2).
+//           12.7 with 8; T = 128 x 16384 x 2048, a tile per compute unit, 12.4, halved 22)
 enum Plan { SKINNY, SMALL, LARGE };
 struct Choice {
     Plan plan;
     int shares;
 };
-static Choice choose(bool mx, int64_t T, int64_t N, int64_t K, int64_t ldx = 0) {
+static Choice choose(bool mx, int64_t T, int64_t N, int64_t K) {
     if (T <= 16 && (mx || T * mx4_quads(K) <= 64)) return {SKINNY, 1};
     const int64_t cu = n_compute_units();
     auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((N + n - 1) / n); };
-    // (ldx: rows of x within 2^31 bytes of the tile's first, for its 32-bit offsets)
-    if (T > 64 && 8 * tiles(128, 256) >= 7 * cu && ldx <= (int64_t)1 << 23) return {LARGE, 1};
+    const int64_t large = tiles(128, 256), round = 2 * cu;
+    if (T > 64 && 8 * large >= 7 * ((large + round - 1) / round * round)) return {LARGE, 1};
     int64_t sh = cu / tiles(64, 128), most = mx4_quads(K);
     if (sh > most) sh = most;
     if (sh > MAX_SHARES) sh = MAX_SHARES;
@@ -534,12 +510,12 @@ size_t mx4_gemm_ws(int64_t T, int64_t N, int64_t K) {
 
 template <bool MX>
 static hipError_t launch_product(GemmArgs a, uint8_t *ws, hipStream_t s) {
-    const Choice c = choose(MX, a.T, a.N, a.K, MX ? 0 : a.ldx);
+    const Choice c = choose(MX, a.T, a.N, a.K);
     a.shares = c.shares;
     a.part = (float *)ws;
     if (c.plan == SKINNY) return launch_skinny<MX>(a, s);
-    if (c.plan == SMALL) return launch_tiled<MX, 2, 2, 1, 2>(a, s);
-    return launch_tiled<MX, 1, 4, 4, 2>(a, s);
+    if (c.plan == SMALL) return launch_tiled<MX, 2, 1>(a, s);
+    return launch_tiled<MX, 4, 2>(a, s);
 }
 
 hipError_t launch_mx4_gemm(const uint8_t *wc, const uint8_t *wsc, int64_t N, int64_t K, const uint16_t *x, int64_t T,

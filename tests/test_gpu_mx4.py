@@ -232,6 +232,17 @@ def test_gemm_rows_far_apart(torch, qs, ldx):
     check(qs.mx4_gemm(wc, ws, N, K, xb[:, :K]), xv @ w.T, ref.product_bound(xv, w), "f32")
 
 
+@pytest.mark.parametrize("T", [9, 21])
+def test_gemm_rows_at_the_limit_apart(torch, qs, T):
+    N, K, ldx = 210, 160, 2 ** 27
+    w, wc, ws = weights(N, K, 10, torch, qs)
+    x = activations(T, K, 11, torch)
+    xb = torch.empty(T * ldx, dtype=torch.bfloat16, device="cuda").view(T, ldx)
+    xb[:, :K] = x
+    xv = np64(x)
+    check(qs.mx4_gemm(wc, ws, N, K, xb[:, :K]), xv @ w.T, ref.product_bound(xv, w), "f32")
+
+
 @pytest.mark.parametrize("T", [1, 6, 40, 300])
 def test_gemm_strides_and_guards(torch, qs, T):
     """Rows of x and y inside wider buffers; what lies beside and behind y is left as it was."""

@@ -76,6 +76,10 @@ def test_pointers_and_strides():
     assert gemm(ldx=60) == INV and gemm(ldx=68) == INV and gemm(ldy=31) == INV and gemm_mx4x(ldy=31) == INV
 
 
+def test_rows_of_x_too_far_apart():
+    assert gemm(ldx=(1 << 27) + 8) == UNS and gemm(ldx=(1 << 27) + 8, T=0) == q.MOE_OK
+
+
 def test_overlapping_repack_is_refused():
     """Sources and destinations of the repack, and its two destinations, must be apart."""
     n = q.lib().mx4_codes_size(32, 64, q.MX4_ROWS)
