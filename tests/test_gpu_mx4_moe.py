@@ -168,16 +168,16 @@ def test_workspace_shared_with_affine_layers_and_graph_replays(torch, qs):
     af = qs.LayerDesc.from_host(A)
     n = max(qs.moe_workspace_size(mx, 170), qs.moe_workspace_size(af, 40))
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
-    xm = {T: to_dev(syn.make_x(T, L.hidden, seed=T), torch) for T in (1, 6, 30, 170)}
+    xm = {T: to_dev(syn.make_x(T, L.hidden, seed=T), torch) for T in (1, 3, 6, 30, 100, 170)}
     xa = {T: to_dev(syn.make_x(T, A.hidden, seed=T), torch) for T in (1, 3, 40)}
     rm = {T: qs.moe_layer_forward(mx, x, workspace=qs.new_workspace(mx, T)) for T, x in xm.items()}
     ra = {T: qs.moe_layer_forward(af, x, workspace=qs.new_workspace(af, T)) for T, x in xa.items()}
     outs = {("m", T): torch.empty_like(r) for T, r in rm.items()} | {("a", T): torch.empty_like(r) for T, r in ra.items()}
 
     def every():
-        for T in (1, 30, 6, 170):
+        for T in (1, 30, 3, 6, 100, 170):
             qs.moe_layer_forward(mx, xm[T], y=outs["m", T], workspace=ws)
-            Ta = {1: 3, 30: 1, 6: 40, 170: 1}[T]
+            Ta = {1: 3, 30: 1, 3: 3, 6: 40, 100: 1, 170: 1}[T]
             qs.moe_layer_forward(af, xa[Ta], y=outs["a", Ta], workspace=ws)
 
     def same():
@@ -390,11 +390,12 @@ def test_not_finite_tokens_stay_alone(torch, qs, T, value):
     check(L, xb, y2, i2, w2, T)
 
 
-def test_two_streams_two_workspaces(torch, qs):
+@pytest.mark.parametrize("Ts", [(1, 7), (2, 4), (3, 128), (1, 200)])
+def test_two_streams_two_workspaces(torch, qs, Ts):
     """Calls that overlap in time, each on its own stream and workspace, give what they give alone."""
     L = layer("skew")
     desc = upload(L, torch, qs)
-    xs = [to_dev(syn.make_x(T, L.hidden, seed=40 + T), torch) for T in (1, 7)]
+    xs = [to_dev(syn.make_x(T, L.hidden, seed=40 + T), torch) for T in Ts]
     ws = [qs.new_workspace(desc, x.shape[0]) for x in xs]
     want = [qs.moe_layer_forward(desc, x, workspace=w).clone() for x, w in zip(xs, ws)]
     ys = [torch.empty((20,) + tuple(y.shape), device="cuda") for y in want]
