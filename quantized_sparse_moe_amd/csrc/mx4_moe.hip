@@ -6,7 +6,7 @@
 //            of tokens last -- counted, so nothing ever waits -- takes their top-k, and the
 //            last of those lists the experts any token chose (ascending) and each one's
 //            tokens.
-//   gate/up  one workgroup per (listed expert, 32 columns of h): gathers the expert's tokens
+//   gate/up  one workgroup per (listed expert, 32 or 16 columns of h): gathers the expert's tokens
 //            as the rows of the activation operand, so each expert's weights are read once
 //            however many tokens chose it, and an expert that one token chose costs one
 //            16-row tile.  h = w silu(g) u carries the token's routing weight and leaves as the
@@ -21,12 +21,12 @@
 // All are bound by the weight stream: (union of the chosen experts + shared) x
 // 3 H I x 17/32 bytes, and at few tokens by the chain of launches and round trips before and
 // after it (2048 x 512, top 8 of 256 and a shared expert, times of the layer in a graph):
-//   T = 1 15.9 us (15 MB: 2.4 at 6.3 TB/s)   T = 2 20.1   T = 4 26.6 (53 MB: 8)   T = 7 36.8 (89 MB: 14)
+//   T = 1 15.9 us (15 MB: 2.4 at 6.3 TB/s)   T = 2 20.1   T = 4 26.4 (53 MB: 8)   T = 7 36.0 (89 MB: 14)
 //   T = 20 61 (209 MB: 33)   T = 32 73 (272 MB: 43)   T = 64 92 (370 MB: 59)
 //   T = 65 101   T = 128 123 (421 MB: 67)
 //   under a skewed router T = 48 49 (52 experts), T = 128 82 (76 experts)
 // From T = 7 on more experts cost 5.2 TB/s; about 20 us do not depend on them.  Of T = 7, route
-// takes 9.0, gate/up 16, down 12.  Every sum is fp32 in a fixed order; there are no float atomics.
+// takes 9, gate/up 15, down 12.  Every sum is fp32 in a fixed order; there are no float atomics.
 #include "decode_state.h"
 #include "mx4.h"
 
@@ -248,18 +248,20 @@ __device__ __forceinline__ int h_place(int block) { return (block >> 2) * 256 + 
 // -------------------------------------------------------------------------- gate/up
 // The tokens' rows of x are staged in LDS, 2048 columns at a time: read as MFMA operands from
 // global memory they are 64 separate 16-byte pieces a load, which costs the address unit four
-// times a contiguous one.  Two panels of 16 columns of h a workgroup: one is faster for few
-// tokens and slower for many (T = 7 36 against 37 us a layer, T = 20 68 against 61), four slower
-// throughout (39, 66); workgroups that loop over items, loading ahead, gain nothing (38, 61).
-constexpr int GU_QUADS = MT_WAVES / 2;                       // quads of a chunk: one per wave pair
+// times a contiguous one.  PN panels of 16 columns of h a workgroup, four waves each: with one, more
+// workgroups and their loads fit a compute unit, with two x is staged half as often (T = 7 35.9 and
+// 37.2 us a layer, T = 12 48.8 and 48.7, T = 20 67.7 and 60.8; four panels 39.0, 51.8, 66.3).
+// Workgroups that loop over items, loading ahead, gain nothing (T = 7 38, T = 20 61).
+constexpr int GU_QUADS = MT_WAVES / 2;                       // quads of a chunk: one per wave of a panel
 constexpr int GU_PITCH = GU_QUADS * 1024 + 16;               // bytes of a staged row (padded: banks)
 
-// One item's block of 32 columns of h, by one workgroup: expert e (sh: the shared one), its cnt
+// One item's block of 16 PN columns of h, by one workgroup: expert e (sh: the shared one), its cnt
 // tokens, the row of h of token lane % 16 in pos (every wave) and its weight in w (wave 0).
 struct GuShared {
     float w[16];
     int pos[16];
 };
+template <int PN>
 __device__ __forceinline__ void gate_up_block(const MxArgs &a, uint8_t *sx, GuShared &s, int blk, bool sh, int e, int cnt,
                                               int pos, float w) {
     // [cnt][GU_PITCH] of x, then the waves' sums in its place
@@ -272,8 +274,8 @@ __device__ __forceinline__ void gate_up_block(const MxArgs &a, uint8_t *sx, GuSh
     const uint8_t *us = (const uint8_t *)(sh ? a.L.s_up.scales : a.L.up.scales);
     const int64_t gst = sh ? a.L.s_gate.stride : a.L.gate.stride, ust = sh ? a.L.s_up.stride : a.L.up.stride;
     const int KS = (H + 127) >> 7, KQ = (KS + 3) >> 2;
-    const int pw = wave & 1, kg = wave >> 1;                 // 16-column panel, quad of a chunk
-    const int p = 2 * blk + pw;
+    const int pw = wave % PN, kg = wave / PN;                // 16-column panel, quad of a chunk
+    const int p = PN * blk + pw;
     const int64_t pg = (e * gst) / 16 + p, pu = (e * ust) / 16 + p;
     u32x4 bg[4], bu[4];
     uint32_t sg = 0, su = 0;
@@ -300,7 +302,7 @@ __device__ __forceinline__ void gate_up_block(const MxArgs &a, uint8_t *sx, GuSh
             if (q0 && q < KQ) load_w(q);                     // (the first is on its way)
             // a wave stages whole rows, 1 KB per load (columns past H meet zero weights: any value
             // of the row will do)
-            for (int i = wave; i < cnt * GU_QUADS; i += MT_WAVES) {
+            for (int i = wave; i < cnt * GU_QUADS; i += GU_QUADS * PN) {
                 const int row = i / GU_QUADS, c = i % GU_QUADS, ps = __builtin_amdgcn_readlane(pos, row);
                 const int t = sh ? ps - T * K : ps / K, k = min((q0 + c) * 512 + 8 * lane, H - 8);
                 *(u32x4 *)(sx + row * GU_PITCH + 1024 * c + 16 * lane) = *(const u32x4 *)(a.x + (int64_t)t * H + k);
@@ -325,34 +327,35 @@ __device__ __forceinline__ void gate_up_block(const MxArgs &a, uint8_t *sx, GuSh
         red[wave][0][lane] = ag;
         red[wave][1][lane] = au;
         __syncthreads();
-        // thread: token tid / 32, column tid % 32 of the block
-        const int tk = tid >> 5, c = tid & 31;
+        // thread: a token and a column
+        const int tk = tid / (16 * PN), cb = tid % (16 * PN), col = 16 * PN * blk + cb, c = col & 31;
         if (tk < cnt) {
-            const int l = (c & 15) + 16 * (tk >> 2), rr = tk & 3, w0 = c >> 4;
+            const int l = (cb & 15) + 16 * (tk >> 2), rr = tk & 3, w0 = cb >> 4;
             float gv = 0.0f, uv = 0.0f;
 #pragma unroll
-            for (int k = 0; k < MT_WAVES / 2; ++k) {
-                gv += red[w0 + 2 * k][0][l][rr];
-                uv += red[w0 + 2 * k][1][l][rr];
+            for (int k = 0; k < GU_QUADS; ++k) {
+                gv += red[w0 + PN * k][0][l][rr];
+                uv += red[w0 + PN * k][1][l][rr];
             }
             // h = w silu(g) u as the bf16 pair hi + lo
             const float h = silu(gv) * uv * s.w[tk];
             const uint16_t hi = f32_to_bf16(h);
             const uint16_t lo = f32_to_bf16(h - bf16_to_f32(hi));
-            uint16_t *d = a.b.h + s.pos[tk] * h_row(I) + h_place(blk) + 64 * (c >> 3) + (c & 7);
+            uint16_t *d = a.b.h + s.pos[tk] * h_row(I) + h_place(col >> 5) + 64 * (c >> 3) + (c & 7);
             d[0] = hi;
             d[8] = lo;
             // a last step of 64 columns: its other two blocks meet zero weights, and must be finite
-            if ((I & 64) && blk == I / 32 - 1)
+            if ((I & 64) && col >= I - 32)
                 for (int x = 1; x <= 2; ++x) {
-                    uint16_t *z = a.b.h + s.pos[tk] * h_row(I) + h_place(blk + x) + 64 * (c >> 3) + (c & 7);
+                    uint16_t *z = a.b.h + s.pos[tk] * h_row(I) + h_place((col >> 5) + x) + 64 * (c >> 3) + (c & 7);
                     z[0] = z[8] = 0;
                 }
         }
     }
 }
 
-__global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_gate_up(MxArgs a) {
+template <int PN>
+__global__ __launch_bounds__(64 * GU_QUADS * PN) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_gate_up(MxArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t sx[];
     __shared__ GuShared s;
     const int lane = threadIdx.x & 63, n = lane & 15, K = a.L.K, T = a.T;
@@ -371,7 +374,7 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
         if (!sh) w = a.b.w[pos];
         else if (a.gated) w = sigmoid(a.b.logits[(16 * item + n) * (a.L.E + 1) + a.L.E]);
     }
-    gate_up_block(a, sx, s, blockIdx.x, sh, it.e, it.count, pos, w);
+    gate_up_block<PN>(a, sx, s, blockIdx.x, sh, it.e, it.count, pos, w);
 }
 
 // Up to this many tokens route and gate/up are one launch: us a layer against two launches (2048 x
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
             if (a.out_w) a.out_w[tid] = s_w[tid];
         }
     }
-    gate_up_block(a, sx, s, blk, sh, e, cnt, pos, w);
+    gate_up_block<2>(a, sx, s, blk, sh, e, cnt, pos, w);
 }
 
 // ----------------------------------------------------------------------------- down
@@ -715,7 +718,10 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     } else {
         hipLaunchKernelGGL(k_mx_route, dim3(nR, (unsigned)((T + 15) / 16)), dim3(RT_THREADS), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess || route_only) return e;
-        hipLaunchKernelGGL(k_mx_gate_up, dim3((unsigned)(L.I / 32), (unsigned)max_items(L, T)), dim3(MT_THREADS), gu_lds, s, a);
+        const unsigned items = (unsigned)max_items(L, T);
+        if (T <= 8)                                          // (figures at gate_up_block)
+            hipLaunchKernelGGL(k_mx_gate_up<1>, dim3((unsigned)(L.I / 16), items), dim3(64 * GU_QUADS), gu_lds, s, a);
+        else hipLaunchKernelGGL(k_mx_gate_up<2>, dim3((unsigned)(L.I / 32), items), dim3(128 * GU_QUADS), gu_lds, s, a);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const dim3 grid((unsigned)(L.H / (16 * d.np)), (unsigned)a.shares), thr((unsigned)(64 * d.waves));
