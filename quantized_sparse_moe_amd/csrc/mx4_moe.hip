@@ -503,7 +503,12 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
                 }
                 total += c;
             }
-            if (j >= total) return;
+            if (j >= total) {
+                // (after a wait that gave up, workgroups may hold different selections: the list has an
+                // entry, here one of no tokens, in every place that the one of j = 0 may count)
+                if (blk == 0 && tid == 0) a.b.act[j] = 0;
+                return;
+            }
             for (; k > 0; --k) word &= word - 1;
             e = base + __builtin_ctz(word);
             constexpr int Q = (MT * 16 + 63) / 64;
@@ -622,6 +627,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
                 }
             }
         }
+        if (cnt == 0 && nx < items) fetch_pos(nx);           // (an entry of no tokens: k_mx_token)
     }
     __syncthreads();
     // thread: a token and four columns

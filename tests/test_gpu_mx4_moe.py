@@ -433,3 +433,56 @@ def test_products_and_layer_run_together(torch, qs):
     check(L, a.view(torch.int16).cpu().numpy().view(np.uint16), y, idx, w, "layer of the projection")
     yq = ref.values(*ref.quantize(y.float().cpu().numpy().astype(np.float64)))
     assert (np.abs(out.cpu().numpy() - yq @ ws[1][0].T) <= ref.product_bound(yq, ws[1][0])).all()
+
+
+def _list_of(ws, L, T):
+    """(nact, act, pos) of the last call of T <= 128 tokens, as views into its workspace: behind the
+    2 MiB state, 256-byte aligned, logits, selections, weights, list, its length and rows."""
+    up = lambda n: -(-n // 256) * 256
+    E, K = L.n_experts, L.top_k
+    act = (2 << 20) + up(T * (E + 1) * 4) + 2 * up(T * K * 4)
+    nact = act + up(384 * 4)
+    pos = nact + up(4)
+    return ws[nact:nact + 4], ws[act:act + 384 * 4], ws[pos:pos + E * 256]
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+def test_give_up_leaves_a_whole_list(torch, qs, T):
+    """Waits that give up over logits that differ from copy to copy: workgroups select differently, and
+    the error word says so, but every entry of the list that the next launch reads was written by this
+    call and lies in range, and the next call is right again."""
+    L = _cache.setdefault("slow route", ref.Layer(hidden=8192, inter=64, n_experts=40, top_k=8, seed=23))
+    desc = upload(L, torch, qs)
+    xb = syn.make_x(T, L.hidden, seed=80 + T)
+    x = to_dev(xb, torch)
+    ws = qs.new_workspace(desc, T)
+    want = run(torch, qs, desc, x, workspace=ws)
+    check(L, xb, *want, T)
+    w32 = ws[:1 << 20].view(torch.int32)
+    empty = status = 0
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ws[2 << 20:].fill_(0xFF)                             # what lies there is no list
+        logits = w32[1216:1216 + 32 * 576]                   # the copies of the tagged logit words
+        logits.copy_(torch.randn(logits.shape, generator=g, device="cuda").view(torch.int32))
+        logits[1::2] = -1                                    # (of another call's tag)
+        torch.empty(1 << 29, dtype=torch.uint8, device="cuda").fill_(seed)   # (weights out of the caches)
+        w32[32] = 1                                          # the bound on a wait's polls
+        qs.moe_layer_forward(desc, x, workspace=ws)
+        torch.cuda.synchronize()
+        w32[32] = 0
+        status |= int(qs.moe_workspace_status(ws, clear=True))
+        nact, act, pos = (v.cpu().numpy().view(t) for v, t in zip(_list_of(ws, L, T), ("i4", "i4", "i2")))
+        n = int(nact[0])
+        assert L.top_k <= n <= T * L.top_k
+        for a in act[:n].tolist():
+            e, slot, tile, count = a & 255, a >> 8 & 255, a >> 16 & 15, a >> 20
+            assert e < L.n_experts and slot < L.n_experts and tile == 0 and 0 <= count <= T, hex(a)
+            rows = pos[slot * 128:slot * 128 + count]
+            assert ((rows >= 0) & (rows < T * L.top_k)).all()
+        empty += int((act[:n] == 0).any())
+        got = run(torch, qs, desc, x, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert int(qs.moe_workspace_status(ws)) == 0
+    assert status == qs.MOE_WS_ERR_DECODE_WAIT
+    print(f"[state] T = {T}: {empty} of 4 lists with empty entries", flush=True)
