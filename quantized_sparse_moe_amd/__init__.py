@@ -202,7 +202,8 @@ class LayerDesc:
         """A layer with microscaled 4-bit experts.  ``gate_up`` = (codes, scales) of the
         [n_experts, 2 inter, hidden] stack and ``down`` of the [n_experts, hidden, inter]
         one, in tiles (``mx4_pack_rows16`` of all the stack's rows); ``shared`` = (gate_up,
-        down) of the shared expert."""
+        down) of the shared expert.  ``router_w`` and ``shared_gate_w`` are bf16 (or its bits as
+        16-bit integers), ``router_bias`` is fp32."""
         for what, m, rows, cols in (("gate_up", gate_up, n_experts * 2 * inter, hidden),
                                     ("down", down, n_experts * hidden, inter)) + (
                 () if shared is None else (("shared gate_up", shared[0], 2 * inter, hidden),
@@ -211,11 +212,14 @@ class LayerDesc:
             _mx4_buf(m[0], nc, f"LayerDesc.from_mx4: {what}"), _mx4_buf(m[1], ns, f"LayerDesc.from_mx4: {what}")
             if m[0].device != router_w.device or m[1].device != router_w.device:
                 _mx4_bad("LayerDesc.from_mx4", f"{what} is on another device than router_w")
-        for what, t, n, size in (("router_w", router_w, n_experts * hidden, 2), ("router_bias", router_bias, n_experts, 4),
-                                 ("shared_gate_w", shared_gate_w, hidden, 2)):
-            if t is not None and (t.element_size() != size or t.numel() != n or not t.is_contiguous()
+        import torch
+        bits = (torch.bfloat16, torch.int16, torch.uint16)   # (16-bit integers are bf16 bits)
+        for what, t, n, types in (("router_w", router_w, n_experts * hidden, bits),
+                                  ("router_bias", router_bias, n_experts, (torch.float32,)),
+                                  ("shared_gate_w", shared_gate_w, hidden, bits)):
+            if t is not None and (t.dtype not in types or t.numel() != n or not t.is_contiguous()
                                   or t.device != router_w.device):
-                _mx4_bad("LayerDesc.from_mx4", f"{what} must be {n} contiguous values of {size} bytes")
+                _mx4_bad("LayerDesc.from_mx4", f"{what} must be {n} contiguous values of type {types[0]}")
 
         def half(m, cols, rows, row0):
             nc, ns = _mx4_sizes(row0, cols, MX4_TILES)

@@ -186,6 +186,22 @@ def test_layer_tensors_are_checked():
             make(**bad)
 
 
+@pytest.mark.parametrize("what,dtype", [("router_w", "float16"), ("shared_gate_w", "float16"), ("router_bias", "int32"),
+                                        ("router_bias", "uint32"), ("router_w", "float32")])
+def test_layer_tensors_of_another_type_of_the_same_width(what, dtype):
+    """from_mx4 refuses 16- and 32-bit types it would read as something else; bits are taken."""
+    import torch
+    H, I, E = 128, 64, 3
+    mat = lambda rows, cols: tuple(torch.zeros(f(rows, cols, q.MX4_TILES), dtype=torch.uint8)
+                                   for f in (q.lib().mx4_codes_size, q.lib().mx4_scales_size))
+    a = dict(router_w=torch.zeros(E, H, dtype=torch.int16), gate_up=mat(E * 2 * I, H), down=mat(E * H, I),
+             router_bias=torch.zeros(E), shared=(mat(2 * I, H), mat(H, I)), shared_gate_w=torch.zeros(H, dtype=torch.uint16))
+    q.LayerDesc.from_mx4(H, I, E, 2, **a)
+    a[what] = torch.zeros(a[what].shape, dtype=getattr(torch, dtype))
+    with pytest.raises(q.QsmoeError, match=what):
+        q.LayerDesc.from_mx4(H, I, E, 2, **a)
+
+
 def test_layer_workspace():
     d = mx4_desc()
     f = lambda T, c=0: q.lib().moe_workspace_size_chunked(ctypes.byref(d), T, c)
