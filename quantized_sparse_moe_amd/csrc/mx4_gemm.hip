@@ -490,10 +490,14 @@ static Choice choose(bool mx, int64_t T, int64_t N, int64_t K) {
     auto tiles = [&](int64_t m, int64_t n) { return ((T + m - 1) / m) * ((N + n - 1) / n); };
     const int64_t large = tiles(128, 256), round = 2 * cu;
     if (T > 64 && 8 * large >= 7 * ((large + round - 1) / round * round)) return {LARGE, 1};
-    int64_t sh = cu / tiles(64, 128), most = mx4_quads(K);
-    if (sh > most) sh = most;
+    const int64_t quads = mx4_quads(K);
+    int64_t sh = cu / tiles(64, 128);
+    if (sh > quads) sh = quads;
     if (sh > MAX_SHARES) sh = MAX_SHARES;
-    return {SMALL, sh < 1 ? 1 : (int)sh};
+    if (sh <= 1) return {SMALL, 1};
+    // (whole quads a share: no more shares than those leave something to)
+    const int64_t per = (quads + sh - 1) / sh;
+    return {SMALL, (int)((quads + per - 1) / per)};
 }
 
 // For either kind of x, and never less than for fewer tokens: the largest shares x tokens of the

@@ -206,6 +206,12 @@ def test_gemm(torch, qs, T, N, K):
     check(qs.mx4_gemm_mx4x(wc, ws, N, K, xc, xs, T, y_dtype=torch.bfloat16), want, bound, "mx bf16")
 
 
+@pytest.mark.parametrize("T,N,K", [(37, 2560, 8192), (20, 3000, 8192), (64, 2700, 2560), (17, 4200, 3584)])
+def test_gemm_columns_that_the_shares_do_not_divide(torch, qs, T, N, K):
+    """Split products whose quads of columns are no multiple of the shares."""
+    test_gemm(torch, qs, T, N, K)
+
+
 # large tiles (128 x 256): whole and partial quads of columns, first and last steps alone
 @pytest.mark.parametrize("K", [32, 96, 128, 416, 512, 544, 640, 1024, 1184, 1664])
 def test_gemm_large_tiles(torch, qs, K):

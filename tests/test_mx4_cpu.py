@@ -116,6 +116,19 @@ def test_workspace_for_more_tokens_serves_fewer(N, K):
     assert sizes == sorted(sizes) and sizes[-1] != BAD
 
 
+@pytest.mark.parametrize("N,K", [(2560, 8192), (3000, 8192), (2048, 8192), (2700, 2560), (1, 65536), (4200, 3584)])
+def test_every_share_of_the_columns_has_some(N, K):
+    """The workspace of a split product holds the sums of its shares: no more of them than there are
+    pieces of the columns, which are dealt out in whole quads of 512."""
+    pitch, quads = -(-N // 4) * 4, -(-K // 512)
+    for T in (17, 37, 64):                                       # (one row of tiles)
+        size = q.lib().mx4_gemm_workspace_size(N, K, T)
+        shares = size // (4 * T * pitch)
+        assert size == shares * 4 * T * pitch and shares > 1
+        per = -(-quads // shares)
+        assert (shares - 1) * per < quads, (N, K, T, shares)
+
+
 def mx4_desc(**kw):
     d = q.moe_layer_desc()
     d.hidden, d.inter, d.n_experts, d.top_k, d.bits, d.group = 2048, 512, 256, 8, 4, 32
