@@ -97,18 +97,12 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, u32x4 b, f32x16 c, int i, u
     }
 }
 
-// direct-to-LDS loads (lane l's bytes land at l times their number), and the waits for them
+// Direct-to-LDS loads (lane l's bytes land at l times their number) through a buffer resource over
+// everything from a wave-uniform pointer on: voff per lane, soff uniform, both in bytes and below
+// 2^31; and the waits for them.  Beside loads into registers only this form will do: the compiler
+// cannot count global_load_lds among them (it may be LDS or memory that a flat instruction waits
+// for) and would wait for every load there is.
 typedef __attribute__((address_space(3))) void lds_void;
-__device__ __forceinline__ void dma16(const void *g, void *l) {
-    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 16, 0, 0);
-}
-__device__ __forceinline__ void dma4(const void *g, void *l) {
-    __builtin_amdgcn_global_load_lds(g, (lds_void *)l, 4, 0, 0);
-}
-// The same through a buffer resource (over everything from a wave-uniform pointer on): voff per
-// lane, soff uniform, both in bytes and below 2^31.  Beside loads into registers only this form
-// will do: the compiler cannot count global_load_lds among them (it may be LDS or memory that a
-// flat instruction waits for) and would wait for every load there is.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_from(const void *p) {
     const uint64_t u = (uint64_t)p;
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));

@@ -54,16 +54,8 @@ struct MxArgs {
     int shares;                       // down: workgroups that share the items of the same output rows
 };
 
-__device__ __forceinline__ void st_agent(uint32_t *p, uint32_t v) {
-    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
 __device__ __forceinline__ float ld_agent(const float *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// 16 bytes written through to device scope (padded: a vector-ALU write to the data registers
-// within two wait states would replace data the store has not yet read)
-__device__ __forceinline__ void st_agent128(void *p, f32x4 v) {
-    asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 4" ::"v"(p), "v"(v) : "memory");
 }
 
 // four times 16 bytes read at device scope, and waited for here (the compiler does not track
@@ -89,7 +81,7 @@ __device__ __forceinline__ bool last_of(uint32_t *cnt, uint32_t n, int *s_last) 
     __syncthreads();
     if (threadIdx.x == 0) {
         const bool last = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
-        if (last) st_agent(cnt, 0u);
+        if (last) st_dev(cnt, 0u);
         *s_last = last;
     }
     __syncthreads();
@@ -156,7 +148,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
 #pragma unroll
             for (int w = 1; w < RT_WAVES; ++w) v += red[w][l][r];
             if (a.L.router_bias && ee < E) v += a.L.router_bias[ee];
-            st_agent((uint32_t *)a.b.logits + t * (E + 1) + ee, __float_as_uint(v));
+            st_dev((uint32_t *)a.b.logits + t * (E + 1) + ee, __float_as_uint(v));
         }
     }
     if (!last_of(a.b.cnt + blockIdx.y, gridDim.x, &s_last)) return;
@@ -174,7 +166,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
         tk.idx = min(max(tk.idx, 0), E - 1);
         if (lane < K) {
             s_sel[t * K + lane] = (int16_t)tk.idx;
-            if (gridDim.y > 1) st_agent((uint32_t *)a.b.idx + t * K + lane, (uint32_t)tk.idx);
+            if (gridDim.y > 1) st_dev((uint32_t *)a.b.idx + t * K + lane, (uint32_t)tk.idx);
             a.b.w[t * K + lane] = tk.w;
             if (a.out_idx) a.out_idx[t * K + lane] = tk.idx;
             if (a.out_w) a.out_w[t * K + lane] = tk.w;
@@ -568,7 +560,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     int it = z * W + wave;
     fetch(it);
     // (the launch before is complete: the generation its logits were tagged with is used up)
-    if (a.tagged && blockIdx.x == 0 && z == 0 && tid == 0) st_agent(a.b.ctl + CTL_GEN, call_tag(a.b.ctl));
+    if (a.tagged && blockIdx.x == 0 && z == 0 && tid == 0) st_dev(a.b.ctl + CTL_GEN, call_tag(a.b.ctl));
     const int items = (*a.b.nact + nsh) * KQ;
     if (it < items) fetch_pos(it);
     for (int i = lane; i < T * C; i += 64) mine[i] = 0.0f;
@@ -640,7 +632,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
 #pragma unroll
         for (int w = 0; w < W; ++w) v += *(const f32x4 *)(sums + (w * T + tk) * C + c4);
     if (a.shares > 1) {
-        if (live) st_agent128(a.b.part + (int64_t)z * T * H + o, v);
+        if (live) st_dev128(a.b.part + (int64_t)z * T * H + o, __builtin_bit_cast(u32x4, v));
         if (!last_of(a.b.cnt + MX_CNT_DOWN + blockIdx.x, a.shares, &s_last)) return;
         if (live) {
             v = (f32x4){0.f, 0.f, 0.f, 0.f};
