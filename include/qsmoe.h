@@ -357,9 +357,12 @@ moe_status mx4_pack_rows16(const void *codes, const void *scales, int64_t rows, 
  *   ws  device workspace of ws_bytes >= mx4_gemm_workspace_size(N, K, T) (NULL when that is
  *       0; one for T tokens also serves fewer), 256-byte aligned, contents undefined before
  *       and after; calls that share it must not overlap in time.
- * Every product is exact; only the fp32 sums round (and y, where it is bf16).  A NaN or
- * infinity in x leaves no finite value in its token's row of y (mx4x: NaN, as the block is)
- * and does not reach the others; a NaN block of W makes its column of y NaN.
+ * Every product is exact; only the fp32 sums round (and y, where it is bf16).  mx4_gemm (and the
+ * layer) multiply the weights as bf16: one of 2^128 or more, which takes a scale byte of 253 or
+ * 254 (mx4_quantize makes none), counts as an infinity there; mx4_gemm_mx4x takes them as they
+ * are.  A NaN or infinity in x leaves no finite value in its token's row of y (mx4x: NaN, as
+ * the block is) and does not reach the others; a NaN block of W makes its column of y NaN, an
+ * infinity in W leaves no finite value there.
  * A token's result may depend on T (the order of its sums), not on the other tokens.
  */
 size_t mx4_gemm_workspace_size(int64_t N, int64_t K, int64_t T);

@@ -307,6 +307,34 @@ def test_gemm_not_finite(torch, qs, T):
     assert torch.isnan(y[:, 17]).all() and torch.equal(y[:, keep], clean[:, keep])
 
 
+@pytest.mark.parametrize("T", [2, 30, 300])
+def test_gemm_of_the_smallest_and_largest_weights(torch, qs, T):
+    """Scale bytes at both ends and subnormal activations against weights that bring them back: exact
+    products; weights of 2^128 and more count as infinities beside bf16 activations, not beside MX4."""
+    N, K = 96, 544
+    rng = np.random.default_rng(T)
+    for lo, hi, std in ((0, 3, 2.0 ** 100), (150, 160, 2.0 ** -130), (250, 252, 2.0 ** -20), (253, 254, 2.0 ** -20)):
+        c = rng.integers(0, 16, (N, K)).astype(np.uint8)
+        if hi > 252:
+            c[::2] &= 9                                          # every other row below 2^127
+        s = rng.integers(lo, hi + 1, (N, K // 32)).astype(np.uint8)
+        wc, ws = qs.mx4_pack_rows16(torch.from_numpy(ref.pack_rows(c)).cuda(), torch.from_numpy(s).cuda(), N, K)
+        w = ref.values(c, s)
+        x = (torch.randn(T, K, generator=torch.Generator().manual_seed(T), dtype=torch.float64) * std).to(torch.bfloat16)
+        xv = np64(x)
+        y = qs.mx4_gemm(wc, ws, N, K, x.cuda())
+        past = (np.abs(w) >= 2.0 ** 128).any(axis=1)
+        assert past.any() == (hi > 252) and not past.all()
+        assert not np.isfinite(np64(y)[:, past]).any()
+        err, bound = np.abs(np64(y) - xv @ w.T), ref.product_bound(xv, w)
+        assert (err[:, ~past] <= bound[:, ~past]).all(), (lo, hi)
+        qc, qsc = ref.quantize(xv)
+        xq = ref.values(qc, qsc)
+        tc, ts = (torch.from_numpy(a).cuda() for a in ref.to_tiles(qc, qsc))
+        y = np64(qs.mx4_gemm_mx4x(wc, ws, N, K, tc, ts, T))
+        assert (np.abs(y - xq @ w.T) <= ref.product_bound(xq, w)).all(), (lo, hi)
+
+
 @pytest.mark.parametrize("T", [1, 16, 100, 600])
 def test_gemm_rows_are_independent(torch, qs, T):
     """A token's result does not depend on the other tokens, bit for bit."""
