@@ -209,14 +209,15 @@ moe_status moe_route(const moe_layer_desc *d, const void *x, int64_t T,
  * fp32 accumulation, fp16 intermediates, each under its range scale).
  * For a given T the result does not depend on whether gate/up are fused or separate,
  * nor on the other tokens of the call (tokens are independent), bit for bit.
- * MX4 layers: up to 128 tokens run in three launches (up to 4 in two) that read each chosen
- * expert once (MFMA on bf16 operands: x as it is, the weights exact, h as a bf16 pair, to
- * 2^-17); more run the grouped path (the same products in tiles, weighted expert outputs in
- * fp16 under range scales before the combine).  There a token's
- * result does not depend on the others, bit for bit; up to 128 tokens it may in its last fp32
- * bits (the order in which its experts are summed depends on the pass's experts).  What they
- * keep in the workspace's state follows the same rules (zero before the first call, then the
- * library's).
+ * MX4 layers: up to 128 tokens run in three launches (up to 4 in two) that load a chosen
+ * expert once for every 16 tokens that chose it (MFMA on bf16 operands: x as it is, the weights
+ * exact, h as a bf16 pair, to 2^-17, so that an fp32 y is off by about 2e-6 of its norm); more run
+ * the grouped path (the same products in tiles, weighted expert outputs in fp16 under range
+ * scales before the combine, as in an affine layer: 2e-4 of y's norm, an eighth of what rounding
+ * y to bf16 costs).  There a token's result does not depend on the others, bit for bit; up to
+ * 128 tokens it may in its last fp32 bits (the order in which its experts are summed depends on
+ * the pass's experts).  What they keep in the workspace's state follows the same rules (zero
+ * before the first call, then the library's).
  */
 moe_status moe_layer_forward(const moe_layer_desc *d, const void *x, int64_t T,
                                void *y, int32_t y_dtype,

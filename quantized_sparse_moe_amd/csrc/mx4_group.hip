@@ -10,8 +10,12 @@
 // three stages of 64 columns (128 bytes a row, chunks XORed by (row / 2) % 8), each wave's weights
 // straight into its registers, both two steps ahead; two workgroups fit a compute unit, and one's
 // prologue and epilogue run under the other's products.  T = 4096, 2048 x 512, top 8 of 256 experts
-// and a shared one: 474 -> 425 us a layer against weights through LDS in a ring of two; fragments past
-// a tile's rows skipped by a branch each (T = 512: 154 us; all five multiplied: 184).
+// and a shared one, skewed router: 474 -> 425 us a layer against weights through LDS in a ring of two;
+// fragments past a tile's rows skipped by a branch each (T = 512: 154 us; all five multiplied: 184).
+// With every expert as likely T = 4096 takes 403 us: gate/up 170, matrix cores busy half of the
+// cycles (about 128 rows a tile, 32 steps and then its h), down 193, busy 0.44 (16 steps, then its slot
+// rows); the router, binning and combine the rest.  T = 512 takes 209: 91 and 85 for 430 MB of weights,
+// with 16 rows a tile too little work to hide the wait for them (busy 0.15).
 //
 //   gate/up  rows of x gathered through perm; the wave's fragments are 32 gate rows and the
 //            same 32 up rows, so h = silu(g) u is formed in registers.  It leaves as the bf16
@@ -19,7 +23,9 @@
 //   down     rows of h; the reduction runs over hi, then over lo, each against the same weights
 //            (a third more matrix work than bf16 h, which would leave 2e-3 x RMS of error in the
 //            layer).  Slot rows as the affine path writes them: w o in fp16 under a scale per row
-//            and 64 columns (a wave's), for the same combine.
+//            and 64 columns (a wave's), for the same combine.  One rounding of each summand of y
+//            (2e-4 of y's norm; bf16 y alone rounds to 2e-3), for half the bytes of fp32 rows:
+//            151 MB written and read again at T = 4096.
 #include "mx4.h"
 
 namespace qs {

@@ -7,9 +7,10 @@
 //            last of those lists the experts any token chose (ascending) and each one's
 //            tokens.
 //   gate/up  one workgroup per (listed expert, 32 or 16 columns of h): gathers the expert's tokens
-//            as the rows of the activation operand, so each expert's weights are read once
-//            however many tokens chose it, and an expert that one token chose costs one
-//            16-row tile.  h = w silu(g) u carries the token's routing weight and leaves as the
+//            as the rows of the activation operand.  A list entry is up to 16 tokens of an
+//            expert: an expert of more is loaded once for each of its entries, which run side by
+//            side, so that the repeats come from the L2 (T = 128: 286 MB fetched past it for 281 MB of
+//            weights), and an expert that one token chose costs one 16-row tile.  h = w silu(g) u carries the token's routing weight and leaves as the
 //            bf16 pair hi + lo (h to 2^-17), two operand rows.
 //   down     one workgroup per 32 rows of the output and share of the listed experts, gathering
 //            each expert's rows of h; hi and lo of a token are neighbouring accumulator
@@ -18,7 +19,7 @@
 //
 // One to four tokens take two: k_mx_token does route and gate/up.
 //
-// All are bound by the weight stream: (union of the chosen experts + shared) x
+// All are bound by the weight stream: (union of the chosen experts + shared), each once, x
 // 3 H I x 17/32 bytes, and at few tokens by the chain of launches and round trips before and
 // after it (2048 x 512, top 8 of 256 and a shared expert, times of the layer in a graph):
 //   T = 1 15.9 us (15 MB: 2.4 at 6.3 TB/s)   T = 2 20.1   T = 4 26.4 (53 MB: 8)   T = 7 36.0 (89 MB: 14)
