@@ -225,6 +225,57 @@ moe_status moe_layer_forward(const moe_layer_desc *d, const void *x, int64_t T,
                                void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * Routing rules: other ways to choose a token's experts and weights than moe_route's.  For the
+ * logits l of a token (live: above -infinity; a NaN is not):
+ *   score     MOE_SCORE_SIGMOID  s_e = 1 / (1 + exp(-l_e))
+ *             MOE_SCORE_SOFTMAX  s_e = exp(l_e) / sum of exp over all live experts
+ *   select_bias  [n_experts] fp32 (or NULL): c_e = s_e + select_bias[e] is what experts are chosen
+ *             by (their weights stay s_e); without it, the scores themselves
+ *   n_groups  groups of n_experts / n_groups consecutive experts, of which the group_top_k best stay:
+ *             by the largest c of the group (MOE_GROUP_MAX) or by the sum of its two largest
+ *             (MOE_GROUP_TOP2); ties go to the lower group.  1: no groups
+ *   the top_k largest c of the groups that stay, ties to the lower expert id
+ *   renorm    1: w_j = s_j / sum over the selected s;  0: w_j = s_j
+ *   scale     a factor on every weight (finite)
+ * An expert that is not live, or whose bias is NaN or -infinity, is chosen only when nothing else
+ * is left, and has weight 0; a row without a live expert has weights 0.  Scores are formed and
+ * compared in 64 bits.  Limits (else MOE_ERR_UNSUPPORTED): n_groups <= 64 divides n_experts,
+ * group_top_k groups hold at least top_k experts.  The rule is read during the call,
+ * select_bias by the kernels.
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX  0
+#define MOE_GROUP_TOP2 1
+typedef struct {
+    int32_t score, renorm;
+    int32_t n_groups, group_top_k, group_score;
+    float   scale;
+    const float *select_bias;
+} moe_router_rule;
+
+/*
+ * A rule applied to logits that are there already.
+ *   logits   [T][n_experts], row stride ld (elements, >= n_experts), MOE_BF16, MOE_F16 or MOE_F32
+ *   topk_idx [T][top_k] int32 ascending, topk_w [T][top_k] fp32 (written)
+ * Limits: T <= 2^20, n_experts <= 256, top_k <= min(n_experts, 16).  T == 0 enqueues nothing.
+ */
+moe_status moe_select(const moe_router_rule *rule, const void *logits, int32_t dtype, int64_t T, int64_t n_experts,
+                      int64_t ld, int32_t top_k, int32_t *topk_idx, float *topk_w, void *stream);
+
+/*
+ * moe_route and moe_layer_forward under a rule instead of their own (rule NULL:
+ * MOE_ERR_INVALID); arguments, limits, paths, workspaces and results otherwise as theirs
+ * (router_bias is part of the logits).  The logits are fp32 sums whose order differs between paths, so
+ * a token whose scores lie within their rounding may be routed otherwise in a batch of another size.
+ */
+moe_status moe_route_rule(const moe_layer_desc *d, const moe_router_rule *rule, const void *x, int64_t T,
+                          int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes, void *stream);
+moe_status moe_layer_forward_rule(const moe_layer_desc *d, const moe_router_rule *rule, const void *x, int64_t T,
+                                  void *y, int32_t y_dtype, int32_t *topk_idx, float *topk_w,
+                                  void *ws, size_t ws_bytes, void *stream);
+
+/*
  * moe_layer_forward for callers that cannot allocate device memory or pass a workspace
  * (code under HIP graph capture, tight serving loops, harnesses that forbid hipMalloc):
  * the same kernels and the same results, bit for bit, with the workspace replaced by a

@@ -57,9 +57,16 @@ class moe_layer_desc(ctypes.Structure):
                 ("shared_gate_w", ctypes.c_void_p)]
 
 
+class moe_router_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("group_top_k", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("select_bias", ctypes.c_void_p)]
+
+
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_size",
            "moe_workspace_size_chunked", "moe_workspace_status", "moe_route",
-           "moe_layer_forward", "moe_layer_forward_static", "q8_gemv", "q8_quantize_x", "q8_gemv_q8x", "q8_gemv_qx",
+           "moe_layer_forward", "moe_layer_forward_static", "moe_select", "moe_route_rule", "moe_layer_forward_rule",
+           "q8_gemv", "q8_quantize_x", "q8_gemv_q8x", "q8_gemv_qx",
            "q8_pack_rows16", "mx4_codes_size", "mx4_scales_size", "mx4_quantize", "mx4_dequantize",
            "mx4_pack_rows16", "mx4_gemm_workspace_size", "mx4_gemm", "mx4_gemm_mx4x",
            "moe_calib_read", "moe_calib_mfma")
@@ -90,6 +97,12 @@ def lib() -> ctypes.CDLL:
         L.moe_layer_forward.argtypes = [P, P, I64, P, I32, P, P, P, SZ, P]
         L.moe_layer_forward_static.restype = I32
         L.moe_layer_forward_static.argtypes = [P, P, I64, P, I32, P, P, P]
+        L.moe_select.restype = I32
+        L.moe_select.argtypes = [P, P, I32, I64, I64, I64, I32, P, P, P]
+        L.moe_route_rule.restype = I32
+        L.moe_route_rule.argtypes = [P, P, P, I64, P, P, P, SZ, P]
+        L.moe_layer_forward_rule.restype = I32
+        L.moe_layer_forward_rule.argtypes = [P, P, P, I64, P, I32, P, P, P, SZ, P]
         L.q8_gemv.restype = I32
         L.q8_gemv.argtypes = [P, I64, I64, P, P, I32, P]
         L.q8_quantize_x.restype = I32
@@ -353,10 +366,13 @@ def moe_workspace_status(workspace, clear: bool = False, out=None, stream=None):
 
 
 def moe_route(desc: LayerDesc, x, topk_idx=None, topk_w=None, workspace=None,
-              stream=None) -> Tuple["object", "object"]:
-    """Router + top-k: returns (topk_idx int32 [T, k], topk_w fp32 [T, k])."""
+              stream=None, rule: Optional["RouterRule"] = None) -> Tuple["object", "object"]:
+    """Router + top-k: returns (topk_idx int32 [T, k], topk_w fp32 [T, k]); ``rule`` selects
+    by a ``RouterRule`` instead of the largest logits."""
     import torch
     T = x.shape[0]
+    if rule is not None:
+        return _ruled(desc, x, rule, None, None, topk_idx, topk_w, workspace, stream, "moe_route")
     if topk_idx is None:
         topk_idx = _empty((T, desc.top_k), torch.int32, x.device, stream)
     if topk_w is None:
@@ -368,12 +384,16 @@ def moe_route(desc: LayerDesc, x, topk_idx=None, topk_w=None, workspace=None,
 
 
 def moe_layer_forward(desc: LayerDesc, x, y=None, y_dtype=None, topk_idx=None, topk_w=None,
-                      workspace=None, stream=None):
-    """The whole MoE layer on bf16 ``x`` [T, hidden]; returns ``y`` (fp32 or bf16)."""
+                      workspace=None, stream=None, rule: Optional["RouterRule"] = None):
+    """The whole MoE layer on bf16 ``x`` [T, hidden]; returns ``y`` (fp32 or bf16).  ``rule``
+    routes by a ``RouterRule`` instead of the largest logits."""
     import torch
     T = x.shape[0]
     if y is None:
         y = _empty((T, desc.hidden), y_dtype or torch.float32, x.device, stream)
+    if rule is not None:
+        return _ruled(desc, x, rule, y, _out_code(y, "moe_layer_forward"), topk_idx, topk_w, workspace, stream,
+                      "moe_layer_forward")
     code = MOE_F32 if y.dtype == torch.float32 else MOE_BF16 if y.dtype == torch.bfloat16 else None
     if code is None:
         raise QsmoeError(MOE_ERR_INVALID, "moe_layer_forward: y must be float32 or bfloat16")
@@ -403,6 +423,92 @@ def _out_code(y, where):
     if code is None:
         raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be float32 or bfloat16")
     return code
+
+
+# ------------------------------------------------------------------- routing rules
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+
+
+class RouterRule:
+    """How a token's experts and weights follow from its logits (``moe_router_rule``).
+
+    ``score`` "softmax" (over all experts) or "sigmoid"; ``select_bias`` fp32 [n_experts] is added
+    to the scores for the selection only; of ``n_groups`` groups of consecutive experts the
+    ``group_top_k`` best are kept, by their best expert (``group_score`` "max") or their two best
+    ("top2"); ``renorm`` divides the weights by their sum, ``scale`` multiplies them."""
+
+    def __init__(self, score: str = "softmax", renorm: bool = True, n_groups: int = 1, group_top_k: int = 1,
+                 group_score: str = "max", scale: float = 1.0, select_bias=None):
+        import torch
+        scores = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+        groups = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+        if score not in scores or group_score not in groups:
+            raise QsmoeError(MOE_ERR_INVALID, "RouterRule: score is softmax or sigmoid, group_score max or top2")
+        if select_bias is not None and (select_bias.dtype != torch.float32 or select_bias.dim() != 1
+                                        or not select_bias.is_contiguous()):
+            raise QsmoeError(MOE_ERR_INVALID, "RouterRule: select_bias must be contiguous fp32 [n_experts]")
+        self.select_bias = select_bias
+        self.desc = moe_router_rule(scores[score], 1 if renorm else 0, n_groups, group_top_k, groups[group_score],
+                                    scale, _ptr(select_bias))
+        self.ptr = ctypes.addressof(self.desc)
+
+
+def _rule_checked(rule: RouterRule, n_experts: int, where: str):
+    """The rule's bias, checked for the number of experts."""
+    bias = rule.select_bias
+    if bias is not None and bias.shape[0] != n_experts:
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: select_bias must have one value per expert")
+    return bias
+
+
+def _topk_buffers(topk_idx, topk_w, T: int, k: int, device, stream, where: str):
+    torch = _torch()
+    if topk_idx is None:
+        topk_idx = _empty((T, k), torch.int32, device, stream)
+    elif topk_idx.dtype != torch.int32 or topk_idx.shape != (T, k) or not topk_idx.is_contiguous():
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: topk_idx must be contiguous int32 [T, top_k]")
+    if topk_w is None:
+        topk_w = _empty((T, k), torch.float32, device, stream)
+    elif topk_w.dtype != torch.float32 or topk_w.shape != (T, k) or not topk_w.is_contiguous():
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: topk_w must be contiguous float32 [T, top_k]")
+    return topk_idx, topk_w
+
+
+def _ruled(desc: LayerDesc, x, rule: RouterRule, y, y_code, topk_idx, topk_w, workspace, stream, where: str):
+    """moe_route (y None) and moe_layer_forward under a rule."""
+    torch = _torch()
+    bias = _rule_checked(rule, desc.n_experts, where)
+    if x.dim() != 2 or x.shape[1] != desc.hidden or x.dtype not in (torch.bfloat16, torch.int16) or not x.is_contiguous():
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: x must be contiguous bf16 [T, hidden]")
+    T, gpu = x.shape[0], x.get_device()
+    if y is None or topk_idx is not None or topk_w is not None:
+        idx, w = _topk_buffers(topk_idx, topk_w, T, desc.top_k, x.device, stream, where)
+        topk_idx, topk_w = (idx, w) if y is None else (None if topk_idx is None else idx, None if topk_w is None else w)
+    ws, nbytes = _workspace(desc, T, workspace, x.device, stream)
+    st, here = _mx4_stream(where, stream, gpu, bias, y, topk_idx, topk_w, ws)
+    if y is None:
+        _mx4_call(where, lib().moe_route_rule, gpu, here, desc.ptr, rule.ptr, x.data_ptr(), T, topk_idx.data_ptr(),
+                  topk_w.data_ptr(), ws.data_ptr(), nbytes, st)
+        return topk_idx, topk_w
+    if y.shape != (T, desc.hidden) or not y.is_contiguous():
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: y must be contiguous [T, hidden]")
+    _mx4_call(where, lib().moe_layer_forward_rule, gpu, here, desc.ptr, rule.ptr, x.data_ptr(), T, y.data_ptr(), y_code,
+              _ptr(topk_idx), _ptr(topk_w), ws.data_ptr(), nbytes, st)
+    return y
+
+
+def moe_select(logits, top_k: int, rule: RouterRule, topk_idx=None, topk_w=None, stream=None):
+    """Experts and weights from router logits [T, n_experts] (bf16, fp16 or fp32; rows may be
+    strided): (topk_idx int32 [T, top_k], topk_w fp32 [T, top_k])."""
+    T, E, ld, code = _mx4_values(logits, "moe_select")
+    bias = _rule_checked(rule, E, "moe_select")
+    topk_idx, topk_w = _topk_buffers(topk_idx, topk_w, T, top_k, logits.device, stream, "moe_select")
+    gpu = logits.get_device()
+    st, here = _mx4_stream("moe_select", stream, gpu, bias, topk_idx, topk_w)
+    _mx4_call("moe_select", lib().moe_select, gpu, here, rule.ptr, logits.data_ptr(), code, T, E, ld, top_k,
+              topk_idx.data_ptr(), topk_w.data_ptr(), st)
+    return topk_idx, topk_w
 
 
 def q8_gemv(w_tiles, N: int, K: int, x, y=None, y_dtype=None, stream=None):

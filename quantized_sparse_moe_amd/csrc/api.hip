@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -77,7 +78,37 @@ QMat to_qmat(const moe_qmat &m) {
     return q;
 }
 
-Layer to_layer(const moe_layer_desc *d) {
+// a routing rule over E experts of which top_k are selected
+moe_status check_rule(const moe_router_rule *r, int64_t E, int64_t top_k) {
+    if (!r) return MOE_ERR_INVALID;
+    if ((r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) || (r->renorm != 0 && r->renorm != 1) ||
+        (r->group_score != MOE_GROUP_MAX && r->group_score != MOE_GROUP_TOP2) || !std::isfinite(r->scale))
+        return MOE_ERR_INVALID;
+    if (r->select_bias && !aligned(r->select_bias, 4)) return MOE_ERR_INVALID;
+    if (r->n_groups < 1 || r->group_top_k < 1 || r->group_top_k > r->n_groups) return MOE_ERR_INVALID;
+    if (r->n_groups > 64 || E % r->n_groups || r->group_top_k * (E / r->n_groups) < top_k) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+RouteRule to_rule(const moe_router_rule *r, int64_t E) {
+    RouteRule q;
+    q.bias = r->select_bias;
+    q.scale = r->scale;
+    q.sigmoid = r->score == MOE_SCORE_SIGMOID;
+    q.renorm = r->renorm;
+    // (all groups kept: none)
+    q.n_groups = r->group_top_k == r->n_groups ? 1 : r->n_groups;
+    q.group_k = r->group_top_k;
+    q.group_top2 = r->group_score == MOE_GROUP_TOP2;
+    q.group_size = (int)(E / q.n_groups);
+    q.group_shift = 6;
+    while ((q.n_groups << q.group_shift) > 64) --q.group_shift;
+    q.group_inv = 65536 / q.group_size + 1;
+    return q;
+}
+
+// (rule: checked, or null)
+Layer to_layer(const moe_layer_desc *d, const moe_router_rule *rule) {
     Layer L;
     L.H = d->hidden;
     L.I = d->inter;
@@ -100,6 +131,8 @@ Layer to_layer(const moe_layer_desc *d) {
     L.sb_bf16 = d->scale_dtype == MOE_BF16;
     L.shared_gate_w = (const uint16_t *)d->shared_gate_w;
     L.mx4 = is_mx4(d);
+    L.ruled = rule != nullptr;
+    L.rule = rule ? to_rule(rule, d->n_experts) : RouteRule{};
     return L;
 }
 
@@ -267,9 +300,9 @@ moe_status check_layer_call(const moe_layer_desc *d, const void *x, int64_t T, c
 }
 
 // an MX4 layer (or its routing only)
-moe_status run_mx4(const moe_layer_desc *d, const uint16_t *x, int64_t T, void *y, int32_t y_dtype, int32_t *topk_idx,
+moe_status run_mx4(const moe_layer_desc *d, const moe_router_rule *rule, const uint16_t *x, int64_t T, void *y, int32_t y_dtype, int32_t *topk_idx,
                    float *topk_w, void *ws, size_t ws_bytes, bool route_only, hipStream_t st) {
-    const Layer L = to_layer(d);
+    const Layer L = to_layer(d, rule);
     const int64_t K = d->top_k, H = d->hidden;
     const size_t ysz = y_dtype == MOE_F32 ? 4 : 2;
     size_t n;
@@ -296,14 +329,15 @@ moe_status run_mx4(const moe_layer_desc *d, const uint16_t *x, int64_t T, void *
     return MOE_OK;
 }
 
-moe_status forward_impl(const moe_layer_desc *d, const void *x, int64_t T, void *y, int32_t y_dtype,
+moe_status forward_impl(const moe_layer_desc *d, const moe_router_rule *rule, const void *x, int64_t T, void *y, int32_t y_dtype,
                         int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes, void *stream) {
     moe_status s = check_layer_call(d, x, T, y, y_dtype, topk_idx, topk_w);
+    if (!s && rule) s = check_rule(rule, d->n_experts, d->top_k);
     if (s || T == 0) return s;
     if ((s = check_ws(d, T, ws, ws_bytes))) return s;
     if (is_mx4(d))
-        return run_mx4(d, (const uint16_t *)x, T, y, y_dtype, topk_idx, topk_w, ws, ws_bytes, false, (hipStream_t)stream);
-    const Layer L = to_layer(d);
+        return run_mx4(d, rule, (const uint16_t *)x, T, y, y_dtype, topk_idx, topk_w, ws, ws_bytes, false, (hipStream_t)stream);
+    const Layer L = to_layer(d, rule);
     hipStream_t st = (hipStream_t)stream;
     const uint16_t *xx = (const uint16_t *)x;
     hipError_t e;
@@ -341,6 +375,54 @@ moe_status forward_impl(const moe_layer_desc *d, const void *x, int64_t T, void 
                                   topk_w ? topk_w + t0 * K : nullptr, st);
         if (e == hipSuccess) e = launch_prefill_binning(L, Tc, b, st);
         if (e == hipSuccess) e = launch_prefill_gemms(L, Tc, b, yc, y_dtype, st);
+        if (e != hipSuccess) return MOE_ERR_DEVICE;
+    }
+    return MOE_OK;
+}
+
+moe_status route_impl(const moe_layer_desc *d, const moe_router_rule *rule, const void *x, int64_t T, int32_t *topk_idx,
+                      float *topk_w, void *ws, size_t ws_bytes, void *stream) {
+    moe_status s = check_desc(d);
+    if (!s && rule) s = check_rule(rule, d->n_experts, d->top_k);
+    if (s) return s;
+    if (T < 0) return MOE_ERR_INVALID;
+    if (T > MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !aligned(x, 16) || !topk_idx || !topk_w || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return MOE_ERR_INVALID;
+    if ((s = check_ws(d, T, ws, ws_bytes))) return s;
+    if (is_mx4(d))
+        return run_mx4(d, rule, (const uint16_t *)x, T, nullptr, MOE_F32, topk_idx, topk_w, ws, ws_bytes, true, (hipStream_t)stream);
+    const Layer L = to_layer(d, rule);
+    hipStream_t st = (hipStream_t)stream;
+    if (T == 1) {
+        size_t n;
+        const DecodeBufs b = carve_decode(d, ws, &n);
+        return dev(launch_decode_route(L, (const uint16_t *)x, b, topk_idx, topk_w, st));
+    }
+    if (decode_small_eligible(L, T)) {
+        size_t n;
+        const DecodeBufs b = carve_decode(d, ws, &n);
+        return dev(launch_decode_small_route(L, (const uint16_t *)x, T, b, topk_idx, topk_w, st));
+    }
+    if (const int64_t T0 = small_split(L, T)) {
+        size_t n;
+        const DecodeBufs b = carve_decode(d, ws, &n);
+        const int64_t K = d->top_k;
+        const uint16_t *xx = (const uint16_t *)x;
+        hipError_t e = launch_decode_small_route(L, xx, T0, b, topk_idx, topk_w, st);
+        if (e == hipSuccess)
+            e = launch_decode_small_route(L, xx + T0 * d->hidden, T - T0, b, topk_idx + T0 * K, topk_w + T0 * K, st);
+        return dev(e);
+    }
+    size_t n;
+    const int64_t C = pick_chunk(d, T, ws_bytes), K = d->top_k, H = d->hidden;
+    PrefillBufs b = carve_prefill(d, C, ws, &n);
+    for (int64_t t0 = 0; t0 < T; t0 += C) {
+        const int64_t Tc = T - t0 < C ? T - t0 : C;
+        b.idx = topk_idx + t0 * K;
+        b.w = topk_w + t0 * K;
+        const hipError_t e = launch_prefill_router(L, (const uint16_t *)x + t0 * H, Tc, b, false, nullptr, nullptr, st);
         if (e != hipSuccess) return MOE_ERR_DEVICE;
     }
     return MOE_OK;
@@ -453,54 +535,40 @@ moe_status moe_workspace_status(void *ws, size_t ws_bytes, uint32_t *status_out,
 
 moe_status moe_route(const moe_layer_desc *d, const void *x, int64_t T, int32_t *topk_idx,
                        float *topk_w, void *ws, size_t ws_bytes, void *stream) {
-    moe_status s = check_desc(d);
-    if (s) return s;
-    if (T < 0) return MOE_ERR_INVALID;
-    if (T > MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
-    if (T == 0) return MOE_OK;
-    if (!x || !aligned(x, 16) || !topk_idx || !topk_w || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
-        return MOE_ERR_INVALID;
-    if ((s = check_ws(d, T, ws, ws_bytes))) return s;
-    if (is_mx4(d))
-        return run_mx4(d, (const uint16_t *)x, T, nullptr, MOE_F32, topk_idx, topk_w, ws, ws_bytes, true, (hipStream_t)stream);
-    const Layer L = to_layer(d);
-    hipStream_t st = (hipStream_t)stream;
-    if (T == 1) {
-        size_t n;
-        const DecodeBufs b = carve_decode(d, ws, &n);
-        return dev(launch_decode_route(L, (const uint16_t *)x, b, topk_idx, topk_w, st));
-    }
-    if (decode_small_eligible(L, T)) {
-        size_t n;
-        const DecodeBufs b = carve_decode(d, ws, &n);
-        return dev(launch_decode_small_route(L, (const uint16_t *)x, T, b, topk_idx, topk_w, st));
-    }
-    if (const int64_t T0 = small_split(L, T)) {
-        size_t n;
-        const DecodeBufs b = carve_decode(d, ws, &n);
-        const int64_t K = d->top_k;
-        const uint16_t *xx = (const uint16_t *)x;
-        hipError_t e = launch_decode_small_route(L, xx, T0, b, topk_idx, topk_w, st);
-        if (e == hipSuccess)
-            e = launch_decode_small_route(L, xx + T0 * d->hidden, T - T0, b, topk_idx + T0 * K, topk_w + T0 * K, st);
-        return dev(e);
-    }
-    size_t n;
-    const int64_t C = pick_chunk(d, T, ws_bytes), K = d->top_k, H = d->hidden;
-    PrefillBufs b = carve_prefill(d, C, ws, &n);
-    for (int64_t t0 = 0; t0 < T; t0 += C) {
-        const int64_t Tc = T - t0 < C ? T - t0 : C;
-        b.idx = topk_idx + t0 * K;
-        b.w = topk_w + t0 * K;
-        const hipError_t e = launch_prefill_router(L, (const uint16_t *)x + t0 * H, Tc, b, false, nullptr, nullptr, st);
-        if (e != hipSuccess) return MOE_ERR_DEVICE;
-    }
-    return MOE_OK;
+    return route_impl(d, nullptr, x, T, topk_idx, topk_w, ws, ws_bytes, stream);
+}
+
+moe_status moe_route_rule(const moe_layer_desc *d, const moe_router_rule *rule, const void *x, int64_t T,
+                          int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes, void *stream) {
+    if (!rule) return MOE_ERR_INVALID;
+    return route_impl(d, rule, x, T, topk_idx, topk_w, ws, ws_bytes, stream);
 }
 
 moe_status moe_layer_forward(const moe_layer_desc *d, const void *x, int64_t T, void *y, int32_t y_dtype,
                              int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes, void *stream) {
-    return forward_impl(d, x, T, y, y_dtype, topk_idx, topk_w, ws, ws_bytes, stream);
+    return forward_impl(d, nullptr, x, T, y, y_dtype, topk_idx, topk_w, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_forward_rule(const moe_layer_desc *d, const moe_router_rule *rule, const void *x, int64_t T, void *y,
+                                  int32_t y_dtype, int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes,
+                                  void *stream) {
+    if (!rule) return MOE_ERR_INVALID;
+    return forward_impl(d, rule, x, T, y, y_dtype, topk_idx, topk_w, ws, ws_bytes, stream);
+}
+
+moe_status moe_select(const moe_router_rule *rule, const void *logits, int32_t dtype, int64_t T, int64_t n_experts,
+                      int64_t ld, int32_t top_k, int32_t *topk_idx, float *topk_w, void *stream) {
+    if (dtype != MOE_BF16 && dtype != MOE_F16 && dtype != MOE_F32) return MOE_ERR_INVALID;
+    if (T < 0) return MOE_ERR_INVALID;
+    if (T > MAX_TOKENS || n_experts < 1 || n_experts > 256) return MOE_ERR_UNSUPPORTED;
+    if (top_k < 1 || top_k > 16 || top_k > n_experts) return MOE_ERR_UNSUPPORTED;
+    const moe_status s = check_rule(rule, n_experts, top_k);
+    if (s || T == 0) return s;
+    if (!logits || !aligned(logits, dtype == MOE_F32 ? 4 : 2) || ld < n_experts || !topk_idx || !topk_w ||
+        !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return MOE_ERR_INVALID;
+    return dev(launch_select(to_rule(rule, n_experts), logits, dtype, T, (int)n_experts, ld, top_k, topk_idx, topk_w,
+                             (hipStream_t)stream));
 }
 
 moe_status moe_layer_forward_static(const moe_layer_desc *d, const void *x, int64_t T, void *y, int32_t y_dtype,
@@ -512,7 +580,7 @@ moe_status moe_layer_forward_static(const moe_layer_desc *d, const void *x, int6
     if (ws_size_chunked(d, T, MIN_CHUNK) > SCRATCH_BYTES) return MOE_ERR_WORKSPACE;
     void *ws = nullptr;
     if ((s = scratch_for_current_device(&ws))) return s;
-    return forward_impl(d, x, T, y, y_dtype, topk_idx, topk_w, ws, SCRATCH_BYTES, stream);
+    return forward_impl(d, nullptr, x, T, y, y_dtype, topk_idx, topk_w, ws, SCRATCH_BYTES, stream);
 }
 
 moe_status q8_gemv(const void *w_tiles, int64_t N, int64_t K, const void *x, void *y,

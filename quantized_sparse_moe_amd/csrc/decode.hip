@@ -167,10 +167,12 @@ __device__ void pairs_swiglu(const QMat &mg, const QMat &mu, int e, int j0, int 
     }
 }
 
-template <bool WEIGHTS = true>
-__device__ TopkOut select_topk(uint32_t *ctl, uint32_t tag, int E, int K, int gated, float *gate) {
-    return select_topk_from<WEIGHTS>(ctl, (const uint64_t *)(ctl + LOGIT_BASE + (blockIdx.x % LOGIT_COPIES) * LOGIT_STRIDE),
-                            tag, E, K, gated, gate);
+template <bool WEIGHTS, int RULE>
+__device__ TopkOut select_topk(uint32_t *ctl, uint32_t tag, int E, int K, int gated, float *gate, const RouteRule &rule) {
+    __shared__ double s_rule[RULE ? 256 : 1];
+    return select_topk_from<WEIGHTS, RULE>(
+        ctl, (const uint64_t *)(ctl + LOGIT_BASE + (blockIdx.x % LOGIT_COPIES) * LOGIT_STRIDE), tag, E, K, gated, gate, rule,
+        s_rule);
 }
 
 // Consumer: wave 0 waits (bounded) for every logit of the call and takes the top-k
@@ -178,12 +180,13 @@ __device__ TopkOut select_topk(uint32_t *ctl, uint32_t tag, int E, int K, int ga
 // workgroup gets (s_idx, s_w): experts in ascending id, renormalised weights (and, gated,
 // entry K: the shared expert's gate in s_w[K]); WEIGHTS = false leaves the weights 0 (G
 // needs only the experts).  Ends with a barrier.
-template <bool WEIGHTS = true>
-__device__ void get_topk(uint32_t *ctl, uint32_t tag, int E, int K, int gated, int *s_idx, float *s_w) {
+template <bool WEIGHTS, int RULE>
+__device__ void get_topk(uint32_t *ctl, uint32_t tag, int E, int K, int gated, int *s_idx, float *s_w,
+                         const RouteRule &rule) {
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
         float gate;
-        const TopkOut tk = select_topk<WEIGHTS>(ctl, tag, E, K, gated, &gate);
+        const TopkOut tk = select_topk<WEIGHTS, RULE>(ctl, tag, E, K, gated, &gate, rule);
         if (lane < K) {
             s_idx[lane] = tk.idx;
             s_w[lane] = tk.w;
@@ -194,8 +197,9 @@ __device__ void get_topk(uint32_t *ctl, uint32_t tag, int E, int K, int gated, i
 }
 
 // SBF: the layer's scales and biases are bf16 (else fp16), fixed per instantiation so that
-// their widening is one instruction
-template <int BITS, int SBF>
+// their widening is one instruction.  RULE: experts by the layer's routing rule (1), which only
+// wave 0 of a workgroup goes through.
+template <int BITS, int SBF, int RULE>
 __global__ __launch_bounds__(DT) __attribute__((amdgpu_waves_per_eu(4))) void k_decode(DecArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t dsm[];
     __shared__ uint32_t s_flag;
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(DT) __attribute__((amdgpu_waves_per_eu(4))) void k_
         // ------------------------------------------- P (routing only): the selector
         if (wave != 0) return;
         float gate;
-        const TopkOut tk = select_topk(ctl, tag, E, K, 0, &gate);
+        const TopkOut tk = select_topk<true, RULE>(ctl, tag, E, K, 0, &gate, L.rule);
         if (lane < K) {
             if (a.out_idx) a.out_idx[lane] = tk.idx;
             if (a.out_w) a.out_w[lane] = tk.w;
@@ -288,7 +292,7 @@ __global__ __launch_bounds__(DT) __attribute__((amdgpu_waves_per_eu(4))) void k_
         const int xe = stage_x<BITS>(a.x, H, xs, xsum, s_wm);     // ends with a barrier
         int e = 0;
         if (!sh) {
-            get_topk<false>(ctl, tag, E, K, gated, s_idx, s_w);   // (experts only); ends with a barrier
+            get_topk<false, RULE>(ctl, tag, E, K, gated, s_idx, s_w, L.rule);   // (experts only); ends with a barrier
             e = __builtin_amdgcn_readfirstlane(s_idx[slot]);
         }
         const int jj = j0 < I ? j0 : I - 2;
@@ -336,7 +340,7 @@ __global__ __launch_bounds__(DT) __attribute__((amdgpu_waves_per_eu(4))) void k_
     {
         // ------------------------------------------ D: down + weighted combine
         const int d = b - nR - nS - nG;
-        get_topk(ctl, tag, E, K, gated, s_idx, s_w);
+        get_topk<true, RULE>(ctl, tag, E, K, gated, s_idx, s_w, L.rule);
         uint32_t arrived = 0, top = 0;                      // replies of the two counters
         if (d == 0 && tid < K) {
             if (a.out_idx) a.out_idx[tid] = s_idx[tid];
@@ -582,8 +586,11 @@ hipError_t launch(DecArgs a, hipStream_t s) {
         lds = lds_g > lds_d ? lds_g : lds_d;
     }
     const int grid = a.nR + a.nP + a.nS + a.nG + a.nD;
-    void (*kern)(DecArgs) = L.bits == 4 ? (L.sb_bf16 ? k_decode<4, 1> : k_decode<4, 0>)
-                                       : (L.sb_bf16 ? k_decode<8, 1> : k_decode<8, 0>);
+    void (*kern)(DecArgs) =
+        L.ruled ? (L.bits == 4 ? (L.sb_bf16 ? k_decode<4, 1, 1> : k_decode<4, 0, 1>)
+                               : (L.sb_bf16 ? k_decode<8, 1, 1> : k_decode<8, 0, 1>))
+                : (L.bits == 4 ? (L.sb_bf16 ? k_decode<4, 1, 0> : k_decode<4, 0, 0>)
+                               : (L.sb_bf16 ? k_decode<8, 1, 0> : k_decode<8, 0, 0>));
     hipLaunchKernelGGL(kern, dim3(grid), dim3(DT), lds, s, a);
     return hipGetLastError();
 }

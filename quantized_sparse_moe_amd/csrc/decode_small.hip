@@ -396,8 +396,8 @@ __device__ void pairs_swiglu_tokens(const QMat &mg, const QMat &mu, int e, int j
 }
 
 // SBF: the layer's scales and biases are bf16 (else fp16), fixed per instantiation so that
-// their widening is one instruction
-template <int BITS, int SBF>
+// their widening is one instruction.  RULE: experts by the layer's routing rule.
+template <int BITS, int SBF, bool RULE>
 __global__ __launch_bounds__(DT) __attribute__((amdgpu_waves_per_eu(4))) void k_decode_small(SmallArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t dsm[];
     __shared__ SmallSel S;
@@ -476,7 +476,8 @@ __global__ __launch_bounds__(DT) __attribute__((amdgpu_waves_per_eu(4))) void k_
         if (wave < T) {
             const uint64_t *lg = (const uint64_t *)(ctl + LOGIT_BASE + (sel % SM_LCOPIES) * SM_LSTRIDE) + wave * SM_TE;
             float gate;
-            const TopkOut tk = select_topk_from(ctl, lg, tag, E, K, gated, &gate);
+            const TopkOut tk = select_topk_from<true, RULE ? SM_TMAX : 0>(ctl, lg, tag, E, K, gated, &gate, L.rule,
+                                                                          (double *)dsm + 256 * wave);
             if (lane < K) {
                 S.si[wave * K + lane] = tk.idx;
                 S.sw[wave * K + lane] = tk.w;
@@ -832,9 +833,13 @@ hipError_t launch_small(SmallArgs a, hipStream_t s) {
         while (a.nP > 1 && a.nP > a.nG + a.nD) a.nP >>= 1;
         lds = small_lds_bytes(L, a.T);
     }
+    if (L.ruled) lds = std::max(lds, (size_t)SM_TMAX * 256 * 8);   // (P: the selection's scratch)
     const int grid = a.nR + a.nP + a.nS + a.nG + a.nD;
-    void (*kern)(SmallArgs) = L.bits == 4 ? (L.sb_bf16 ? k_decode_small<4, 1> : k_decode_small<4, 0>)
-                                       : (L.sb_bf16 ? k_decode_small<8, 1> : k_decode_small<8, 0>);
+    void (*kern)(SmallArgs) =
+        L.ruled ? (L.bits == 4 ? (L.sb_bf16 ? k_decode_small<4, 1, true> : k_decode_small<4, 0, true>)
+                               : (L.sb_bf16 ? k_decode_small<8, 1, true> : k_decode_small<8, 0, true>))
+                : (L.bits == 4 ? (L.sb_bf16 ? k_decode_small<4, 1, false> : k_decode_small<4, 0, false>)
+                               : (L.sb_bf16 ? k_decode_small<8, 1, false> : k_decode_small<8, 0, false>));
     hipLaunchKernelGGL(kern, dim3(grid), dim3(DT), lds, s, a);
     return hipGetLastError();
 }

@@ -11,6 +11,7 @@
 #pragma once
 #include "common.h"
 #include "internal.h"
+#include "rule.h"
 
 namespace qs {
 
@@ -221,10 +222,11 @@ __device__ __forceinline__ float chunk_dot(const u32x4 &q, const uint32_t *xs, u
 // id.  One poll is in flight at a time: a read still in flight when the data is found
 // would have to be waited for before its registers are reused, a full extra round trip.
 // gated: logit E is the shared-expert gate's, polled with the others; *gate gets
-// sigmoid of it (every lane).  WEIGHTS = false: the experts only (w = 0).
-template <bool WEIGHTS = true>
+// sigmoid of it (every lane).  WEIGHTS = false: the experts only (w = 0).  RW > 0: by the
+// routing rule instead, at most RW waves of the workgroup at once, with E doubles of LDS each.
+template <bool WEIGHTS = true, int RW = 0>
 __device__ TopkOut select_topk_from(uint32_t *ctl, const uint64_t *lg, uint32_t tag, int E, int K, int gated,
-                                    float *gate) {
+                                    float *gate, const RouteRule &rule, double *scratch) {
     const int lane = threadIdx.x & 63;
     const uint64_t none = (uint64_t)tag << 32;
     uint64_t w[4], wg;
@@ -246,7 +248,9 @@ __device__ TopkOut select_topk_from(uint32_t *ctl, const uint64_t *lg, uint32_t 
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = no_nan(__uint_as_float((uint32_t)w[i]));
-    TopkOut tk = wave_topk_regs<WEIGHTS>(v, E, K);
+    TopkOut tk;
+    if constexpr (RW > 0) tk = wave_select<RW>(rule, v, E, K, scratch);
+    else tk = wave_topk_regs<WEIGHTS>(v, E, K);
     tk.idx = min(max(tk.idx, 0), E - 1);
     *gate = sigmoid(__builtin_bit_cast(float, __builtin_amdgcn_readfirstlane((int)(uint32_t)wg)));
     return tk;

@@ -16,6 +16,16 @@ struct QMat {                      // one stack of affine-quantized matrices
     int64_t stride;                // rows between matrices
 };
 
+// A routing rule (moe_router_rule; selection in rule.h), as the kernels read it
+struct RouteRule {
+    const float *bias;             // [E] added to the scores for the selection, or null
+    float scale;                   // of the weights
+    int sigmoid, renorm;
+    int n_groups, group_k, group_top2, group_size;
+    int group_shift;               // 2^group_shift lanes look through a group: the most with n_groups of them in a wave
+    int group_inv;                 // 65536 / group_size, rounded up: e * group_inv >> 16 is e / group_size for e < 256
+};
+
 struct Layer {
     int H, I, E, K, bits;          // hidden, inter, experts, top_k, code bits
     const uint16_t *router_w;      // bf16 [E][H]
@@ -26,6 +36,8 @@ struct Layer {
     int sb_bf16;                   // scales and biases are bf16 (else fp16)
     const uint16_t *shared_gate_w; // bf16 [H]: shared output scaled by sigmoid(g . x); or null
     int mx4;                       // MX4 tiles instead of affine codes (scales: E8M0 tiles, no biases)
+    int ruled;                     // experts are selected by `rule` (else: the largest logits, softmax over them)
+    RouteRule rule;
 };
 
 // -------------------------------------------------------------------- decode T = 1
@@ -165,6 +177,10 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
 // The expert products of a prompt (mx4_group.hip), between the binning and the combine:
 // b.h holds bf16 pairs there, [T*K + T][hi, lo][I].
 hipError_t launch_mx_group(const Layer &L, const uint16_t *x, int64_t T, const PrefillBufs &b, hipStream_t s);
+
+// ---------------------------------------------------------- around the layer's blocks
+hipError_t launch_select(const RouteRule &rule, const void *logits, int dtype, int64_t T, int E, int64_t ld, int K,
+                         int32_t *idx, float *w, hipStream_t s);
 
 // ---------------------------------------------------------------- measured ceilings
 hipError_t launch_calib_read(const void *buf, int64_t bytes, uint32_t *out, hipStream_t s);

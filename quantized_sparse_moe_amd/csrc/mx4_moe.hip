@@ -108,7 +108,8 @@ __device__ __forceinline__ MxItem mx_unpack(int i, int nsh, int act, int T) {
 // One workgroup per 16 experts (row E: the shared expert's gate) and 16 tokens, the columns
 // split over its waves.  The workgroup that finishes a tile of 16 tokens last takes their
 // top-k, a wave per token (one compute unit takes 4 us over 16 of them, so tiles do not wait
-// for one another); the last of those lists the experts.
+// for one another); the last of those lists the experts.  RULE: by the layer's routing rule.
+template <bool RULE>
 __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
     __shared__ f32x4 red[RT_WAVES][64];
     __shared__ int s_last;
@@ -163,7 +164,13 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
             const float l = e < E ? ld_agent(lg + e) : 0.0f;
             v[i] = l != l ? -__builtin_inff() : l;
         }
-        TopkOut tk = wave_topk_regs(v, E, K);
+        TopkOut tk;
+        if constexpr (RULE) {
+            __shared__ double scratch[RT_WAVES][256];
+            tk = wave_select<RT_WAVES>(a.L.rule, v, E, K, scratch[wave]);
+        } else {
+            tk = wave_topk_regs(v, E, K);
+        }
         tk.idx = min(max(tk.idx, 0), E - 1);
         if (lane < K) {
             s_sel[t * K + lane] = (int16_t)tk.idx;
@@ -382,7 +389,7 @@ constexpr int TOKEN_MAX = 4;
 // the top-k themselves (decode_state.h: a wait is bounded, and only for workgroups of lower
 // index).  The workgroup of (j, 32 columns of h) takes the j-th of the experts any token chose.
 // Saves the last router workgroup's counting, selecting and listing and a launch.
-template <int MT>
+template <int MT, bool RULE>
 __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4))) void k_mx_token(MxArgs a, int nR) {
     static_assert(MT <= MT_WAVES && MT * 16 <= LOGIT_COPIES * 16, "a wave and a logit copy per token");
     extern __shared__ __attribute__((aligned(16))) uint8_t sx[];
@@ -461,8 +468,9 @@ __global__ __launch_bounds__(MT_THREADS) __attribute__((amdgpu_waves_per_eu(4)))
     }
     if (wave < T && (!sh || a.gated)) {
         float gate;
-        const TopkOut tk = select_topk_from(
-            ctl, (const uint64_t *)(ctl + LOGIT_BASE + (wave * per + b % per) * LOGIT_STRIDE), tag, E, K, a.gated, &gate);
+        const TopkOut tk = select_topk_from<true, RULE ? MT : 0>(
+            ctl, (const uint64_t *)(ctl + LOGIT_BASE + (wave * per + b % per) * LOGIT_STRIDE), tag, E, K, a.gated, &gate,
+            a.L.rule, (double *)sx + 256 * wave);
         if (lane < K) {
             s_idx[wave * K + lane] = tk.idx;
             s_w[wave * K + lane] = tk.w;
@@ -712,10 +720,13 @@ hipError_t launch_mx_layer(const Layer &L, const uint16_t *x, int64_t T, const M
     hipError_t e;
     if (a.tagged) {
         const dim3 grid(nR + (unsigned)(L.I / 32 * (T * L.K + (L.has_shared ? 1 : 0))));
-        if (T == 1) hipLaunchKernelGGL(k_mx_token<1>, grid, dim3(MT_THREADS), gu_lds, s, a, (int)nR);
-        else hipLaunchKernelGGL(k_mx_token<TOKEN_MAX>, grid, dim3(MT_THREADS), gu_lds, s, a, (int)nR);
+        // (gu_lds holds the selection's scratch too, 2 KB a token)
+        void (*kern)(MxArgs, int) = T == 1 ? (L.ruled ? k_mx_token<1, true> : k_mx_token<1, false>)
+                                           : (L.ruled ? k_mx_token<TOKEN_MAX, true> : k_mx_token<TOKEN_MAX, false>);
+        hipLaunchKernelGGL(kern, grid, dim3(MT_THREADS), gu_lds, s, a, (int)nR);
     } else {
-        hipLaunchKernelGGL(k_mx_route, dim3(nR, (unsigned)((T + 15) / 16)), dim3(RT_THREADS), 0, s, a);
+        hipLaunchKernelGGL(L.ruled ? k_mx_route<true> : k_mx_route<false>, dim3(nR, (unsigned)((T + 15) / 16)),
+                           dim3(RT_THREADS), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess || route_only) return e;
         const unsigned items = (unsigned)max_items(L, T);
         if (T <= 8)                                          // (figures at gate_up_block)

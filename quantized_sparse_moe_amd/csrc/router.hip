@@ -18,6 +18,7 @@
 // outside fp16's range, writes the copy again as x 2^a.
 #include "common.h"
 #include "internal.h"
+#include "rule.h"
 
 namespace qs {
 
@@ -178,11 +179,13 @@ struct TopkArgs {
     int nxmax;                      // expert blocks of the logits grid (words of xmax used)
     int32_t *xexp;                  // [T] the exponent a of each token's copy (x 2^a)
     int H;
+    RouteRule rule;
 };
 
 // One wave per token (4 tokens per wave), 16 tokens per workgroup: the block's expert
-// histogram is counted in LDS with integer atomics and written once.
-template <int BITS>
+// histogram is counted in LDS with integer atomics and written once.  RULE: experts by the
+// layer's routing rule.
+template <int BITS, bool RULE>
 __global__ __launch_bounds__(64 * TK_TOKENS) void k_topk(TopkArgs a) {
     __shared__ int hist[256];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -215,7 +218,13 @@ __global__ __launch_bounds__(64 * TK_TOKENS) void k_topk(TopkArgs a) {
                 }
             }
         }
-        const TopkOut tk = wave_topk_regs(v, E, K);
+        TopkOut tk;
+        if constexpr (RULE) {
+            __shared__ double scratch[TK_TOKENS][256];
+            tk = wave_select<TK_TOKENS>(a.rule, v, E, K, scratch[wave]);
+        } else {
+            tk = wave_topk_regs(v, E, K);
+        }
         if (a.sgate && lane == 0) a.sgate[t] = sigmoid(a.logits[t * a.LS + E]);
         if (lane < K) {
             a.idx[t * K + lane] = tk.idx;
@@ -273,11 +282,11 @@ hipError_t launch_prefill_router(const Layer &L, const uint16_t *x, int64_t T,
     ta.nxmax = (int)lgrid.y;
     ta.xexp = b.xexp;
     ta.H = L.H;
+    ta.rule = L.rule;
     const dim3 tgrid((unsigned)((T + TK_TOKENS - 1) / TK_TOKENS));
-    if (L.bits == 4)
-        hipLaunchKernelGGL((k_topk<4>), tgrid, dim3(64 * TK_TOKENS), 0, s, ta);
-    else
-        hipLaunchKernelGGL((k_topk<8>), tgrid, dim3(64 * TK_TOKENS), 0, s, ta);
+    void (*topk)(TopkArgs) = L.bits == 4 ? (L.ruled ? k_topk<4, true> : k_topk<4, false>)
+                                         : (L.ruled ? k_topk<8, true> : k_topk<8, false>);
+    hipLaunchKernelGGL(topk, tgrid, dim3(64 * TK_TOKENS), 0, s, ta);
     return hipGetLastError();
 }
 
