@@ -294,6 +294,42 @@ moe_status moe_layer_forward_static(const moe_layer_desc *d, const void *x, int6
                                     int32_t *topk_idx, float *topk_w, void *stream);
 
 /*
+ * The norms around a block, joined with its gate, residual scale and the residual stream, row by
+ * row:
+ *     z  = post(y) * act(gate)            (post, gate: where given)
+ *     r' = r + scale * z                  (r NULL: scale * z;  y NULL: r' = r)
+ *     x  = pre(r')
+ * A norm (moe_norm) is  v -> u / sqrt(mean(u^2) + eps) * (offset + weight) + bias  with u = v
+ * (MOE_NORM_RMS) or u = v - mean(v) (MOE_NORM_LAYER); weight NULL: no gain (nor offset), bias NULL: none.
+ *   y, r, r_out, x  [T][H], row strides ldy, ldr, ldro, ldx in elements (>= H), each MOE_BF16, MOE_F16
+ *               or MOE_F32; r_out receives r', x the second norm.  Either may be NULL, x exactly
+ *               when pre is
+ *   gate        [T][H] (gate_cols == H) or a value per row (gate_cols == 1), row stride ldg;
+ *               gate_act MOE_ACT_NONE, MOE_ACT_SIGMOID 1 / (1 + exp(-g)), MOE_ACT_SILU g / (1 + exp(-g))
+ *   weight, bias  [H] of the norm's dtype
+ * Sums, norms and r' are fp32 until they are stored (pre reads r' before its rounding), so the mean
+ * square must fit in fp32: |v| up to 2^63 or so.  NaN and infinities stay in their row.
+ * r_out or x may be y, r or gate itself (same pointer, type and stride: in place), or other columns of the
+ * same matrix; any other overlap with an input, and any of the outputs with each other, is
+ * MOE_ERR_INVALID, as are a post, gate or r_out without y.
+ * Limits (else MOE_ERR_UNSUPPORTED): 1 <= H <= 32768, T <= 2^26.  T == 0 enqueues nothing.
+ */
+#define MOE_NORM_RMS   0
+#define MOE_NORM_LAYER 1
+#define MOE_ACT_NONE    0
+#define MOE_ACT_SIGMOID 1
+#define MOE_ACT_SILU    2
+typedef struct {
+    int32_t kind, dtype;
+    float   eps, offset;
+    const void *weight, *bias;
+} moe_norm;
+moe_status moe_block_norm(const void *y, int32_t y_dtype, int64_t ldy, const void *r, int32_t r_dtype, int64_t ldr,
+                          const moe_norm *post, const void *gate, int32_t gate_dtype, int64_t ldg, int64_t gate_cols,
+                          int32_t gate_act, float scale, const moe_norm *pre, void *r_out, int32_t r_out_dtype, int64_t ldro,
+                          void *x, int32_t x_dtype, int64_t ldx, int64_t T, int64_t H, void *stream);
+
+/*
  * Dense Q8_0 decode GEMV over 16-row packed tiles ([EMBER] packed 16-row tile):
  *     y[n] = sum_b d[n][b] * sum_{c<32} q[n][32b + c] * x[32b + c]
  * with fp32 accumulation.

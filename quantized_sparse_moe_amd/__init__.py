@@ -63,10 +63,15 @@ class moe_router_rule(ctypes.Structure):
                 ("scale", ctypes.c_float), ("select_bias", ctypes.c_void_p)]
 
 
+class moe_norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("offset", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
 EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_size",
            "moe_workspace_size_chunked", "moe_workspace_status", "moe_route",
            "moe_layer_forward", "moe_layer_forward_static", "moe_select", "moe_route_rule", "moe_layer_forward_rule",
-           "q8_gemv", "q8_quantize_x", "q8_gemv_q8x", "q8_gemv_qx",
+           "moe_block_norm", "q8_gemv", "q8_quantize_x", "q8_gemv_q8x", "q8_gemv_qx",
            "q8_pack_rows16", "mx4_codes_size", "mx4_scales_size", "mx4_quantize", "mx4_dequantize",
            "mx4_pack_rows16", "mx4_gemm_workspace_size", "mx4_gemm", "mx4_gemm_mx4x",
            "moe_calib_read", "moe_calib_mfma")
@@ -103,6 +108,9 @@ def lib() -> ctypes.CDLL:
         L.moe_route_rule.argtypes = [P, P, P, I64, P, P, P, SZ, P]
         L.moe_layer_forward_rule.restype = I32
         L.moe_layer_forward_rule.argtypes = [P, P, P, I64, P, I32, P, P, P, SZ, P]
+        L.moe_block_norm.restype = I32
+        L.moe_block_norm.argtypes = [P, I32, I64, P, I32, I64, P, P, I32, I64, I64, I32, ctypes.c_float, P, P, I32, I64,
+                                     P, I32, I64, I64, I64, P]
         L.q8_gemv.restype = I32
         L.q8_gemv.argtypes = [P, I64, I64, P, P, I32, P]
         L.q8_quantize_x.restype = I32
@@ -509,6 +517,108 @@ def moe_select(logits, top_k: int, rule: RouterRule, topk_idx=None, topk_w=None,
     _mx4_call("moe_select", lib().moe_select, gpu, here, rule.ptr, logits.data_ptr(), code, T, E, ld, top_k,
               topk_idx.data_ptr(), topk_w.data_ptr(), st)
     return topk_idx, topk_w
+
+
+# --------------------------------------------------------- norms around a block
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
+MOE_ACT_NONE, MOE_ACT_SIGMOID, MOE_ACT_SILU = 0, 1, 2
+_ACTS = {"none": MOE_ACT_NONE, "sigmoid": MOE_ACT_SIGMOID, "silu": MOE_ACT_SILU}
+
+
+class Norm:
+    """A norm of ``moe_block_norm`` (``moe_norm``): ``kind`` "rms" or "layer", gain ``offset`` +
+    ``weight`` [H] and ``bias`` [H] (bf16, fp16 or fp32, both of one type; either may be None)."""
+
+    def __init__(self, kind: str = "rms", weight=None, bias=None, eps: float = 1e-6, offset: float = 0.0):
+        kinds = {"rms": MOE_NORM_RMS, "layer": MOE_NORM_LAYER}
+        if kind not in kinds:
+            raise QsmoeError(MOE_ERR_INVALID, "Norm: kind is rms or layer")
+        code = MOE_F32
+        for t in (weight, bias):
+            if t is not None:
+                code = _mx4_code(t.dtype)
+                if code is None or t.dim() != 1 or not t.is_contiguous() or \
+                        (weight is not None and (t.dtype != weight.dtype or t.shape != weight.shape)):
+                    raise QsmoeError(MOE_ERR_INVALID, "Norm: weight and bias must be contiguous [H] of one type")
+        self.weight, self.bias = weight, bias
+        self.desc = moe_norm(kinds[kind], code, eps, offset, _ptr(weight), _ptr(bias))
+        self.ptr = ctypes.addressof(self.desc)
+
+
+def _norm_tensors(n, H: int):
+    """The norm's address and its tensors, checked for their length."""
+    if n is None:
+        return None, None, None
+    for t in (n.weight, n.bias):
+        if t is not None and t.shape[0] != H:
+            raise QsmoeError(MOE_ERR_INVALID, "moe_block_norm: a norm's weight and bias must have one value per column")
+    return n.ptr, n.weight, n.bias
+
+
+def moe_block_norm(y=None, residual=None, post: Optional[Norm] = None, gate=None, gate_act: str = "none",
+                   scale: float = 1.0, pre: Optional[Norm] = None, r_out=None, x_out=None, r_dtype=None, x_dtype=None,
+                   stream=None):
+    """The norms around a block: z = post(y) * act(gate), r = residual + scale * z, x = pre(r), row
+    by row over [T, H]; returns (r, x).
+
+    ``y`` is a block's output (None: ``residual`` goes straight to ``pre``, and r is None), ``residual`` the
+    stream it joins (None: r is scale * z), ``gate`` [T, H] or one value per row ([T] or [T, 1]).  Without
+    ``pre`` x is None.  r has ``residual``'s type and x ``y``'s (or that of the one there is) unless
+    ``r_dtype`` / ``x_dtype`` say otherwise; ``r_out=residual`` updates the stream in place."""
+    where = "moe_block_norm"
+    one = residual if y is None else y
+    if one is None:
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: neither y nor residual")
+    T, H, ld, code = _mx4_values(one, where)
+    py = pr = pg = po = px = None
+    dy = dr = dg = do = dx = ldy = ldr = ldg = ldo = ldx = 0
+    if y is not None:
+        py, ldy, dy = y.data_ptr(), ld, code
+        if residual is not None:
+            rows, cols, ldr, dr = _mx4_values(residual, where)
+            if rows != T or cols != H:
+                raise QsmoeError(MOE_ERR_INVALID, f"{where}: y and residual must have one shape")
+            pr = residual.data_ptr()
+    else:
+        pr, ldr, dr = residual.data_ptr(), ld, code
+    cols = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.unsqueeze(1)
+        rows, cols, ldg, dg = _mx4_values(gate, where)
+        if rows != T or (cols != 1 and cols != H):
+            raise QsmoeError(MOE_ERR_INVALID, f"{where}: gate must be [T, H], [T, 1] or [T]")
+        pg = gate.data_ptr()
+    post_ptr, w1, b1 = _norm_tensors(post, H)
+    pre_ptr, w2, b2 = _norm_tensors(pre, H)
+    if y is None:
+        if r_out is not None:
+            raise QsmoeError(MOE_ERR_INVALID, f"{where}: r_out without y")
+    else:
+        if r_out is None:
+            r_out = _empty((T, H), r_dtype or (y if residual is None else residual).dtype, y.device, stream)
+        rows, c, ldo, do = _mx4_values(r_out, where)
+        if rows != T or c != H:
+            raise QsmoeError(MOE_ERR_INVALID, f"{where}: r_out must be [T, H]")
+        po = r_out.data_ptr()
+    if pre is None:
+        if x_out is not None:
+            raise QsmoeError(MOE_ERR_INVALID, f"{where}: x_out without pre")
+    else:
+        if x_out is None:
+            x_out = _empty((T, H), x_dtype or one.dtype, one.device, stream)
+        rows, c, ldx, dx = _mx4_values(x_out, where)
+        if rows != T or c != H:
+            raise QsmoeError(MOE_ERR_INVALID, f"{where}: x_out must be [T, H]")
+        px = x_out.data_ptr()
+    act = _ACTS.get(gate_act)
+    if act is None:
+        raise QsmoeError(MOE_ERR_INVALID, f"{where}: gate_act is none, sigmoid or silu")
+    gpu = one.get_device()
+    st, here = _mx4_stream(where, stream, gpu, residual, gate, r_out, x_out, w1, b1, w2, b2)
+    _mx4_call(where, lib().moe_block_norm, gpu, here, py, dy, ldy, pr, dr, ldr, post_ptr, pg, dg, ldg, cols, act, scale,
+              pre_ptr, po, do, ldo, px, dx, ldx, T, H, st)
+    return r_out, x_out
 
 
 def q8_gemv(w_tiles, N: int, K: int, x, y=None, y_dtype=None, stream=None):

@@ -472,6 +472,9 @@ moe_status check_mx4_codes(const void *codes, const void *scales) {
     return codes && aligned(codes, 16) && scales && aligned(scales, 4) ? MOE_OK : MOE_ERR_INVALID;
 }
 
+inline bool is_value_type(int32_t t) { return t == MOE_BF16 || t == MOE_F16 || t == MOE_F32; }
+inline size_t type_size(int32_t t) { return t == MOE_F32 ? 4 : 2; }
+
 // a matrix of values with 16-byte aligned rows
 moe_status check_values(const void *x, int32_t dtype, int64_t K, int64_t ld) {
     const int64_t per16 = dtype == MOE_F32 ? 4 : 8;
@@ -495,6 +498,49 @@ moe_status check_mx4_product(const void *wc, const void *wsc, int64_t N, int64_t
 
 bool overlap(const void *a, size_t an, const void *b, size_t bn) {
     return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
+
+constexpr int64_t NORM_MAX_H = 32768;
+
+moe_status check_norm(const moe_norm *n, NormArgs *out) {
+    *out = NormArgs{};
+    if (!n) return MOE_OK;
+    if ((n->kind != MOE_NORM_RMS && n->kind != MOE_NORM_LAYER) || !is_value_type(n->dtype)) return MOE_ERR_INVALID;
+    if (!std::isfinite(n->eps) || n->eps < 0.0f || !std::isfinite(n->offset)) return MOE_ERR_INVALID;
+    const size_t a = type_size(n->dtype);
+    if ((n->weight && !aligned(n->weight, a)) || (n->bias && !aligned(n->bias, a))) return MOE_ERR_INVALID;
+    out->on = 1;
+    out->layer = n->kind == MOE_NORM_LAYER;
+    out->dtype = n->dtype;
+    out->eps = n->eps;
+    out->offset = n->offset;
+    out->w = n->weight;
+    out->b = n->bias;
+    return MOE_OK;
+}
+
+// rows of `cols` values, `ld` apart
+struct Rows {
+    const void *p;
+    int32_t dtype;
+    int64_t ld, cols;
+    bool ok() const { return p && is_value_type(dtype) && aligned(p, type_size(dtype)) && ld >= cols; }
+    size_t width() const { return (size_t)cols * type_size(dtype); }
+    size_t pitch() const { return (size_t)ld * type_size(dtype); }
+    size_t bytes(int64_t T) const { return (size_t)(T - 1) * pitch() + width(); }
+};
+
+// whether an output shares memory with another tensor otherwise than value for value (which is
+// fine where a row is read whole before it is written); same: allow that
+bool rows_clash(const Rows &o, const Rows &q, int64_t T, bool same) {
+    if (!o.p || !q.p) return false;
+    if (same && o.p == q.p && o.dtype == q.dtype && (o.ld == q.ld || T == 1) && o.cols == q.cols) return false;
+    if (!overlap(o.p, o.bytes(T), q.p, q.bytes(T))) return false;
+    if (o.pitch() != q.pitch() || T == 1) return true;
+    // rows as far apart in both: column ranges of one matrix
+    const uintptr_t a = (uintptr_t)o.p, b = (uintptr_t)q.p, pitch = o.pitch();
+    const size_t d = a < b ? (b - a) % pitch : (pitch - (a - b) % pitch) % pitch;     // q's columns behind o's
+    return !(d >= o.width() && d + q.width() <= pitch);
 }
 
 }  // namespace
@@ -581,6 +627,58 @@ moe_status moe_layer_forward_static(const moe_layer_desc *d, const void *x, int6
     void *ws = nullptr;
     if ((s = scratch_for_current_device(&ws))) return s;
     return forward_impl(d, nullptr, x, T, y, y_dtype, topk_idx, topk_w, ws, SCRATCH_BYTES, stream);
+}
+
+moe_status moe_block_norm(const void *y, int32_t y_dtype, int64_t ldy, const void *r, int32_t r_dtype, int64_t ldr,
+                          const moe_norm *post, const void *gate, int32_t gate_dtype, int64_t ldg, int64_t gate_cols,
+                          int32_t gate_act, float scale, const moe_norm *pre, void *r_out, int32_t r_out_dtype, int64_t ldro,
+                          void *x, int32_t x_dtype, int64_t ldx, int64_t T, int64_t H, void *stream) {
+    if (T < 0 || H < 0) return MOE_ERR_INVALID;
+    if (H < 1 || H > NORM_MAX_H || T > MX4_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+    if (gate_act != MOE_ACT_NONE && gate_act != MOE_ACT_SIGMOID && gate_act != MOE_ACT_SILU) return MOE_ERR_INVALID;
+    if (!std::isfinite(scale)) return MOE_ERR_INVALID;
+    if (gate && gate_cols != 1 && gate_cols != H) return MOE_ERR_INVALID;
+    BlockNormArgs a{};
+    moe_status s;
+    if ((s = check_norm(post, &a.post)) || (s = check_norm(pre, &a.pre))) return s;
+    if (T == 0) return MOE_OK;
+    // what there is has to make sense: an output, something it comes from, nothing that no one reads
+    if ((!y && (!r || post || gate || r_out)) || (!x != !pre) || (!r_out && !x)) return MOE_ERR_INVALID;
+    const Rows in[3] = {{y, y_dtype, ldy, H}, {r, r_dtype, ldr, H}, {gate, gate_dtype, ldg, gate_cols}},
+               out[2] = {{r_out, r_out_dtype, ldro, H}, {x, x_dtype, ldx, H}};
+    for (const Rows &q : in)
+        if (q.p && !q.ok()) return MOE_ERR_INVALID;
+    for (const Rows &o : out) {
+        if (!o.p) continue;
+        if (!o.ok()) return MOE_ERR_INVALID;
+        for (const Rows &q : in)
+            if (rows_clash(o, q, T, true)) return MOE_ERR_INVALID;
+        for (const NormArgs *n : {&a.post, &a.pre})
+            for (const void *w : {n->w, n->b})
+                if (w && overlap(o.p, o.bytes(T), w, (size_t)H * type_size(n->dtype))) return MOE_ERR_INVALID;
+    }
+    if (rows_clash(out[0], out[1], T, false)) return MOE_ERR_INVALID;
+    a.y = y;
+    a.r = r;
+    a.gate = gate;
+    a.ro = r_out;
+    a.xo = x;
+    a.dy = y_dtype;
+    a.dr = r_dtype;
+    a.dg = gate_dtype;
+    a.dro = r_out_dtype;
+    a.dxo = x_dtype;
+    a.ldy = ldy;
+    a.ldr = ldr;
+    a.ldg = ldg;
+    a.ldro = ldro;
+    a.ldxo = ldx;
+    a.gate_cols = H == 1 ? 1 : (int)gate_cols;
+    a.act = gate_act;
+    a.scale = scale;
+    a.T = T;
+    a.H = (int)H;
+    return dev(launch_block_norm(a, (hipStream_t)stream));
 }
 
 moe_status q8_gemv(const void *w_tiles, int64_t N, int64_t K, const void *x, void *y,

@@ -182,6 +182,24 @@ hipError_t launch_mx_group(const Layer &L, const uint16_t *x, int64_t T, const P
 hipError_t launch_select(const RouteRule &rule, const void *logits, int dtype, int64_t T, int E, int64_t ld, int K,
                          int32_t *idx, float *w, hipStream_t s);
 
+struct NormArgs {
+    int on, layer, dtype;          // dtype: of w and b
+    float eps, offset;
+    const void *w, *b;             // [H] or null
+};
+struct BlockNormArgs {
+    const void *y, *r, *gate;      // null: absent
+    void *ro, *xo;
+    int dy, dr, dg, dro, dxo;      // types
+    int64_t ldy, ldr, ldg, ldro, ldxo;
+    NormArgs post, pre;
+    int gate_cols, act;            // 1: a value per row; else elementwise
+    float scale;
+    int64_t T;
+    int H;
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t s);
+
 // ---------------------------------------------------------------- measured ceilings
 hipError_t launch_calib_read(const void *buf, int64_t bytes, uint32_t *out, hipStream_t s);
 hipError_t launch_calib_mfma(int iters, int blocks, float *out, hipStream_t s);
