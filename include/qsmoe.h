@@ -461,6 +461,34 @@ moe_status mx4_gemm_mx4x(const void *w_codes, const void *w_scales, int64_t N, i
                          void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * Low-rank adapters of many requests, added to a shared projection's result (mx4_gemm, q8_gemv or
+ * any other):
+ *     y[t] = base[t] + scales[a] B_a (A_a x[t]),  a = ids[t];   y[t] = base[t] where a token has none
+ *   a       [n_adapters][R][K] bf16, b [n_adapters][N][R] bf16, contiguous, 16-byte aligned
+ *   scales  [n_adapters] fp32, or NULL: 1
+ *   ranks   [n_adapters] int32, or NULL: R.  Rows of A and columns of B past an adapter's rank are
+ *           not used, whatever they hold (a rank above R counts as R, a negative one as 0)
+ *   ids     [T] int32; an id outside [0, n_adapters) is a token without an adapter
+ *   x       [T][K] bf16, row stride ldx, rows 16-byte aligned
+ *   base    [T][N] of y's type, row stride ldb, or NULL: zeros
+ *   y       [T][N], row stride ldy, y_dtype MOE_BF16 (rounded to nearest even) or MOE_F32; it may be base
+ *           (same pointer and stride: in place, tokens without an adapter are not touched), or other
+ *           columns of its matrix; any other overlap with an input is MOE_ERR_INVALID
+ *   ws      device workspace of ws_bytes >= lora_workspace_size(T, R), 256-byte aligned, contents undefined
+ *           before and after (one for T tokens also serves fewer); calls that share it must not
+ *           overlap in time.
+ * Products are exact and sums fp32; A_a x[t] times its scale is carried to 2^-16 of itself for a bf16 y,
+ * to 2^-24 for an fp32 one.  A token's result does not depend on the other tokens.
+ * Limits (else MOE_ERR_UNSUPPORTED): R % 8 == 0, 8 <= R <= 256, K % 8 == 0, 8 <= K <= 65536, N <= 2^23,
+ * 1 <= n_adapters <= 65536, T <= 2^20.  T == 0 or N == 0 enqueues nothing.
+ */
+size_t lora_workspace_size(int64_t T, int64_t R);
+moe_status lora_gemm(const void *a, const void *b, const float *scales, const int32_t *ranks, int64_t n_adapters,
+                     int64_t R, int64_t K, int64_t N, const int32_t *ids, const void *x, int64_t T, int64_t ldx,
+                     const void *base, int64_t ldb, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
+                     void *stream);
+
+/*
  * Measured ceilings ([LILY] "Limits of further optimization": kernels are judged
  * against the fastest sustained rate of their resource, next to the data-sheet peak).
  * Measurement helpers only; they compute nothing the layer uses.

@@ -8,7 +8,11 @@ are allocated here with torch.  The functions carry the names of the C entry poi
     moe_workspace_size, moe_workspace_status, moe_route, moe_layer_forward, q8_gemv,
     q8_quantize_x, q8_gemv_q8x, q8_gemv_qx, q8_pack_rows16,
     mx4_quantize, mx4_dequantize, mx4_pack_rows16, mx4_gemm, mx4_gemm_mx4x,
-    mx4_codes_size, mx4_scales_size, mx4_gemm_workspace_size
+    mx4_codes_size, mx4_scales_size, mx4_gemm_workspace_size,
+    moe_select, moe_block_norm, lora_gemm, lora_workspace_size
+
+``RouterRule`` (``rule=`` of moe_route and moe_layer_forward), ``Norm`` and ``LoraAdapters``
+(``adapters=`` of mx4_gemm) hold what describes a rule, a norm and a projection's adapters.
 
 ``LayerDesc.from_host`` uploads an affine-quantized layer, ``LayerDesc.from_mx4`` takes one
 whose expert matrices are MX4 (quantized or repacked on the device by the functions above).
@@ -74,7 +78,7 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_size",
            "moe_block_norm", "q8_gemv", "q8_quantize_x", "q8_gemv_q8x", "q8_gemv_qx",
            "q8_pack_rows16", "mx4_codes_size", "mx4_scales_size", "mx4_quantize", "mx4_dequantize",
            "mx4_pack_rows16", "mx4_gemm_workspace_size", "mx4_gemm", "mx4_gemm_mx4x",
-           "moe_calib_read", "moe_calib_mfma")
+           "lora_workspace_size", "lora_gemm", "moe_calib_read", "moe_calib_mfma")
 
 
 def lib() -> ctypes.CDLL:
@@ -137,6 +141,10 @@ def lib() -> ctypes.CDLL:
         L.mx4_gemm.argtypes = [P, P, I64, I64, P, I64, I64, P, I32, I64, P, SZ, P]
         L.mx4_gemm_mx4x.restype = I32
         L.mx4_gemm_mx4x.argtypes = [P, P, I64, I64, P, P, I64, P, I32, I64, P, SZ, P]
+        L.lora_workspace_size.restype = SZ
+        L.lora_workspace_size.argtypes = [I64, I64]
+        L.lora_gemm.restype = I32
+        L.lora_gemm.argtypes = [P, P, P, P, I64, I64, I64, I64, P, P, I64, I64, P, I64, P, I32, I64, P, SZ, P]
         L.moe_calib_read.restype = I32
         L.moe_calib_read.argtypes = [P, SZ, P]
         L.moe_calib_mfma.restype = I32
@@ -850,8 +858,17 @@ def _mx4_product(where, f, w_codes, w_scales, N, K, T, x1, x2, x_args, y, y_dtyp
     return y
 
 
-def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspace=None, stream=None):
-    """``y`` [T, N] = ``x`` [T, K] (bf16) times the transpose of an MX4 matrix in tiles."""
+def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspace=None, stream=None,
+             adapters: Optional["LoraAdapters"] = None, adapter_ids=None, adapter_workspace=None):
+    """``y`` [T, N] = ``x`` [T, K] (bf16) times the transpose of an MX4 matrix in tiles, plus each
+    token's adapter where ``adapters`` and ``adapter_ids`` are given (``lora_gemm`` in place: where
+    ``y`` is bf16 the product is rounded to it before the adapter is added)."""
+    if adapters is not None:
+        if adapters.N != N or adapters.K != K:
+            _mx4_bad("mx4_gemm", "the adapters are of a matrix of another size")
+        _lora_ids(adapters, adapter_ids, x.shape[0], "mx4_gemm")
+        y = mx4_gemm(w_codes, w_scales, N, K, x, y, y_dtype, workspace, stream)
+        return lora_gemm(adapters, adapter_ids, x, base=y, y=y, workspace=adapter_workspace, stream=stream)
     T, k, ldx, code = _mx4_values(x, "mx4_gemm")
     if k != K or code != MOE_BF16:
         _mx4_bad("mx4_gemm", "x must be bf16 with K columns")
@@ -865,6 +882,79 @@ def mx4_gemm_mx4x(w_codes, w_scales, N: int, K: int, x_codes, x_scales, T: int, 
     xc, xs = _mx4_weights(x_codes, x_scales, T, K, "mx4_gemm_mx4x")
     return _mx4_product("mx4_gemm_mx4x", lib().mx4_gemm_mx4x, w_codes, w_scales, N, K, T, x_codes, x_scales,
                         (xc, xs, T), y, y_dtype, workspace, stream)
+
+
+# ------------------------------------------------------------- low-rank adapters
+class LoraAdapters:
+    """Adapters of one projection: ``a`` [n, R, K] and ``b`` [n, N, R] bf16, ``scales`` fp32 [n]
+    (default 1) and ``ranks`` int32 [n] (default R), all on one device."""
+
+    def __init__(self, a, b, scales=None, ranks=None):
+        import torch
+        where = "LoraAdapters"
+        bits = (torch.bfloat16, torch.int16)
+        if a.dim() != 3 or b.dim() != 3 or a.dtype not in bits or b.dtype not in bits \
+                or not a.is_contiguous() or not b.is_contiguous():
+            _mx4_bad(where, "a and b must be contiguous bf16 [n, R, K] and [n, N, R]")
+        self.n, self.R, self.K = a.shape
+        self.N = b.shape[1]
+        if b.shape[0] != self.n or b.shape[2] != self.R:
+            _mx4_bad(where, "a and b must have the same n and R")
+        for t, dtype, what in ((scales, torch.float32, "scales"), (ranks, torch.int32, "ranks")):
+            if t is not None and (t.dtype != dtype or t.shape != (self.n,) or not t.is_contiguous()):
+                _mx4_bad(where, f"{what} must be contiguous [n] of type {dtype}")
+        if any(t is not None and t.device != a.device for t in (b, scales, ranks)):
+            _mx4_bad(where, "the tensors must be on one device")
+        self.a, self.b, self.scales, self.ranks = a, b, scales, ranks
+        self._args = (a.data_ptr(), b.data_ptr(), _ptr(scales), _ptr(ranks), self.n, self.R, self.K, self.N)
+
+
+@functools.lru_cache(maxsize=4096)
+def lora_workspace_size(T: int, R: int) -> int:
+    """Bytes of workspace of ``lora_gemm`` calls of T tokens (or fewer) with adapters of rank R."""
+    n = lib().lora_workspace_size(int(T), int(R))
+    if n == ctypes.c_size_t(-1).value:
+        raise QsmoeError(MOE_ERR_UNSUPPORTED, "lora_workspace_size")
+    return n
+
+
+def lora_new_workspace(adapters: LoraAdapters, T: int, stream=None):
+    """A workspace for calls of T tokens or fewer with these adapters."""
+    return _empty((max(lora_workspace_size(T, adapters.R), 256),), _torch().uint8, adapters.a.device, stream)
+
+
+def _lora_ids(adapters: LoraAdapters, ids, T: int, where: str) -> None:
+    if ids is None or ids.dtype != _torch().int32 or ids.shape != (T,) or not ids.is_contiguous():
+        _mx4_bad(where, "adapter ids must be contiguous int32 [T]")
+
+
+def lora_gemm(adapters: LoraAdapters, ids, x, base=None, y=None, y_dtype=None, workspace=None, stream=None):
+    """``y`` [T, N] = ``base`` + scale B (A x) with each token's adapter (``ids`` int32 [T]; out of range: none)
+    for ``x`` [T, K] (bf16).  ``base`` (None: zeros) has y's type; ``y=base`` adds in place."""
+    where = "lora_gemm"
+    T, k, ldx, code = _mx4_values(x, where)
+    N = adapters.N
+    if k != adapters.K or code != MOE_BF16:
+        _mx4_bad(where, "x must be bf16 with K columns")
+    _lora_ids(adapters, ids, T, where)
+    if y is None:
+        y = _empty((T, N), y_dtype or (_torch().float32 if base is None else base.dtype), x.device, stream)
+    rows, cols, ldy, code = _mx4_values(y, where)
+    if rows != T or cols != N:
+        _mx4_bad(where, "y must be [T, N]")
+    pb, ldb = None, 0
+    if base is not None:
+        rows, cols, ldb, bcode = _mx4_values(base, where)
+        if rows != T or cols != N or bcode != code:
+            _mx4_bad(where, "base must be [T, N] of y's type")
+        pb = base.data_ptr()
+    if workspace is None:
+        workspace = lora_new_workspace(adapters, T, stream)
+    gpu = x.get_device()
+    st, here = _mx4_stream(where, stream, gpu, adapters.a, ids, y, base, workspace)
+    _mx4_call(where, lib().lora_gemm, gpu, here, *adapters._args, ids.data_ptr(), x.data_ptr(), T, ldx, pb, ldb,
+              y.data_ptr(), code, ldy, _mx4_buf(workspace, 0, where), workspace.nbytes, st)
+    return y
 
 
 def moe_calib_read(buf, stream=None):

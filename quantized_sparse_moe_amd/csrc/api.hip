@@ -501,6 +501,7 @@ bool overlap(const void *a, size_t an, const void *b, size_t bn) {
 }
 
 constexpr int64_t NORM_MAX_H = 32768;
+constexpr int64_t LORA_MAX_R = 256, LORA_MAX_N = 1 << 23, LORA_MAX_ADAPTERS = 65536;
 
 moe_status check_norm(const moe_norm *n, NormArgs *out) {
     *out = NormArgs{};
@@ -679,6 +680,57 @@ moe_status moe_block_norm(const void *y, int32_t y_dtype, int64_t ldy, const voi
     a.T = T;
     a.H = (int)H;
     return dev(launch_block_norm(a, (hipStream_t)stream));
+}
+
+size_t lora_workspace_size(int64_t T, int64_t R) {
+    if (R < 8 || R > LORA_MAX_R || R % 8 || T > MAX_TOKENS) return SIZE_MAX;
+    return T <= 0 ? 0 : up((size_t)T * LORA_PARTS * R * 2);
+}
+
+moe_status lora_gemm(const void *a, const void *b, const float *scales, const int32_t *ranks, int64_t n_adapters,
+                     int64_t R, int64_t K, int64_t N, const int32_t *ids, const void *x, int64_t T, int64_t ldx,
+                     const void *base, int64_t ldb, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
+                     void *stream) {
+    if (T < 0 || N < 0 || n_adapters < 0) return MOE_ERR_INVALID;
+    if (y_dtype != MOE_BF16 && y_dtype != MOE_F32) return MOE_ERR_INVALID;
+    if (R < 8 || R > LORA_MAX_R || R % 8 || K < 8 || K > MX4_MAX_K || K % 8 || N > LORA_MAX_N ||
+        n_adapters < 1 || n_adapters > LORA_MAX_ADAPTERS || T > MAX_TOKENS)
+        return MOE_ERR_UNSUPPORTED;
+    if (T == 0 || N == 0) return MOE_OK;
+    if (!a || !aligned(a, 16) || !b || !aligned(b, 16) || !ids || !aligned(ids, 4) || (scales && !aligned(scales, 4)) ||
+        (ranks && !aligned(ranks, 4)))
+        return MOE_ERR_INVALID;
+    if (!x || !aligned(x, 16) || ldx < K || (T > 1 && ldx % 8)) return MOE_ERR_INVALID;
+    const Rows xr{x, MOE_BF16, ldx, K}, br{base, y_dtype, ldb, N}, yr{y, y_dtype, ldy, N};
+    if (!yr.ok() || (base && !br.ok())) return MOE_ERR_INVALID;
+    if (rows_clash(yr, br, T, true) || rows_clash(yr, xr, T, false)) return MOE_ERR_INVALID;
+    const size_t nb = yr.bytes(T), need = lora_workspace_size(T, R);
+    if (overlap(y, nb, a, (size_t)(n_adapters * R * K) * 2) || overlap(y, nb, b, (size_t)(n_adapters * N * R) * 2) ||
+        overlap(y, nb, ids, (size_t)T * 4) || (scales && overlap(y, nb, scales, (size_t)n_adapters * 4)) ||
+        (ranks && overlap(y, nb, ranks, (size_t)n_adapters * 4)))
+        return MOE_ERR_INVALID;
+    if (!ws || !aligned(ws, ALIGN) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if (overlap(y, nb, ws, need)) return MOE_ERR_INVALID;
+    LoraArgs g{};
+    g.a = (const uint16_t *)a;
+    g.b = (const uint16_t *)b;
+    g.scales = scales;
+    g.ranks = ranks;
+    g.ids = ids;
+    g.x = (const uint16_t *)x;
+    g.base = base;
+    g.y = y;
+    g.v = (uint16_t *)ws;
+    g.T = T;
+    g.ldx = ldx;
+    g.ldb = ldb;
+    g.ldy = ldy;
+    g.N = N;
+    g.n = (int)n_adapters;
+    g.R = (int)R;
+    g.K = (int)K;
+    g.f32 = y_dtype == MOE_F32;
+    return dev(launch_lora(g, (hipStream_t)stream));
 }
 
 moe_status q8_gemv(const void *w_tiles, int64_t N, int64_t K, const void *x, void *y,

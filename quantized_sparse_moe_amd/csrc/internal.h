@@ -200,6 +200,21 @@ struct BlockNormArgs {
 };
 hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t s);
 
+struct LoraArgs {
+    const uint16_t *a, *b;         // [n][R][K], [n][N][R] bf16
+    const float *scales;           // [n] or null
+    const int32_t *ranks;          // [n] or null
+    const int32_t *ids;            // [T]
+    const uint16_t *x;             // [T] rows, ldx apart
+    const void *base;              // [T] rows of y's type, or null
+    void *y;
+    uint16_t *v;                   // workspace: [T][parts][R] bf16
+    int64_t T, ldx, ldb, ldy, N;
+    int n, R, K, f32;
+};
+constexpr int LORA_PARTS = 3;      // bf16 parts of a value of v, at most
+hipError_t launch_lora(const LoraArgs &a, hipStream_t s);
+
 // ---------------------------------------------------------------- measured ceilings
 hipError_t launch_calib_read(const void *buf, int64_t bytes, uint32_t *out, hipStream_t s);
 hipError_t launch_calib_mfma(int iters, int blocks, float *out, hipStream_t s);

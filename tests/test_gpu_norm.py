@@ -178,7 +178,7 @@ def test_large_small_and_constant_rows(torch, qs):
 
 
 def test_offsets_past_32_bits(torch, qs):
-    ld = (1 << 31) // 3 + 8                                  # (whole 16-byte pieces)
+    ld = ((1 << 31) // 3 + 8) // 8 * 8                       # (16-byte aligned rows)
     for off in (0, 1):
         H = 64
         buf = torch.empty(4 * ld + H + 1, dtype=torch.bfloat16, device="cuda")
