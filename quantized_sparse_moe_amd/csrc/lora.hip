@@ -5,11 +5,11 @@
 //   shrink  v = scale_a A_a x_t, summed in fp32 over the columns, which the waves of a workgroup share.  v is kept
 //           as a sum of bf16 parts (two, or three where y is fp32: v to 2^-16 or 2^-24), one behind the
 //           other, so that the second product runs on the same instruction.
-//   expand  y = base + B_a v over those parts, each against the same rows of B.
+//   expand  y = base + B_a v, each part of v against the same rows of B in registers.
 //
 // A tile's tokens need not share an adapter: its distinct ones are taken one after another, each against
-// all 16 rows of the tile, and a token keeps the result of its own.  A token's result depends on its own
-// row only, bit for bit.
+// all 16 rows of the tile, and a token keeps the result of its own (few tokens: by workgroups of their
+// own, "slots").  A token's result depends on its own row only, bit for bit.
 #include "common.h"
 #include "internal.h"
 
@@ -17,19 +17,22 @@ namespace qs {
 
 namespace {
 
-// lane n < 16 of every 16 holds token n's adapter (-1: none); the distinct ones in token order
+// lane n < 16 of every 16 holds token n's adapter (-1: none) and its place among the tile's distinct
+// ones, which are numbered in token order
 struct TileIds {
-    int id;                                                  // of token lane % 16
+    int id, ord;
     uint32_t first;                                          // bit n: token n is its adapter's first
     __device__ __forceinline__ void load(const int32_t *ids, int64_t t0, int64_t T, int n_adapters) {
         const int n = threadIdx.x & 15;
         id = t0 + n < T ? ids[t0 + n] : -1;
         if (id < 0 || id >= n_adapters) id = -1;
-        bool dup = id < 0;
+        int lead = n;
 #pragma unroll
-        for (int j = 0; j < 15; ++j) dup |= j < n && __builtin_amdgcn_readlane(id, j) == id;
-        first = (uint32_t)__ballot(!dup) & 0xffffu;
+        for (int j = 14; j >= 0; --j) lead = j < n && __builtin_amdgcn_readlane(id, j) == id ? j : lead;
+        first = (uint32_t)__ballot(id >= 0 && lead == n) & 0xffffu;
+        ord = id < 0 ? 0 : __popc(first & ((1u << lead) - 1u));
     }
+    __device__ __forceinline__ int adapter(uint32_t m) const { return __builtin_amdgcn_readlane(id, __builtin_ctz(m)); }
 };
 
 __device__ __forceinline__ int rank_of(const LoraArgs &a, int ad) {
@@ -38,10 +41,10 @@ __device__ __forceinline__ int rank_of(const LoraArgs &a, int ad) {
 
 // -------------------------------------------------------------------------- shrink
 // One workgroup per (tile, 16 RB ranks, slot): the slot-th, slot + slots-th .. distinct adapters of the
-// tile.
+// tile.  SU column steps a wave are loaded at a time.
 constexpr int SH_WAVES = 8;
 
-template <int RB, int PARTS>
+template <int RB, int SU, int PARTS>
 __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
     __shared__ f32x4 red[SH_WAVES][RB][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
@@ -53,23 +56,31 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
     int k = 0;
     for (uint32_t m = tile.first; m; m &= m - 1, ++k) {
         if (k % (int)gridDim.z != (int)blockIdx.z) continue;
-        const int ad = __builtin_amdgcn_readlane(tile.id, __builtin_ctz(m)), rank = rank_of(a, ad);
+        const int ad = tile.adapter(m), rank = rank_of(a, ad);
         f32x4 acc[RB];
 #pragma unroll
         for (int i = 0; i < RB; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
         const uint16_t *ar = a.a + (int64_t)ad * R * K;
-        for (int s = wave; s < steps; s += SH_WAVES) {
-            const int c = 32 * s + 8 * g;
-            u32x4 A = {0u, 0u, 0u, 0u};
-            if (c < K) A = *(const u32x4 *)(xr + c);
+        for (int s0 = wave; s0 < steps; s0 += SU * SH_WAVES) {
+            u32x4 A[SU], B[SU][RB];
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const int r = r0 + 16 * i + n;
-                u32x4 B = {0u, 0u, 0u, 0u};
-                if (c < K && r < rank) B = *(const u32x4 *)(ar + (int64_t)r * K + c);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A), __builtin_bit_cast(bf16x8, B),
-                                                                 acc[i], 0, 0, 0);
+            for (int u = 0; u < SU; ++u) {
+                const int c = 32 * (s0 + u * SH_WAVES) + 8 * g;
+                A[u] = (u32x4){0u, 0u, 0u, 0u};
+                if (c < K) A[u] = *(const u32x4 *)(xr + c);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    const int r = r0 + 16 * i + n;
+                    B[u][i] = (u32x4){0u, 0u, 0u, 0u};
+                    if (c < K && r < rank) B[u][i] = *(const u32x4 *)(ar + (int64_t)r * K + c);
+                }
             }
+#pragma unroll
+            for (int u = 0; u < SU; ++u)
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A[u]),
+                                                                     __builtin_bit_cast(bf16x8, B[u][i]), acc[i], 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i) red[wave][i][lane] = acc[i];
@@ -97,92 +108,180 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
 }
 
 // -------------------------------------------------------------------------- expand
-// A wave takes 64 columns of y: lane n + 16 g holds the 16 columns 16 g .. + 15 of them for token n
-// (operand row i of product m is column 16 (i / 4) + 4 m + i % 4 of B).
+// A wave takes 64 columns of y for `tt` tiles of tokens, and keeps an adapter's rows of B (RS steps of 32
+// ranks) in registers until a tile has another.  The weights are the first operand, so that a
+// lane's registers are columns of one token (lane % 16): operand row n of product i is column
+// 16 i + n of the 64 (fp32 y: 16 bytes a register quad), or 32 (i / 2) + 8 (n / 4) + 4 (i % 2) + n % 4 (bf16: two
+// quads make 16 bytes), so that four lanes read and write 64 bytes in a row.
 constexpr int EX_WAVES = 4;
 
-template <int PARTS, bool F32>
-__global__ __launch_bounds__(64 * EX_WAVES) void k_lora_expand(LoraArgs a) {
+template <int PARTS, bool F32, bool VEC, int RS>
+__global__ __launch_bounds__(64 * EX_WAVES) void k_lora_expand(LoraArgs a, int tt) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-    const int64_t t0 = (int64_t)blockIdx.x * 16;
-    TileIds tile;
-    tile.load(a.ids, t0, a.T, a.n);
-    const int R = a.R, R8 = R / 8, steps = (PARTS * R8 + 3) / 4;
-    const int64_t c0 = ((int64_t)blockIdx.y * EX_WAVES + wave) * 64, N = a.N, t = t0 + n;
+    const int R = a.R, slot = blockIdx.z, slots = gridDim.z;
+    const int64_t c0 = ((int64_t)blockIdx.y * EX_WAVES + wave) * 64, N = a.N;
     if (c0 >= N) return;
-    float out[16];
+    auto column = [&](int i, int row) { return c0 + (F32 ? 16 * i + row : 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3)); };
+    u32x4 B[RS][4];
+    int held = -1, rank = 0;
+    auto load_b = [&](int ad, int s0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) out[i] = 0.0f;
-    const int slot = blockIdx.z, slots = gridDim.z;
-    bool have = slot == 0 && tile.id < 0;                    // (tokens without an adapter: the first slot's)
-    int k = 0;
-    for (uint32_t m = tile.first; m; m &= m - 1, ++k) {
-        if (k % slots != slot) continue;
-        const int ad = __builtin_amdgcn_readlane(tile.id, __builtin_ctz(m)), rank = rank_of(a, ad);
-        f32x4 acc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        const bool mine = tile.id == ad;
-        const uint16_t *vr = a.v + t * PARTS * R;
-        for (int s = 0; s < steps; ++s) {
-            const int q = 4 * s + g, r8 = 8 * (q % R8);      // 8 ranks of a part
-            u32x4 V = {0u, 0u, 0u, 0u};
-            if (mine && q < PARTS * R8) V = *(const u32x4 *)(vr + 8 * q);
+        for (int s = 0; s < RS; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t c = c0 + 16 * (n >> 2) + 4 * i + (n & 3);
-                u32x4 B = {0u, 0u, 0u, 0u};
-                if (c < N && q < PARTS * R8 && r8 < rank) {
-                    B = *(const u32x4 *)(a.b + ((int64_t)ad * N + c) * R + r8);
-                    if (r8 + 8 > rank)                       // (past the rank: anything)
+                const int r8 = 32 * (s0 + s) + 8 * g;
+                const int64_t c = column(i, n);
+                B[s][i] = (u32x4){0u, 0u, 0u, 0u};
+                if (c < N && r8 < rank) B[s][i] = *(const u32x4 *)(a.b + ((int64_t)ad * N + c) * R + r8);
+            }
+        if (rank & 7)                                        // (past the rank: anything)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (r8 + 2 * j >= rank) B[j] = 0u;
-                            else if (r8 + 2 * j + 1 >= rank) B[j] &= 0xffffu;
-                        }
-                }
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, B), __builtin_bit_cast(bf16x8, V),
-                                                                 acc[i], 0, 0, 0);
+            for (int s = 0; s < RS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 32 * (s0 + s) + 8 * g + 2 * j;
+                        if (r >= rank) B[s][i][j] = 0u;
+                        else if (r + 1 >= rank) B[s][i][j] &= 0xffffu;
+                    }
+    };
+    const int64_t tiles = (a.T + 15) / 16, last = min((int64_t)(blockIdx.x + 1) * tt, tiles);
+    for (int64_t ti = (int64_t)blockIdx.x * tt; ti < last; ++ti) {
+        TileIds tile;
+        tile.load(a.ids, ti * 16, a.T, a.n);
+        const int64_t t = ti * 16 + n;
+        // rows of this slot; in place, rows without an adapter stay
+        const bool live = t < a.T && tile.ord % slots == slot && (tile.id >= 0 || a.base != a.y);
+        // base, as its register quads
+        f32x4 out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        u32x4 raw[F32 ? 4 : 2];
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+                raw[i] = (u32x4){0u, 0u, 0u, 0u};
+                const int64_t c = column(F32 ? i : 2 * i, 4 * g);
+                if (a.base && live && c < N)
+                    raw[i] = F32 ? *(const u32x4 *)((const float *)a.base + t * a.ldb + c)
+                                 : *(const u32x4 *)((const uint16_t *)a.base + t * a.ldb + c);
             }
         }
-        if (mine) {
-            have = true;
+        for (uint32_t m = tile.first, k = 0; m; m &= m - 1, ++k) {
+            if ((int)k % slots != slot) continue;
+            const int ad = tile.adapter(m);
+            const bool mine = tile.id == ad;
+            if (ad != held) rank = rank_of(a, ad);
+            f32x4 acc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            const uint16_t *vr = a.v + t * PARTS * R;
+            for (int s0 = 0; 32 * s0 < rank; s0 += RS) {
+                u32x4 V[RS][PARTS];
+#pragma unroll
+                for (int s = 0; s < RS; ++s)
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) {
+                        const int r8 = 32 * (s0 + s) + 8 * g;
+                        V[s][p] = (u32x4){0u, 0u, 0u, 0u};
+                        if (mine && r8 < rank) V[s][p] = *(const u32x4 *)(vr + p * R + r8);
+                    }
+                if (ad != held || R > 32 * RS) load_b(ad, s0);
+#pragma unroll
+                for (int s = 0; s < RS; ++s)
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, B[s][i]),
+                                                                             __builtin_bit_cast(bf16x8, V[s][p]), acc[i], 0, 0, 0);
+            }
+            held = ad;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) out[4 * i + r] = acc[i][r];
+                for (int r = 0; r < 4; ++r) out[i][r] = mine ? acc[i][r] : out[i][r];
         }
-    }
-    if (!have || t >= a.T) return;
-    if (tile.id < 0 && a.base == a.y) return;                // (in place: nothing to add)
-    const int64_t c = c0 + 16 * g;
+        if (!live) continue;
+        if constexpr (VEC) {
+            if constexpr (F32) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if (c + i >= N) break;
-        if constexpr (F32) {
-            float v = out[i];
-            if (a.base) v += ((const float *)a.base)[t * a.ldb + c + i];
-            ((float *)a.y)[t * a.ldy + c + i] = v;
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t c = column(i, 4 * g);
+                    if (c < N) *(f32x4 *)((float *)a.y + t * a.ldy + c) = out[i] + __builtin_bit_cast(f32x4, raw[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t c = column(2 * i, 4 * g);
+                    u32x4 w;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float lo = out[2 * i + (j >> 1)][2 * (j & 1)] + __uint_as_float(raw[i][j] << 16);
+                        const float hi = out[2 * i + (j >> 1)][2 * (j & 1) + 1] + __uint_as_float(raw[i][j] & 0xffff0000u);
+                        w[j] = f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
+                    }
+                    if (c < N) *(u32x4 *)((uint16_t *)a.y + t * a.ldy + c) = w;
+                }
+            }
         } else {
-            float v = out[i];
-            if (a.base) v += bf16_to_f32(((const uint16_t *)a.base)[t * a.ldb + c + i]);
-            ((uint16_t *)a.y)[t * a.ldy + c + i] = f32_to_bf16(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t c = column(i, 4 * g + r);
+                    if (c >= N) continue;
+                    float v = out[i][r];
+                    if constexpr (F32) {
+                        if (a.base) v += ((const float *)a.base)[t * a.ldb + c];
+                        ((float *)a.y)[t * a.ldy + c] = v;
+                    } else {
+                        if (a.base) v += bf16_to_f32(((const uint16_t *)a.base)[t * a.ldb + c]);
+                        ((uint16_t *)a.y)[t * a.ldy + c] = f32_to_bf16(v);
+                    }
+                }
         }
     }
+}
+
+template <int PARTS, bool F32>
+hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
+    const int64_t tiles = (a.T + 15) / 16, rblk = (a.R + 15) / 16, cus = n_compute_units();
+    // a tile's distinct adapters, at most; workgroups of their own until two a compute unit
+    const int64_t most = a.T < 16 ? (a.T < a.n ? a.T : a.n) : (a.n < 16 ? a.n : 16);
+    auto slots = [&](int64_t groups) {
+        int64_t k = (2 * cus + groups - 1) / groups;
+        return (unsigned)(k < most ? k : most);
+    };
+    const int rb = tiles >= cus && rblk >= 4 ? 4 : tiles >= cus && rblk >= 2 ? 2 : 1;
+    const unsigned ry = (unsigned)((rblk + rb - 1) / rb);
+    const dim3 sg((unsigned)tiles, ry, slots(tiles * ry));
+    if (rb == 4) hipLaunchKernelGGL((k_lora_shrink<4, 2, PARTS>), sg, dim3(64 * SH_WAVES), 0, s, a);
+    else if (rb == 2) hipLaunchKernelGGL((k_lora_shrink<2, 4, PARTS>), sg, dim3(64 * SH_WAVES), 0, s, a);
+    else hipLaunchKernelGGL((k_lora_shrink<1, 8, PARTS>), sg, dim3(64 * SH_WAVES), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+
+    const int64_t sz = F32 ? 4 : 2, per = 16 / sz;
+    auto wide = [&](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && (a.T == 1 || ld % per == 0); };
+    const bool vec = a.N % per == 0 && wide(a.y, a.ldy) && (!a.base || wide(a.base, a.ldb));
+    const int64_t cblk = (a.N + 64 * EX_WAVES - 1) / (64 * EX_WAVES);
+    int tt = 8;                                              // tiles a wave: while eight workgroups a compute unit remain
+    while (tt > 1 && (tiles + tt - 1) / tt * cblk < 8 * cus) tt >>= 1;
+    const unsigned tx = (unsigned)((tiles + tt - 1) / tt);
+    const dim3 eg(tx, (unsigned)cblk, slots((int64_t)tx * cblk / 4 + 1));
+    const int rs = a.R <= 32 ? 1 : a.R <= 64 ? 2 : 4;
+    auto go = [&](void (*k)(LoraArgs, int)) { hipLaunchKernelGGL(k, eg, dim3(64 * EX_WAVES), 0, s, a, tt); };
+    if (vec) go(rs == 1 ? k_lora_expand<PARTS, F32, true, 1> : rs == 2 ? k_lora_expand<PARTS, F32, true, 2> : k_lora_expand<PARTS, F32, true, 4>);
+    else go(rs == 1 ? k_lora_expand<PARTS, F32, false, 1> : rs == 2 ? k_lora_expand<PARTS, F32, false, 2> : k_lora_expand<PARTS, F32, false, 4>);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_lora(const LoraArgs &a, hipStream_t s) {
-    const unsigned tiles = (unsigned)((a.T + 15) / 16);
-    const dim3 sg(tiles, (unsigned)((a.R + 15) / 16), 1), eg(tiles, (unsigned)((a.N + 64 * EX_WAVES - 1) / (64 * EX_WAVES)), 1);
-    if (a.f32) hipLaunchKernelGGL((k_lora_shrink<1, 3>), sg, dim3(64 * SH_WAVES), 0, s, a);
-    else hipLaunchKernelGGL((k_lora_shrink<1, 2>), sg, dim3(64 * SH_WAVES), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.f32) hipLaunchKernelGGL((k_lora_expand<3, true>), eg, dim3(64 * EX_WAVES), 0, s, a);
-    else hipLaunchKernelGGL((k_lora_expand<2, false>), eg, dim3(64 * EX_WAVES), 0, s, a);
-    return hipGetLastError();
+    return a.f32 ? launch_parts<3, true>(a, s) : launch_parts<2, false>(a, s);
 }
 
 }  // namespace qs
