@@ -48,22 +48,19 @@ __device__ __forceinline__ void load_row(Raw<VEC, V> &w, const void *p, int dt, 
                 if ((t + P * i) * 8 < H) w.q[i][0] = *(const u32x4 *)((const uint16_t *)p + off + (t + P * i) * 8);
         }
     } else {
+        // (past the row's end: its last value, not used)
         if (dt == MOE_F32) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = Row<VEC, P, V>::at(t, i, j);
-                    if (c < H) w.q[i][j >> 2][j & 3] = ((const uint32_t *)p)[off + c];
-                }
+                for (int j = 0; j < 8; ++j)
+                    w.q[i][j >> 2][j & 3] = ((const uint32_t *)p)[off + min(Row<VEC, P, V>::at(t, i, j), H - 1)];
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = Row<VEC, P, V>::at(t, i, j);
-                    if (c < H) w.q[i][j >> 2][j & 3] = ((const uint16_t *)p)[off + c];
-                }
+                for (int j = 0; j < 8; ++j)
+                    w.q[i][j >> 2][j & 3] = ((const uint16_t *)p)[off + min(Row<VEC, P, V>::at(t, i, j), H - 1)];
         }
     }
 }
@@ -141,10 +138,21 @@ __device__ __forceinline__ float row_sum(float v, int slot) {
     return s;
 }
 
+// values past the row's end to 0
+template <bool VEC, int P, int V>
+__device__ __forceinline__ void mask_row(float (&f)[V][8], int t, int H) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = Row<VEC, P, V>::at(t, i, j) < H ? f[i][j] : 0.0f;
+}
+
 // f -> its norm (values past the row's end are 0 before and not used after)
 template <bool VEC, int P, int V>
-__device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs &n, const Raw<VEC, V> &w, const Raw<VEC, V> &b,
-                                         int t, int H, int slot) {
+__device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs &n, int t, int H, int slot) {
+    Raw<VEC, V> w{}, b{};
+    if (n.w) load_row<VEC, P, V>(w, n.w, n.dtype, 0, t, H);
+    if (n.b) load_row<VEC, P, V>(b, n.b, n.dtype, 0, t, H);
     const float ih = 1.0f / (float)H;
     if (n.layer) {
         float s = 0.0f;
@@ -186,9 +194,18 @@ __device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs &n, co
     }
 }
 
+// exp(x) = 2^t (1 + ln2 d) for t = x log2 e rounded and d what it was rounded by (and the rest of the constant):
+// within 2 steps for every x (2^t alone is off by |x| / 2 steps), a quarter of expf's instructions
+__device__ __forceinline__ float exp_near(float x) {
+    constexpr float L = 1.44269502162933349609f, LO = 1.92596299112661746887e-8f, LN2 = 0.69314718055994530942f;
+    const float t = x * L;
+    const float d = __builtin_fmaf(x, LO, __builtin_fmaf(x, L, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fabsf(t) < 200.0f ? __builtin_fmaf(e, d * LN2, e) : e;        // (0, infinity, NaN as they are)
+}
 __device__ __forceinline__ float activate(float g, int act) {
     if (act == MOE_ACT_NONE) return g;
-    const float s = 1.0f / (1.0f + expf(-g));
+    const float s = __builtin_amdgcn_rcpf(1.0f + exp_near(-g));                    // (the reciprocal is within a step)
     return act == MOE_ACT_SIGMOID ? s : g * s;
 }
 
@@ -198,7 +215,7 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
     const int t = threadIdx.x % P, H = a.H;
     const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / P;
     if (row >= a.T) return;                                  // (whole rows; P > 64: never)
-    Raw<VEC, V> y{}, r{}, g{}, w1{}, b1{}, w2{}, b2{};
+    Raw<VEC, V> y{}, r{}, g{};
     if (a.y) load_row<VEC, P, V>(y, a.y, a.dy, row * a.ldy, t, H);
     if (a.r) load_row<VEC, P, V>(r, a.r, a.dr, row * a.ldr, t, H);
     if (a.gate && a.gate_cols > 1) load_row<VEC, P, V>(g, a.gate, a.dg, row * a.ldg, t, H);
@@ -209,14 +226,13 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
                              : a.dg == MOE_BF16 ? bf16_to_f32(((const uint16_t *)a.gate)[o])
                                                 : f16_to_f32(((const uint16_t *)a.gate)[o]);
     }
-    if (a.post.w) load_row<VEC, P, V>(w1, a.post.w, a.post.dtype, 0, t, H);
-    if (a.post.b) load_row<VEC, P, V>(b1, a.post.b, a.post.dtype, 0, t, H);
-    if (a.pre.w) load_row<VEC, P, V>(w2, a.pre.w, a.pre.dtype, 0, t, H);
-    if (a.pre.b) load_row<VEC, P, V>(b2, a.pre.b, a.pre.dtype, 0, t, H);
     float z[V][8], f[V][8];
     if (a.y) {
         widen(y, a.dy, z);
-        if (a.post.on) norm_row<VEC, P, V>(z, a.post, w1, b1, t, H, 0);
+        if (a.post.on) {
+            if constexpr (!VEC) mask_row<VEC, P, V>(z, t, H);
+            norm_row<VEC, P, V>(z, a.post, t, H, 0);
+        }
         float s = a.scale;
         if (a.gate) {
             if (a.gate_cols == 1) {
@@ -250,29 +266,31 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
         widen(r, a.dr, z);
     }
     if (a.pre.on) {
-        // (what lies past the row's end may have met a bias)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[i][j] = Row<VEC, P, V>::at(t, i, j) < H ? z[i][j] : 0.0f;
-        norm_row<VEC, P, V>(z, a.pre, w2, b2, t, H, 2);
+        mask_row<VEC, P, V>(z, t, H);
+        norm_row<VEC, P, V>(z, a.pre, t, H, 2);
         store_row<VEC, P, V>(a.xo, a.dxo, row * a.ldxo, t, H, z);
     }
 }
 
+// Threads per row: 8 values each while a row has up to 512 or 1025 to 2048 of them, 16 up to 16384, in us for
+// both norms of bf16 rows (TB/s):
+//   16384 x 2048  256 threads 46.0 (5.83), 64 threads of 32 values 56.9      131072 x 1024  64 of 16: 183.4 (5.85)
+//   16384 x 4096  256 of 16: 95.9 (5.60), 512 of 8: 96.0                     131072 x 512   64 of 8: 93.9 (5.72)
+//   16384 x 8192  512 of 16: 210 (5.11), 256 of 32: 214, 1024 of 8: 266      8192 x 16384   1024 of 16: 224 (4.80)
+//   (with a gate: 266 (5.05), 291, 370; a large copy moves 4.8)
 template <bool VEC>
 void launch_p(const BlockNormArgs &a, hipStream_t s) {
-    const bool few = a.T < 2 * n_compute_units();
     auto go = [&](void (*k)(BlockNormArgs), int p) {
         const int64_t rpw = p < 256 ? 256 / p : 1;
         hipLaunchKernelGGL(k, dim3((unsigned)((a.T + rpw - 1) / rpw)), dim3((unsigned)(p < 256 ? 256 : p)), 0, s, a);
     };
-    // threads per row: as few as hold the row in registers where rows fill the device, four times as many
-    // for a few rows
     if (a.H <= 128) go(k_block_norm<VEC, 16, 1>, 16);
     else if (a.H <= 512) go(k_block_norm<VEC, 64, 1>, 64);
-    else if (a.H <= 2048) few ? go(k_block_norm<VEC, 256, 1>, 256) : go(k_block_norm<VEC, 64, 4>, 64);
-    else if (a.H <= 8192) few ? go(k_block_norm<VEC, 1024, 1>, 1024) : go(k_block_norm<VEC, 256, 4>, 256);
+    else if (a.H <= 1024) go(k_block_norm<VEC, 64, 2>, 64);
+    else if (a.H <= 2048) go(k_block_norm<VEC, 256, 1>, 256);
+    else if (a.H <= 4096) go(k_block_norm<VEC, 256, 2>, 256);
+    else if (a.H <= 8192) go(k_block_norm<VEC, 512, 2>, 512);
+    else if (a.H <= 16384) go(k_block_norm<VEC, 1024, 2>, 1024);
     else go(k_block_norm<VEC, 1024, 4>, 1024);
 }
 
