@@ -8,9 +8,14 @@
 //   the top_k largest c of those that stay (ties to the lower expert; ones that are not live
 //   last, with weight 0), w_j = s_j, divided by their sum and scaled
 //
-// Scores are formed and compared in 64 bits: in a prompt of 16384 tokens some pair of scores at
-// the edge of a selection lies closer than 32 bits resolve, and the selection would depend on
-// how exp rounds there.  Every step is a chain of one wave, so its length is its time.
+// The selection is that of scores formed and compared in 64 bits: in a prompt of 16384 tokens some pair
+// of scores at the edge of a selection lies closer than 32 bits resolve, and the choice would depend
+// on how exp rounds there.  Such tokens are few, so scores are formed in fp32 first, to a known
+// error: a token whose cuts (between the last expert taken and the first left, the same of groups)
+// are wider than that is done, the others (one in 300 at 256 sigmoid scores) are selected again in
+// 64 bits.  Where c is the logit itself nothing is rounded, and ties are ties.  The weights are formed in
+// 64 bits, by the lanes that hold them, and rounded once.  Every step is a chain of one wave: the
+// number of its instructions is the time.
 #pragma once
 #include "common.h"
 #include "internal.h"
@@ -19,15 +24,33 @@ namespace qs {
 
 namespace {
 
+// What cuts must be wider than, times 2 + the largest |bias|.  In fp32 exp(x) is off by (|x| + 2) 2^-23 of
+// itself, which moves a sigmoid by less than 2^-22 and a softmax by less than 2^-20 (its sum of 256: |x|
+// averages at most ln 256 there), a reciprocal and the sums by 2^-21 of s <= 1, the bias's addition by 2^-24 of
+// 1 + |bias|: less than 2^-19.5 (1 + |bias|) in all, so 2^-17.5 for the difference of two sums of two.
+constexpr float EDGE = 1.0f / (1 << 17);
+
 __device__ __forceinline__ uint64_t order_key64(double v) {
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);          // (-0 and 0 are equal)
     return (u >> 63) ? ~u : u | (1ull << 63);                            // monotone in v, above 1
+}
+// the same of fp32 (its keys are above 1 too), and its inverse
+__device__ __forceinline__ uint32_t order_key32(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 template <int CTRL>
 __device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
     return (uint64_t)dpp_u32<CTRL>((uint32_t)(v >> 32)) << 32 | dpp_u32<CTRL>((uint32_t)v);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    return __longlong_as_double((long long)dpp_u64<CTRL>((uint64_t)__double_as_longlong(v)));
 }
 // largest over the wave, in every lane
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
@@ -37,78 +60,64 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
     v = max64(v, dpp_u64<0x140>(v));
     return max64(max64(readlane64(v, 0), readlane64(v, 16)), max64(readlane64(v, 32), readlane64(v, 48)));
 }
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+// sums over 16 lanes (a row) and over the wave, in every lane of it
+__device__ __forceinline__ double row_sum_f64(double v) {
+    v += dpp_f64<0xB1>(v);
+    v += dpp_f64<0x4E>(v);
+    v += dpp_f64<0x141>(v);
+    v += dpp_f64<0x140>(v);
     return v;
 }
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v = row_sum_f64(v);
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
 
-// v[i]: the logit of expert lane + 64 i (ignored for ids >= E).  On return lanes j < K hold the
-// j-th selected expert in ascending id and its weight.  W: waves of the workgroup that may be
-// in here at once (wave w uses slot w % W); scratch: E doubles of LDS for this wave, needed (with
-// groups) until the selection is done.
-template <int W>
-__device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (&v)[4], int E, int K, double *scratch) {
-    __shared__ int rs_idx[W][16];
-    __shared__ float rs_w[W][16];
-    const int lane = threadIdx.x & 63, wv = (threadIdx.x >> 6) % W;
-    const uint64_t lt = (1ull << lane) - 1;
-    bool live[4];
-    double s[4];
+__device__ __forceinline__ int group_of(const RouteRule &r, int e) { return min((e * r.group_inv) >> 16, r.n_groups - 1); }
+
+// a >= b: the two largest of a group's values so far, joined with another part of the group's
+template <typename V>
+__device__ __forceinline__ void join_two(V &a, V &b, V a2, V b2) {
+    b = fmax(fmax(b, b2), fmin(a, a2));
+    a = fmax(a, a2);
+}
+
+// The selection by 64-bit scores, as bit masks (sel[i] bit l: expert l + 64 i).  on: the logit is live; live: the
+// bias too.
+__device__ __forceinline__ void select64(const RouteRule &r, const float (&v)[4], const bool (&on)[4], const bool (&live)[4],
+                                         float top, int E, int K, double *scratch, uint64_t (&sel)[4]) {
+    const int lane = threadIdx.x & 63;
+    double s[4], z = 0.0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) live[i] = lane + 64 * i < E && v[i] > -__builtin_inff();
-    if (r.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = live[i] ? 1.0 / (1.0 + exp(-(double)v[i])) : 0.0;
-    } else {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, live[i] ? order_key(v[i]) : 0u);
-        m = wave_max_bcast(m);
-        const float top = __uint_as_float((m & 0x80000000u) ? (m & 0x7fffffffu) : ~m);
-        double z = 0.0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // (an infinite largest logit: 1 for those, 0 for the others)
-            s[i] = !live[i] ? 0.0 : v[i] == top ? 1.0 : exp((double)v[i] - (double)top);
-            z += s[i];
-        }
+    for (int i = 0; i < 4; ++i) {
+        // (softmax, an infinite largest logit: 1 for those, 0 for the others)
+        if (r.sigmoid) s[i] = on[i] ? 1.0 / (1.0 + exp(-(double)v[i])) : 0.0;
+        else s[i] = !on[i] ? 0.0 : v[i] == top ? 1.0 : exp((double)v[i] - (double)top);
+        z += s[i];
+    }
+    if (!r.sigmoid) {
         z = wave_sum_f64(z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = z > 0.0 ? s[i] / z : 0.0;
     }
-    // selection values, and their keys: 1 for experts that are not live, 0 for none at all
-    double c[4];
-    uint64_t key[4];
+    uint64_t key[4];                                         // 1: not live, 0: no candidate
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = lane + 64 * i;
-        c[i] = (double)v[i];
-        double g = s[i];
-        if (r.bias && e < E) {
-            c[i] = g = s[i] + (double)r.bias[e];
-            live[i] = live[i] && g > -__builtin_inf();
-        }
-        key[i] = e >= E ? 0ull : live[i] ? order_key64(c[i]) : 1ull;
-        if (r.n_groups > 1 && e < E) scratch[e] = !live[i] ? -__builtin_inf() : r.group_top2 ? g : c[i];
+        double c = (double)v[i], g = s[i];
+        if (r.bias && e < E) c = g = s[i] + (double)r.bias[e];
+        key[i] = e >= E ? 0ull : live[i] ? order_key64(c) : 1ull;
+        if (r.n_groups > 1 && e < E) scratch[e] = !live[i] ? -__builtin_inf() : r.group_top2 ? g : c;
     }
     if (r.n_groups > 1) {
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        // 2^group_shift lanes per group look through its experts for the two largest
         const int q = 1 << r.group_shift, g = lane >> r.group_shift;
         double a = -__builtin_inf(), b = a;
         if (g < r.n_groups)
-            for (int j = lane & (q - 1); j < r.group_size; j += q) {
-                const double t = scratch[g * r.group_size + j];
-                b = fmax(b, fmin(a, t));
-                a = fmax(a, t);
-            }
-        for (int o = 1; o < q; o <<= 1) {
-            const double a2 = __shfl_xor(a, o, 64), b2 = __shfl_xor(b, o, 64);
-            b = fmax(fmax(b, b2), fmin(a, a2));
-            a = fmax(a, a2);
-        }
+            for (int j = lane & (q - 1); j < r.group_size; j += q) join_two(a, b, scratch[g * r.group_size + j], -__builtin_inf());
+        for (int o = 1; o < q; o <<= 1) join_two(a, b, __shfl_xor(a, o, 64), __shfl_xor(b, o, 64));
         const uint64_t gk = order_key64(r.group_top2 && b > -__builtin_inf() ? a + b : a);
         int rank = 0;
         for (int j = 0; j < r.n_groups; ++j) {
@@ -117,13 +126,12 @@ __device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (
         }
         const uint64_t kept = __ballot(g < r.n_groups && rank < r.group_k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ge = min((int)(((lane + 64 * i) * r.group_inv) >> 16), r.n_groups - 1);
-            if (!((kept >> (ge << r.group_shift)) & 1)) key[i] = 0ull;
-        }
+        for (int i = 0; i < 4; ++i)
+            if (!((kept >> (group_of(r, lane + 64 * i) << r.group_shift)) & 1)) key[i] = 0ull;
     }
     // top_k rounds, each taking the largest key, the lowest expert among equal ones
-    uint64_t sel[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sel[i] = 0;
     for (int n = 0; n < K; ++n) {
         const uint64_t m = wave_max_u64(max64(max64(key[0], key[1]), max64(key[2], key[3])));
         bool done = false;
@@ -136,21 +144,151 @@ __device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (
             done = done || at != 0;
         }
     }
-    double sum = 1.0;
-    if (r.renorm) {
-        double part = 0.0;
+}
+
+// v[i]: the logit of expert lane + 64 i (ignored for ids >= E).  On return lanes j < K hold the
+// j-th selected expert in ascending id and its weight.  W: waves of the workgroup that may be
+// in here at once (wave w uses slot w % W); scratch: E doubles of LDS for this wave, needed (with
+// groups) until the selection is done.
+template <int W>
+__device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (&v)[4], int E, int K, double *scratch) {
+    __shared__ int rs_idx[W][16];
+    __shared__ float rs_v[W][16];
+    const int lane = threadIdx.x & 63, wv = (threadIdx.x >> 6) % W;
+    const uint64_t lt = (1ull << lane) - 1;
+    const float NONE = -__builtin_inff();
+    bool on[4], live[4];
+    float bias[4], edge = 2.0f * EDGE;
+    if (r.bias) {
+        uint32_t m = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part += ((sel[i] >> lane) & 1) && live[i] ? s[i] : 0.0;
-        sum = wave_sum_f64(part);
+        for (int i = 0; i < 4; ++i) {
+            bias[i] = lane + 64 * i < E ? r.bias[lane + 64 * i] : 0.0f;
+            m = max(m, __float_as_uint(bias[i]) & 0x7fffffffu);
+        }
+        edge = EDGE * (2.0f + __uint_as_float(wave_max_bcast(m)));       // (infinity, NaN: no cut is wide enough)
     }
-    const double f = sum > 0.0 ? (double)r.scale / sum : 0.0;
+    uint32_t mk = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        on[i] = lane + 64 * i < E && v[i] > NONE;
+        live[i] = on[i] && (!r.bias || bias[i] > NONE);
+        mk = max(mk, on[i] ? order_key32(v[i]) : 0u);
+    }
+    const float top = r.sigmoid ? 0.0f : key_value(wave_max_bcast(mk));  // the largest live logit
+    // fp32 scores where they are compared (rather than logits)
+    const bool scored = r.bias || (r.n_groups > 1 && r.group_top2);
+    float c[4], g[4];                                        // for the selection, for the groups
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = g[i] = v[i];
+    if (scored) {
+        float s[4], z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (r.sigmoid) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-v[i]));
+            else s[i] = !on[i] ? 0.0f : v[i] == top ? 1.0f : __expf(v[i] - top);
+            z += s[i];
+        }
+        z = r.sigmoid ? 1.0f : __builtin_amdgcn_rcpf(wave_sum(z));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!r.sigmoid) s[i] *= z;
+            g[i] = s[i];
+            if (r.bias) c[i] = g[i] = s[i] + bias[i];
+            else if (!r.group_top2) g[i] = c[i];
+        }
+    }
+    uint32_t key[4];                                         // 1: not live, 0: no candidate
+#pragma unroll
+    for (int i = 0; i < 4; ++i) key[i] = lane + 64 * i >= E ? 0u : live[i] ? order_key32(c[i]) : 1u;
+    bool close = false;                                      // a cut is not wide enough to be sure
+    if (r.n_groups > 1) {
+        float *sc = (float *)scratch;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane + 64 * i < E) sc[lane + 64 * i] = live[i] ? g[i] : NONE;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        // 2^group_shift lanes per group look through its experts for the two largest
+        const int q = 1 << r.group_shift, gr = lane >> r.group_shift;
+        float a = NONE, b = NONE;
+        if (gr < r.n_groups)
+            for (int j = lane & (q - 1); j < r.group_size; j += q) join_two(a, b, sc[gr * r.group_size + j], NONE);
+        if (q > 1) join_two(a, b, dpp<0xB1>(a), dpp<0xB1>(b));
+        if (q > 2) join_two(a, b, dpp<0x4E>(a), dpp<0x4E>(b));
+        if (q > 4) join_two(a, b, dpp<0x141>(a), dpp<0x141>(b));
+        if (q > 8) join_two(a, b, dpp<0x140>(a), dpp<0x140>(b));
+        if (q > 16) join_two(a, b, __shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
+        const uint32_t gk = order_key32(r.group_top2 && b > NONE ? a + b : a);
+        int rank = 0;
+        for (int j = 0; j < r.n_groups; ++j) {
+            const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, j << r.group_shift);
+            rank += o > gk || (o == gk && j < gr);
+        }
+        const bool stays = gr < r.n_groups && rank < r.group_k;
+        const uint64_t kept = __ballot(stays);
+        if (scored) {
+            const float worst = key_value(~wave_max_bcast(stays ? ~gk : 0u));
+            const float next = key_value(wave_max_bcast(gr < r.n_groups && !stays ? gk : 0x007fffffu));   // (-infinity)
+            close = next > NONE && !(worst - next > edge);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (!((kept >> (group_of(r, lane + 64 * i) << r.group_shift)) & 1)) key[i] = 0u;
+        // (the scratch is read before select64 writes it: one wave, in order)
+    }
+    // the top_k-th largest key T, counting repeats: each lane's four in order, rounds that take every
+    // head equal to the largest
+    uint32_t q0 = max(key[0], key[1]), q1 = min(key[0], key[1]), q2 = max(key[2], key[3]), q3 = min(key[2], key[3]);
+    {
+        const uint32_t h0 = max(q0, q2), l0 = min(q0, q2), h1 = max(q1, q3), l1 = min(q1, q3);
+        q0 = h0;
+        q1 = max(l0, h1);
+        q2 = min(l0, h1);
+        q3 = l1;
+    }
+    uint32_t T;
+    for (int left = K;;) {
+        T = wave_max_bcast(q0);
+        const bool pop = q0 == T;
+        left -= __popcll(__ballot(pop));
+        q0 = pop ? q1 : q0;
+        q1 = pop ? q2 : q1;
+        q2 = pop ? q3 : q2;
+        q3 = pop ? 0u : q3;
+        if (left <= 0) break;
+    }
+    uint64_t gt[4], eq[4], sel[4];
+    int need = K, ties = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        gt[i] = __ballot(key[i] > T);
+        eq[i] = __ballot(key[i] == T);
+        need -= __popcll(gt[i]);
+        ties += __popcll(eq[i]);
+    }
+    if (scored && __builtin_amdgcn_readfirstlane((int)T) != 1) {
+        const uint32_t N = wave_max_bcast(q0);               // the next one
+        close |= ties > need || (N > 1u && !(key_value(T) - key_value(N) > edge));
+    }
+    if (__builtin_amdgcn_readfirstlane((int)close)) {
+        select64(r, v, on, live, top, E, K, scratch, sel);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // of the ties the lowest `need`
+            const int n = __popcll(eq[i]);
+            sel[i] = gt[i] | (n <= need ? eq[i] : __ballot(((eq[i] >> lane) & 1) && __popcll(eq[i] & lt) < need));
+            need = max(need - n, 0);
+        }
+    }
     int base = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if ((sel[i] >> lane) & 1) {
             const int p = base + __popcll(sel[i] & lt);
             rs_idx[wv][p] = lane + 64 * i;
-            rs_w[wv][p] = live[i] ? (float)(s[i] * f) : 0.0f;
+            rs_v[wv][p] = live[i] ? v[i] : NONE;
         }
         base += __popcll(sel[i]);
     }
@@ -158,9 +296,23 @@ __device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (
     __builtin_amdgcn_wave_barrier();
     TopkOut out;
     out.idx = lane < K ? rs_idx[wv][lane] : 0;
-    out.w = lane < K ? rs_w[wv][lane] : 0.0f;
+    const float x = lane < K ? rs_v[wv][lane] : NONE;
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    // the weights, each in its lane (K <= 16: one row of lanes)
+    double w = 0.0, sum = 1.0;
+    if (lane < 16) {
+        if (r.sigmoid) w = x > NONE ? 1.0 / (1.0 + exp(-(double)x)) : 0.0;
+        else w = !(x > NONE) ? 0.0 : x == top ? 1.0 : exp((double)x - (double)top);
+        if (r.renorm) sum = row_sum_f64(w);
+    }
+    if (!r.renorm && !r.sigmoid) {                           // softmax over every live expert
+        double z = 0.0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z += !on[i] ? 0.0 : v[i] == top ? 1.0 : exp((double)v[i] - (double)top);
+        sum = wave_sum_f64(z);
+    }
+    out.w = sum > 0.0 ? (float)(w * ((double)r.scale / sum)) : 0.0f;
     return out;
 }
 
