@@ -146,57 +146,70 @@ __device__ __forceinline__ void select64(const RouteRule &r, const float (&v)[4]
     }
 }
 
-// v[i]: the logit of expert lane + 64 i (ignored for ids >= E).  On return lanes j < K hold the
-// j-th selected expert in ascending id and its weight.  W: waves of the workgroup that may be
+// What a token's selection leaves to its weights.
+struct Chosen {
+    int idx;                                                 // lanes j < K: the j-th expert in ascending id
+    float x;                                                 // and its logit (-infinity: weight 0)
+    float top;                                               // the largest live logit (softmax)
+    double z;                                                // sum of exp(l - top) (softmax without renorm; else 0)
+};
+
+// v[i]: the logit of expert lane + 64 i (ignored for ids >= E).  W: waves of the workgroup that may be
 // in here at once (wave w uses slot w % W); scratch: E doubles of LDS for this wave, needed (with
 // groups) until the selection is done.
 template <int W>
-__device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (&v)[4], int E, int K, double *scratch) {
+__device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&v)[4], int E, int K, double *scratch) {
     __shared__ int rs_idx[W][16];
     __shared__ float rs_v[W][16];
     const int lane = threadIdx.x & 63, wv = (threadIdx.x >> 6) % W;
     const uint64_t lt = (1ull << lane) - 1;
     const float NONE = -__builtin_inff();
     bool on[4], live[4];
-    float bias[4], edge = 2.0f * EDGE;
-    if (r.bias) {
-        uint32_t m = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bias[i] = lane + 64 * i < E ? r.bias[lane + 64 * i] : 0.0f;
-            m = max(m, __float_as_uint(bias[i]) & 0x7fffffffu);
-        }
-        edge = EDGE * (2.0f + __uint_as_float(wave_max_bcast(m)));       // (infinity, NaN: no cut is wide enough)
-    }
-    uint32_t mk = 0u;
+    for (int i = 0; i < 4; ++i) live[i] = on[i] = lane + 64 * i < E && v[i] > NONE;
+    float c[4], g[4], edge = 2.0f * EDGE, top = 0.0f;        // c: for the selection, g: for the groups
+    if (!r.sigmoid) {
+        uint32_t mk = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        on[i] = lane + 64 * i < E && v[i] > NONE;
-        live[i] = on[i] && (!r.bias || bias[i] > NONE);
-        mk = max(mk, on[i] ? order_key32(v[i]) : 0u);
+        for (int i = 0; i < 4; ++i) mk = max(mk, on[i] ? order_key32(v[i]) : 0u);
+        top = key_value(wave_max_bcast(mk));
     }
-    const float top = r.sigmoid ? 0.0f : key_value(wave_max_bcast(mk));  // the largest live logit
     // fp32 scores where they are compared (rather than logits)
     const bool scored = r.bias || (r.n_groups > 1 && r.group_top2);
-    float c[4], g[4];                                        // for the selection, for the groups
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = g[i] = v[i];
     if (scored) {
-        float s[4], z = 0.0f;
+        if (r.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (r.sigmoid) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-v[i]));
-            else s[i] = !on[i] ? 0.0f : v[i] == top ? 1.0f : __expf(v[i] - top);
-            z += s[i];
-        }
-        z = r.sigmoid ? 1.0f : __builtin_amdgcn_rcpf(wave_sum(z));
+            for (int i = 0; i < 4; ++i) g[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-v[i]));
+        } else {
+            float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!r.sigmoid) s[i] *= z;
-            g[i] = s[i];
-            if (r.bias) c[i] = g[i] = s[i] + bias[i];
-            else if (!r.group_top2) g[i] = c[i];
+            for (int i = 0; i < 4; ++i) {
+                g[i] = !on[i] ? 0.0f : v[i] == top ? 1.0f : __expf(v[i] - top);
+                z += g[i];
+            }
+            z = __builtin_amdgcn_rcpf(wave_sum(z));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] *= z;
         }
+        if (r.bias) {
+            uint32_t m = 0u;
+            float bias[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bias[i] = r.bias[min(lane + 64 * i, E - 1)];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m = max(m, __float_as_uint(bias[i]) & 0x7fffffffu);
+                live[i] = live[i] && bias[i] > NONE;
+                c[i] = g[i] = g[i] + bias[i];
+            }
+            edge = EDGE * (2.0f + __uint_as_float(wave_max_bcast(m)));   // (infinity, NaN: no cut is wide enough)
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = g[i] = v[i];
     }
     uint32_t key[4];                                         // 1: not live, 0: no candidate
 #pragma unroll
@@ -294,25 +307,41 @@ __device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    TopkOut out;
+    Chosen out;
     out.idx = lane < K ? rs_idx[wv][lane] : 0;
-    const float x = lane < K ? rs_v[wv][lane] : NONE;
+    out.x = lane < K ? rs_v[wv][lane] : NONE;
+    out.top = top;
+    out.z = 0.0;
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    // the weights, each in its lane (K <= 16: one row of lanes)
-    double w = 0.0, sum = 1.0;
-    if (lane < 16) {
-        if (r.sigmoid) w = x > NONE ? 1.0 / (1.0 + exp(-(double)x)) : 0.0;
-        else w = !(x > NONE) ? 0.0 : x == top ? 1.0 : exp((double)x - (double)top);
-        if (r.renorm) sum = row_sum_f64(w);
-    }
     if (!r.renorm && !r.sigmoid) {                           // softmax over every live expert
-        double z = 0.0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z += !on[i] ? 0.0 : v[i] == top ? 1.0 : exp((double)v[i] - (double)top);
-        sum = wave_sum_f64(z);
+        for (int i = 0; i < 4; ++i) out.z += !on[i] ? 0.0 : v[i] == top ? 1.0 : exp((double)v[i] - (double)top);
+        out.z = wave_sum_f64(out.z);
     }
-    out.w = sum > 0.0 ? (float)(w * ((double)r.scale / sum)) : 0.0f;
+    return out;
+}
+
+// The weight of a lane's logit x, over the 16 lanes of a token (every lane of them comes here).
+__device__ __forceinline__ float row_weight(const RouteRule &r, float x, float top, double z) {
+    const double d = r.sigmoid ? -(double)x : (double)x - (double)top;
+    double w = exp(d), sum = 1.0;
+    if (r.sigmoid) w = 1.0 / (1.0 + w);
+    else if (x == top) w = 1.0;                              // (an infinite one too)
+    if (!(x > -__builtin_inff())) w = 0.0;
+    if (r.renorm) sum = row_sum_f64(w);
+    else if (!r.sigmoid) sum = z;
+    return sum > 0.0 ? (float)(w * ((double)r.scale / sum)) : 0.0f;
+}
+
+// Both: lanes j < K return the j-th selected expert in ascending id and its weight.
+template <int W>
+__device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (&v)[4], int E, int K, double *scratch) {
+    const Chosen c = wave_choose<W>(r, v, E, K, scratch);
+    TopkOut out;
+    out.idx = c.idx;
+    out.w = 0.0f;
+    if ((threadIdx.x & 63) < 16) out.w = row_weight(r, c.x, c.top, c.z);
     return out;
 }
 

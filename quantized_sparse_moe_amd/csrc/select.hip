@@ -1,5 +1,5 @@
 // select.hip -- experts and weights of tokens whose router logits are given (moe_select): one
-// wave per token over rule.h's selection, logits read once, 16-byte results of a token together.
+// wave per token over rule.h's selection, then the weights of a workgroup's tokens in one wave.
 #include "rule.h"
 
 namespace qs {
@@ -19,25 +19,33 @@ struct SelectArgs {
 
 template <int DT>
 __global__ __launch_bounds__(64 * SW) void k_select(SelectArgs a) {
-    __shared__ double scratch[SW][256];
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * SW + (threadIdx.x >> 6);
-    if (t >= a.T) return;
-    float v[4];
+    __shared__ double scratch[SW][256], s_z[SW];
+    __shared__ float s_x[SW][16], s_top[SW];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t0 = (int64_t)blockIdx.x * SW, t = t0 + wave;
+    if (t < a.T) {
+        float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = 0.0f;
-        if (e < a.E) {
-            if constexpr (DT == MOE_F32) v[i] = ((const float *)a.logits)[t * a.ld + e];
-            else if constexpr (DT == MOE_F16) v[i] = f16_to_f32(((const uint16_t *)a.logits)[t * a.ld + e]);
-            else v[i] = bf16_to_f32(((const uint16_t *)a.logits)[t * a.ld + e]);
+        for (int i = 0; i < 4; ++i) {
+            const int64_t o = t * a.ld + min(lane + 64 * i, a.E - 1);
+            if constexpr (DT == MOE_F32) v[i] = ((const float *)a.logits)[o];
+            else if constexpr (DT == MOE_F16) v[i] = f16_to_f32(((const uint16_t *)a.logits)[o]);
+            else v[i] = bf16_to_f32(((const uint16_t *)a.logits)[o]);
+        }
+        const Chosen c = wave_choose<SW>(a.rule, v, a.E, a.K, scratch[wave]);
+        if (lane < a.K) a.idx[t * a.K + lane] = c.idx;
+        if (lane < 16) s_x[wave][lane] = c.x;
+        if (lane == 0) {
+            s_top[wave] = c.top;
+            s_z[wave] = c.z;
         }
     }
-    const TopkOut tk = wave_select<SW>(a.rule, v, a.E, a.K, scratch[threadIdx.x >> 6]);
-    if (lane < a.K) {
-        a.idx[t * a.K + lane] = tk.idx;
-        a.w[t * a.K + lane] = tk.w;
+    // the weights of all four tokens in one wave, 16 lanes each
+    __syncthreads();
+    const int row = lane >> 4, j = lane & 15;
+    if (wave == 0 && t0 + row < a.T) {
+        const float w = row_weight(a.rule, s_x[row][j], s_top[row], s_z[row]);
+        if (j < a.K) a.w[(t0 + row) * a.K + j] = w;
     }
 }
 
