@@ -17,6 +17,8 @@ namespace qs {
 
 namespace {
 
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
 // lane n < 16 of every 16 holds token n's adapter (-1: none) and its place among the tile's distinct
 // ones, which are numbered in token order
 struct TileIds {
@@ -27,8 +29,12 @@ struct TileIds {
         id = t0 + n < T ? ids[t0 + n] : -1;
         if (id < 0 || id >= n_adapters) id = -1;
         int lead = n;
+        if (__ballot(id != __builtin_amdgcn_readfirstlane(id)) == 0) {
+            lead = 0;                                        // (a request's tokens)
+        } else {
 #pragma unroll
-        for (int j = 14; j >= 0; --j) lead = j < n && __builtin_amdgcn_readlane(id, j) == id ? j : lead;
+            for (int j = 14; j >= 0; --j) lead = j < n && __builtin_amdgcn_readlane(id, j) == id ? j : lead;
+        }
         first = (uint32_t)__ballot(id >= 0 && lead == n) & 0xffffu;
         ord = id < 0 ? 0 : __popc(first & ((1u << lead) - 1u));
     }
@@ -113,13 +119,18 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
 // lane's registers are columns of one token (lane % 16): operand row n of product i is column
 // 16 i + n of the 64 (fp32 y: 16 bytes a register quad), or 32 (i / 2) + 8 (n / 4) + 4 (i % 2) + n % 4 (bf16: two
 // quads make 16 bytes), so that four lanes read and write 64 bytes in a row.
+//
+// Bound by memory: y read and written, each request's rows of B. T = 4096 x 16384, rank 32: 68 us, 268 MB of y at 3.9 TB/s
+// (shrink 11); columns before tiles in the grid, so that neighbouring workgroups write neighbouring
+// columns (the other way 80 us); the next tile's loads ahead of this one's products gain nothing
+// (four waves a SIMD hide them, and spill fewer registers).
 constexpr int EX_WAVES = 4;
 
 template <int PARTS, bool F32, bool VEC, int RS>
-__global__ __launch_bounds__(64 * EX_WAVES) void k_lora_expand(LoraArgs a, int tt) {
+__global__ __launch_bounds__(64 * EX_WAVES) __attribute__((amdgpu_waves_per_eu(RS == 1 ? 4 : RS == 2 ? 3 : 2))) void k_lora_expand(LoraArgs a, int tt) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int R = a.R, slot = blockIdx.z, slots = gridDim.z;
-    const int64_t c0 = ((int64_t)blockIdx.y * EX_WAVES + wave) * 64, N = a.N;
+    const int64_t c0 = ((int64_t)blockIdx.x * EX_WAVES + wave) * 64, N = a.N;
     if (c0 >= N) return;
     auto column = [&](int i, int row) { return c0 + (F32 ? 16 * i + row : 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3)); };
     u32x4 B[RS][4];
@@ -146,8 +157,8 @@ __global__ __launch_bounds__(64 * EX_WAVES) void k_lora_expand(LoraArgs a, int t
                         else if (r + 1 >= rank) B[s][i][j] &= 0xffffu;
                     }
     };
-    const int64_t tiles = (a.T + 15) / 16, last = min((int64_t)(blockIdx.x + 1) * tt, tiles);
-    for (int64_t ti = (int64_t)blockIdx.x * tt; ti < last; ++ti) {
+    const int64_t tiles = (a.T + 15) / 16, last = min((int64_t)(blockIdx.y + 1) * tt, tiles);
+    for (int64_t ti = (int64_t)blockIdx.y * tt; ti < last; ++ti) {
         TileIds tile;
         tile.load(a.ids, ti * 16, a.T, a.n);
         const int64_t t = ti * 16 + n;
@@ -215,14 +226,13 @@ __global__ __launch_bounds__(64 * EX_WAVES) void k_lora_expand(LoraArgs a, int t
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int64_t c = column(2 * i, 4 * g);
-                    u32x4 w;
+                    f32x8 w;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float lo = out[2 * i + (j >> 1)][2 * (j & 1)] + __uint_as_float(raw[i][j] << 16);
-                        const float hi = out[2 * i + (j >> 1)][2 * (j & 1) + 1] + __uint_as_float(raw[i][j] & 0xffff0000u);
-                        w[j] = f32_to_bf16(lo) | (uint32_t)f32_to_bf16(hi) << 16;
+                        w[2 * j] = out[2 * i + (j >> 1)][2 * (j & 1)] + __uint_as_float(raw[i][j] << 16);
+                        w[2 * j + 1] = out[2 * i + (j >> 1)][2 * (j & 1) + 1] + __uint_as_float(raw[i][j] & 0xffff0000u);
                     }
-                    if (c < N) *(u32x4 *)((uint16_t *)a.y + t * a.ldy + c) = w;
+                    if (c < N) *(bf16x8 *)((uint16_t *)a.y + t * a.ldy + c) = __builtin_convertvector(w, bf16x8);
                 }
             }
         } else {
@@ -248,7 +258,8 @@ __global__ __launch_bounds__(64 * EX_WAVES) void k_lora_expand(LoraArgs a, int t
 template <int PARTS, bool F32>
 hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     const int64_t tiles = (a.T + 15) / 16, rblk = (a.R + 15) / 16, cus = n_compute_units();
-    // a tile's distinct adapters, at most; workgroups of their own until two a compute unit
+    // a tile's distinct adapters, at most; workgroups of their own until two a compute unit (T = 48 with 40
+    // adapters of 16384 x 64: expand with 3 slots 21 us, with 6 23, with 11 25)
     const int64_t most = a.T < 16 ? (a.T < a.n ? a.T : a.n) : (a.n < 16 ? a.n : 16);
     auto slots = [&](int64_t groups) {
         int64_t k = (2 * cus + groups - 1) / groups;
@@ -270,7 +281,7 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     int tt = 8;                                              // tiles a wave: while eight workgroups a compute unit remain
     while (tt > 1 && (tiles + tt - 1) / tt * cblk < 8 * cus) tt >>= 1;
     const unsigned tx = (unsigned)((tiles + tt - 1) / tt);
-    const dim3 eg(tx, (unsigned)cblk, slots((int64_t)tx * cblk / 4 + 1));
+    const dim3 eg((unsigned)cblk, tx, slots((int64_t)tx * cblk));
     const int rs = a.R <= 32 ? 1 : a.R <= 64 ? 2 : 4;
     auto go = [&](void (*k)(LoraArgs, int)) { hipLaunchKernelGGL(k, eg, dim3(64 * EX_WAVES), 0, s, a, tt); };
     if (vec) go(rs == 1 ? k_lora_expand<PARTS, F32, true, 1> : rs == 2 ? k_lora_expand<PARTS, F32, true, 2> : k_lora_expand<PARTS, F32, true, 4>);
