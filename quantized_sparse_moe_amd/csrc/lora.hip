@@ -1,6 +1,6 @@
 // lora.hip -- low-rank adapters of many requests beside a shared projection (lora_gemm):
 //     y[t] = base[t] + scale_a B_a (A_a x_t),  a = ids[t]     (y[t] = base[t] without an adapter)
-// Two launches over tiles of 16 tokens on v_mfma_f32_16x16x32_bf16:
+// Two launches over tiles of 16 tokens on v_mfma_f32_16x16x32_bf16 (one for up to 16 tokens, where A is small):
 //
 //   shrink  v = scale_a A_a x_t, summed in fp32 over the columns, which the waves of a workgroup share.  v is kept
 //           as a sum of bf16 parts (two, or three where y is fp32: v to 2^-16 or 2^-24), one behind the
@@ -24,10 +24,9 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 struct TileIds {
     int id, ord;
     uint32_t first;                                          // bit n: token n is its adapter's first
-    __device__ __forceinline__ void load(const int32_t *ids, int64_t t0, int64_t T, int n_adapters) {
+    __device__ __forceinline__ void set(int of_token, int n_adapters) {
         const int n = threadIdx.x & 15;
-        id = t0 + n < T ? ids[t0 + n] : -1;
-        if (id < 0 || id >= n_adapters) id = -1;
+        id = of_token < 0 || of_token >= n_adapters ? -1 : of_token;
         int lead = n;
         if (__ballot(id != __builtin_amdgcn_readfirstlane(id)) == 0) {
             lead = 0;                                        // (a request's tokens)
@@ -46,70 +45,77 @@ __device__ __forceinline__ int rank_of(const LoraArgs &a, int ad) {
 }
 
 // -------------------------------------------------------------------------- shrink
-// One workgroup per (tile, 16 RB ranks, slot): the slot-th, slot + slots-th .. distinct adapters of the
-// tile.  SU column steps a wave are loaded at a time.
+// Ranks r0 .. r0 + 16 RB - 1 of v for the tokens of a tile that have adapter ad, by a whole workgroup: its
+// waves share the columns, SU steps of 32 loaded at a time.  v: the tile's first row, [16][PARTS][R].
+// Ends with a barrier.
 constexpr int SH_WAVES = 8;
 
 template <int RB, int SU, int PARTS>
+__device__ __forceinline__ void shrink(const LoraArgs &a, const TileIds &tile, int ad, int rank, int64_t t0, int r0,
+                                       f32x4 (*red)[RB][64], uint16_t *v0) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+    const int K = a.K, R = a.R, steps = (K + 31) / 32;
+    const uint16_t *xr = a.x + min(t0 + n, a.T - 1) * a.ldx, *ar = a.a + (int64_t)ad * R * K;
+    f32x4 acc[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int s0 = wave; s0 < steps; s0 += SU * SH_WAVES) {
+        u32x4 A[SU], B[SU][RB];
+#pragma unroll
+        for (int u = 0; u < SU; ++u) {
+            const int c = 32 * (s0 + u * SH_WAVES) + 8 * g;
+            A[u] = (u32x4){0u, 0u, 0u, 0u};
+            if (c < K) A[u] = *(const u32x4 *)(xr + c);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const int r = r0 + 16 * i + n;
+                B[u][i] = (u32x4){0u, 0u, 0u, 0u};
+                if (c < K && r < rank) B[u][i] = *(const u32x4 *)(ar + (int64_t)r * K + c);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SU; ++u)
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A[u]),
+                                                                 __builtin_bit_cast(bf16x8, B[u][i]), acc[i], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) red[wave][i][lane] = acc[i];
+    __syncthreads();
+    // thread: a token and a rank
+    for (int i = tid; i < 256 * RB; i += 64 * SH_WAVES) {
+        const int rr = i & 15, tk = (i >> 4) & 15, b = i >> 8, l = rr + 16 * (tk >> 2), r = r0 + 16 * b + rr;
+        const bool mine = __shfl(tile.id, tk, 64) == ad;
+        if (!mine || r >= R) continue;
+        float v = red[0][b][l][tk & 3];
+#pragma unroll
+        for (int w = 1; w < SH_WAVES; ++w) v += red[w][b][l][tk & 3];
+        if (a.scales) v *= a.scales[ad];
+        if (r >= rank) v = 0.0f;
+        uint16_t *d = v0 + tk * PARTS * R + r;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            const uint16_t h = f32_to_bf16(v);
+            d[p * R] = h;
+            v = __builtin_isfinite(v) ? v - bf16_to_f32(h) : 0.0f;
+        }
+    }
+    __syncthreads();
+}
+
+// One workgroup per (tile, 16 RB ranks, slot): the slot-th, slot + slots-th .. distinct adapters of the
+// tile.
+template <int RB, int SU, int PARTS>
 __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
     __shared__ f32x4 red[SH_WAVES][RB][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
-    const int64_t t0 = (int64_t)blockIdx.x * 16;
+    const int64_t t0 = (int64_t)blockIdx.x * 16, t = t0 + (threadIdx.x & 15);
     TileIds tile;
-    tile.load(a.ids, t0, a.T, a.n);
-    const int K = a.K, R = a.R, steps = (K + 31) / 32, r0 = blockIdx.y * 16 * RB;
-    const uint16_t *xr = a.x + min(t0 + n, a.T - 1) * a.ldx;
-    int k = 0;
-    for (uint32_t m = tile.first; m; m &= m - 1, ++k) {
-        if (k % (int)gridDim.z != (int)blockIdx.z) continue;
-        const int ad = tile.adapter(m), rank = rank_of(a, ad);
-        f32x4 acc[RB];
-#pragma unroll
-        for (int i = 0; i < RB; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        const uint16_t *ar = a.a + (int64_t)ad * R * K;
-        for (int s0 = wave; s0 < steps; s0 += SU * SH_WAVES) {
-            u32x4 A[SU], B[SU][RB];
-#pragma unroll
-            for (int u = 0; u < SU; ++u) {
-                const int c = 32 * (s0 + u * SH_WAVES) + 8 * g;
-                A[u] = (u32x4){0u, 0u, 0u, 0u};
-                if (c < K) A[u] = *(const u32x4 *)(xr + c);
-#pragma unroll
-                for (int i = 0; i < RB; ++i) {
-                    const int r = r0 + 16 * i + n;
-                    B[u][i] = (u32x4){0u, 0u, 0u, 0u};
-                    if (c < K && r < rank) B[u][i] = *(const u32x4 *)(ar + (int64_t)r * K + c);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < SU; ++u)
-#pragma unroll
-                for (int i = 0; i < RB; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, A[u]),
-                                                                     __builtin_bit_cast(bf16x8, B[u][i]), acc[i], 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < RB; ++i) red[wave][i][lane] = acc[i];
-        __syncthreads();
-        // thread: a token and a rank
-        for (int i = tid; i < 256 * RB; i += 64 * SH_WAVES) {
-            const int rr = i & 15, tk = (i >> 4) & 15, b = i >> 8, l = rr + 16 * (tk >> 2), r = r0 + 16 * b + rr;
-            const bool mine = __shfl(tile.id, tk, 64) == ad;
-            if (!mine || r >= R) continue;
-            float v = red[0][b][l][tk & 3];
-#pragma unroll
-            for (int w = 1; w < SH_WAVES; ++w) v += red[w][b][l][tk & 3];
-            if (a.scales) v *= a.scales[ad];
-            if (r >= rank) v = 0.0f;
-            uint16_t *d = a.v + (t0 + tk) * PARTS * R + r;
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-                const uint16_t h = f32_to_bf16(v);
-                d[p * R] = h;
-                v = __builtin_isfinite(v) ? v - bf16_to_f32(h) : 0.0f;
-            }
-        }
-        __syncthreads();
+    tile.set(t < a.T ? a.ids[t] : -1, a.n);
+    for (uint32_t m = tile.first, k = 0; m; m &= m - 1, ++k) {
+        if (k % gridDim.z != blockIdx.z) continue;
+        const int ad = tile.adapter(m);
+        shrink<RB, SU, PARTS>(a, tile, ad, rank_of(a, ad), t0, blockIdx.y * 16 * RB, red, a.v + t0 * PARTS * a.R);
     }
 }
 
@@ -124,14 +130,23 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
 // (shrink 11); columns before tiles in the grid, so that neighbouring workgroups write neighbouring
 // columns (the other way 80 us); the next tile's loads ahead of this one's products gain nothing
 // (four waves a SIMD hide them, and spill fewer registers).
+//
+// FEW > 0: up to 16 tokens of up to 16 FEW ranks in one launch; every workgroup (of SH_WAVES) shrinks for
+// itself, v stays in LDS.  us a call in a graph against two launches (K = 2048): T = 1, N = 2048, rank 16
+// 7.1 and 9.1, rank 32 9.1 and 9.3, T = 16 with 8 adapters 8.9 and 11.3, T = 1, N = 16384, rank 16 7.3 and 9.2;
+// ranks of 64 in turns of 32 9.8 and 9.2, so they take two launches, as do calls whose workgroups would read A
+// too often (T = 16, N = 16384, 16 adapters: 15.0 and 14.6).
 constexpr int EX_WAVES = 4;
 
-template <int PARTS, bool F32, bool VEC, int RS>
-__global__ __launch_bounds__(64 * EX_WAVES) __attribute__((amdgpu_waves_per_eu(RS == 1 ? 4 : RS == 2 ? 3 : 2))) void k_lora_expand(LoraArgs a, int tt) {
+template <int PARTS, bool F32, bool VEC, int RS, int FEW = 0>
+__global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
+    __attribute__((amdgpu_waves_per_eu(FEW ? 2 : RS == 1 ? 4 : RS == 2 ? 3 : 2))) void k_lora_expand(LoraArgs a, int tt) {
+    __shared__ f32x4 red[FEW ? SH_WAVES : 1][FEW ? FEW : 1][64];
+    extern __shared__ __attribute__((aligned(16))) uint16_t few_v[];     // [16][PARTS][R]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int R = a.R, slot = blockIdx.z, slots = gridDim.z;
-    const int64_t c0 = ((int64_t)blockIdx.x * EX_WAVES + wave) * 64, N = a.N;
-    if (c0 >= N) return;
+    const int64_t c0 = ((int64_t)blockIdx.x * (FEW ? SH_WAVES : EX_WAVES) + wave) * 64, N = a.N;
+    if (!FEW && c0 >= N) return;
     auto column = [&](int i, int row) { return c0 + (F32 ? 16 * i + row : 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3)); };
     u32x4 B[RS][4];
     int held = -1, rank = 0;
@@ -159,9 +174,9 @@ __global__ __launch_bounds__(64 * EX_WAVES) __attribute__((amdgpu_waves_per_eu(R
     };
     const int64_t tiles = (a.T + 15) / 16, last = min((int64_t)(blockIdx.y + 1) * tt, tiles);
     for (int64_t ti = (int64_t)blockIdx.y * tt; ti < last; ++ti) {
-        TileIds tile;
-        tile.load(a.ids, ti * 16, a.T, a.n);
         const int64_t t = ti * 16 + n;
+        TileIds tile;
+        tile.set(t < a.T ? a.ids[t] : -1, a.n);
         // rows of this slot; in place, rows without an adapter stay
         const bool live = t < a.T && tile.ord % slots == slot && (tile.id >= 0 || a.base != a.y);
         // base, as its register quads
@@ -187,7 +202,11 @@ __global__ __launch_bounds__(64 * EX_WAVES) __attribute__((amdgpu_waves_per_eu(R
             f32x4 acc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-            const uint16_t *vr = a.v + t * PARTS * R;
+            if constexpr (FEW > 0) {
+                load_b(ad, 0);                               // (under the first product)
+                shrink<FEW, 8 / FEW, PARTS>(a, tile, ad, rank, 0, 0, red, few_v);
+            }
+            const uint16_t *vr = FEW ? few_v + n * PARTS * R : a.v + t * PARTS * R;
             for (int s0 = 0; 32 * s0 < rank; s0 += RS) {
                 u32x4 V[RS][PARTS];
 #pragma unroll
@@ -198,7 +217,7 @@ __global__ __launch_bounds__(64 * EX_WAVES) __attribute__((amdgpu_waves_per_eu(R
                         V[s][p] = (u32x4){0u, 0u, 0u, 0u};
                         if (mine && r8 < rank) V[s][p] = *(const u32x4 *)(vr + p * R + r8);
                     }
-                if (ad != held || R > 32 * RS) load_b(ad, s0);
+                if (!FEW && (ad != held || R > 32 * RS)) load_b(ad, s0);
 #pragma unroll
                 for (int s = 0; s < RS; ++s)
 #pragma unroll
@@ -209,6 +228,7 @@ __global__ __launch_bounds__(64 * EX_WAVES) __attribute__((amdgpu_waves_per_eu(R
                                                                              __builtin_bit_cast(bf16x8, V[s][p]), acc[i], 0, 0, 0);
             }
             held = ad;
+            if constexpr (FEW > 0) __syncthreads();          // (v is read)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -255,6 +275,9 @@ __global__ __launch_bounds__(64 * EX_WAVES) __attribute__((amdgpu_waves_per_eu(R
     }
 }
 
+// values of A: of one adapter, and of all workgroups together
+constexpr int64_t FEW_A = 65536, FEW_ALL = 8 << 20;
+
 template <int PARTS, bool F32>
 hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     const int64_t tiles = (a.T + 15) / 16, rblk = (a.R + 15) / 16, cus = n_compute_units();
@@ -265,6 +288,18 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
         int64_t k = (2 * cus + groups - 1) / groups;
         return (unsigned)(k < most ? k : most);
     };
+    const int64_t sz = F32 ? 4 : 2, per = 16 / sz;
+    auto wide = [&](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && (a.T == 1 || ld % per == 0); };
+    const bool vec = a.N % per == 0 && wide(a.y, a.ldy) && (!a.base || wide(a.base, a.ldb));
+    // Up to 16 tokens in one launch where the workgroups' reading of A, each for itself, is little
+    const int64_t fblk = (a.N + 64 * SH_WAVES - 1) / (64 * SH_WAVES);
+    if (tiles == 1 && a.R <= 32 && (int64_t)a.R * a.K <= FEW_A && fblk * most * a.R * a.K <= FEW_ALL) {
+        const size_t lds = (size_t)16 * PARTS * a.R * 2;
+        void (*k)(LoraArgs, int) = rblk == 1 ? (vec ? k_lora_expand<PARTS, F32, true, 1, 1> : k_lora_expand<PARTS, F32, false, 1, 1>)
+                                             : (vec ? k_lora_expand<PARTS, F32, true, 1, 2> : k_lora_expand<PARTS, F32, false, 1, 2>);
+        hipLaunchKernelGGL(k, dim3((unsigned)fblk, 1, (unsigned)most), dim3(64 * SH_WAVES), lds, s, a, 1);
+        return hipGetLastError();
+    }
     const int rb = tiles >= cus && rblk >= 4 ? 4 : tiles >= cus && rblk >= 2 ? 2 : 1;
     const unsigned ry = (unsigned)((rblk + rb - 1) / rb);
     const dim3 sg((unsigned)tiles, ry, slots(tiles * ry));
@@ -274,9 +309,6 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 
-    const int64_t sz = F32 ? 4 : 2, per = 16 / sz;
-    auto wide = [&](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && (a.T == 1 || ld % per == 0); };
-    const bool vec = a.N % per == 0 && wide(a.y, a.ldy) && (!a.base || wide(a.base, a.ldb));
     const int64_t cblk = (a.N + 64 * EX_WAVES - 1) / (64 * EX_WAVES);
     int tt = 8;                                              // tiles a wave: while eight workgroups a compute unit remain
     while (tt > 1 && (tiles + tt - 1) / tt * cblk < 8 * cus) tt >>= 1;
