@@ -230,6 +230,8 @@ __device__ TopkOut select_topk_from(uint32_t *ctl, const uint64_t *lg, uint32_t 
     const int lane = threadIdx.x & 63;
     const uint64_t none = (uint64_t)tag << 32;
     uint64_t w[4], wg;
+    float bias[4];
+    if constexpr (RW > 0) load_bias(rule, E, bias);
     const uint32_t lim = wait_bound(ctl);
     for (uint32_t n = 0;; ++n) {
 #pragma unroll
@@ -249,7 +251,7 @@ __device__ TopkOut select_topk_from(uint32_t *ctl, const uint64_t *lg, uint32_t 
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = no_nan(__uint_as_float((uint32_t)w[i]));
     TopkOut tk;
-    if constexpr (RW > 0) tk = wave_select<RW>(rule, v, E, K, scratch);
+    if constexpr (RW > 0) tk = wave_select<RW>(rule, v, bias, E, K, scratch);
     else tk = wave_topk_regs<WEIGHTS>(v, E, K);
     tk.idx = min(max(tk.idx, 0), E - 1);
     *gate = sigmoid(__builtin_bit_cast(float, __builtin_amdgcn_readfirstlane((int)(uint32_t)wg)));

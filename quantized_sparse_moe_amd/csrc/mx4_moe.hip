@@ -167,7 +167,9 @@ __global__ __launch_bounds__(RT_THREADS) void k_mx_route(MxArgs a) {
         TopkOut tk;
         if constexpr (RULE) {
             __shared__ double scratch[RT_WAVES][256];
-            tk = wave_select<RT_WAVES>(a.L.rule, v, E, K, scratch[wave]);
+            float bias[4];
+            load_bias(a.L.rule, E, bias);
+            tk = wave_select<RT_WAVES>(a.L.rule, v, bias, E, K, scratch[wave]);
         } else {
             tk = wave_topk_regs(v, E, K);
         }

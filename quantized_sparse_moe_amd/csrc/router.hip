@@ -221,7 +221,9 @@ __global__ __launch_bounds__(64 * TK_TOKENS) void k_topk(TopkArgs a) {
         TopkOut tk;
         if constexpr (RULE) {
             __shared__ double scratch[TK_TOKENS][256];
-            tk = wave_select<TK_TOKENS>(a.rule, v, E, K, scratch[wave]);
+            float bias[4];
+            load_bias(a.rule, E, bias);
+            tk = wave_select<TK_TOKENS>(a.rule, v, bias, E, K, scratch[wave]);
         } else {
             tk = wave_topk_regs(v, E, K);
         }

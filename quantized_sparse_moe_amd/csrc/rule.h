@@ -154,11 +154,18 @@ struct Chosen {
     double z;                                                // sum of exp(l - top) (softmax without renorm; else 0)
 };
 
-// v[i]: the logit of expert lane + 64 i (ignored for ids >= E).  W: waves of the workgroup that may be
+// The bias of experts lane + 64 i (not used without one): loaded before the logits are waited for.
+__device__ __forceinline__ void load_bias(const RouteRule &r, int E, float (&bias)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bias[i] = r.bias ? r.bias[min((int)(threadIdx.x & 63) + 64 * i, E - 1)] : 0.0f;
+}
+
+// v[i]: the logit of expert lane + 64 i (ignored for ids >= E), bias from load_bias.  W: waves of the workgroup that may be
 // in here at once (wave w uses slot w % W); scratch: E doubles of LDS for this wave, needed (with
 // groups) until the selection is done.
 template <int W>
-__device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&v)[4], int E, int K, double *scratch) {
+__device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&v)[4], const float (&bias)[4], int E, int K,
+                                              double *scratch) {
     __shared__ int rs_idx[W][16];
     __shared__ float rs_v[W][16];
     const int lane = threadIdx.x & 63, wv = (threadIdx.x >> 6) % W;
@@ -193,9 +200,6 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
         }
         if (r.bias) {
             uint32_t m = 0u;
-            float bias[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bias[i] = r.bias[min(lane + 64 * i, E - 1)];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 m = max(m, __float_as_uint(bias[i]) & 0x7fffffffu);
@@ -336,8 +340,9 @@ __device__ __forceinline__ float row_weight(const RouteRule &r, float x, float t
 
 // Both: lanes j < K return the j-th selected expert in ascending id and its weight.
 template <int W>
-__device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (&v)[4], int E, int K, double *scratch) {
-    const Chosen c = wave_choose<W>(r, v, E, K, scratch);
+__device__ __forceinline__ TopkOut wave_select(const RouteRule &r, const float (&v)[4], const float (&bias)[4], int E, int K,
+                                               double *scratch) {
+    const Chosen c = wave_choose<W>(r, v, bias, E, K, scratch);
     TopkOut out;
     out.idx = c.idx;
     out.w = 0.0f;

@@ -24,7 +24,8 @@ __global__ __launch_bounds__(64 * SW) void k_select(SelectArgs a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t0 = (int64_t)blockIdx.x * SW, t = t0 + wave;
     if (t < a.T) {
-        float v[4];
+        float v[4], bias[4];
+        load_bias(a.rule, a.E, bias);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t o = t * a.ld + min(lane + 64 * i, a.E - 1);
@@ -32,7 +33,7 @@ __global__ __launch_bounds__(64 * SW) void k_select(SelectArgs a) {
             else if constexpr (DT == MOE_F16) v[i] = f16_to_f32(((const uint16_t *)a.logits)[o]);
             else v[i] = bf16_to_f32(((const uint16_t *)a.logits)[o]);
         }
-        const Chosen c = wave_choose<SW>(a.rule, v, a.E, a.K, scratch[wave]);
+        const Chosen c = wave_choose<SW>(a.rule, v, bias, a.E, a.K, scratch[wave]);
         if (lane < a.K) a.idx[t * a.K + lane] = c.idx;
         if (lane < 16) s_x[wave][lane] = c.x;
         if (lane == 0) {
