@@ -74,13 +74,19 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
+// whether this lane's bit of a mask is set (the mask as an execution mask: no instruction)
+__device__ __forceinline__ bool lane_bit(uint64_t m) { return __builtin_amdgcn_inverse_ballot_w64(m); }
+
 __device__ __forceinline__ int group_of(const RouteRule &r, int e) { return min((e * r.group_inv) >> 16, r.n_groups - 1); }
 
 // a >= b: the two largest of a group's values so far, joined with another part of the group's
-template <typename V>
-__device__ __forceinline__ void join_two(V &a, V &b, V a2, V b2) {
+__device__ __forceinline__ void join_two(double &a, double &b, double a2, double b2) {
     b = fmax(fmax(b, b2), fmin(a, a2));
     a = fmax(a, a2);
+}
+__device__ __forceinline__ void join_two(uint32_t &a, uint32_t &b, uint32_t a2, uint32_t b2) {
+    b = max(max(b, b2), min(a, a2));
+    a = max(a, a2);
 }
 
 // The selection by 64-bit scores, as bit masks (sel[i] bit l: expert l + 64 i).  on: the logit is live; live: the
@@ -140,7 +146,7 @@ __device__ __forceinline__ void select64(const RouteRule &r, const float (&v)[4]
             const uint64_t at = done ? 0ull : __ballot(key[i] == m);
             const uint64_t one = at & (0ull - at);
             sel[i] |= one;
-            if ((one >> lane) & 1) key[i] = 0ull;
+            if (lane_bit(one)) key[i] = 0ull;
             done = done || at != 0;
         }
     }
@@ -220,23 +226,24 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
     for (int i = 0; i < 4; ++i) key[i] = lane + 64 * i >= E ? 0u : live[i] ? order_key32(c[i]) : 1u;
     bool close = false;                                      // a cut is not wide enough to be sure
     if (r.n_groups > 1) {
-        float *sc = (float *)scratch;
+        // (as keys: 1 for experts that are not live; the experts' own where a group's values are theirs)
+        uint32_t *sc = (uint32_t *)scratch;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (lane + 64 * i < E) sc[lane + 64 * i] = live[i] ? g[i] : NONE;
+            if (lane + 64 * i < E) sc[lane + 64 * i] = r.bias || !r.group_top2 ? key[i] : live[i] ? order_key32(g[i]) : 1u;
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         __builtin_amdgcn_wave_barrier();
         // 2^group_shift lanes per group look through its experts for the two largest
         const int q = 1 << r.group_shift, gr = lane >> r.group_shift;
-        float a = NONE, b = NONE;
+        uint32_t a = 1u, b = 1u;
         if (gr < r.n_groups)
-            for (int j = lane & (q - 1); j < r.group_size; j += q) join_two(a, b, sc[gr * r.group_size + j], NONE);
-        if (q > 1) join_two(a, b, dpp<0xB1>(a), dpp<0xB1>(b));
-        if (q > 2) join_two(a, b, dpp<0x4E>(a), dpp<0x4E>(b));
-        if (q > 4) join_two(a, b, dpp<0x141>(a), dpp<0x141>(b));
-        if (q > 8) join_two(a, b, dpp<0x140>(a), dpp<0x140>(b));
-        if (q > 16) join_two(a, b, __shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
-        const uint32_t gk = order_key32(r.group_top2 && b > NONE ? a + b : a);
+            for (int j = lane & (q - 1); j < r.group_size; j += q) join_two(a, b, sc[gr * r.group_size + j], 1u);
+        if (q > 1) join_two(a, b, dpp_u32<0xB1>(a), dpp_u32<0xB1>(b));
+        if (q > 2) join_two(a, b, dpp_u32<0x4E>(a), dpp_u32<0x4E>(b));
+        if (q > 4) join_two(a, b, dpp_u32<0x141>(a), dpp_u32<0x141>(b));
+        if (q > 8) join_two(a, b, dpp_u32<0x140>(a), dpp_u32<0x140>(b));
+        if (q > 16) join_two(a, b, (uint32_t)__shfl_xor((int)a, 16, 64), (uint32_t)__shfl_xor((int)b, 16, 64));
+        const uint32_t gk = r.group_top2 && b > 1u ? order_key32(key_value(a) + key_value(b)) : a;
         int rank = 0;
         for (int j = 0; j < r.n_groups; ++j) {
             const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, j << r.group_shift);
@@ -245,9 +252,8 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
         const bool stays = gr < r.n_groups && rank < r.group_k;
         const uint64_t kept = __ballot(stays);
         if (scored) {
-            const float worst = key_value(~wave_max_bcast(stays ? ~gk : 0u));
-            const float next = key_value(wave_max_bcast(gr < r.n_groups && !stays ? gk : 0x007fffffu));   // (-infinity)
-            close = next > NONE && !(worst - next > edge);
+            const uint32_t worst = ~wave_max_bcast(stays ? ~gk : 0u), next = wave_max_bcast(gr < r.n_groups && !stays ? gk : 1u);
+            close = next > 1u && !(key_value(worst) - key_value(next) > edge);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -295,14 +301,14 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
         for (int i = 0; i < 4; ++i) {
             // of the ties the lowest `need`
             const int n = __popcll(eq[i]);
-            sel[i] = gt[i] | (n <= need ? eq[i] : __ballot(((eq[i] >> lane) & 1) && __popcll(eq[i] & lt) < need));
+            sel[i] = gt[i] | (n <= need ? eq[i] : __ballot(lane_bit(eq[i]) && __popcll(eq[i] & lt) < need));
             need = max(need - n, 0);
         }
     }
     int base = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if ((sel[i] >> lane) & 1) {
+        if (lane_bit(sel[i])) {
             const int p = base + __popcll(sel[i] & lt);
             rs_idx[wv][p] = lane + 64 * i;
             rs_v[wv][p] = live[i] ? v[i] : NONE;

@@ -21,17 +21,17 @@ template <int DT>
 __global__ __launch_bounds__(64 * SW) void k_select(SelectArgs a) {
     __shared__ double scratch[SW][256], s_z[SW];
     __shared__ float s_x[SW][16], s_top[SW];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0 = (int64_t)blockIdx.x * SW, t = t0 + wave;
     if (t < a.T) {
         float v[4], bias[4];
         load_bias(a.rule, a.E, bias);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t o = t * a.ld + min(lane + 64 * i, a.E - 1);
-            if constexpr (DT == MOE_F32) v[i] = ((const float *)a.logits)[o];
-            else if constexpr (DT == MOE_F16) v[i] = f16_to_f32(((const uint16_t *)a.logits)[o]);
-            else v[i] = bf16_to_f32(((const uint16_t *)a.logits)[o]);
+            const uint32_t o = min(lane + 64 * i, a.E - 1);
+            if constexpr (DT == MOE_F32) v[i] = ((const float *)a.logits + t * a.ld)[o];
+            else if constexpr (DT == MOE_F16) v[i] = f16_to_f32(((const uint16_t *)a.logits + t * a.ld)[o]);
+            else v[i] = bf16_to_f32(((const uint16_t *)a.logits + t * a.ld)[o]);
         }
         const Chosen c = wave_choose<SW>(a.rule, v, bias, a.E, a.K, scratch[wave]);
         if (lane < a.K) a.idx[t * a.K + lane] = c.idx;
