@@ -120,6 +120,18 @@ def test_a_token_does_not_depend_on_the_others(torch, qs, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 64, 136])
+def test_the_same_bits_in_any_batch(torch, qs, R, dtype):
+    """One token, 16 (one launch for small ranks), 70 and a prompt that fills the device: the sums of a token run
+    in one order."""
+    d = make(torch, 4500, 576, 80, R, 5, dtype=dtype, ragged=True)
+    y = call(torch, qs, d, dtype)
+    for lo, hi in ((3, 4), (0, 16), (16, 27), (100, 170)):
+        e = dict(d, ids=d["ids"][lo:hi].contiguous(), x=d["x"][lo:hi], base=d["base"][lo:hi])
+        assert torch.equal(call(torch, qs, e, dtype), y[lo:hi]), (lo, hi)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_strides_in_place_and_rows_behind(torch, qs, dtype):
     T, K, N = 33, 96, 120
     d = make(torch, T, K, N, 24, 4, dtype=dtype, ragged=True)
