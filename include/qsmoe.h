@@ -258,6 +258,7 @@ typedef struct {
  * A rule applied to logits that are there already.
  *   logits   [T][n_experts], row stride ld (elements, >= n_experts), MOE_BF16, MOE_F16 or MOE_F32
  *   topk_idx [T][top_k] int32 ascending, topk_w [T][top_k] fp32 (written)
+ * The outputs must not overlap the logits or each other (MOE_ERR_INVALID).
  * Limits: T <= 2^20, n_experts <= 256, top_k <= min(n_experts, 16).  T == 0 enqueues nothing.
  */
 moe_status moe_select(const moe_router_rule *rule, const void *logits, int32_t dtype, int64_t T, int64_t n_experts,
@@ -475,8 +476,8 @@ moe_status mx4_gemm_mx4x(const void *w_codes, const void *w_scales, int64_t N, i
  *           (same pointer and stride: in place, tokens without an adapter are not touched), or other
  *           columns of its matrix; any other overlap with an input is MOE_ERR_INVALID
  *   ws      device workspace of ws_bytes >= lora_workspace_size(T, R), 256-byte aligned, contents undefined
- *           before and after (one for T tokens also serves fewer); calls that share it must not
- *           overlap in time.
+ *           before and after (one for T tokens also serves fewer), apart from every other buffer; calls
+ *           that share it must not overlap in time.
  * Products are exact and sums fp32; A_a x[t] times its scale is carried to 2^-16 of itself for a bf16 y,
  * to 2^-24 for an fp32 one.  A token's result does not depend on the other tokens.
  * Limits (else MOE_ERR_UNSUPPORTED): R % 8 == 0, 8 <= R <= 256, K % 8 == 0, 8 <= K <= 65536, N <= 2^23,

@@ -882,6 +882,10 @@ def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspa
         if adapters.N != N or adapters.K != K:
             _mx4_bad("mx4_gemm", "the adapters are of a matrix of another size")
         _lora_ids(adapters, adapter_ids, x.shape[0], "mx4_gemm")
+        if adapter_workspace is None:
+            adapter_workspace = lora_new_workspace(adapters, x.shape[0], stream)
+        elif _mx4_buf(adapter_workspace, lora_workspace_size(x.shape[0], adapters.R), "mx4_gemm") % 256:
+            raise QsmoeError(MOE_ERR_WORKSPACE, "mx4_gemm: adapter_workspace must be 256-byte aligned")
         y = mx4_gemm(w_codes, w_scales, N, K, x, y, y_dtype, workspace, stream)
         return lora_gemm(adapters, adapter_ids, x, base=y, y=y, workspace=adapter_workspace, stream=stream)
     T, k, ldx, code = _mx4_values(x, "mx4_gemm")
@@ -915,6 +919,8 @@ class LoraAdapters:
         self.N = b.shape[1]
         if b.shape[0] != self.n or b.shape[2] != self.R:
             _mx4_bad(where, "a and b must have the same n and R")
+        if self.R % 8 or not 8 <= self.R <= 256 or self.K % 8 or not 8 <= self.K <= 65536:
+            raise QsmoeError(MOE_ERR_UNSUPPORTED, f"{where}: R is a multiple of 8 up to 256, K one up to 65536")
         for t, dtype, what in ((scales, torch.float32, "scales"), (ranks, torch.int32, "ranks")):
             if t is not None and (t.dtype != dtype or t.shape != (self.n,) or not t.is_contiguous()):
                 _mx4_bad(where, f"{what} must be contiguous [n] of type {dtype}")

@@ -614,6 +614,9 @@ moe_status moe_select(const moe_router_rule *rule, const void *logits, int32_t d
     if (!logits || !aligned(logits, dtype == MOE_F32 ? 4 : 2) || ld < n_experts || !topk_idx || !topk_w ||
         !aligned(topk_idx, 4) || !aligned(topk_w, 4))
         return MOE_ERR_INVALID;
+    const size_t nl = Rows{logits, dtype, ld, n_experts}.bytes(T), nk = (size_t)(T * top_k) * 4;
+    if (overlap(topk_idx, nk, topk_w, nk) || overlap(topk_idx, nk, logits, nl) || overlap(topk_w, nk, logits, nl))
+        return MOE_ERR_INVALID;
     return dev(launch_select(to_rule(rule, n_experts), logits, dtype, T, (int)n_experts, ld, top_k, topk_idx, topk_w,
                              (hipStream_t)stream));
 }
@@ -710,7 +713,9 @@ moe_status lora_gemm(const void *a, const void *b, const float *scales, const in
         (ranks && overlap(y, nb, ranks, (size_t)n_adapters * 4)))
         return MOE_ERR_INVALID;
     if (!ws || !aligned(ws, ALIGN) || ws_bytes < need) return MOE_ERR_WORKSPACE;
-    if (overlap(y, nb, ws, need)) return MOE_ERR_INVALID;
+    if (overlap(y, nb, ws, need) || overlap(x, xr.bytes(T), ws, need) || overlap(ids, (size_t)T * 4, ws, need) ||
+        (base && overlap(base, br.bytes(T), ws, need)))
+        return MOE_ERR_INVALID;
     LoraArgs g{};
     g.a = (const uint16_t *)a;
     g.b = (const uint16_t *)b;

@@ -195,7 +195,7 @@ struct BlockNormArgs {
     NormArgs post, pre;
     int gate_cols, act;            // 1: a value per row; else elementwise
     float scale;
-    int64_t T;
+    int64_t T, row0;               // rows row0 .. of T (set by the launcher)
     int H;
 };
 hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t s);

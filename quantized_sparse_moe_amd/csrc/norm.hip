@@ -213,7 +213,7 @@ template <bool VEC, int P, int V>
 __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs a) {
     constexpr int RPW = P < 256 ? 256 / P : 1;               // rows per workgroup
     const int t = threadIdx.x % P, H = a.H;
-    const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / P;
+    const int64_t row = a.row0 + (int64_t)blockIdx.x * RPW + threadIdx.x / P;
     if (row >= a.T) return;                                  // (whole rows; P > 64: never)
     Raw<VEC, V> y{}, r{}, g{};
     if (a.y) load_row<VEC, P, V>(y, a.y, a.dy, row * a.ldy, t, H);
@@ -279,10 +279,14 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
 //   16384 x 8192  512 of 16: 210 (5.11), 256 of 32: 214, 1024 of 8: 266      8192 x 16384   1024 of 16: 224 (4.80)
 //   (with a gate: 266 (5.05), 291, 370; a large copy moves 4.8)
 template <bool VEC>
-void launch_p(const BlockNormArgs &a, hipStream_t s) {
+void launch_p(BlockNormArgs a, hipStream_t s) {
+    // (a launch has fewer than 2^32 threads)
     auto go = [&](void (*k)(BlockNormArgs), int p) {
-        const int64_t rpw = p < 256 ? 256 / p : 1;
-        hipLaunchKernelGGL(k, dim3((unsigned)((a.T + rpw - 1) / rpw)), dim3((unsigned)(p < 256 ? 256 : p)), 0, s, a);
+        const int64_t rpw = p < 256 ? 256 / p : 1, most = ((int64_t)1 << 31) / p;
+        for (a.row0 = 0; a.row0 < a.T; a.row0 += most) {
+            const int64_t rows = a.T - a.row0 < most ? a.T - a.row0 : most;
+            hipLaunchKernelGGL(k, dim3((unsigned)((rows + rpw - 1) / rpw)), dim3((unsigned)(p < 256 ? 256 : p)), 0, s, a);
+        }
     };
     if (a.H <= 128) go(k_block_norm<VEC, 16, 1>, 16);
     else if (a.H <= 512) go(k_block_norm<VEC, 64, 1>, 64);

@@ -290,7 +290,7 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
         need -= __popcll(gt[i]);
         ties += __popcll(eq[i]);
     }
-    if (scored && __builtin_amdgcn_readfirstlane((int)T) != 1) {
+    if (r.bias && __builtin_amdgcn_readfirstlane((int)T) != 1) {         // (without one c is exact)
         const uint32_t N = wave_max_bcast(q0);               // the next one
         close |= ties > need || (N > 1u && !(key_value(T) - key_value(N) > edge));
     }

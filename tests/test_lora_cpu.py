@@ -23,7 +23,7 @@ INVALID = [dict(T=-1), dict(N=-1), dict(n=-1), dict(dt=q.MOE_F16), dict(a=None),
            dict(scales=A + 7 * S + 2), dict(ranks=A + 7 * S + 1), dict(y=None), dict(y=A + 5 * S + 1), dict(ldy=79),
            dict(base=A + 4 * S + 1), dict(ldb=79), dict(dt=q.MOE_F32, y=A + 5 * S + 2), dict(y=A + 4 * S, ldy=88),
            dict(y=A + 4 * S + 2), dict(y=A + 3 * S), dict(y=A), dict(y=A + S + 64), dict(y=A + 2 * S), dict(y=A + 6 * S),
-           dict(scales=A + 5 * S + 4), dict(ranks=A + 5 * S + 4)]
+           dict(scales=A + 5 * S + 4), dict(ranks=A + 5 * S + 4), dict(x=A + 6 * S), dict(base=A + 6 * S + 256), dict(ids=A + 6 * S)]
 UNSUPPORTED = [dict(R=4), dict(R=12), dict(R=264), dict(R=0), dict(K=4), dict(K=68), dict(K=65544), dict(N=(1 << 23) + 1),
                dict(n=0), dict(n=65537), dict(T=(1 << 20) + 1)]
 
@@ -54,7 +54,7 @@ def test_limits_workspace_and_nothing_to_do():
 def test_binding_checks_its_arguments():
     import torch
     a, b = torch.zeros(3, 8, 16, dtype=torch.bfloat16), torch.zeros(3, 24, 8, dtype=torch.bfloat16)
-    for bad in ((a.float(), b), (a, b[:2]), (a, b[:, :, :4].contiguous()), (a[0], b), (a[:, :, ::2], b)):
+    for bad in ((a[:, :4].contiguous(), b[:, :, :4].contiguous()), (a[:, :, :4].contiguous(), b), (a.float(), b), (a, b[:2]), (a, b[:, :, :4].contiguous()), (a[0], b), (a[:, :, ::2], b)):
         with pytest.raises(q.QsmoeError):
             q.LoraAdapters(*bad)
     for kw in (dict(scales=torch.ones(2)), dict(scales=torch.ones(3).half()), dict(ranks=torch.ones(3)),
@@ -72,6 +72,8 @@ def test_binding_checks_its_arguments():
         q.mx4_gemm(None, None, 25, 16, x, adapters=ad, adapter_ids=ids)
     with pytest.raises(q.QsmoeError):
         q.mx4_gemm(None, None, 24, 16, x, adapters=ad)
+    with pytest.raises(q.QsmoeError):                        # (before the product is enqueued)
+        q.mx4_gemm(None, None, 24, 16, x, adapters=ad, adapter_ids=ids, adapter_workspace=torch.zeros(8, dtype=torch.uint8))
 
 
 def test_reference_by_hand():

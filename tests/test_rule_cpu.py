@@ -57,6 +57,9 @@ def test_select_arguments():
     assert select(rule(), k=17) == q.MOE_ERR_UNSUPPORTED
     assert select(rule(n_groups=1, group_top_k=1), E=4, k=5) == q.MOE_ERR_UNSUPPORTED
     assert select(rule(), logits=None, T=0) == q.MOE_OK
+    far = dict(idx=FAKE + (1 << 32), w=FAKE + (2 << 32))
+    for kw in (dict(far, idx=FAKE + 4092), dict(far, w=FAKE), dict(far, w=far["idx"] + 124), dict(far, logits=far["w"] + 64)):
+        assert select(rule(), **kw) == q.MOE_ERR_INVALID, kw        # (T = 4: 4096 bytes of logits, 128 of results)
 
 
 def test_layer_calls_need_a_rule_and_keep_their_checks():
