@@ -199,6 +199,18 @@ LAYERS = {
 }
 
 
+_cache = {}
+
+
+def layer(lname, name=None):
+    """A layer under a rule, or (no rule) with its own routing: made once."""
+    if (lname, name) not in _cache:
+        kw = LAYERS[lname]
+        _cache[lname, name] = (ref.Layer(seed=3, **kw) if name is None else
+                               rule_ref.RuledLayer(dict(rule_for(name, kw["n_experts"], kw["top_k"])), seed=3, **kw))
+    return _cache[lname, name]
+
+
 @pytest.mark.parametrize("name", ["group2bias", "all"])
 @pytest.mark.parametrize("lname", sorted(LAYERS))
 @pytest.mark.parametrize("T", [1, 3, 9, 40, 150])
@@ -208,7 +220,7 @@ def test_mx4_layer_under_a_rule(torch, qs, name, lname, T):
     selection: a sigmoid's and a softmax's logarithm have slopes of at most 1 and 2)."""
     kw = LAYERS[lname]
     r = rule_for(name, kw["n_experts"], kw["top_k"])
-    L = rule_ref.RuledLayer(dict(r), seed=3, **kw)
+    L = layer(lname, name)
     desc = upload(L, torch, qs)
     xb = syn.make_x(T, L.hidden, seed=T)
     x = to_dev(xb, torch)
@@ -222,8 +234,7 @@ def test_mx4_layer_under_a_rule(torch, qs, name, lname, T):
     assert int(qs.moe_workspace_status(ws)) == 0
     # and the layer's own routing afterwards, in the same workspace
     y0, i0, w0 = run(torch, qs, desc, x, workspace=ws)
-    plain = ref.Layer(seed=3, **kw)
-    check(plain, xb, y0, i0, w0, "own routing")
+    check(layer(lname), xb, y0, i0, w0, "own routing")
 
 
 @pytest.mark.parametrize("name", ["group2bias", "all"])
