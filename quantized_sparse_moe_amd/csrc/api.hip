@@ -687,7 +687,7 @@ moe_status moe_block_norm(const void *y, int32_t y_dtype, int64_t ldy, const voi
 
 size_t lora_workspace_size(int64_t T, int64_t R) {
     if (R < 8 || R > LORA_MAX_R || R % 8 || T > MAX_TOKENS) return SIZE_MAX;
-    return T <= 0 ? 0 : up((size_t)T * LORA_PARTS * R * 2);
+    return T <= 0 ? 0 : up((size_t)T * LORA_PARTS * R * 2) + up((size_t)T * 4) * 2;
 }
 
 moe_status lora_gemm(const void *a, const void *b, const float *scales, const int32_t *ranks, int64_t n_adapters,
@@ -725,7 +725,12 @@ moe_status lora_gemm(const void *a, const void *b, const float *scales, const in
     g.x = (const uint16_t *)x;
     g.base = base;
     g.y = y;
-    g.v = (uint16_t *)ws;
+    Carver c{(char *)ws};
+    g.v = c.take<uint16_t>((size_t)(T * LORA_PARTS * R));
+    if (lora_ordered(T, n_adapters, N, R)) {
+        g.perm = c.take<int32_t>((size_t)T);
+        g.sid = c.take<int32_t>((size_t)T);
+    }
     g.T = T;
     g.ldx = ldx;
     g.ldb = ldb;

@@ -208,11 +208,17 @@ struct LoraArgs {
     const uint16_t *x;             // [T] rows, ldx apart
     const void *base;              // [T] rows of y's type, or null
     void *y;
-    uint16_t *v;                   // workspace: [T][parts][R] bf16
+    int32_t *perm, *sid;           // workspace: tokens ordered by adapter, and their adapters; or null
+    uint16_t *v;                   // workspace: [T][parts][R] bf16, in that order
     int64_t T, ldx, ldb, ldy, N;
     int n, R, K, f32;
 };
 constexpr int LORA_PARTS = 3;      // bf16 parts of a value of v, at most
+// whether tokens are ordered first: where reading an adapter's B once more for every tile that holds one of
+// its tokens costs more than the launch (lora.hip)
+inline bool lora_ordered(int64_t T, int64_t n_adapters, int64_t N, int64_t R) {
+    return n_adapters > 1 && T > 64 && T <= 65536 && (T / 16) * N * R >= 4 << 20;
+}
 hipError_t launch_lora(const LoraArgs &a, hipStream_t s);
 
 // ---------------------------------------------------------------- measured ceilings

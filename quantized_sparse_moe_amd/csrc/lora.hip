@@ -44,18 +44,86 @@ __device__ __forceinline__ int rank_of(const LoraArgs &a, int ad) {
     return a.ranks ? min(max(a.ranks[ad], 0), a.R) : a.R;
 }
 
+// --------------------------------------------------------------------------- order
+// The tokens of a batch of many requests, ordered by adapter (those without one last), so that tiles
+// hold few distinct ones: perm[i] is the i-th token, sid[i] its adapter.  Tokens that come in runs already (at
+// most one change in four tiles) stay as they are.  A counting sort by one workgroup; the order within an
+// adapter is not fixed and changes no result.
+// us of a call with and without, 8 mixed adapters of rank 32, T = 4096 x 16384 @ORD1@;
+// 40 of rank 64, T = 256 @ORD2@; the launch costs packed prompts @ORD3@.
+constexpr int OR_THREADS = 1024, OR_BINS = 8192;             // (more adapters share bins: any order will do)
+
+__global__ __launch_bounds__(OR_THREADS) void k_lora_order(LoraArgs a) {
+    __shared__ int bins[OR_BINS + 1];
+    __shared__ int wsum[OR_THREADS / 64], changes;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, T = (int)a.T;
+    const int nb = min(a.n, OR_BINS) + 1;
+    auto bin = [&](int id) { return id < 0 || id >= a.n ? nb - 1 : a.n <= OR_BINS ? id : id % OR_BINS; };
+    if (tid == 0) changes = 0;
+    for (int i = tid; i < nb; i += OR_THREADS) bins[i] = 0;
+    __syncthreads();
+    // (whole waves go through the loops: every lane takes part in the ballots)
+    int mine = 0;
+    for (int t0 = wave * 64; t0 < T; t0 += OR_THREADS) {
+        const int t = t0 + lane, id = a.ids[min(t, T - 1)], b = bin(id);
+        const bool in = t < T;
+        mine += __popcll(__ballot(in && t > 0 && a.ids[max(min(t, T - 1) - 1, 0)] != id));
+        const int tokens = __popcll(__ballot(in));
+        if (__ballot(in && b != __builtin_amdgcn_readfirstlane(b)) == 0) {
+            if (lane == 0) atomicAdd(&bins[b], tokens);      // (one bin: one addition)
+        } else if (in) {
+            atomicAdd(&bins[b], 1);
+        }
+    }
+    if (lane == 0) atomicAdd(&changes, mine);
+    __syncthreads();
+    if (changes * 64 <= T) {
+        for (int t = tid; t < T; t += OR_THREADS) {
+            a.perm[t] = t;
+            a.sid[t] = a.ids[t];
+        }
+        return;
+    }
+    // first places of the bins
+    const int per = (nb + OR_THREADS - 1) / OR_THREADS, b0 = min(tid * per, nb), b1 = min(b0 + per, nb);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += bins[b];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 63) wsum[wave] = incl;
+    __syncthreads();
+    int at = incl - sum;
+    for (int w = 0; w < wave; ++w) at += wsum[w];
+    for (int b = b0; b < b1; ++b) {
+        const int n = bins[b];
+        bins[b] = at;
+        at += n;
+    }
+    __syncthreads();
+    for (int t = tid; t < T; t += OR_THREADS) {
+        const int id = a.ids[t], p = atomicAdd(&bins[bin(id)], 1);
+        a.perm[p] = t;
+        a.sid[p] = id;
+    }
+}
+
 // -------------------------------------------------------------------------- shrink
 // Ranks r0 .. r0 + 16 RB - 1 of v for the tokens of a tile that have adapter ad, by a whole workgroup: its
-// waves share the columns, SU steps of 32 loaded at a time.  v: the tile's first row, [16][PARTS][R].
+// waves share the columns, SU steps of 32 loaded at a time.  tok: the token of lane % 16 (past the last: any); v0:
+// v of the tile's first, [16][PARTS][R].
 // Ends with a barrier.
 constexpr int SH_WAVES = 8;
 
 template <int RB, int SU, int PARTS>
-__device__ __forceinline__ void shrink(const LoraArgs &a, const TileIds &tile, int ad, int rank, int64_t t0, int r0,
+__device__ __forceinline__ void shrink(const LoraArgs &a, const TileIds &tile, int ad, int rank, int64_t tok, int r0,
                                        f32x4 (*red)[RB][64], uint16_t *v0) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int K = a.K, R = a.R, steps = (K + 31) / 32;
-    const uint16_t *xr = a.x + min(t0 + n, a.T - 1) * a.ldx, *ar = a.a + (int64_t)ad * R * K;
+    const uint16_t *xr = a.x + tok * a.ldx, *ar = a.a + (int64_t)ad * R * K;
     f32x4 acc[RB];
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -109,13 +177,14 @@ __device__ __forceinline__ void shrink(const LoraArgs &a, const TileIds &tile, i
 template <int RB, int SU, int PARTS>
 __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
     __shared__ f32x4 red[SH_WAVES][RB][64];
-    const int64_t t0 = (int64_t)blockIdx.x * 16, t = t0 + (threadIdx.x & 15);
+    const int64_t t0 = (int64_t)blockIdx.x * 16, p = min(t0 + (threadIdx.x & 15), a.T - 1);
+    const int64_t tok = a.perm ? a.perm[p] : p;
     TileIds tile;
-    tile.set(t < a.T ? a.ids[t] : -1, a.n);
+    tile.set(t0 + (threadIdx.x & 15) < a.T ? (a.perm ? a.sid : a.ids)[p] : -1, a.n);
     for (uint32_t m = tile.first, k = 0; m; m &= m - 1, ++k) {
         if (k % gridDim.z != blockIdx.z) continue;
         const int ad = tile.adapter(m);
-        shrink<RB, SU, PARTS>(a, tile, ad, rank_of(a, ad), t0, blockIdx.y * 16 * RB, red, a.v + t0 * PARTS * a.R);
+        shrink<RB, SU, PARTS>(a, tile, ad, rank_of(a, ad), tok, blockIdx.y * 16 * RB, red, a.v + t0 * PARTS * a.R);
     }
 }
 
@@ -173,12 +242,21 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
                     }
     };
     const int64_t tiles = (a.T + 15) / 16, last = min((int64_t)(blockIdx.y + 1) * tt, tiles);
+    // a tile's tokens and their adapters, read a tile ahead
+    const int32_t *ids = a.perm ? a.sid : a.ids;
+    int64_t p1 = min((int64_t)blockIdx.y * tt * 16 + n, a.T - 1);
+    int t1 = a.perm ? a.perm[p1] : (int)p1, id1 = ids[p1];
     for (int64_t ti = (int64_t)blockIdx.y * tt; ti < last; ++ti) {
-        const int64_t t = ti * 16 + n;
+        const int64_t p = p1, t = t1;                        // place, token
         TileIds tile;
-        tile.set(t < a.T ? a.ids[t] : -1, a.n);
+        tile.set(ti * 16 + n < a.T ? id1 : -1, a.n);
+        if (ti + 1 < last) {
+            p1 = min(p1 + 16, a.T - 1);
+            t1 = a.perm ? a.perm[p1] : (int)p1;
+            id1 = ids[p1];
+        }
         // rows of this slot; in place, rows without an adapter stay
-        const bool live = t < a.T && tile.ord % slots == slot && (tile.id >= 0 || a.base != a.y);
+        const bool live = ti * 16 + n < a.T && tile.ord % slots == slot && (tile.id >= 0 || a.base != a.y);
         // base, as its register quads
         f32x4 out[4];
 #pragma unroll
@@ -204,9 +282,9 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
             for (int i = 0; i < 4; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
             if constexpr (FEW > 0) {
                 load_b(ad, 0);                               // (under the first product)
-                shrink<FEW, 8 / FEW, PARTS>(a, tile, ad, rank, 0, 0, red, few_v);
+                shrink<FEW, 8 / FEW, PARTS>(a, tile, ad, rank, t, 0, red, few_v);
             }
-            const uint16_t *vr = FEW ? few_v + n * PARTS * R : a.v + t * PARTS * R;
+            const uint16_t *vr = FEW ? few_v + n * PARTS * R : a.v + p * PARTS * R;
             for (int s0 = 0; 32 * s0 < rank; s0 += RS) {
                 u32x4 V[RS][PARTS];
 #pragma unroll
@@ -299,6 +377,11 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
                                              : (vec ? k_lora_expand<PARTS, F32, true, 1, 2> : k_lora_expand<PARTS, F32, false, 1, 2>);
         hipLaunchKernelGGL(k, dim3((unsigned)fblk, 1, (unsigned)most), dim3(64 * SH_WAVES), lds, s, a, 1);
         return hipGetLastError();
+    }
+    if (a.perm) {
+        hipLaunchKernelGGL(k_lora_order, dim3(1), dim3(OR_THREADS), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
     const int rb = tiles >= cus && rblk >= 4 ? 4 : tiles >= cus && rblk >= 2 ? 2 : 1;
     const unsigned ry = (unsigned)((rblk + rb - 1) / rb);

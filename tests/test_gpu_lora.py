@@ -224,3 +224,38 @@ def test_streams_and_graphs(torch, qs):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, qs.lora_gemm(ad, d["ids"], d["x"], base=d["base"]))
+
+
+@pytest.mark.parametrize("n,T", [(1, 65), (3, 200), (40, 512), (40, 65), (9000, 700), (70, 3000), (2, 70000)])
+def test_orders_of_requests(torch, qs, n, T):
+    """Batches that are ordered by adapter first (more adapters than the order tells apart among them),
+    runs that are not, and batches too long for it: each token's bits are those of its own call."""
+    g = torch.Generator().manual_seed(n + T)
+    K, R = 32, 8
+    N = (4 << 20) // (T // 16 * R) + 8 if T <= 65536 else 24 # (as wide as it takes for a batch to be ordered)
+    rnd = lambda *s: torch.randn(*s, device="cuda")
+    torch.manual_seed(n + T)
+    a, b, x, base = rnd(n, R, K).bfloat16(), rnd(n, N, R).bfloat16(), rnd(T, K).bfloat16(), rnd(T, N)
+    ad = qs.LoraAdapters(a, b)
+    mixed = torch.randint(-2, n + 2, (T,), generator=g, dtype=torch.int32)
+    runs = (torch.arange(T) // 50 % n).int()
+    for ids in (mixed, runs, torch.full((T,), n - 1, dtype=torch.int32), torch.full((T,), -1, dtype=torch.int32)):
+        ids = ids.cuda()
+        y = qs.lora_gemm(ad, ids, x, base=base)
+        again = base.clone()
+        qs.lora_gemm(ad, ids, x, base=again, y=again)
+        assert torch.equal(y, again)
+        part = torch.cat([qs.lora_gemm(ad, ids[i:i + 16], x[i:i + 16], base=base[i:i + 16]) for i in range(0, min(T, 800), 16)])
+        assert torch.equal(y[:len(part)], part)
+        rows = [0, T // 2, T - 1]
+        w, bound = lora_of(a, b, ids, x, base, rows)
+        ref.check(np64(y)[rows], w, bound, False)
+
+
+def lora_of(a, b, ids, x, base, rows):
+    """The reference for some rows, on their adapters only."""
+    i = ids.cpu().numpy()[rows]
+    ok = [int(v) if 0 <= v < a.shape[0] else -1 for v in i]
+    use = [max(v, 0) for v in ok]
+    return ref.forward(np64(a[use]), np64(b[use]), [j if v >= 0 else -1 for j, v in enumerate(ok)], np64(x)[rows],
+                       np64(base)[rows], f32=True)
