@@ -194,15 +194,6 @@ __device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs &n, in
     }
 }
 
-// exp(x) = 2^t (1 + ln2 d) for t = x log2 e rounded and d what it was rounded by (and the rest of the constant):
-// within 2 steps for every x (2^t alone is off by |x| / 2 steps), a quarter of expf's instructions
-__device__ __forceinline__ float exp_near(float x) {
-    constexpr float L = 1.44269502162933349609f, LO = 1.92596299112661746887e-8f, LN2 = 0.69314718055994530942f;
-    const float t = x * L;
-    const float d = __builtin_fmaf(x, LO, __builtin_fmaf(x, L, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fabsf(t) < 200.0f ? __builtin_fmaf(e, d * LN2, e) : e;        // (0, infinity, NaN as they are)
-}
 __device__ __forceinline__ float activate(float g, int act) {
     if (act == MOE_ACT_NONE) return g;
     const float s = __builtin_amdgcn_rcpf(1.0f + exp_near(-g));                    // (the reciprocal is within a step)

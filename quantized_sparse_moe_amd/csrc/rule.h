@@ -12,7 +12,7 @@
 // of scores at the edge of a selection lies closer than 32 bits resolve, and the choice would depend
 // on how exp rounds there.  Such tokens are few, so scores are formed in fp32 first, to a known
 // error: a token whose cuts (between the last expert taken and the first left, the same of groups)
-// are wider than that is done, the others (one in 300 at 256 sigmoid scores) are selected again in
+// are wider than that is done, the others (one in 2400 at 256 sigmoid scores) are selected again in
 // 64 bits.  Where c is the logit itself nothing is rounded, and ties are ties.  The weights are formed in
 // 64 bits, by the lanes that hold them, and rounded once.  Every step is a chain of one wave: the
 // number of its instructions is the time.
@@ -24,11 +24,17 @@ namespace qs {
 
 namespace {
 
-// What cuts must be wider than, times 2 + the largest |bias|.  In fp32 exp(x) is off by (|x| + 2) 2^-23 of
-// itself, which moves a sigmoid by less than 2^-22 and a softmax by less than 2^-20 (its sum of 256: |x|
-// averages at most ln 256 there), a reciprocal and the sums by 2^-21 of s <= 1, the bias's addition by 2^-24 of
-// 1 + |bias|: less than 2^-19.5 (1 + |bias|) in all, so 2^-17.5 for the difference of two sums of two.
-constexpr float EDGE = 1.0f / (1 << 17);
+// What cuts must be wider than, times 2 + the largest |bias|: the error of the difference of two sums of two scores in
+// fp32, the bias's addition (2^-24 of 1 + |bias|) included.  A sigmoid s from exp_near (2^-22.3 of itself, times
+// s (1 - s)) and a reciprocal with one step of Newton's (with 1 + e's rounding 2^-23 s) is off by less than
+// 2^-22.4.  Softmax by __expf, off by (|x| + 2) 2^-23 of itself: less than 2^-20 (its sum of 256: |x| averages
+// at most ln 256 there), and 2^-21 for the sums and the reciprocal.
+constexpr float EDGE_SIGMOID = 1.0f / (1 << 20), EDGE_SOFTMAX = 1.0f / (1 << 17);
+
+__device__ __forceinline__ float score_sigmoid(float x) {
+    const float d = 1.0f + fminf(exp_near(-x), 1e30f), s = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, s, 1.0f), s, s);
+}
 
 __device__ __forceinline__ uint64_t order_key64(double v) {
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);          // (-0 and 0 are equal)
@@ -180,7 +186,8 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
     bool on[4], live[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) live[i] = on[i] = lane + 64 * i < E && v[i] > NONE;
-    float c[4], g[4], edge = 2.0f * EDGE, top = 0.0f;        // c: for the selection, g: for the groups
+    const float unit = r.sigmoid ? EDGE_SIGMOID : EDGE_SOFTMAX;
+    float c[4], g[4], edge = 2.0f * unit, top = 0.0f;        // c: for the selection, g: for the groups
     if (!r.sigmoid) {
         uint32_t mk = 0u;
 #pragma unroll
@@ -192,7 +199,7 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
     if (scored) {
         if (r.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-v[i]));
+            for (int i = 0; i < 4; ++i) g[i] = score_sigmoid(v[i]);
         } else {
             float z = 0.0f;
 #pragma unroll
@@ -212,7 +219,7 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
                 live[i] = live[i] && bias[i] > NONE;
                 c[i] = g[i] = g[i] + bias[i];
             }
-            edge = EDGE * (2.0f + __uint_as_float(wave_max_bcast(m)));   // (infinity, NaN: no cut is wide enough)
+            edge = unit * (2.0f + __uint_as_float(wave_max_bcast(m)));   // (infinity, NaN: no cut is wide enough)
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = v[i];

@@ -116,6 +116,21 @@ def test_close_scores(torch, qs, name):
     check_select(idx, w, l.astype(np.float64), k, r, name)
 
 
+@pytest.mark.parametrize("name", ["bias", "group2", "group2bias", "softbias", "softgroup2", "groupbias"])
+@pytest.mark.parametrize("spread", [1e-2, 1e-3, 1e-4, 1e-5])
+def test_crowded_scores(torch, qs, name, spread):
+    """Rows whose scores all lie close together: the cuts fall on either side of what fp32 scores can
+    decide, and the selection is that of 64-bit scores on both."""
+    E, k, T = 240, 6, 500
+    rng = np.random.default_rng(21)
+    l = (rng.uniform(-3, 3, (T, 1)) + spread * rng.standard_normal((T, E))).astype(np.float32)
+    r = rule_for(name, E, k)
+    if r.get("select_bias") is not None:
+        r["select_bias"] = (spread * rng.standard_normal(E) + rng.choice([0.0, 3.0])).astype(np.float32)
+    idx, w = qs.moe_select(torch.from_numpy(l).cuda(), k, to_rule(r, torch, qs))
+    check_select(idx, w, l.astype(np.float64), k, r, name)
+
+
 @pytest.mark.parametrize("name", sorted(RULES))
 def test_masked_logits(torch, qs, name):
     """-infinity, NaN, the type's lowest value and +infinity; rows with few live experts or none."""
