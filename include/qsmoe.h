@@ -313,7 +313,7 @@ moe_status moe_layer_forward_static(const moe_layer_desc *d, const void *x, int6
  * r_out or x may be y, r or gate itself (same pointer, type and stride: in place), or other columns of the
  * same matrix; any other overlap with an input, and any of the outputs with each other, is
  * MOE_ERR_INVALID, as are a post, gate or r_out without y.
- * Limits (else MOE_ERR_UNSUPPORTED): 1 <= H <= 32768, T <= 2^26.  T == 0 enqueues nothing.
+ * Limits (else MOE_ERR_UNSUPPORTED): 1 <= H <= 16384, T <= 2^26.  T == 0 enqueues nothing.
  */
 #define MOE_NORM_RMS   0
 #define MOE_NORM_LAYER 1

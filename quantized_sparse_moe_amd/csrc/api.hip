@@ -500,7 +500,7 @@ bool overlap(const void *a, size_t an, const void *b, size_t bn) {
     return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
 }
 
-constexpr int64_t NORM_MAX_H = 32768;
+constexpr int64_t NORM_MAX_H = 16384;
 constexpr int64_t LORA_MAX_R = 256, LORA_MAX_N = 1 << 23, LORA_MAX_ADAPTERS = 65536;
 
 moe_status check_norm(const moe_norm *n, NormArgs *out) {

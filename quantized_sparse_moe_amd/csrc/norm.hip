@@ -18,64 +18,76 @@ namespace {
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
-// 8 V values of a row as a thread holds them: V chunks of 8 neighbours, P chunks apart (VEC), or
-// values P apart (rows that are not 16-byte aligned, or whose length is no multiple of 8).
-template <bool VEC, int P, int V>
-struct Row {
-    static __device__ __forceinline__ int at(int t, int i, int j) { return VEC ? (t + P * i) * 8 + j : t + P * (8 * i + j); }
+// 16 bytes wherever they lie (the hardware takes any alignment of a value's)
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+
+// The V chunks of 8 neighbouring values of a row that a thread holds, P chunks apart.  Rows of odd width or
+// offset (ODD): chunks begin where the row's memory is 16-byte aligned, `skew` values before its first, so
+// that only the first and the last are not whole; these are read as the 8 values nearest to them, of which
+// values lo .. hi - 1 count.  ODD 2: rows of fewer than 8 values.
+template <int ODD, int P, int V>
+struct Chunks {
+    int H, col[V], lo[V], hi[V];                             // col: first column
+    __device__ __forceinline__ Chunks(int t, int h, int skew) : H(h) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int s = (t + P * i) * 8 - skew;
+            col[i] = ODD ? max(min(s, H - 8), 0) : s;        // (H < 8: 0)
+            lo[i] = max(s - col[i], 0);
+            hi[i] = min(min(s + 8 - col[i], 8), H);
+        }
+    }
+    __device__ __forceinline__ bool whole(int i) const { return ODD ? (lo[i] == 0) & (hi[i] == 8) : col[i] < H; }
+    __device__ __forceinline__ bool in(int i, int j) const { return ODD ? (j >= lo[i]) & (j < hi[i]) : col[i] < H; }
 };
 
 // loaded and not yet widened
-template <bool VEC, int V>
+template <int V>
 struct Raw {
     u32x4 q[V][2];
 };
 
-template <bool VEC, int P, int V>
-__device__ __forceinline__ void load_row(Raw<VEC, V> &w, const void *p, int dt, int64_t off, int t, int H) {
-    if constexpr (VEC) {
-        if (dt == MOE_F32) {
+template <int ODD, int P, int V>
+__device__ __forceinline__ void load_row(Raw<V> &w, const void *p, int dt, int64_t off, const Chunks<ODD, P, V> &c) {
+    if constexpr (ODD == 2) {                                // (one chunk: values past the row repeat its last)
+        uint32_t e[8];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if ((t + P * i) * 8 < H) {
-                    const u32x4 *s = (const u32x4 *)((const float *)p + off + (t + P * i) * 8);
-                    w.q[i][0] = s[0];
-                    w.q[i][1] = s[1];
-                }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if ((t + P * i) * 8 < H) w.q[i][0] = *(const u32x4 *)((const uint16_t *)p + off + (t + P * i) * 8);
+        for (int j = 0; j < 8; ++j) {
+            const int64_t o = off + min(j, c.H - 1);
+            e[j] = dt == MOE_F32 ? ((const uint32_t *)p)[o] : ((const uint16_t *)p)[o];
         }
+        const u32x4 a = {e[0], e[1], e[2], e[3]}, b = {e[4], e[5], e[6], e[7]};
+        const u32x4 h = {e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+        w.q[0][0] = dt == MOE_F32 ? a : h;
+        w.q[0][1] = b;
+    } else if (dt == MOE_F32) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (ODD || c.col[i] < c.H) {
+                const u32x4_any *s = (const u32x4_any *)((const float *)p + off + c.col[i]);
+                w.q[i][0] = s[0];
+                w.q[i][1] = s[1];
+            }
     } else {
-        // (past the row's end: its last value, not used)
-        if (dt == MOE_F32) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w.q[i][j >> 2][j & 3] = ((const uint32_t *)p)[off + min(Row<VEC, P, V>::at(t, i, j), H - 1)];
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w.q[i][j >> 2][j & 3] = ((const uint16_t *)p)[off + min(Row<VEC, P, V>::at(t, i, j), H - 1)];
-        }
+        for (int i = 0; i < V; ++i)
+            if (ODD || c.col[i] < c.H) {
+                // (both words in both branches: their last stores merge, and must be to one place)
+                w.q[i][0] = *(const u32x4_any *)((const uint16_t *)p + off + c.col[i]);
+                w.q[i][1] = (u32x4){0u, 0u, 0u, 0u};
+            }
     }
 }
 
-// the values (VEC: two 16-bit ones a word; else one a word)
-template <bool VEC, int V>
-__device__ __forceinline__ float value(const Raw<VEC, V> &w, int dt, int i, int j) {
+template <int V>
+__device__ __forceinline__ float value(const Raw<V> &w, int dt, int i, int j) {
     if (dt == MOE_F32) return __uint_as_float(w.q[i][j >> 2][j & 3]);
-    uint32_t u;
-    if constexpr (VEC) u = (j & 1) ? w.q[i][0][j >> 1] >> 16 : w.q[i][0][j >> 1] & 0xffffu;
-    else u = w.q[i][j >> 2][j & 3];
+    const uint32_t u = (j & 1) ? w.q[i][0][j >> 1] >> 16 : w.q[i][0][j >> 1] & 0xffffu;
     return dt == MOE_BF16 ? __uint_as_float(u << 16) : f16_to_f32((uint16_t)u);
 }
-template <bool VEC, int V>
-__device__ __forceinline__ void widen(const Raw<VEC, V> &w, int dt, float (&f)[V][8]) {
+template <int V>
+__device__ __forceinline__ void widen(const Raw<V> &w, int dt, float (&f)[V][8]) {
     if (dt == MOE_F32) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -94,31 +106,32 @@ __device__ __forceinline__ void widen(const Raw<VEC, V> &w, int dt, float (&f)[V
     }
 }
 
-template <bool VEC, int P, int V>
-__device__ __forceinline__ void store_row(void *p, int dt, int64_t off, int t, int H, const float (&f)[V][8]) {
+template <int ODD, int P, int V>
+__device__ __forceinline__ void store_row(void *p, int dt, int64_t off, const Chunks<ODD, P, V> &c, const float (&f)[V][8]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if constexpr (VEC) {
-            if ((t + P * i) * 8 >= H) continue;
-            const int64_t o = off + (t + P * i) * 8;
-            if (dt == MOE_F32) {
-                f32x4 *d = (f32x4 *)((float *)p + o);
-                d[0] = (f32x4){f[i][0], f[i][1], f[i][2], f[i][3]};
-                d[1] = (f32x4){f[i][4], f[i][5], f[i][6], f[i][7]};
-                continue;
-            }
-            const f32x8 v = {f[i][0], f[i][1], f[i][2], f[i][3], f[i][4], f[i][5], f[i][6], f[i][7]};
-            *(u32x4 *)((uint16_t *)p + o) = dt == MOE_BF16 ? __builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8v))
-                                                           : __builtin_bit_cast(u32x4, __builtin_convertvector(v, f16x8));
-        } else {
+        const f32x8 v = {f[i][0], f[i][1], f[i][2], f[i][3], f[i][4], f[i][5], f[i][6], f[i][7]};
+        if (dt == MOE_F32) {
+            float *d = (float *)p + off + c.col[i];
+            if (c.whole(i)) {
+                ((f32x4_any *)d)[0] = (f32x4){v[0], v[1], v[2], v[3]};
+                ((f32x4_any *)d)[1] = (f32x4){v[4], v[5], v[6], v[7]};
+            } else if (ODD) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = Row<VEC, P, V>::at(t, i, j);
-                if (c >= H) continue;
-                if (dt == MOE_F32) ((float *)p)[off + c] = f[i][j];
-                else if (dt == MOE_BF16) ((uint16_t *)p)[off + c] = f32_to_bf16(f[i][j]);
-                else ((_Float16 *)p)[off + c] = (_Float16)f[i][j];
+                for (int j = 0; j < 8; ++j)
+                    if (c.in(i, j)) d[j] = v[j];
             }
+            continue;
+        }
+        const u32x4 w = dt == MOE_BF16 ? __builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8v))
+                                       : __builtin_bit_cast(u32x4, __builtin_convertvector(v, f16x8));
+        uint16_t *d = (uint16_t *)p + off + c.col[i];
+        if (c.whole(i)) {
+            *(u32x4_any *)d = w;
+        } else if (ODD) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c.in(i, j)) d[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
         }
     }
 }
@@ -138,22 +151,22 @@ __device__ __forceinline__ float row_sum(float v, int slot) {
     return s;
 }
 
-// values past the row's end to 0
-template <bool VEC, int P, int V>
-__device__ __forceinline__ void mask_row(float (&f)[V][8], int t, int H) {
+// values that are not of the row, or another chunk's, to 0
+template <int ODD, int P, int V>
+__device__ __forceinline__ void mask_row(float (&f)[V][8], const Chunks<ODD, P, V> &c) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = Row<VEC, P, V>::at(t, i, j) < H ? f[i][j] : 0.0f;
+        for (int j = 0; j < 8; ++j) f[i][j] = c.in(i, j) ? f[i][j] : 0.0f;
 }
 
 // f -> its norm (values past the row's end are 0 before and not used after)
-template <bool VEC, int P, int V>
-__device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs &n, int t, int H, int slot) {
-    Raw<VEC, V> w{}, b{};
-    if (n.w) load_row<VEC, P, V>(w, n.w, n.dtype, 0, t, H);
-    if (n.b) load_row<VEC, P, V>(b, n.b, n.dtype, 0, t, H);
-    const float ih = 1.0f / (float)H;
+template <int ODD, int P, int V>
+__device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs &n, const Chunks<ODD, P, V> &c, int slot) {
+    Raw<V> w{}, b{};
+    if (n.w) load_row<ODD, P, V>(w, n.w, n.dtype, 0, c);
+    if (n.b) load_row<ODD, P, V>(b, n.b, n.dtype, 0, c);
+    const float ih = 1.0f / (float)c.H;
     if (n.layer) {
         float s = 0.0f;
 #pragma unroll
@@ -164,7 +177,7 @@ __device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs &n, in
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = Row<VEC, P, V>::at(t, i, j) < H ? f[i][j] - m : 0.0f;
+            for (int j = 0; j < 8; ++j) f[i][j] = c.in(i, j) ? f[i][j] - m : 0.0f;
     }
     float q = 0.0f;
 #pragma unroll
@@ -200,16 +213,24 @@ __device__ __forceinline__ float activate(float g, int act) {
     return act == MOE_ACT_SIGMOID ? s : g * s;
 }
 
-template <bool VEC, int P, int V>
+template <int ODD, int P, int V>
 __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs a) {
     constexpr int RPW = P < 256 ? 256 / P : 1;               // rows per workgroup
-    const int t = threadIdx.x % P, H = a.H;
     const int64_t row = a.row0 + (int64_t)blockIdx.x * RPW + threadIdx.x / P;
     if (row >= a.T) return;                                  // (whole rows; P > 64: never)
-    Raw<VEC, V> y{}, r{}, g{};
-    if (a.y) load_row<VEC, P, V>(y, a.y, a.dy, row * a.ldy, t, H);
-    if (a.r) load_row<VEC, P, V>(r, a.r, a.dr, row * a.ldr, t, H);
-    if (a.gate && a.gate_cols > 1) load_row<VEC, P, V>(g, a.gate, a.dg, row * a.ldg, t, H);
+    int skew = 0;
+    if constexpr (ODD == 1) {
+        // (of the tensor read first; the others lie the same way where their rows are as far apart)
+        const uintptr_t p = a.y ? (uintptr_t)a.y + row * a.ldy * (a.dy == MOE_F32 ? 4 : 2)
+                                : (uintptr_t)a.r + row * a.ldr * (a.dr == MOE_F32 ? 4 : 2);
+        skew = (int)(p >> ((a.y ? a.dy : a.dr) == MOE_F32 ? 2 : 1)) & 7;
+        if (a.H + 7 > 8 * P * V) skew = 0;                   // (no chunk to spare: as they lie)
+    }
+    const Chunks<ODD, P, V> c(threadIdx.x % P, a.H, skew);
+    Raw<V> y{}, r{}, g{};
+    if (a.y) load_row<ODD, P, V>(y, a.y, a.dy, row * a.ldy, c);
+    if (a.r) load_row<ODD, P, V>(r, a.r, a.dr, row * a.ldr, c);
+    if (a.gate && a.gate_cols > 1) load_row<ODD, P, V>(g, a.gate, a.dg, row * a.ldg, c);
     float gt = 1.0f;
     if (a.gate && a.gate_cols == 1) {
         const int64_t o = row * a.ldg;
@@ -221,8 +242,8 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
     if (a.y) {
         widen(y, a.dy, z);
         if (a.post.on) {
-            if constexpr (!VEC) mask_row<VEC, P, V>(z, t, H);
-            norm_row<VEC, P, V>(z, a.post, t, H, 0);
+            if constexpr (ODD > 0) mask_row<ODD, P, V>(z, c);
+            norm_row<ODD, P, V>(z, a.post, c, 0);
         }
         float s = a.scale;
         if (a.gate) {
@@ -252,14 +273,14 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) z[i][j] *= s;
         }
-        if (a.ro) store_row<VEC, P, V>(a.ro, a.dro, row * a.ldro, t, H, z);
+        if (a.ro) store_row<ODD, P, V>(a.ro, a.dro, row * a.ldro, c, z);
     } else {
         widen(r, a.dr, z);
     }
     if (a.pre.on) {
-        mask_row<VEC, P, V>(z, t, H);
-        norm_row<VEC, P, V>(z, a.pre, t, H, 2);
-        store_row<VEC, P, V>(a.xo, a.dxo, row * a.ldxo, t, H, z);
+        mask_row<ODD, P, V>(z, c);
+        norm_row<ODD, P, V>(z, a.pre, c, 2);
+        store_row<ODD, P, V>(a.xo, a.dxo, row * a.ldxo, c, z);
     }
 }
 
@@ -269,7 +290,9 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
 //   16384 x 4096  256 of 16: 95.9 (5.60), 512 of 8: 96.0                     131072 x 512   64 of 8: 93.9 (5.72)
 //   16384 x 8192  512 of 16: 210 (5.11), 256 of 32: 214, 1024 of 8: 266      8192 x 16384   1024 of 16: 224 (4.80)
 //   (with a gate: 266 (5.05), 291, 370; a large copy moves 4.8)
-template <bool VEC>
+// Odd widths (read and written value by value before): 32768 x 2047 117 (4.6; 156), 16384 x 8191 303 (3.5; 530),
+// 16384 x 5001 238 (2.8; 430).
+template <int ODD>
 void launch_p(BlockNormArgs a, hipStream_t s) {
     // (a launch has fewer than 2^32 threads)
     auto go = [&](void (*k)(BlockNormArgs), int p) {
@@ -279,35 +302,31 @@ void launch_p(BlockNormArgs a, hipStream_t s) {
             hipLaunchKernelGGL(k, dim3((unsigned)((rows + rpw - 1) / rpw)), dim3((unsigned)(p < 256 ? 256 : p)), 0, s, a);
         }
     };
-    if (a.H <= 128) go(k_block_norm<VEC, 16, 1>, 16);
-    else if (a.H <= 512) go(k_block_norm<VEC, 64, 1>, 64);
-    else if (a.H <= 1024) go(k_block_norm<VEC, 64, 2>, 64);
-    else if (a.H <= 2048) go(k_block_norm<VEC, 256, 1>, 256);
-    else if (a.H <= 4096) go(k_block_norm<VEC, 256, 2>, 256);
-    else if (a.H <= 8192) go(k_block_norm<VEC, 512, 2>, 512);
-    else if (a.H <= 16384) go(k_block_norm<VEC, 1024, 2>, 1024);
-    else go(k_block_norm<VEC, 1024, 4>, 1024);
+    const int w = a.H;
+    if (ODD && w < 8) go(k_block_norm<2, 16, 1>, 16);
+    else if (w <= 128) go(k_block_norm<ODD, 16, 1>, 16);
+    else if (w <= 512) go(k_block_norm<ODD, 64, 1>, 64);
+    else if (w <= 1024) go(k_block_norm<ODD, 64, 2>, 64);
+    else if (w <= 2048) go(k_block_norm<ODD, 256, 1>, 256);
+    else if (w <= 4096) go(k_block_norm<ODD, 256, 2>, 256);
+    else if (w <= 8192) go(k_block_norm<ODD, 512, 2>, 512);
+    else go(k_block_norm<ODD, 1024, 2>, 1024);
 }
 
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t s) {
-    // 16-byte accesses where every row of every tensor allows them
-    bool vec = a.H % 8 == 0;
+    // rows whose chunks are all whole and aligned
+    bool even = a.H % 8 == 0;
     auto check = [&](const void *p, int dt, int64_t ld) {
-        if (p && ((uintptr_t)p % 16 || (a.T > 1 && ld * (dt == MOE_F32 ? 4 : 2) % 16))) vec = false;
+        if (p && ((uintptr_t)p % 16 || (a.T > 1 && ld * (dt == MOE_F32 ? 4 : 2) % 16))) even = false;
     };
     check(a.y, a.dy, a.ldy);
     check(a.r, a.dr, a.ldr);
-    if (a.gate_cols > 1) check(a.gate, a.dg, a.ldg);
     check(a.ro, a.dro, a.ldro);
     check(a.xo, a.dxo, a.ldxo);
-    for (const NormArgs *n : {&a.post, &a.pre}) {
-        check(n->w, n->dtype, 0);
-        check(n->b, n->dtype, 0);
-    }
-    if (vec) launch_p<true>(a, s);
-    else launch_p<false>(a, s);
+    if (even) launch_p<0>(a, s);
+    else launch_p<1>(a, s);
     return hipGetLastError();
 }
 

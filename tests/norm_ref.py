@@ -2,7 +2,7 @@
 its definition.  Test infrastructure: shares no code with the library.
 
 Bound, with u = 2^-24 (half a step of fp32, what one operation rounds by, relative to its result):
-a sum of n <= 32768 values is a chain of at most 34 additions in a thread and 18 more across threads,
+a sum of n <= 16384 values is a chain of at most 18 additions in a thread and 26 more across threads,
 so it is off by at most SUM u of the sum of magnitudes, SUM = 64."""
 import numpy as np
 

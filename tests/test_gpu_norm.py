@@ -64,7 +64,8 @@ def check(torch, a, e, types, out, what):
 
 SHAPES = [(1, 1), (3, 7), (5, 8), (2, 64), (67, 128), (9, 129), (33, 512), (3, 513), (5, 1024), (6, 1023), (4, 1032),
           (2, 4096), (3, 4095), (2, 16384), (2, 16381), (1, 2048), (600, 2048), (5, 2047),
-          (520, 2047), (2, 2056), (4, 8192), (530, 8192), (3, 8191), (2, 8200), (2, 32768), (2, 32767)]
+          (520, 2047), (2, 2056), (4, 8192), (530, 8192), (3, 8191), (2, 8200), (2, 8193), (3, 15), (4, 1001), (3, 16383), (2, 16378), (5, 2041),
+          (5, 2042), (9, 505), (9, 506), (17, 121), (17, 122), (40, 9), (30, 5)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)

@@ -52,7 +52,7 @@ def test_invalid(i):
 
 def test_limits_and_nothing_to_do():
     assert call(H=0) == q.MOE_ERR_UNSUPPORTED
-    assert call(H=32769) == q.MOE_ERR_UNSUPPORTED
+    assert call(H=16385) == q.MOE_ERR_UNSUPPORTED
     assert call(T=(1 << 26) + 1) == q.MOE_ERR_UNSUPPORTED
     assert call(T=0, y=None, r=None, x=None) == q.MOE_OK
 
