@@ -19,6 +19,10 @@ namespace qs {
 namespace {
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+// rows of y and base may lie at any alignment of their values
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+typedef bf16x8 __attribute__((aligned(2))) bf16x8_any;
 
 // lane n < 16 of every 16 holds token n's adapter (-1: none) and its place among the tile's distinct
 // ones, which are numbered in token order
@@ -200,7 +204,9 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
 // Bound by memory: y read and written, each request's rows of B. T = 4096 x 16384, rank 32: 68 us, 268 MB of y at 3.9 TB/s
 // (shrink 11); columns before tiles in the grid, so that neighbouring workgroups write neighbouring
 // columns (the other way 80 us); the next tile's loads ahead of this one's products gain nothing
-// (four waves a SIMD hide them, and spill fewer registers).
+// (four waves a SIMD hide them, and spill fewer registers; with fp32 y four would spill, 155 us and 149 with three).
+// Rows of other widths and strides are read and written by 16 bytes as they lie, but for the last 64 columns
+// (N = 16381 160 us, value by value 287; fp32 y, N = 8191 126 and 268).
 //
 // FEW > 0: up to 16 tokens of up to 16 FEW ranks in one launch; every workgroup (of SH_WAVES) shrinks for
 // itself, v stays in LDS.  us a call in a graph against two launches (K = 2048): T = 1, N = 2048, rank 16
@@ -209,15 +215,16 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
 // too often (T = 16, N = 16384, 16 adapters: 15.0 and 14.6).
 constexpr int EX_WAVES = 4;
 
-template <int PARTS, bool F32, bool VEC, int RS, int FEW = 0>
+template <int PARTS, bool F32, int RS, int FEW = 0>
 __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
-    __attribute__((amdgpu_waves_per_eu(FEW ? 2 : RS == 1 ? 4 : RS == 2 ? 3 : 2))) void k_lora_expand(LoraArgs a, int tt) {
+    __attribute__((amdgpu_waves_per_eu(FEW ? 2 : RS == 1 && !F32 ? 4 : RS <= 2 ? 3 : 2))) void k_lora_expand(LoraArgs a, int tt) {
     __shared__ f32x4 red[FEW ? SH_WAVES : 1][FEW ? FEW : 1][64];
     extern __shared__ __attribute__((aligned(16))) uint16_t few_v[];     // [16][PARTS][R]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int R = a.R, slot = blockIdx.z, slots = gridDim.z;
     const int64_t c0 = ((int64_t)blockIdx.x * (FEW ? SH_WAVES : EX_WAVES) + wave) * 64, N = a.N;
     if (!FEW && c0 >= N) return;
+    const bool whole = c0 + 64 <= N;                         // (the last columns of other widths: value by value)
     auto column = [&](int i, int row) { return c0 + (F32 ? 16 * i + row : 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3)); };
     u32x4 B[RS][4];
     int held = -1, rank = 0;
@@ -264,15 +271,13 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
         u32x4 raw[F32 ? 4 : 2];
-        if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < (F32 ? 4 : 2); ++i) {
-                raw[i] = (u32x4){0u, 0u, 0u, 0u};
-                const int64_t c = column(F32 ? i : 2 * i, 4 * g);
-                if (a.base && live && c < N)
-                    raw[i] = F32 ? *(const u32x4 *)((const float *)a.base + t * a.ldb + c)
-                                 : *(const u32x4 *)((const uint16_t *)a.base + t * a.ldb + c);
-            }
+        for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+            raw[i] = (u32x4){0u, 0u, 0u, 0u};
+            const int64_t c = column(F32 ? i : 2 * i, 4 * g);
+            if (a.base && live && whole)
+                raw[i] = F32 ? *(const u32x4_any *)((const float *)a.base + t * a.ldb + c)
+                             : *(const u32x4_any *)((const uint16_t *)a.base + t * a.ldb + c);
         }
         for (uint32_t m = tile.first, k = 0; m; m &= m - 1, ++k) {
             if ((int)k % slots != slot) continue;
@@ -315,12 +320,12 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
                 for (int r = 0; r < 4; ++r) out[i][r] = mine ? acc[i][r] : out[i][r];
         }
         if (!live) continue;
-        if constexpr (VEC) {
+        if (whole) {
             if constexpr (F32) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int64_t c = column(i, 4 * g);
-                    if (c < N) *(f32x4 *)((float *)a.y + t * a.ldy + c) = out[i] + __builtin_bit_cast(f32x4, raw[i]);
+                    *(f32x4_any *)((float *)a.y + t * a.ldy + c) = out[i] + __builtin_bit_cast(f32x4, raw[i]);
                 }
             } else {
 #pragma unroll
@@ -332,7 +337,7 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
                         w[2 * j] = out[2 * i + (j >> 1)][2 * (j & 1)] + __uint_as_float(raw[i][j] << 16);
                         w[2 * j + 1] = out[2 * i + (j >> 1)][2 * (j & 1) + 1] + __uint_as_float(raw[i][j] & 0xffff0000u);
                     }
-                    if (c < N) *(bf16x8 *)((uint16_t *)a.y + t * a.ldy + c) = __builtin_convertvector(w, bf16x8);
+                    *(bf16x8_any *)((uint16_t *)a.y + t * a.ldy + c) = __builtin_convertvector(w, bf16x8);
                 }
             }
         } else {
@@ -368,15 +373,11 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
         int64_t k = (2 * cus + groups - 1) / groups;
         return (unsigned)(k < most ? k : most);
     };
-    const int64_t sz = F32 ? 4 : 2, per = 16 / sz;
-    auto wide = [&](const void *p, int64_t ld) { return (uintptr_t)p % 16 == 0 && (a.T == 1 || ld % per == 0); };
-    const bool vec = a.N % per == 0 && wide(a.y, a.ldy) && (!a.base || wide(a.base, a.ldb));
     // Up to 16 tokens in one launch where the workgroups' reading of A, each for itself, is little
     const int64_t fblk = (a.N + 64 * SH_WAVES - 1) / (64 * SH_WAVES);
     if (tiles == 1 && a.R <= 32 && (int64_t)a.R * a.K <= FEW_A && fblk * most * a.R * a.K <= FEW_ALL) {
         const size_t lds = (size_t)16 * PARTS * a.R * 2;
-        void (*k)(LoraArgs, int) = rblk == 1 ? (vec ? k_lora_expand<PARTS, F32, true, 1, 1> : k_lora_expand<PARTS, F32, false, 1, 1>)
-                                             : (vec ? k_lora_expand<PARTS, F32, true, 1, 2> : k_lora_expand<PARTS, F32, false, 1, 2>);
+        void (*k)(LoraArgs, int) = rblk == 1 ? k_lora_expand<PARTS, F32, 1, 1> : k_lora_expand<PARTS, F32, 1, 2>;
         hipLaunchKernelGGL(k, dim3((unsigned)fblk, 1, (unsigned)most), dim3(64 * SH_WAVES), lds, s, a, 1);
         return hipGetLastError();
     }
@@ -399,10 +400,10 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     while (tt > 1 && (tiles + tt - 1) / tt * cblk < 8 * cus) tt >>= 1;
     const unsigned tx = (unsigned)((tiles + tt - 1) / tt);
     const dim3 eg((unsigned)cblk, tx, slots((int64_t)tx * cblk));
-    const int rs = a.R <= 32 ? 1 : a.R <= 64 ? 2 : 4;
-    auto go = [&](void (*k)(LoraArgs, int)) { hipLaunchKernelGGL(k, eg, dim3(64 * EX_WAVES), 0, s, a, tt); };
-    if (vec) go(rs == 1 ? k_lora_expand<PARTS, F32, true, 1> : rs == 2 ? k_lora_expand<PARTS, F32, true, 2> : k_lora_expand<PARTS, F32, true, 4>);
-    else go(rs == 1 ? k_lora_expand<PARTS, F32, false, 1> : rs == 2 ? k_lora_expand<PARTS, F32, false, 2> : k_lora_expand<PARTS, F32, false, 4>);
+    void (*k)(LoraArgs, int) = a.R <= 32   ? k_lora_expand<PARTS, F32, 1>
+                               : a.R <= 64 ? k_lora_expand<PARTS, F32, 2>
+                                           : k_lora_expand<PARTS, F32, 4>;
+    hipLaunchKernelGGL(k, eg, dim3(64 * EX_WAVES), 0, s, a, tt);
     return hipGetLastError();
 }
 
