@@ -204,27 +204,29 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
 // Bound by memory: y read and written, each request's rows of B. T = 4096 x 16384, rank 32: 68 us, 268 MB of y at 3.9 TB/s
 // (shrink 11); columns before tiles in the grid, so that neighbouring workgroups write neighbouring
 // columns (the other way 80 us); the next tile's loads ahead of this one's products gain nothing
-// (four waves a SIMD hide them, and spill fewer registers; with fp32 y four would spill, 155 us and 149 with three).
-// Rows of other widths and strides are read and written by 16 bytes as they lie, but for the last 64 columns
-// (N = 16381 160 us, value by value 287; fp32 y, N = 8191 126 and 268).
+// (four waves a SIMD hide them, and spill fewer registers).
+// Rows of any stride and alignment are read and written by 16 bytes as they lie.  TAIL: a width that is no
+// multiple of 64, whose last columns go value by value (N = 16381 160 us, all of them so 287; fp32 y, N = 8191 126 and
+// 268, three waves a SIMD, for four would spill: 136); the code for them costs the other widths 0.1 to
+// 0.4 us of a call of few tokens, so they have kernels without it.
 //
 // FEW > 0: up to 16 tokens of up to 16 FEW ranks in one launch; every workgroup (of SH_WAVES) shrinks for
 // itself, v stays in LDS.  us a call in a graph against two launches (K = 2048): T = 1, N = 2048, rank 16
-// 7.1 and 9.1, rank 32 9.1 and 9.3, T = 16 with 8 adapters 8.9 and 11.3, T = 1, N = 16384, rank 16 7.3 and 9.2;
+// 6.8 and 9.1, rank 32 8.7 and 9.3, T = 16 with 8 adapters 8.7 and 11.3, T = 1, N = 16384, rank 16 7.0 and 9.2;
 // ranks of 64 in turns of 32 9.8 and 9.2, so they take two launches, as do calls whose workgroups would read A
 // too often (T = 16, N = 16384, 16 adapters: 15.0 and 14.6).
 constexpr int EX_WAVES = 4;
 
-template <int PARTS, bool F32, int RS, int FEW = 0>
+template <int PARTS, bool F32, bool TAIL, int RS, int FEW = 0>
 __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
-    __attribute__((amdgpu_waves_per_eu(FEW ? 2 : RS == 1 && !F32 ? 4 : RS <= 2 ? 3 : 2))) void k_lora_expand(LoraArgs a, int tt) {
+    __attribute__((amdgpu_waves_per_eu(FEW ? 2 : RS == 1 && !(F32 && TAIL) ? 4 : RS <= 2 ? 3 : 2))) void k_lora_expand(LoraArgs a, int tt) {
     __shared__ f32x4 red[FEW ? SH_WAVES : 1][FEW ? FEW : 1][64];
     extern __shared__ __attribute__((aligned(16))) uint16_t few_v[];     // [16][PARTS][R]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
     const int R = a.R, slot = blockIdx.z, slots = gridDim.z;
     const int64_t c0 = ((int64_t)blockIdx.x * (FEW ? SH_WAVES : EX_WAVES) + wave) * 64, N = a.N;
     if (!FEW && c0 >= N) return;
-    const bool whole = c0 + 64 <= N;                         // (the last columns of other widths: value by value)
+    const bool whole = c0 + (TAIL ? 64 : 1) <= N;            // (FEW: the last waves may have no columns)
     auto column = [&](int i, int row) { return c0 + (F32 ? 16 * i + row : 32 * (i >> 1) + 8 * (row >> 2) + 4 * (i & 1) + (row & 3)); };
     u32x4 B[RS][4];
     int held = -1, rank = 0;
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
                     *(bf16x8_any *)((uint16_t *)a.y + t * a.ldy + c) = __builtin_convertvector(w, bf16x8);
                 }
             }
-        } else {
+        } else if constexpr (TAIL) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -363,7 +365,7 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
 // values of A: of one adapter, and of all workgroups together
 constexpr int64_t FEW_A = 65536, FEW_ALL = 8 << 20;
 
-template <int PARTS, bool F32>
+template <int PARTS, bool F32, bool TAIL>
 hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     const int64_t tiles = (a.T + 15) / 16, rblk = (a.R + 15) / 16, cus = n_compute_units();
     // a tile's distinct adapters, at most; workgroups of their own until two a compute unit (T = 48 with 40
@@ -377,7 +379,7 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     const int64_t fblk = (a.N + 64 * SH_WAVES - 1) / (64 * SH_WAVES);
     if (tiles == 1 && a.R <= 32 && (int64_t)a.R * a.K <= FEW_A && fblk * most * a.R * a.K <= FEW_ALL) {
         const size_t lds = (size_t)16 * PARTS * a.R * 2;
-        void (*k)(LoraArgs, int) = rblk == 1 ? k_lora_expand<PARTS, F32, 1, 1> : k_lora_expand<PARTS, F32, 1, 2>;
+        void (*k)(LoraArgs, int) = rblk == 1 ? k_lora_expand<PARTS, F32, TAIL, 1, 1> : k_lora_expand<PARTS, F32, TAIL, 1, 2>;
         hipLaunchKernelGGL(k, dim3((unsigned)fblk, 1, (unsigned)most), dim3(64 * SH_WAVES), lds, s, a, 1);
         return hipGetLastError();
     }
@@ -400,9 +402,9 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
     while (tt > 1 && (tiles + tt - 1) / tt * cblk < 8 * cus) tt >>= 1;
     const unsigned tx = (unsigned)((tiles + tt - 1) / tt);
     const dim3 eg((unsigned)cblk, tx, slots((int64_t)tx * cblk));
-    void (*k)(LoraArgs, int) = a.R <= 32   ? k_lora_expand<PARTS, F32, 1>
-                               : a.R <= 64 ? k_lora_expand<PARTS, F32, 2>
-                                           : k_lora_expand<PARTS, F32, 4>;
+    void (*k)(LoraArgs, int) = a.R <= 32   ? k_lora_expand<PARTS, F32, TAIL, 1>
+                               : a.R <= 64 ? k_lora_expand<PARTS, F32, TAIL, 2>
+                                           : k_lora_expand<PARTS, F32, TAIL, 4>;
     hipLaunchKernelGGL(k, eg, dim3(64 * EX_WAVES), 0, s, a, tt);
     return hipGetLastError();
 }
@@ -410,7 +412,8 @@ hipError_t launch_parts(const LoraArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_lora(const LoraArgs &a, hipStream_t s) {
-    return a.f32 ? launch_parts<3, true>(a, s) : launch_parts<2, false>(a, s);
+    if (a.f32) return a.N % 64 ? launch_parts<3, true, true>(a, s) : launch_parts<3, true, false>(a, s);
+    return a.N % 64 ? launch_parts<2, false, true>(a, s) : launch_parts<2, false, false>(a, s);
 }
 
 }  // namespace qs
