@@ -151,6 +151,27 @@ def test_strides_in_place_and_rows_behind(torch, qs, dtype):
         call(torch, qs, d, dtype, base=v, y=wide[:T, 2:N + 2])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T, N, R", [(5, 64, 16), (5, 65, 32), (16, 576, 8), (16, 511, 16), (33, 64, 64), (33, 127, 16), (70, 640, 128),
+                                     (70, 63, 40)])
+def test_rows_at_any_alignment(torch, qs, T, N, R, dtype):
+    """y and base as views whose rows begin anywhere and end beside other values, which stay."""
+    d = make(torch, T, 96, N, R, 4, dtype=dtype, ragged=True)
+    want = call(torch, qs, d, dtype)
+    for left, right in ((1, 0), (3, 6), (8, 1)):
+        views = []
+        for fill in (5.0, -7.0):
+            wide = torch.full((T + 2, left + N + right), fill, dtype=want.dtype, device="cuda")
+            views.append(wide[1:T + 1, left:left + N])
+            keep = torch.ones_like(wide, dtype=torch.bool)
+            keep[1:T + 1, left:left + N] = False
+            views.append((wide, keep, fill))
+        base, _, y, (wide, keep, fill) = views
+        base.copy_(d["base"])
+        call(torch, qs, d, dtype, base=base, y=y)
+        assert torch.equal(y, want) and (wide[keep] == fill).all(), (left, right)
+
+
 def test_in_place_leaves_tokens_without_adapter(torch, qs):
     """A NaN with a payload of its own in such a row of a bf16 y stays bit for bit."""
     d = make(torch, 20, 64, 40, 8, 2)
