@@ -201,7 +201,7 @@ __global__ __launch_bounds__(64 * SH_WAVES) void k_lora_shrink(LoraArgs a) {
 // 16 i + n of the 64 (fp32 y: 16 bytes a register quad), or 32 (i / 2) + 8 (n / 4) + 4 (i % 2) + n % 4 (bf16: two
 // quads make 16 bytes), so that four lanes read and write 64 bytes in a row.
 //
-// Bound by memory: y read and written, each request's rows of B. T = 4096 x 16384, rank 32: 68 us, 268 MB of y at 3.9 TB/s
+// Bound by memory: y read and written, each request's rows of B. T = 4096 x 16384, rank 32: 63 us, 268 MB of y at 4.2 TB/s
 // (shrink 11); columns before tiles in the grid, so that neighbouring workgroups write neighbouring
 // columns (the other way 80 us); the next tile's loads ahead of this one's products gain nothing
 // (four waves a SIMD hide them, and spill fewer registers).

@@ -61,22 +61,18 @@ __device__ __forceinline__ void load_row(Raw<V> &w, const void *p, int dt, int64
         const u32x4 h = {e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
         w.q[0][0] = dt == MOE_F32 ? a : h;
         w.q[0][1] = b;
-    } else if (dt == MOE_F32) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (ODD || c.col[i] < c.H) {
-                const u32x4_any *s = (const u32x4_any *)((const float *)p + off + c.col[i]);
-                w.q[i][0] = s[0];
-                w.q[i][1] = s[1];
-            }
     } else {
+        // (the first 16 bytes without a branch on the type: with one, fp32 rows waited for the tensor before; us,
+        // with one and so: 16384 x 8192 222 and 211, fp32 stream 302 and 305, 16384 x 5001 238 and 213)
+        const int sh = dt == MOE_F32 ? 2 : 1;
+        const char *s = (const char *)p + (off << sh);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (ODD || c.col[i] < c.H) {
-                // (both words in both branches: their last stores merge, and must be to one place)
-                w.q[i][0] = *(const u32x4_any *)((const uint16_t *)p + off + c.col[i]);
-                w.q[i][1] = (u32x4){0u, 0u, 0u, 0u};
-            }
+            if (ODD || c.col[i] < c.H) w.q[i][0] = *(const u32x4_any *)(s + ((int64_t)c.col[i] << sh));
+        if (dt == MOE_F32)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (ODD || c.col[i] < c.H) w.q[i][1] = *(const u32x4_any *)(s + ((int64_t)c.col[i] << 2) + 16);
     }
 }
 
@@ -290,8 +286,8 @@ __global__ __launch_bounds__(P < 256 ? 256 : P) void k_block_norm(BlockNormArgs 
 //   16384 x 4096  256 of 16: 95.9 (5.60), 512 of 8: 96.0                     131072 x 512   64 of 8: 93.9 (5.72)
 //   16384 x 8192  512 of 16: 210 (5.11), 256 of 32: 214, 1024 of 8: 266      8192 x 16384   1024 of 16: 224 (4.80)
 //   (with a gate: 266 (5.05), 291, 370; a large copy moves 4.8)
-// Odd widths (read and written value by value before): 32768 x 2047 117 (4.6; 156), 16384 x 8191 303 (3.5; 530),
-// 16384 x 5001 238 (2.8; 430).
+// Odd widths (read and written value by value before): 32768 x 2047 117 (4.6; 156), 16384 x 8191 286 (3.8; 530),
+// 16384 x 5001 213 (3.1; 430).
 template <int ODD>
 void launch_p(BlockNormArgs a, hipStream_t s) {
     // (a launch has fewer than 2^32 threads)
