@@ -49,13 +49,14 @@ __device__ __forceinline__ float sb_to_f32(uint32_t bits, int bf16) {
     return bf16 ? __uint_as_float(bits << 16) : f16_to_f32((uint16_t)bits);
 }
 // exp(x) = 2^t (1 + ln2 d) for t = x log2 e rounded and d what it was rounded by (and the rest of the constant):
-// within 2 steps for every x (2^t alone is off by |x| / 2 steps), a quarter of expf's instructions
+// within 2 steps (2^t alone is off by |x| / 2 steps) and, below 2^-126, 0; a quarter of expf's instructions.  Where 2^t is
+// infinite it stays so: its correction would be infinity - infinity or infinity times 0.
 __device__ __forceinline__ float exp_near(float x) {
     constexpr float L = 1.44269502162933349609f, LO = 1.92596299112661746887e-8f, LN2 = 0.69314718055994530942f;
     const float t = x * L;
     const float d = __builtin_fmaf(x, LO, __builtin_fmaf(x, L, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fabsf(t) < 200.0f ? __builtin_fmaf(e, d * LN2, e) : e;        // (0, infinity, NaN as they are)
+    return __builtin_fabsf(t) < 128.0f ? __builtin_fmaf(e, d * LN2, e) : e;        // (0, infinity, NaN as they are)
 }
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
 

@@ -211,3 +211,54 @@ def test_streams_and_graphs(torch, qs):
         torch.cuda.synchronize()
         want = qs.moe_block_norm(**a)
         assert torch.equal(r, want[0]) and torch.equal(x, want[1])
+
+
+def gates(torch, dtype):
+    """Every finite bf16 value; for the wider types also values between them where a sigmoid's exponential
+    leaves fp32's range on either side, and the type's largest."""
+    g = (torch.arange(65536, dtype=torch.int32) << 16).view(torch.float32)
+    g = g[g.isfinite() & (g.abs() <= torch.finfo(dtype).max)]
+    if dtype != torch.bfloat16:
+        d = torch.linspace(80.0, 210.0, 8192)
+        g = torch.cat([g, d, -d, torch.tensor([-1.0, 1.0]) * torch.finfo(dtype).max])
+    return g.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_gates_of_any_size(torch, qs, act, dtype):
+    """The whole range of a gate: its activation is finite, and 0 where the exponential is infinite."""
+    D = dtypes(torch)[dtype]
+    g = gates(torch, D)
+    H = 128
+    g = torch.cat([g, g[:-len(g) % H]]).reshape(-1, H)
+    for gate in (g, g[:, ::9].reshape(-1, 1)):
+        y = torch.ones(gate.shape[0], H).to(D)
+        y[:, ::3] = -0.75
+        a = dict(y=y.cuda(), residual=None, gate=gate.cuda(), gate_act=act, scale=1.0, post=None, pre=None)
+        r, _ = qs.moe_block_norm(**a, r_dtype=torch.float32)
+        assert r.isfinite().all()
+        check(torch, a, dict(post=None, pre=None), dict(r="f32", x="f32"), (r, None), (act, dtype, gate.shape))
+        low = (gate.float() < -105.0).cuda().expand(-1, H)
+        assert (r[low] == 0).all()
+    # a row is normed beside such gates
+    g = g[(g.float().abs() <= 1e4)]
+    g = torch.cat([g, g[:-len(g) % H]]).reshape(-1, H)
+    a = dict(y=torch.ones(g.shape[0], H).to(D).cuda(), residual=torch.randn(g.shape[0], H, device="cuda"), gate=g.cuda(),
+             gate_act=act, scale=0.5, post=None, pre=qs.Norm(eps=1e-5))
+    e = dict(post=None, pre=dict(kind="rms", eps=float(np.float32(1e-5)), offset=0.0, weight=None, bias=None))
+    out = qs.moe_block_norm(**a, x_dtype=torch.float32)
+    assert out[0].isfinite().all() and out[1].isfinite().all()
+    check(torch, a, e, dict(r="f32", x="f32"), out, (act, dtype, "normed"))
+
+
+def test_infinite_gates(torch, qs):
+    inf = float("inf")
+    for H in (8, 9):
+        for gate in (torch.full((2, H), inf), torch.full((2, 1), inf)):
+            gate[1] = -inf
+            y = torch.full((2, H), 3.0, device="cuda")
+            r, _ = qs.moe_block_norm(y, gate=gate.cuda(), gate_act="sigmoid")
+            assert (r[0] == 3).all() and (r[1] == 0).all()
+            r, _ = qs.moe_block_norm(y, gate=gate.cuda(), gate_act="silu")
+            assert (r[0] == inf).all() and r[1].isnan().all()            # (-infinity times 0)
