@@ -348,7 +348,8 @@ __device__ __forceinline__ float row_weight(const RouteRule &r, float x, float t
     if (!(x > -__builtin_inff())) w = 0.0;
     if (r.renorm) sum = row_sum_f64(w);
     else if (!r.sigmoid) sum = z;
-    return sum > 0.0 ? (float)(w * ((double)r.scale / sum)) : 0.0f;
+    // (divided first: scale / sum overflows where the selected scores are all below 2^-1024 or so)
+    return sum > 0.0 ? (float)(w / sum * (double)r.scale) : 0.0f;
 }
 
 // Both: lanes j < K return the j-th selected expert in ascending id and its weight.

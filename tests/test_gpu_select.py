@@ -156,6 +156,33 @@ def test_masked_logits(torch, qs, name):
     check_select(idx, w, l.astype(np.float64), k, r, name)
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.5, -3.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_weights_of_scores_near_the_end_of_64_bits(torch, qs, score, scale):
+    """Selected scores of 6e-310 to 2e-308, one over which is no 64-bit number, beside experts that are not live.
+    (64-bit numbers are 4.9e-324 apart there: a score, the sum and the quotient of two evaluations
+    differ by some 4 e-15 each, within the slack of 6e-14 that check_select has.)"""
+    E, T = 40, 24
+    rng = np.random.default_rng(8)
+    bias = None
+    if score == "softmax":                                  # chosen by their bias, far below the row's largest
+        l = rng.uniform(-712.0, -709.9, (T, E)).astype(np.float32)
+        l[:, 17] = 0.0
+        bias = np.full(E, 4.0, np.float32)
+        bias[17] = 0.0
+    else:
+        l = rng.uniform(-709.5, -708.5, (T, E)).astype(np.float32)
+    l[1::2, 3:] = np.where(np.arange(3, E) == 17, l[1::2, 3:], -np.inf)  # (three of them, and the largest)
+    for k in (1, 2, 6):
+        for b in ([bias] if bias is not None else [None, np.zeros(E, np.float32)]):
+            r = dict(score=score, renorm=True, scale=scale, select_bias=b)
+            idx, w = qs.moe_select(torch.from_numpy(l).cuda(), k, to_rule(r, torch, qs))
+            assert w.isfinite().all()
+            if k < 4:
+                assert ((w.double().sum(1) / scale - 1).abs() < 1e-6).all()
+            check_select(idx, w, l.astype(np.float64), k, r, (score, scale, k))
+
+
 def test_strided_logits_and_caller_buffers(torch, qs):
     E, k, T = 100, 5, 37
     r = rule_for("bias", E, k)
