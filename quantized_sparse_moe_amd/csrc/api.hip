@@ -708,13 +708,17 @@ moe_status lora_gemm(const void *a, const void *b, const float *scales, const in
     if (!yr.ok() || (base && !br.ok())) return MOE_ERR_INVALID;
     if (rows_clash(yr, br, T, true) || rows_clash(yr, xr, T, false)) return MOE_ERR_INVALID;
     const size_t nb = yr.bytes(T), need = lora_workspace_size(T, R);
-    if (overlap(y, nb, a, (size_t)(n_adapters * R * K) * 2) || overlap(y, nb, b, (size_t)(n_adapters * N * R) * 2) ||
-        overlap(y, nb, ids, (size_t)T * 4) || (scales && overlap(y, nb, scales, (size_t)n_adapters * 4)) ||
-        (ranks && overlap(y, nb, ranks, (size_t)n_adapters * 4)))
-        return MOE_ERR_INVALID;
+    const struct {
+        const void *p;
+        size_t n;
+    } in[] = {{a, (size_t)(n_adapters * R * K) * 2}, {b, (size_t)(n_adapters * N * R) * 2}, {ids, (size_t)T * 4},
+              {scales, (size_t)n_adapters * 4},      {ranks, (size_t)n_adapters * 4}};
+    for (const auto &q : in)
+        if (q.p && overlap(y, nb, q.p, q.n)) return MOE_ERR_INVALID;
     if (!ws || !aligned(ws, ALIGN) || ws_bytes < need) return MOE_ERR_WORKSPACE;
-    if (overlap(y, nb, ws, need) || overlap(x, xr.bytes(T), ws, need) || overlap(ids, (size_t)T * 4, ws, need) ||
-        (base && overlap(base, br.bytes(T), ws, need)))
+    for (const auto &q : in)
+        if (q.p && overlap(q.p, q.n, ws, need)) return MOE_ERR_INVALID;
+    if (overlap(y, nb, ws, need) || overlap(x, xr.bytes(T), ws, need) || (base && overlap(base, br.bytes(T), ws, need)))
         return MOE_ERR_INVALID;
     LoraArgs g{};
     g.a = (const uint16_t *)a;

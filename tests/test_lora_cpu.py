@@ -51,6 +51,12 @@ def test_limits_workspace_and_nothing_to_do():
         q.lora_workspace_size(5, 12)
 
 
+@pytest.mark.parametrize("kw", [dict(a=A + 6 * S), dict(b=A + 6 * S + 256), dict(scales=A + 6 * S), dict(ranks=A + 6 * S + 4),
+                                dict(a=A + 6 * S - 4 * 16 * 64 * 2 + 16), dict(b=A + 6 * S - 4 * 80 * 16 * 2 + 16)])
+def test_a_workspace_over_the_adapters_is_refused(kw):
+    assert call(**kw) == q.MOE_ERR_INVALID
+
+
 def test_binding_checks_its_arguments():
     import torch
     a, b = torch.zeros(3, 8, 16, dtype=torch.bfloat16), torch.zeros(3, 24, 8, dtype=torch.bfloat16)
