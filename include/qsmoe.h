@@ -258,7 +258,7 @@ typedef struct {
  * A rule applied to logits that are there already.
  *   logits   [T][n_experts], row stride ld (elements, >= n_experts), MOE_BF16, MOE_F16 or MOE_F32
  *   topk_idx [T][top_k] int32 ascending, topk_w [T][top_k] fp32 (written)
- * The outputs must not overlap the logits or each other (MOE_ERR_INVALID).
+ * The outputs must not overlap the logits, select_bias or each other (MOE_ERR_INVALID).
  * Limits: T <= 2^20, n_experts <= 256, top_k <= min(n_experts, 16).  T == 0 enqueues nothing.
  */
 moe_status moe_select(const moe_router_rule *rule, const void *logits, int32_t dtype, int64_t T, int64_t n_experts,

@@ -617,6 +617,9 @@ moe_status moe_select(const moe_router_rule *rule, const void *logits, int32_t d
     const size_t nl = Rows{logits, dtype, ld, n_experts}.bytes(T), nk = (size_t)(T * top_k) * 4;
     if (overlap(topk_idx, nk, topk_w, nk) || overlap(topk_idx, nk, logits, nl) || overlap(topk_w, nk, logits, nl))
         return MOE_ERR_INVALID;
+    const void *bias = rule->select_bias;
+    const size_t nbias = (size_t)n_experts * 4;
+    if (bias && (overlap(topk_idx, nk, bias, nbias) || overlap(topk_w, nk, bias, nbias))) return MOE_ERR_INVALID;
     return dev(launch_select(to_rule(rule, n_experts), logits, dtype, T, (int)n_experts, ld, top_k, topk_idx, topk_w,
                              (hipStream_t)stream));
 }

@@ -62,6 +62,12 @@ def test_select_arguments():
         assert select(rule(), **kw) == q.MOE_ERR_INVALID, kw        # (T = 4: 4096 bytes of logits, 128 of results)
 
 
+def test_select_results_over_the_bias_are_refused():
+    far = dict(idx=FAKE + (1 << 32), w=FAKE + (2 << 32), logits=FAKE + (3 << 32))
+    for kw in (dict(idx=FAKE), dict(w=FAKE + 1020), dict(w=FAKE - 124)):     # (256 values of bias, 128 bytes of results)
+        assert select(rule(), **dict(far, **kw)) == q.MOE_ERR_INVALID, kw
+
+
 def test_layer_calls_need_a_rule_and_keep_their_checks():
     L, d, r = q.lib(), desc(), rule()
     fwd = lambda d, r, x=FAKE, T=4, yt=q.MOE_F32, ws=FAKE, n=1 << 40: L.moe_layer_forward_rule(
