@@ -488,6 +488,11 @@ moe_status lora_gemm(const void *a, const void *b, const float *scales, const in
                      int64_t R, int64_t K, int64_t N, const int32_t *ids, const void *x, int64_t T, int64_t ldx,
                      const void *base, int64_t ldb, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
                      void *stream);
+/* What lora_gemm would return for these arguments before it enqueues anything: for callers that enqueue
+ * the base first. */
+moe_status lora_gemm_check(const void *a, const void *b, const float *scales, const int32_t *ranks, int64_t n_adapters,
+                           int64_t R, int64_t K, int64_t N, const int32_t *ids, const void *x, int64_t T, int64_t ldx,
+                           const void *base, int64_t ldb, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes);
 
 /*
  * Measured ceilings ([LILY] "Limits of further optimization": kernels are judged

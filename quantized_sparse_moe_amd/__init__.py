@@ -78,7 +78,7 @@ EXPORTS = ("moe_abi_version", "moe_status_string", "moe_workspace_size",
            "moe_block_norm", "q8_gemv", "q8_quantize_x", "q8_gemv_q8x", "q8_gemv_qx",
            "q8_pack_rows16", "mx4_codes_size", "mx4_scales_size", "mx4_quantize", "mx4_dequantize",
            "mx4_pack_rows16", "mx4_gemm_workspace_size", "mx4_gemm", "mx4_gemm_mx4x",
-           "lora_workspace_size", "lora_gemm", "moe_calib_read", "moe_calib_mfma")
+           "lora_workspace_size", "lora_gemm", "lora_gemm_check", "moe_calib_read", "moe_calib_mfma")
 
 
 def lib() -> ctypes.CDLL:
@@ -145,6 +145,8 @@ def lib() -> ctypes.CDLL:
         L.lora_workspace_size.argtypes = [I64, I64]
         L.lora_gemm.restype = I32
         L.lora_gemm.argtypes = [P, P, P, P, I64, I64, I64, I64, P, P, I64, I64, P, I64, P, I32, I64, P, SZ, P]
+        L.lora_gemm_check.restype = I32
+        L.lora_gemm_check.argtypes = L.lora_gemm.argtypes[:-1]
         L.moe_calib_read.restype = I32
         L.moe_calib_read.argtypes = [P, SZ, P]
         L.moe_calib_mfma.restype = I32
@@ -881,13 +883,13 @@ def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspa
     if adapters is not None:
         if adapters.N != N or adapters.K != K:
             _mx4_bad("mx4_gemm", "the adapters are of a matrix of another size")
-        _lora_ids(adapters, adapter_ids, x.shape[0], "mx4_gemm")
-        if adapter_workspace is None:
-            adapter_workspace = lora_new_workspace(adapters, x.shape[0], stream)
-        elif _mx4_buf(adapter_workspace, lora_workspace_size(x.shape[0], adapters.R), "mx4_gemm") % 256:
-            raise QsmoeError(MOE_ERR_WORKSPACE, "mx4_gemm: adapter_workspace must be 256-byte aligned")
-        y = mx4_gemm(w_codes, w_scales, N, K, x, y, y_dtype, workspace, stream)
-        return lora_gemm(adapters, adapter_ids, x, base=y, y=y, workspace=adapter_workspace, stream=stream)
+        # (refused before the product is enqueued)
+        y, gpu, here, st, keep, args = _lora_args("mx4_gemm", adapters, adapter_ids, x, None, y, y_dtype, adapter_workspace,
+                                                  stream, True)
+        _mx4_call("mx4_gemm", lib().lora_gemm_check, gpu, here, *args)
+        mx4_gemm(w_codes, w_scales, N, K, x, y, None, workspace, stream)
+        _mx4_call("mx4_gemm", lib().lora_gemm, gpu, here, *args, st)
+        return y
     T, k, ldx, code = _mx4_values(x, "mx4_gemm")
     if k != K or code != MOE_BF16:
         _mx4_bad("mx4_gemm", "x must be bf16 with K columns")
@@ -944,25 +946,22 @@ def lora_new_workspace(adapters: LoraAdapters, T: int, stream=None):
     return _empty((max(lora_workspace_size(T, adapters.R), 256),), _torch().uint8, adapters.a.device, stream)
 
 
-def _lora_ids(adapters: LoraAdapters, ids, T: int, where: str) -> None:
-    if ids is None or ids.dtype != _torch().int32 or ids.shape != (T,) or not ids.is_contiguous():
-        _mx4_bad(where, "adapter ids must be contiguous int32 [T]")
-
-
-def lora_gemm(adapters: LoraAdapters, ids, x, base=None, y=None, y_dtype=None, workspace=None, stream=None):
-    """``y`` [T, N] = ``base`` + scale B (A x) with each token's adapter (``ids`` int32 [T]; out of range: none)
-    for ``x`` [T, K] (bf16).  ``base`` (None: zeros) has y's type; ``y=base`` adds in place."""
-    where = "lora_gemm"
+def _lora_args(where: str, adapters: LoraAdapters, ids, x, base, y, y_dtype, workspace, stream, in_place: bool = False):
+    """(y, GPU, whether it is the current device, stream handle, the workspace, the C call's arguments but the
+    stream), checked for what the C call cannot see; in_place: base is y."""
     T, k, ldx, code = _mx4_values(x, where)
     N = adapters.N
     if k != adapters.K or code != MOE_BF16:
         _mx4_bad(where, "x must be bf16 with K columns")
-    _lora_ids(adapters, ids, T, where)
+    if ids is None or ids.dtype != _torch().int32 or ids.shape != (T,) or not ids.is_contiguous():
+        _mx4_bad(where, "adapter ids must be contiguous int32 [T]")
     if y is None:
         y = _empty((T, N), y_dtype or (_torch().float32 if base is None else base.dtype), x.device, stream)
     rows, cols, ldy, code = _mx4_values(y, where)
     if rows != T or cols != N:
         _mx4_bad(where, "y must be [T, N]")
+    if in_place:
+        base = y
     pb, ldb = None, 0
     if base is not None:
         rows, cols, ldb, bcode = _mx4_values(base, where)
@@ -973,8 +972,15 @@ def lora_gemm(adapters: LoraAdapters, ids, x, base=None, y=None, y_dtype=None, w
         workspace = lora_new_workspace(adapters, T, stream)
     gpu = x.get_device()
     st, here = _mx4_stream(where, stream, gpu, adapters.a, ids, y, base, workspace)
-    _mx4_call(where, lib().lora_gemm, gpu, here, *adapters._args, ids.data_ptr(), x.data_ptr(), T, ldx, pb, ldb,
-              y.data_ptr(), code, ldy, _mx4_buf(workspace, 0, where), workspace.nbytes, st)
+    return y, gpu, here, st, workspace, (*adapters._args, ids.data_ptr(), x.data_ptr(), T, ldx, pb, ldb, y.data_ptr(), code,
+                                         ldy, _mx4_buf(workspace, 0, where), workspace.nbytes)
+
+
+def lora_gemm(adapters: LoraAdapters, ids, x, base=None, y=None, y_dtype=None, workspace=None, stream=None):
+    """``y`` [T, N] = ``base`` + scale B (A x) with each token's adapter (``ids`` int32 [T]; out of range: none)
+    for ``x`` [T, K] (bf16).  ``base`` (None: zeros) has y's type; ``y=base`` adds in place."""
+    y, gpu, here, st, keep, args = _lora_args("lora_gemm", adapters, ids, x, base, y, y_dtype, workspace, stream)
+    _mx4_call("lora_gemm", lib().lora_gemm, gpu, here, *args, st)
     return y
 
 

@@ -693,10 +693,9 @@ size_t lora_workspace_size(int64_t T, int64_t R) {
     return T <= 0 ? 0 : up((size_t)T * LORA_PARTS * R * 2) + up((size_t)T * 4) * 2;
 }
 
-moe_status lora_gemm(const void *a, const void *b, const float *scales, const int32_t *ranks, int64_t n_adapters,
-                     int64_t R, int64_t K, int64_t N, const int32_t *ids, const void *x, int64_t T, int64_t ldx,
-                     const void *base, int64_t ldb, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
-                     void *stream) {
+moe_status lora_gemm_check(const void *a, const void *b, const float *scales, const int32_t *ranks, int64_t n_adapters,
+                           int64_t R, int64_t K, int64_t N, const int32_t *ids, const void *x, int64_t T, int64_t ldx,
+                           const void *base, int64_t ldb, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes) {
     if (T < 0 || N < 0 || n_adapters < 0) return MOE_ERR_INVALID;
     if (y_dtype != MOE_BF16 && y_dtype != MOE_F32) return MOE_ERR_INVALID;
     if (R < 8 || R > LORA_MAX_R || R % 8 || K < 8 || K > MX4_MAX_K || K % 8 || N > LORA_MAX_N ||
@@ -723,6 +722,16 @@ moe_status lora_gemm(const void *a, const void *b, const float *scales, const in
         if (q.p && overlap(q.p, q.n, ws, need)) return MOE_ERR_INVALID;
     if (overlap(y, nb, ws, need) || overlap(x, xr.bytes(T), ws, need) || (base && overlap(base, br.bytes(T), ws, need)))
         return MOE_ERR_INVALID;
+    return MOE_OK;
+}
+
+moe_status lora_gemm(const void *a, const void *b, const float *scales, const int32_t *ranks, int64_t n_adapters,
+                     int64_t R, int64_t K, int64_t N, const int32_t *ids, const void *x, int64_t T, int64_t ldx,
+                     const void *base, int64_t ldb, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
+                     void *stream) {
+    const moe_status s = lora_gemm_check(a, b, scales, ranks, n_adapters, R, K, N, ids, x, T, ldx, base, ldb, y, y_dtype, ldy, ws,
+                                         ws_bytes);
+    if (s || T == 0 || N == 0) return s;
     LoraArgs g{};
     g.a = (const uint16_t *)a;
     g.b = (const uint16_t *)b;

@@ -82,6 +82,40 @@ def test_binding_checks_its_arguments():
         q.mx4_gemm(None, None, 24, 16, x, adapters=ad, adapter_ids=ids, adapter_workspace=torch.zeros(8, dtype=torch.uint8))
 
 
+def test_adapters_are_checked_before_a_product_is_enqueued(monkeypatch):
+    """mx4_gemm(adapters=): whatever lora_gemm refuses, y is not written first.  (Host tensors, taken as if
+    they were on a GPU but in the first case; every call is refused.)"""
+    import torch
+    enqueued = []
+    monkeypatch.setattr(q, "_mx4_product", lambda *a: enqueued.append(a))
+    bf = torch.bfloat16
+    a, b = torch.zeros(3, 8, 32, dtype=bf), torch.zeros(3, 24, 8, dtype=bf)
+    x, ids = torch.zeros(5, 32, dtype=bf), torch.zeros(5, dtype=torch.int32)
+    buf = torch.zeros(1 << 14, dtype=torch.uint8)
+    buf = buf[-buf.data_ptr() % 256:]
+    ws = buf[:8192]
+
+    def refused(ad=q.LoraAdapters(a, b), N=24, ids=ids, y=None, ws=ws, **kw):
+        with pytest.raises(q.QsmoeError):
+            q.mx4_gemm(None, None, N, 32, x, y=y, adapters=ad, adapter_ids=ids, adapter_workspace=ws, **kw)
+        assert not enqueued
+
+    refused()                                                # another device
+    monkeypatch.setattr(q, "_mx4_stream", lambda *a: (0, True))
+    many = q.LoraAdapters(torch.zeros(65537, 8, 8, dtype=bf), torch.zeros(65537, 1, 8, dtype=bf))
+    with pytest.raises(q.QsmoeError):
+        q.mx4_gemm(None, None, 1, 8, x[:, :8].contiguous(), adapters=many, adapter_ids=ids, adapter_workspace=ws)
+    refused(q.LoraAdapters(torch.zeros(3 * 8 * 32 + 1, dtype=bf)[1:].view(3, 8, 32), b))     # not aligned
+    over = ws.view(torch.float32)
+    refused(y=over[:120].view(5, 24))                        # y over the workspace
+    refused(ids=ws.view(torch.int32)[:5])
+    refused(y=b.view(-1)[:120].view(5, 24))                  # and over an adapter
+    refused(y_dtype=torch.float16)
+    refused(ws=buf[:64])
+    refused(ws=buf[64:8256])
+    assert not enqueued
+
+
 def test_reference_by_hand():
     a = np.array([[[1.0, 0.0], [0.0, 2.0]], [[1.0, 1.0], [0.0, 0.0]]])
     b = np.array([[[1.0, 1.0]], [[3.0, np.nan]]])
