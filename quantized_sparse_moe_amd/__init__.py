@@ -890,6 +890,8 @@ def mx4_gemm(w_codes, w_scales, N: int, K: int, x, y=None, y_dtype=None, workspa
         mx4_gemm(w_codes, w_scales, N, K, x, y, None, workspace, stream)
         _mx4_call("mx4_gemm", lib().lora_gemm, gpu, here, *args, st)
         return y
+    if adapter_ids is not None:
+        _mx4_bad("mx4_gemm", "adapter_ids without adapters")
     T, k, ldx, code = _mx4_values(x, "mx4_gemm")
     if k != K or code != MOE_BF16:
         _mx4_bad("mx4_gemm", "x must be bf16 with K columns")

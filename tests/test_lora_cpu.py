@@ -116,6 +116,13 @@ def test_adapters_are_checked_before_a_product_is_enqueued(monkeypatch):
     assert not enqueued
 
 
+def test_adapter_ids_without_adapters_are_refused(monkeypatch):
+    import torch
+    monkeypatch.setattr(q, "_mx4_product", lambda *a: pytest.fail("enqueued"))
+    with pytest.raises(q.QsmoeError):
+        q.mx4_gemm(None, None, 24, 32, torch.zeros(5, 32, dtype=torch.bfloat16), adapter_ids=torch.zeros(5, dtype=torch.int32))
+
+
 def test_reference_by_hand():
     a = np.array([[[1.0, 0.0], [0.0, 2.0]], [[1.0, 1.0], [0.0, 0.0]]])
     b = np.array([[[1.0, 1.0]], [[3.0, np.nan]]])
