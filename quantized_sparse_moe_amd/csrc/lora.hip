@@ -268,10 +268,11 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
         }
         // rows of this slot; in place, rows without an adapter stay
         const bool live = ti * 16 + n < a.T && tile.ord % slots == slot && (tile.id >= 0 || a.base != a.y);
-        // base, as its register quads
+        // (-0, which leaves every value of base as it is: rows without an adapter)
         f32x4 out[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i) out[i] = (f32x4){-0.f, -0.f, -0.f, -0.f};
+        // base, as its register quads
         u32x4 raw[F32 ? 4 : 2];
 #pragma unroll
         for (int i = 0; i < (F32 ? 4 : 2); ++i) {
@@ -351,10 +352,10 @@ __global__ __launch_bounds__(64 * (FEW ? SH_WAVES : EX_WAVES))
                     if (c >= N) continue;
                     float v = out[i][r];
                     if constexpr (F32) {
-                        if (a.base) v += ((const float *)a.base)[t * a.ldb + c];
+                        v += a.base ? ((const float *)a.base)[t * a.ldb + c] : 0.0f;
                         ((float *)a.y)[t * a.ldy + c] = v;
                     } else {
-                        if (a.base) v += bf16_to_f32(((const uint16_t *)a.base)[t * a.ldb + c]);
+                        v += a.base ? bf16_to_f32(((const uint16_t *)a.base)[t * a.ldb + c]) : 0.0f;
                         ((uint16_t *)a.y)[t * a.ldy + c] = f32_to_bf16(v);
                     }
                 }

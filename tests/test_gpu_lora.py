@@ -183,6 +183,23 @@ def test_in_place_leaves_tokens_without_adapter(torch, qs):
     assert (y.view(torch.int16)[3] == 0x7FA5).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,R", [(5, 64, 16), (5, 71, 16), (40, 128, 64), (40, 130, 64), (200, 192, 16)])
+def test_tokens_without_adapter_keep_the_sign_of_zero(torch, qs, T, N, R, dtype):
+    """y[t] = base[t] bit for bit where a token has no adapter, zeros of either sign and subnormal values among
+    them; without a base such rows are +0."""
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    d = make(torch, T, 64, N, R, 3, dtype=dtype)
+    d["ids"][1::2] = -1
+    d["base"][:, ::3] = -0.0
+    d["base"][:, 1::3] *= 0.0
+    d["base"][:, 5::9] = -1e-39
+    y = call(torch, qs, d, dtype)
+    assert torch.equal(y[1::2].view(bits), d["base"][1::2].view(bits))
+    check(d, y, dtype, "others")
+    assert (call(torch, qs, d, dtype, base=None)[1::2].view(bits) == 0).all()
+
+
 def test_offsets_past_32_bits(torch, qs):
     T, K, N, R = 4, 64, 48, 8
     d = make(torch, T, K, N, R, 3)
