@@ -170,7 +170,9 @@ __device__ __forceinline__ void shrink(const LoraArgs &a, const TileIds &tile, i
         uint16_t *d = v0 + tk * PARTS * R + r;
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-            const uint16_t h = f32_to_bf16(v);
+            uint16_t h = f32_to_bf16(v);
+            // (past bf16's largest value, within fp32's: that value, and the rest in the next part)
+            if (__builtin_isfinite(v) && (h & 0x7fff) == 0x7f80) --h;
             d[p * R] = h;
             v = __builtin_isfinite(v) ? v - bf16_to_f32(h) : 0.0f;
         }

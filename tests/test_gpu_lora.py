@@ -200,6 +200,28 @@ def test_tokens_without_adapter_keep_the_sign_of_zero(torch, qs, T, N, R, dtype)
     assert (call(torch, qs, d, dtype, base=None)[1::2].view(bits) == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N", [(3, 64), (3, 70), (20, 128)])
+def test_values_of_A_x_past_the_largest_bf16(torch, qs, T, N, dtype):
+    """scale A x between the largest values of bf16 and fp32 (rounded to bf16 it would be infinite) is carried
+    like any other."""
+    K, R = 32, 8
+    big = torch.finfo(torch.bfloat16).max
+    d = dict(a=torch.zeros(2, R, K), b=torch.zeros(2, N, R), x=torch.zeros(T, K), ids=torch.arange(T).int() % 2,
+             scales=torch.tensor([1 + 2.0 ** -8, -(1 + 2.0 ** -8 - 2.0 ** -20)]), ranks=None, base=torch.randn(T, N))
+    d["a"][:, 0, 0] = 1.0
+    d["x"][:, 0] = big
+    d["b"][:, :, 0] = torch.linspace(-1, 1, N) * 2.0 ** -100
+    D = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for k in ("a", "b", "x"):
+        d[k] = d[k].bfloat16()
+    d["base"] = d["base"].to(D)
+    d = {k: None if v is None else v.cuda() for k, v in d.items()}
+    y = call(torch, qs, d, dtype)
+    assert y.isfinite().all()
+    check(d, y, dtype, (T, N))
+
+
 def test_offsets_past_32_bits(torch, qs):
     T, K, N, R = 4, 64, 48, 8
     d = make(torch, T, K, N, R, 3)
