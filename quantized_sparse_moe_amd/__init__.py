@@ -448,7 +448,16 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 
-class RouterRule:
+class _Fixed:
+    """What holds the addresses of its tensors: an attribute is set once, so that none is replaced while calls
+    go on with the old one's memory (``x.t += 1`` and other writes into the tensor are fine)."""
+
+    def __setattr__(self, name, value):
+        if self.__dict__.setdefault(name, value) is not value:
+            raise QsmoeError(MOE_ERR_INVALID, f"{type(self).__name__}.{name} cannot be replaced: make a new one")
+
+
+class RouterRule(_Fixed):
     """How a token's experts and weights follow from its logits (``moe_router_rule``).
 
     ``score`` "softmax" (over all experts) or "sigmoid"; ``select_bias`` fp32 [n_experts] is added
@@ -535,7 +544,7 @@ MOE_ACT_NONE, MOE_ACT_SIGMOID, MOE_ACT_SILU = 0, 1, 2
 _ACTS = {"none": MOE_ACT_NONE, "sigmoid": MOE_ACT_SIGMOID, "silu": MOE_ACT_SILU}
 
 
-class Norm:
+class Norm(_Fixed):
     """A norm of ``moe_block_norm`` (``moe_norm``): ``kind`` "rms" or "layer", gain ``offset`` +
     ``weight`` [H] and ``bias`` [H] (bf16, fp16 or fp32, both of one type; either may be None)."""
 
@@ -908,7 +917,7 @@ def mx4_gemm_mx4x(w_codes, w_scales, N: int, K: int, x_codes, x_scales, T: int, 
 
 
 # ------------------------------------------------------------- low-rank adapters
-class LoraAdapters:
+class LoraAdapters(_Fixed):
     """Adapters of one projection: ``a`` [n, R, K] and ``b`` [n, N, R] bf16, ``scales`` fp32 [n]
     (default 1) and ``ranks`` int32 [n] (default R), all on one device."""
 

@@ -102,6 +102,25 @@ def test_rule_object_checks_its_arguments():
         q.moe_select(torch.zeros(2, 8), 2, q.RouterRule(), topk_w=torch.zeros(2, 2, dtype=torch.float64))
 
 
+def test_tensors_whose_addresses_are_held_cannot_be_replaced():
+    """A call after such an assignment would read the old tensor, which may be gone; writes into the tensors go
+    through."""
+    import torch
+    bf = torch.bfloat16
+    rule = q.RouterRule(score="sigmoid", select_bias=torch.zeros(8))
+    norm = q.Norm(weight=torch.ones(8), bias=torch.zeros(8))
+    ad = q.LoraAdapters(torch.zeros(2, 8, 16, dtype=bf), torch.zeros(2, 24, 8, dtype=bf), scales=torch.ones(2))
+    for o, name in ((rule, "select_bias"), (norm, "weight"), (norm, "bias"), (ad, "a"), (ad, "b"), (ad, "scales"), (ad, "ranks"),
+                    (ad, "N")):
+        old = getattr(o, name)
+        with pytest.raises(q.QsmoeError):
+            setattr(o, name, torch.ones(8))
+        assert getattr(o, name) is old
+    rule.select_bias += 1
+    norm.weight[:] = 2.0
+    assert rule.desc.select_bias == rule.select_bias.data_ptr() and (rule.select_bias == 1).all()
+
+
 def test_reference_by_hand():
     l = np.log(np.array([[1.0, 2.0, 4.0, 1.0, 3.0, 5.0, 0.0, 0.0]]) + 0.0, where=np.array([[1] * 6 + [0] * 2], bool),
                out=np.full((1, 8), -np.inf))
