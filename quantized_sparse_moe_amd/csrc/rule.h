@@ -24,9 +24,10 @@ namespace qs {
 
 namespace {
 
-// What cuts must be wider than, times 2 + the largest |bias|: the error of the difference of two sums of two scores in
-// fp32, the bias's addition (2^-24 of 1 + |bias|) included.  A sigmoid s from exp_near (2^-22.3 of itself, times
-// s (1 - s)) and a reciprocal with one step of Newton's (with 1 + e's rounding 2^-23 s) is off by less than
+// What cuts must be wider than, times 2 + the largest |bias| of a live expert (one that is not live is not compared: with
+// its infinite bias every token would be close, 44 us instead of 20): the error of the difference of two sums of
+// two scores in fp32, the bias's addition (2^-24 of 1 + |bias|) included.  A sigmoid s from exp_near (2^-22.3 of
+// itself, times s (1 - s)) and a reciprocal with one step of Newton's (with 1 + e's rounding 2^-23 s) is off by less than
 // 2^-22.4.  Softmax by __expf, off by (|x| + 2) 2^-23 of itself: less than 2^-20 (its sum of 256: |x| averages
 // at most ln 256 there), and 2^-21 for the sums and the reciprocal.
 constexpr float EDGE_SIGMOID = 1.0f / (1 << 20), EDGE_SOFTMAX = 1.0f / (1 << 17);
@@ -215,11 +216,11 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
             uint32_t m = 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                m = max(m, __float_as_uint(bias[i]) & 0x7fffffffu);
                 live[i] = live[i] && bias[i] > NONE;
+                m = max(m, live[i] ? __float_as_uint(bias[i]) & 0x7fffffffu : 0u);
                 c[i] = g[i] = g[i] + bias[i];
             }
-            edge = unit * (2.0f + __uint_as_float(wave_max_bcast(m)));   // (infinity, NaN: no cut is wide enough)
+            edge = unit * (2.0f + __uint_as_float(wave_max_bcast(m)));   // (infinity: no cut is wide enough)
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = v[i];

@@ -131,6 +131,24 @@ def test_crowded_scores(torch, qs, name, spread):
     check_select(idx, w, l.astype(np.float64), k, r, name)
 
 
+@pytest.mark.parametrize("name", ["bias", "softbias", "group2bias", "groupbias"])
+@pytest.mark.parametrize("spread", [1e-1, 1e-3, 1e-5])
+def test_disabled_experts(torch, qs, name, spread):
+    """Experts disabled by a bias of -infinity or NaN, or by their logit under a huge bias, beside scores on
+    either side of what fp32 decides: the cut's error is that of the others."""
+    E, k, T = 240, 6, 300
+    rng = np.random.default_rng(31)
+    l = (rng.uniform(-3, 3, (T, 1)) + spread * rng.standard_normal((T, E))).astype(np.float32)
+    r = rule_for(name, E, k)
+    b = (spread * rng.standard_normal(E)).astype(np.float32)
+    b[[3, 40, 41, 200]] = [-np.inf, -np.inf, np.nan, 3e38]
+    l[:, 200] = -np.inf
+    r["select_bias"] = b
+    idx, w = qs.moe_select(torch.from_numpy(l).cuda(), k, to_rule(r, torch, qs))
+    assert not np.isin(idx.cpu().numpy(), [3, 40, 41, 200]).any()
+    check_select(idx, w, l.astype(np.float64), k, r, (name, spread))
+
+
 @pytest.mark.parametrize("name", sorted(RULES))
 def test_masked_logits(torch, qs, name):
     """-infinity, NaN, the type's lowest value and +infinity; rows with few live experts or none."""
