@@ -172,7 +172,7 @@ __device__ __forceinline__ void shrink(const LoraArgs &a, const TileIds &tile, i
         for (int p = 0; p < PARTS; ++p) {
             uint16_t h = f32_to_bf16(v);
             // (past bf16's largest value, within fp32's: that value, and the rest in the next part)
-            if (__builtin_isfinite(v) && (h & 0x7fff) == 0x7f80) --h;
+            if (p == 0 && __builtin_isfinite(v) && (h & 0x7fff) == 0x7f80) --h;
             d[p * R] = h;
             v = __builtin_isfinite(v) ? v - bf16_to_f32(h) : 0.0f;
         }
