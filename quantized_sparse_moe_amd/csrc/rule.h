@@ -216,8 +216,8 @@ __device__ __forceinline__ Chosen wave_choose(const RouteRule &r, const float (&
             uint32_t m = 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                live[i] = live[i] && bias[i] > NONE;
-                m = max(m, live[i] ? __float_as_uint(bias[i]) & 0x7fffffffu : 0u);
+                live[i] = live[i] & (bias[i] > NONE);
+                m = max(m, __float_as_uint(live[i] ? bias[i] : 0.0f) & 0x7fffffffu);
                 c[i] = g[i] = g[i] + bias[i];
             }
             edge = unit * (2.0f + __uint_as_float(wave_max_bcast(m)));   // (infinity: no cut is wide enough)
