@@ -230,12 +230,13 @@ moe_status moe_layer_forward(const moe_layer_desc *d, const void *x, int64_t T,
  *   score     MOE_SCORE_SIGMOID  s_e = 1 / (1 + exp(-l_e))
  *             MOE_SCORE_SOFTMAX  s_e = exp(l_e) / sum of exp over all live experts
  *   select_bias  [n_experts] fp32 (or NULL): c_e = s_e + select_bias[e] is what experts are chosen
- *             by (their weights stay s_e); without it, the scores themselves
+ *             by (their weights stay s_e); without it, the scores themselves, in the order of the logits also
+ *             where 64 bits hold them equal (sigmoid above 37, softmax 745 below the largest)
  *   n_groups  groups of n_experts / n_groups consecutive experts, of which the group_top_k best stay:
  *             by the largest c of the group (MOE_GROUP_MAX) or by the sum of its two largest
  *             (MOE_GROUP_TOP2); ties go to the lower group.  1: no groups
  *   the top_k largest c of the groups that stay, ties to the lower expert id
- *   renorm    1: w_j = s_j / sum over the selected s;  0: w_j = s_j
+ *   renorm    1: w_j = s_j / sum over the selected s (0 where that sum is 0 in 64 bits);  0: w_j = s_j
  *   scale     a factor on every weight (finite)
  * An expert that is not live, or whose bias is NaN or -infinity, is chosen only when nothing else
  * is left, and has weight 0; a row without a live expert has weights 0.  Scores are formed and
@@ -309,7 +310,8 @@ moe_status moe_layer_forward_static(const moe_layer_desc *d, const void *x, int6
  *               gate_act MOE_ACT_NONE, MOE_ACT_SIGMOID 1 / (1 + exp(-g)), MOE_ACT_SILU g / (1 + exp(-g))
  *   weight, bias  [H] of the norm's dtype
  * Sums, norms and r' are fp32 until they are stored (pre reads r' before its rounding), so the mean
- * square must fit in fp32: |v| up to 2^63 or so.  NaN and infinities stay in their row.
+ * square must fit in fp32: |v| up to 2^63 or so.  A gate's sigmoid below fp32's normal range counts as 0.  NaN
+ * and infinities stay in their row.
  * r_out or x may be y, r or gate itself (same pointer, type and stride: in place), or other columns of the
  * same matrix; any other overlap with an input, and any of the outputs with each other, is
  * MOE_ERR_INVALID, as are a post, gate or r_out without y.
@@ -479,7 +481,9 @@ moe_status mx4_gemm_mx4x(const void *w_codes, const void *w_scales, int64_t N, i
  *           before and after (one for T tokens also serves fewer), apart from every other buffer; calls
  *           that share it must not overlap in time.
  * Products are exact and sums fp32; A_a x[t] times its scale is carried to 2^-16 of itself for a bf16 y,
- * to 2^-24 for an fp32 one.  A token's result does not depend on the other tokens.
+ * to 2^-24 for an fp32 one, as two or three parts: an infinity in B gives NaN where one of them is 0.  A token's result
+ * does not depend on the other tokens.  More than 65536 tokens are not ordered by adapter: where adapters
+ * change from token to token, such a call takes longer than pieces of 65536 (8 adapters: 2.5 times).
  * Limits (else MOE_ERR_UNSUPPORTED): R % 8 == 0, 8 <= R <= 256, K % 8 == 0, 8 <= K <= 65536, N <= 2^23,
  * 1 <= n_adapters <= 65536, T <= 2^20.  T == 0 or N == 0 enqueues nothing.
  */

@@ -215,7 +215,10 @@ struct LoraArgs {
 };
 constexpr int LORA_PARTS = 3;      // bf16 parts of a value of v, at most
 // whether tokens are ordered first: where reading an adapter's B once more for every tile that holds one of
-// its tokens costs more than the launch (lora.hip)
+// its tokens costs more than the launch (lora.hip).  Not past 65536 tokens: batches that long are prompts, whose tokens
+// come in runs, and one workgroup's pass over the ids would cost these more than it gives (us of 131072 tokens not
+// ordered and ordered: N = 2048, rank 16 in runs 392 and 500, mixed 1503 and 582; N = 16384, rank 32 in runs 2103 and 2217,
+// mixed 6629 and 2536)
 inline bool lora_ordered(int64_t T, int64_t n_adapters, int64_t N, int64_t R) {
     return n_adapters > 1 && T > 64 && T <= 65536 && (T / 16) * N * R >= 4 << 20;
 }

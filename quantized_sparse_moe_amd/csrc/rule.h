@@ -25,7 +25,7 @@ namespace qs {
 namespace {
 
 // What cuts must be wider than, times 2 + the largest |bias| of a live expert (one that is not live is not compared: with
-// its infinite bias every token would be close, 44 us instead of 20): the error of the difference of two sums of
+// its infinite bias every token would be close, 16384 x 256 44 us instead of 20): the error of the difference of two sums of
 // two scores in fp32, the bias's addition (2^-24 of 1 + |bias|) included.  A sigmoid s from exp_near (2^-22.3 of
 // itself, times s (1 - s)) and a reciprocal with one step of Newton's (with 1 + e's rounding 2^-23 s) is off by less than
 // 2^-22.4.  Softmax by __expf, off by (|x| + 2) 2^-23 of itself: less than 2^-20 (its sum of 256: |x| averages

@@ -1,7 +1,7 @@
 // select.hip -- experts and weights of tokens whose router logits are given (moe_select): one
 // wave per token over rule.h's selection, then the weights of a workgroup's tokens in one wave.
 //
-// Bound by the selection's own instructions, some 560 vector ones a token at 256 experts in 8 biased groups
+// Bound by the selection's own instructions, some 590 vector ones a token at 256 experts in 8 biased groups
 // (top-8: 18 a round; 44 to rank the groups; 30 cycles' worth of exponentials): 16384 tokens take 20 us,
 // where their 18 MB would pass in 3.7; 60 experts of softmax 11, one token 4.1 (a launch and a chain).
 // Two tokens a wave, 32 lanes each, take 29: what each lane does for twice as many experts outweighs the
